@@ -863,6 +863,153 @@ qsa_status qsa_block_select(const void *q, int32_t rows, int32_t H, const void *
 }  // extern "C"
 
 // ---------------------------------------------------------------------------
+// K/V cache
+
+namespace {
+
+qsa_status check_cache(const qsa_kv_cache *c)
+{
+    if (!c || !c->k || !c->v || !c->block_table) return QSA_ERR_INVALID_ARG;
+    if (c->num_pages < 1 || c->num_reqs < 1 || c->max_pages < 1 || c->hkv < 1) return QSA_ERR_INVALID_ARG;
+    if (c->dtype != QSA_KV_FP16 && c->dtype != QSA_KV_E4M3) return QSA_ERR_INVALID_ARG;
+    if (c->dtype == QSA_KV_E4M3 ? (!c->k_scale || !c->v_scale) : (c->k_scale || c->v_scale)) return QSA_ERR_INVALID_ARG;
+    if ((c->head_dim != 128 && c->head_dim != 256) || c->hkv > 1024) return QSA_ERR_UNSUPPORTED;
+    const int32_t P = c->page_tokens;
+    if (P < 8 || P > 256 || (P & (P - 1)) != 0) return QSA_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(c->num_pages) * P >= INT32_MAX || static_cast<int64_t>(c->max_pages) * P >= INT32_MAX)
+        return QSA_ERR_UNSUPPORTED;
+    if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->block_table, 4)) return QSA_ERR_INVALID_ARG;
+    return QSA_OK;
+}
+
+// Checks shared by the three calls; `any` is false when there is nothing to do.
+qsa_status check_batch(int32_t rows, int32_t n_reqs, const int32_t *seq_start, const int32_t *pos_start,
+                       const qsa_kv_cache *cache, bool *any)
+{
+    *any = false;
+    if (rows < 0 || n_reqs < 0) return QSA_ERR_INVALID_ARG;
+    const qsa_status st = check_cache(cache);
+    if (st != QSA_OK) return st;
+    if (n_reqs > cache->num_reqs || n_reqs > 65535) return QSA_ERR_UNSUPPORTED;
+    if (rows == 0 || n_reqs == 0) return QSA_OK;
+    if (!seq_start || !pos_start) return QSA_ERR_INVALID_ARG;
+    if (!aligned(seq_start, 4) || !aligned(pos_start, 4)) return QSA_ERR_INVALID_ARG;
+    *any = true;
+    return QSA_OK;
+}
+
+// A row array of `width` contiguous FP16 values per row.
+bool row_array_ok(const void *p, int64_t stride, int64_t width)
+{
+    return p && aligned(p, 16) && stride >= width && stride % 8 == 0 && stride < (int64_t{1} << 31);
+}
+
+KvParams kv_params(const qsa_kv_cache *c, int32_t rows, int32_t n_reqs, const int32_t *seq_start,
+                   const int32_t *pos_start, const DeviceInfo *d)
+{
+    KvParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.k = static_cast<uint8_t *>(c->k);
+    p.v = static_cast<uint8_t *>(c->v);
+    p.k_scale = c->k_scale;
+    p.v_scale = c->v_scale;
+    p.block_table = c->block_table;
+    p.seq_start = seq_start;
+    p.pos_start = pos_start;
+    p.rows = rows;
+    p.n_reqs = n_reqs;
+    p.num_pages = c->num_pages;
+    p.page_tokens = c->page_tokens;
+    p.page_shift = log2_exact(c->page_tokens);
+    p.max_pages = c->max_pages;
+    p.hkv = c->hkv;
+    p.head_dim = c->head_dim;
+    p.e4m3 = c->dtype == QSA_KV_E4M3;
+    p.status = d->status;
+    return p;
+}
+
+}  // namespace
+
+extern "C" {
+
+qsa_status qsa_kv_store(const void *k, int64_t k_stride, const void *v, int64_t v_stride, int32_t rows,
+                        int32_t n_reqs, const int32_t *seq_start, const int32_t *pos_start,
+                        const qsa_kv_cache *cache, void *stream)
+{
+    g_launches = 0;
+    bool any;
+    qsa_status st = check_batch(rows, n_reqs, seq_start, pos_start, cache, &any);
+    if (st != QSA_OK || !any) return st;
+    const int64_t width = static_cast<int64_t>(cache->hkv) * cache->head_dim;
+    if (!row_array_ok(k, k_stride, width) || !row_array_ok(v, v_stride, width)) return QSA_ERR_INVALID_ARG;
+    DeviceInfo *d = nullptr;
+    if ((st = device_info(&d)) != QSA_OK) return st;
+    return launch_rc(launch_kv_store(kv_params(cache, rows, n_reqs, seq_start, pos_start, d), k, k_stride, v, v_stride,
+                                     d->sms, stream));
+}
+
+qsa_status qsa_kv_load(void *k, int64_t k_stride, void *v, int64_t v_stride, int32_t rows, int32_t n_reqs,
+                       const int32_t *seq_start, const int32_t *pos_start, const qsa_kv_cache *cache, void *stream)
+{
+    g_launches = 0;
+    bool any;
+    qsa_status st = check_batch(rows, n_reqs, seq_start, pos_start, cache, &any);
+    if (st != QSA_OK || !any) return st;
+    const int64_t width = static_cast<int64_t>(cache->hkv) * cache->head_dim;
+    if (!row_array_ok(k, k_stride, width) || !row_array_ok(v, v_stride, width)) return QSA_ERR_INVALID_ARG;
+    DeviceInfo *d = nullptr;
+    if ((st = device_info(&d)) != QSA_OK) return st;
+    return launch_rc(launch_kv_load(kv_params(cache, rows, n_reqs, seq_start, pos_start, d), k, k_stride, v, v_stride,
+                                    d->sms, stream));
+}
+
+size_t qsa_chunk_attention_workspace_bytes(int32_t rows, int32_t hq, int32_t hkv, int32_t head_dim)
+{
+    (void)rows;
+    (void)hq;
+    (void)hkv;
+    (void)head_dim;
+    return 256;
+}
+
+qsa_status qsa_chunk_attention(const void *q, int64_t q_stride, int32_t rows, int32_t hq, int32_t n_reqs,
+                               const int32_t *seq_start, const int32_t *pos_start, const qsa_kv_cache *cache,
+                               int32_t window, float scale, void *out, void *ws, size_t ws_bytes, void *stream)
+{
+    g_launches = 0;
+    bool any;
+    if (hq < 1 || window < 0 || !(scale > 0.0f) || !std::isfinite(scale)) return QSA_ERR_INVALID_ARG;
+    qsa_status st = check_batch(rows, n_reqs, seq_start, pos_start, cache, &any);
+    if (st != QSA_OK) return st;
+    if (hq % cache->hkv != 0 || hq / cache->hkv > 128) return QSA_ERR_UNSUPPORTED;
+    if (!any) return QSA_OK;
+    const int64_t width = static_cast<int64_t>(hq) * cache->head_dim;
+    if (static_cast<int64_t>(rows) * hq >= INT32_MAX) return QSA_ERR_UNSUPPORTED;
+    if (!row_array_ok(q, q_stride, width) || !out || !aligned(out, 16)) return QSA_ERR_INVALID_ARG;
+    if (!ws || ws_bytes < qsa_chunk_attention_workspace_bytes(rows, hq, cache->hkv, cache->head_dim))
+        return QSA_ERR_WORKSPACE;
+    if (!aligned(ws, 256)) return QSA_ERR_INVALID_ARG;
+    DeviceInfo *d = nullptr;
+    if ((st = device_info(&d)) != QSA_OK) return st;
+    ChunkParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.kv = kv_params(cache, rows, n_reqs, seq_start, pos_start, d);
+    p.q = q;
+    p.q_stride = q_stride;
+    p.out = out;
+    p.hq = hq;
+    p.group = hq / cache->hkv;
+    p.window = window;
+    p.scale = scale;
+    p.ws = static_cast<uint8_t *>(ws);
+    p.wait_limit_ns = g_wait_ns;
+    return launch_rc(launch_chunk(p, d->sms, g_overlap, stream));
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
 // Allocation-free variant: the workspace is a buffer inside the library.
 
 namespace {

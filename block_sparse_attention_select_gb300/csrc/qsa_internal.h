@@ -175,6 +175,30 @@ struct AttendParams {
     uint64_t wait_limit_ns;     // a tensor-core wait that takes longer gives up (QSA_ERR_TIMEOUT)
 };
 
+// K/V cache store, load and dense attention: see qsa_kv.cu and qsa_chunk.cu.
+struct KvParams {
+    uint8_t *k, *v;             // FP16 or E4M3 [num_pages, page_tokens, hkv, D]
+    uint8_t *k_scale, *v_scale; // E4M3: scale bytes [num_pages, page_tokens, hkv]
+    const int32_t *block_table; // [>= n_reqs, max_pages]
+    const int32_t *seq_start;   // [n_reqs + 1]
+    const int32_t *pos_start;   // [n_reqs]
+    int32_t rows, n_reqs, num_pages, page_tokens, page_shift, max_pages, hkv, head_dim;
+    int32_t e4m3;
+    uint32_t *status;
+};
+
+struct ChunkParams {
+    KvParams kv;
+    const void *q;              // FP16, row r at q + r * q_stride
+    int64_t q_stride;           // elements
+    void *out;                  // FP16 [rows, hq, D]
+    int32_t hq, group;          // query heads, query heads per KV head
+    int32_t window;             // 0: none
+    float scale;
+    uint8_t *ws;
+    uint64_t wait_limit_ns;
+};
+
 // Launchers (one translation unit each); return cudaError_t as int.  With
 // `overlap` the launch carries programmatic stream serialization: the kernel
 // may be scheduled while the previous kernel of the stream is still running
@@ -218,5 +242,10 @@ int launch_block_rows(const int32_t *row_req, const int32_t *row_token, int32_t 
 int launch_produce(const ProduceParams &p, int32_t max_tokens, void *stream);
 int launch_rope_table(float *table, int32_t n_blocks, int32_t rope_dim, double theta, void *stream);
 int launch_attend(const AttendParams &p, void *stream);
+// rows k, v (FP16, strides in elements) to the cache's slots, or back
+int launch_kv_store(const KvParams &p, const void *k, int64_t k_stride, const void *v, int64_t v_stride, int sms,
+                    void *stream);
+int launch_kv_load(const KvParams &p, void *k, int64_t k_stride, void *v, int64_t v_stride, int sms, void *stream);
+int launch_chunk(const ChunkParams &p, int sms, bool overlap, void *stream);
 
 }  // namespace qsa

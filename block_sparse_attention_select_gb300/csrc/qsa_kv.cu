@@ -1,0 +1,228 @@
+// K/V cache: new tokens written into their pages, as FP16 or quantised to E4M3
+// with a power-of-two scale per token and head, and read back as FP16.
+//
+// With e the least integer of [-15, 8] that has max |x| <= 448 * 2^e, a vector
+// x of head_dim values is stored as rne_e4m3(x * 2^-e) and the byte e + 127.
+// Scaling by a power of two is exact in FP32, so each value is rounded once.
+// The bounds of e make every stored value an FP16 number: the finest E4M3 step,
+// 2^-9, times 2^-15 is FP16's finest, and at e = 8 codes stop at 240 (240 * 256
+// < 65504 < 256 * 256).  A power of two costs no accuracy against a scale of
+// amax / 448: E4M3 is a floating type, only its range below the maximum moves,
+// by less than one binade of fourteen.
+//
+// Both are bound by memory: each vector is read once and written once.  A
+// vector belongs to head_dim / 8 lanes, 16 bytes of FP16 in each; the lanes
+// reduce the maximum by shuffles.  A CTA takes a few consecutive rows: its
+// warps first look up the rows' cache lines, then every thread issues its loads
+// (KV_BATCH vectors of one row set) before it uses the first.
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "qsa_device.cuh"
+#include "qsa_internal.h"
+#include "qsa_seq.cuh"
+
+namespace qsa {
+namespace {
+
+constexpr int KV_THREADS = 256;
+constexpr int KV_BATCH = 4;        // vectors in flight per thread
+constexpr int KV_MAX_ROWS = 32;    // rows per CTA
+
+// Cache line (page * page_tokens + slot) of each of the CTA's rows: -1 no
+// request or skipped, -2 a page outside the cache.
+__device__ __forceinline__ void find_lines(const KvParams &p, int32_t row0, int32_t rows_per_cta, int32_t *line)
+{
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int32_t i = warp; i < rows_per_cta; i += KV_THREADS / 32) {
+        const int32_t row = row0 + i;
+        int32_t l = -1;
+        const int32_t b = row < p.rows ? find_request(p, row, lane) : -1;
+        if (b >= 0) {
+            bool bad;
+            const Seq s = seq_of(p, b, &bad);
+            if (row >= s.s0 && row - s.s0 < s.n) {
+                const int32_t pos = s.p0 + (row - s.s0);
+                const int32_t page = __ldg(p.block_table + static_cast<int64_t>(b) * p.max_pages + (pos >> p.page_shift));
+                if (page >= 0 && page < p.num_pages) {
+                    l = (page << p.page_shift) + (pos & (p.page_tokens - 1));
+                } else {
+                    l = -2;
+                    if (lane == 0) record_error(p.status, ST_BAD_PAGE);
+                }
+            }
+        }
+        if (lane == 0) line[i] = l;
+    }
+    __syncthreads();
+}
+
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d)
+{
+    uint16_t lo, hi;
+    // the first source operand is the upper byte
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+    return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
+}
+
+__device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t two)
+{
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(two)));
+    return h;
+}
+
+// The scale exponent of a vector with largest magnitude a.
+__device__ __forceinline__ int scale_exponent(float a)
+{
+    const uint32_t u = __float_as_uint(a);
+    const int x = static_cast<int>(u >> 23) - 127;              // a = m * 2^x, 1 <= m < 2
+    const int e = (u & 0x7fffffu) <= 0x600000u ? x - 8 : x - 7;  // 448 = 1.75 * 2^8
+    return max(-15, min(8, e));
+}
+
+// LOAD false: rows k, v -> cache; true: cache -> rows.
+template <int D, bool E4M3, bool LOAD>
+__global__ void __launch_bounds__(KV_THREADS)
+kv_kernel(const KvParams p, uint8_t *kr, uint8_t *vr, int64_t k_stride, int64_t v_stride, int32_t rows_per_cta)
+{
+    constexpr int LPV = D / 8;                     // lanes per vector
+    constexpr int VPP = KV_THREADS / LPV;           // vectors per pass of the CTA
+    constexpr int ES = E4M3 ? 1 : 2;                // bytes of a cache element
+    __shared__ int32_t line[KV_MAX_ROWS];
+    wait_prior_grid();
+    if (blockIdx.x == 0) flag_bad_requests(p);
+    const int32_t row0 = blockIdx.x * rows_per_cta;
+    find_lines(p, row0, rows_per_cta, line);
+
+    const int sub = threadIdx.x / LPV, l = threadIdx.x % LPV;
+    const int32_t per_row = 2 * p.hkv;              // vectors of a row: K heads, then V heads
+    const int32_t n = rows_per_cta * per_row;
+    for (int32_t base = sub; base < n + sub; base += VPP * KV_BATCH) {     // the same trips for every thread
+        uint4 x[KV_BATCH];
+        int64_t vec[KV_BATCH];                      // (line, head) vector of the cache, negative: none
+        uint8_t *row[KV_BATCH];                     // this lane's 16 bytes of the row array
+        uint8_t sc[KV_BATCH];
+        bool is_v[KV_BATCH];
+#pragma unroll
+        for (int j = 0; j < KV_BATCH; ++j) {
+            const int32_t i = base + j * VPP;
+            vec[j] = -1;
+            x[j] = make_uint4(0u, 0u, 0u, 0u);
+            sc[j] = 0;
+            if (i < n) {
+                const int32_t r = i / per_row, hv = i - r * per_row;
+                const int32_t ln = line[r];
+                is_v[j] = hv >= p.hkv;
+                const int32_t h = is_v[j] ? hv - p.hkv : hv;
+                row[j] = (is_v[j] ? vr + (static_cast<int64_t>(row0) + r) * v_stride * 2
+                                  : kr + (static_cast<int64_t>(row0) + r) * k_stride * 2) + (h * D + l * 8) * 2;
+                vec[j] = ln < 0 ? ln : static_cast<int64_t>(ln) * p.hkv + h;
+                if (!LOAD) {
+                    if (ln >= 0) x[j] = __ldg(reinterpret_cast<const uint4 *>(row[j]));
+                } else if (ln >= 0) {
+                    const uint8_t *src = (is_v[j] ? p.v : p.k) + (vec[j] * D + l * 8) * ES;
+                    if (E4M3) {
+                        const uint2 u = *reinterpret_cast<const uint2 *>(src);
+                        x[j].x = u.x;
+                        x[j].y = u.y;
+                        sc[j] = (is_v[j] ? p.v_scale : p.k_scale)[vec[j]];
+                    } else {
+                        x[j] = *reinterpret_cast<const uint4 *>(src);
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < KV_BATCH; ++j) {
+            if constexpr (LOAD) {
+                if (vec[j] == -1) continue;
+                uint4 o = x[j];
+                if (E4M3 && vec[j] >= 0) {
+                    // code * 2^(byte - 127): exact in FP16 for the bytes that
+                    // kv_store writes; the product is taken in FP32 for the rest
+                    const float s = __uint_as_float(static_cast<uint32_t>(sc[j]) << 23);
+                    const uint32_t in[4] = {x[j].x & 0xffffu, x[j].x >> 16, x[j].y & 0xffffu, x[j].y >> 16};
+                    uint32_t w[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const uint32_t h = e4m3x2_to_half2(in[c]);
+                        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+                        const __half2 y = __floats2half2_rn(f.x * s, f.y * s);
+                        w[c] = *reinterpret_cast<const uint32_t *>(&y);
+                    }
+                    o = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+                *reinterpret_cast<uint4 *>(row[j]) = o;      // zeros for a page outside the cache
+            } else if constexpr (!E4M3) {
+                if (vec[j] >= 0) *reinterpret_cast<uint4 *>((is_v[j] ? p.v : p.k) + (vec[j] * D + l * 8) * 2) = x[j];
+            } else {
+                float f[8];
+                const uint32_t in[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const float2 t = __half22float2(*reinterpret_cast<const __half2 *>(&in[c]));
+                    f[2 * c] = t.x;
+                    f[2 * c + 1] = t.y;
+                }
+                float a = 0.0f;
+#pragma unroll
+                for (int c = 0; c < 8; ++c) a = fmaxf(a, fabsf(f[c]));        // a NaN does not count
+#pragma unroll
+                for (int o = LPV / 2; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+                const int e = a > 0.0f ? scale_exponent(a) : -15;
+                const float s = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    f[c] *= s;
+                    if (e == 8 && fabsf(f[c]) > 240.0f) f[c] = copysignf(240.0f, f[c]);
+                }
+                if (vec[j] >= 0) {
+                    *reinterpret_cast<uint2 *>((is_v[j] ? p.v : p.k) + vec[j] * D + l * 8) =
+                        make_uint2(e4m3x4(f[0], f[1], f[2], f[3]), e4m3x4(f[4], f[5], f[6], f[7]));
+                    if (l == 0) (is_v[j] ? p.v_scale : p.k_scale)[vec[j]] = static_cast<uint8_t>(e + 127);
+                }
+            }
+        }
+    }
+}
+
+template <bool LOAD>
+int launch(const KvParams &p, void *k, int64_t k_stride, void *v, int64_t v_stride, int sms, void *stream)
+{
+    // enough rows to fill the batch of loads once, but no fewer CTAs than SMs
+    const int vectors = KV_THREADS / (p.head_dim / 8) * KV_BATCH;
+    int rows_per_cta = std::max(1, std::min(KV_MAX_ROWS, vectors / (2 * p.hkv)));
+    rows_per_cta = std::max(1, std::min(rows_per_cta, p.rows / sms));
+    const dim3 grid((p.rows + rows_per_cta - 1) / rows_per_cta);
+    KvParams pp = p;
+    uint8_t *kr = static_cast<uint8_t *>(k), *vr = static_cast<uint8_t *>(v);
+    int32_t rpc = rows_per_cta;
+    void *args[] = {&pp, &kr, &vr, &k_stride, &v_stride, &rpc};
+    const void *f;
+    if (p.head_dim == 128)
+        f = p.e4m3 ? reinterpret_cast<const void *>(&kv_kernel<128, true, LOAD>)
+                   : reinterpret_cast<const void *>(&kv_kernel<128, false, LOAD>);
+    else
+        f = p.e4m3 ? reinterpret_cast<const void *>(&kv_kernel<256, true, LOAD>)
+                   : reinterpret_cast<const void *>(&kv_kernel<256, false, LOAD>);
+    return launch_kernel(f, grid, dim3(KV_THREADS), 0, static_cast<cudaStream_t>(stream), false, args);
+}
+
+}  // namespace
+
+int launch_kv_store(const KvParams &p, const void *k, int64_t k_stride, const void *v, int64_t v_stride, int sms,
+                    void *stream)
+{
+    return launch<false>(p, const_cast<void *>(k), k_stride, const_cast<void *>(v), v_stride, sms, stream);
+}
+
+int launch_kv_load(const KvParams &p, void *k, int64_t k_stride, void *v, int64_t v_stride, int sms, void *stream)
+{
+    return launch<true>(p, k, k_stride, v, v_stride, sms, stream);
+}
+
+}  // namespace qsa

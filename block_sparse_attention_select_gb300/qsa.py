@@ -31,6 +31,9 @@ QSA_ERR_CUDA = 7
 QSA_ERR_NO_DEVICE = 8
 QSA_ERR_STATIC_LIMIT = 9
 
+QSA_KV_FP16 = 0
+QSA_KV_E4M3 = 1
+
 QSA_CFG_PATH = 1
 QSA_CFG_WAIT_LIMIT_NS = 2
 QSA_CFG_KERNEL_TIMING = 3
@@ -61,6 +64,13 @@ class PagedKeysC(ctypes.Structure):
                 ("page_positions", ctypes.c_int32), ("head_dim", ctypes.c_int32),
                 ("block_table", ctypes.c_void_p), ("num_reqs", ctypes.c_int32),
                 ("max_pages_per_req", ctypes.c_int32)]
+
+
+class KVCacheC(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("num_pages", ctypes.c_int32),
+                ("page_tokens", ctypes.c_int32), ("hkv", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("block_table", ctypes.c_void_p), ("num_reqs", ctypes.c_int32), ("max_pages", ctypes.c_int32)]
 
 
 _lib = None
@@ -110,6 +120,15 @@ def load(path: str = LIB_PATH):
     lib.qsa_index_key_produce.restype = ctypes.c_int
     lib.qsa_index_key_produce.argtypes = [vp, vp, i32, vp, vp, i32, vp, ctypes.c_float, vp, i32, i32, i32,
                                           kp, vp]
+    cp = ctypes.POINTER(KVCacheC)
+    lib.qsa_kv_store.restype = ctypes.c_int
+    lib.qsa_kv_store.argtypes = [vp, i64, vp, i64, i32, i32, vp, vp, cp, vp]
+    lib.qsa_kv_load.restype = ctypes.c_int
+    lib.qsa_kv_load.argtypes = [vp, i64, vp, i64, i32, i32, vp, vp, cp, vp]
+    lib.qsa_chunk_attention_workspace_bytes.restype = sz
+    lib.qsa_chunk_attention_workspace_bytes.argtypes = [i32, i32, i32, i32]
+    lib.qsa_chunk_attention.restype = ctypes.c_int
+    lib.qsa_chunk_attention.argtypes = [vp, i64, i32, i32, i32, vp, vp, cp, i32, ctypes.c_float, vp, vp, sz, vp]
     _lib = lib
     return lib
 
@@ -308,6 +327,172 @@ def block_select(q, k_cache, block_table, row_req, row_token, k: int, out_idx=No
                                  ws.numel(), _stream(stream))
     _check(st, "qsa_block_select")
     return out_idx, out_val
+
+
+class KVCache:
+    """Paged K/V cache: k, v FP16 or float8_e4m3fn [num_pages, page_tokens, hkv,
+    head_dim] (quantised: with uint8 scale bytes k_scale, v_scale [num_pages,
+    page_tokens, hkv]), block_table int32 [B, max_pages]."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, block_table: torch.Tensor, k_scale=None, v_scale=None):
+        if k.dtype not in (torch.float16, torch.float8_e4m3fn):
+            raise TypeError(f"k must be torch.float16 or torch.float8_e4m3fn, got {k.dtype}")
+        _need(k, k.dtype, "k"), _need(v, k.dtype, "v"), _need(block_table, torch.int32, "block_table")
+        if k.dim() != 4 or k.shape != v.shape or block_table.dim() != 2:
+            raise ValueError("k and v must be [num_pages, page_tokens, hkv, head_dim], block_table [B, max_pages]")
+        quantised = k.dtype == torch.float8_e4m3fn
+        if quantised != (k_scale is not None) or quantised != (v_scale is not None):
+            raise ValueError("k_scale and v_scale go with a float8_e4m3fn cache, and with no other")
+        for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            if t is not None:
+                _need(t, torch.uint8, name)
+                if t.shape != k.shape[:3]:
+                    raise ValueError(f"{name} must be [num_pages, page_tokens, hkv]")
+        if any(t is not None and t.device != k.device for t in (v, block_table, k_scale, v_scale)):
+            raise ValueError("the tensors of a cache must be on one device")
+        self.k, self.v, self.block_table, self.k_scale, self.v_scale = k, v, block_table, k_scale, v_scale
+        self.device = k.device
+        npg, pt, self.hkv, self.head_dim = (int(x) for x in k.shape)
+        self.c = KVCacheC(k.data_ptr(), v.data_ptr(), 0 if k_scale is None else k_scale.data_ptr(),
+                          0 if v_scale is None else v_scale.data_ptr(), QSA_KV_E4M3 if quantised else QSA_KV_FP16,
+                          npg, pt, self.hkv, self.head_dim, block_table.data_ptr(), int(block_table.shape[0]),
+                          int(block_table.shape[1]))
+        self.ref = ctypes.byref(self.c)
+
+    @classmethod
+    def empty(cls, num_pages: int, page_tokens: int, hkv: int, head_dim: int, block_table: torch.Tensor,
+              quantised: bool = False):
+        """A cache with uninitialised pages on the block table's device."""
+        dev = block_table.device
+        shape = (int(num_pages), int(page_tokens), int(hkv), int(head_dim))
+        if not quantised:
+            return cls(torch.empty(shape, dtype=torch.float16, device=dev),
+                       torch.empty(shape, dtype=torch.float16, device=dev), block_table)
+        codes = [torch.empty(shape, dtype=torch.uint8, device=dev).view(torch.float8_e4m3fn) for _ in range(2)]
+        scales = [torch.empty(shape[:3], dtype=torch.uint8, device=dev) for _ in range(2)]
+        return cls(*codes, block_table, *scales)
+
+
+def _row_stride(t, cache: KVCache, heads: int, name: str) -> int:
+    """Checks an FP16 row array [rows, heads, head_dim] and returns its row
+    stride: rows may be slices of wider ones, a row itself is contiguous."""
+    if t.dtype != torch.float16:
+        raise TypeError(f"{name} must be {torch.float16}, got {t.dtype}")
+    if t.device != cache.device:
+        raise ValueError(f"{name} must be on the cache's device")
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[1] != heads or shape[2] != cache.head_dim:
+        raise ValueError(f"{name} must be [rows, {heads}, {cache.head_dim}], got {list(shape)}")
+    if stride[2] != 1 or (heads > 1 and stride[1] != cache.head_dim):
+        raise ValueError(f"each row of {name} must be contiguous")
+    return stride[0] if shape[0] > 1 else heads * cache.head_dim
+
+
+def _requests(seq_start, pos_start, cache: KVCache) -> int:
+    _need(seq_start, torch.int32, "seq_start"), _need(pos_start, torch.int32, "pos_start")
+    n = pos_start.shape[0]
+    if seq_start.dim() != 1 or pos_start.dim() != 1 or seq_start.shape[0] != n + 1:
+        raise ValueError("seq_start must be int32 [n + 1] and pos_start int32 [n]")
+    if seq_start.device != cache.device or pos_start.device != cache.device:
+        raise ValueError("seq_start and pos_start must be on the cache's device")
+    return n
+
+
+def _call(cache: KVCache, stream, fn, *args, made=()):
+    """fn(*args, stream) on the cache's device.  `made`: tensors that the call
+    allocated itself, on the current stream: their memory must not be handed out
+    again before the work on another stream is done."""
+    dev = cache.device
+    if stream is None:
+        handle = torch.cuda.current_stream(dev).cuda_stream
+    else:
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=dev)
+        handle = stream.cuda_stream
+        current = torch.cuda.current_stream(dev)
+        if handle != current.cuda_stream and made:
+            stream.wait_stream(current)
+            for t in made:
+                t.record_stream(stream)
+    if torch.cuda.current_device() == dev.index:
+        status = fn(*args, handle)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, handle)
+    if status != QSA_OK:
+        raise QSAError(status, fn.__name__)
+
+
+def kv_store(k, v, seq_start, pos_start, cache: KVCache, stream=None):
+    """Write the new tokens' keys and values (FP16 [T, hkv, head_dim], rows may be
+    strided) into their cache slots, quantised when the cache is.  Request b's
+    tokens are rows seq_start[b] .. seq_start[b + 1] - 1, at positions
+    pos_start[b] ..; rows past the last request are ignored."""
+    n = _requests(seq_start, pos_start, cache)
+    ks, vs = _row_stride(k, cache, cache.hkv, "k"), _row_stride(v, cache, cache.hkv, "v")
+    if k.shape[0] != v.shape[0]:
+        raise ValueError("k and v must have the same rows")
+    _call(cache, stream, load().qsa_kv_store, k.data_ptr(), ks, v.data_ptr(), vs, k.shape[0], n,
+          seq_start.data_ptr(), pos_start.data_ptr(), cache.ref)
+
+
+def kv_load(seq_start, pos_start, rows: int, cache: KVCache, out_k=None, out_v=None, stream=None):
+    """Read tokens pos_start[b] .. of each request back as FP16, into rows
+    seq_start[b] .. of (out_k, out_v) [rows, hkv, head_dim]; rows past the last
+    request are left as they are."""
+    n = _requests(seq_start, pos_start, cache)
+    made = []
+    if out_k is None or out_v is None:
+        new = [torch.empty((int(rows), cache.hkv, cache.head_dim), dtype=torch.float16, device=cache.device)
+               for x in (out_k, out_v) if x is None]
+        made = list(new)
+        out_k = new.pop(0) if out_k is None else out_k
+        out_v = new.pop(0) if out_v is None else out_v
+    ks, vs = _row_stride(out_k, cache, cache.hkv, "out_k"), _row_stride(out_v, cache, cache.hkv, "out_v")
+    if out_k.shape[0] != rows or out_v.shape[0] != rows:
+        raise ValueError("out_k and out_v must have `rows` rows")
+    _call(cache, stream, load().qsa_kv_load, out_k.data_ptr(), ks, out_v.data_ptr(), vs, int(rows), n,
+          seq_start.data_ptr(), pos_start.data_ptr(), cache.ref, made=made)
+    return out_k, out_v
+
+
+def chunk_attention_workspace_bytes(rows: int, hq: int, hkv: int, head_dim: int) -> int:
+    return int(load().qsa_chunk_attention_workspace_bytes(int(rows), int(hq), int(hkv), int(head_dim)))
+
+
+def alloc_chunk_attention_workspace(cache: KVCache, rows: int, hq: int) -> torch.Tensor:
+    n = chunk_attention_workspace_bytes(rows, hq, cache.hkv, cache.head_dim)
+    return torch.empty(n, dtype=torch.uint8, device=cache.device)
+
+
+def chunk_attention(q, seq_start, pos_start, cache: KVCache, window: int = 0, scale=None, out=None, ws=None,
+                    stream=None):
+    """Attention of new tokens (a prefill chunk, decode tokens, or both) over the
+    cache, which already holds them (kv_store): the row at position p attends
+    tokens p - window + 1 .. p of its request (window 0: all up to p).  q FP16 [T,
+    hq, head_dim] (rows may be strided); returns FP16 [T, hq, head_dim], rows
+    past the last request left as they are."""
+    n = _requests(seq_start, pos_start, cache)
+    hq = q.shape[1] if q.dim() == 3 else 0
+    qs = _row_stride(q, cache, hq, "q")
+    rows = q.shape[0]
+    made = []
+    if out is None:
+        out = torch.empty((rows, hq, cache.head_dim), dtype=torch.float16, device=cache.device)
+        made.append(out)
+    elif out.shape != q.shape or out.device != cache.device:
+        raise ValueError("out must have q's shape and device")
+    _need(out, torch.float16, "out")
+    if ws is None:
+        ws = alloc_chunk_attention_workspace(cache, rows, hq)
+        made.append(ws)
+    elif ws.device != cache.device or not ws.is_contiguous():
+        raise ValueError("ws must be contiguous, on the cache's device")
+    scale = cache.head_dim ** -0.5 if scale is None else float(scale)
+    _call(cache, stream, load().qsa_chunk_attention, q.data_ptr(), qs, rows, hq, n, seq_start.data_ptr(),
+          pos_start.data_ptr(), cache.ref, int(window), scale, out.data_ptr(), ws.data_ptr(),
+          ws.numel() * ws.element_size(), made=made)
+    return out
 
 
 def get_device_status(stream=None) -> int:

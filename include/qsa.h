@@ -220,6 +220,80 @@ qsa_status qsa_block_select(const void *q, int32_t rows, int32_t H, const void *
                             const int32_t *row_req, const int32_t *row_token, int32_t k, int32_t *out_idx,
                             float *out_val, void *ws, size_t ws_bytes, void *stream);
 
+/* ---- K/V cache: writing, reading back, and dense attention over it --------
+ * The paged cache that the sparse-attention consumer reads, and the attention
+ * of rows that select nothing (layers without an indexer, contexts no longer
+ * than the top-k).  A batch is described as for qsa_index_key_produce: request
+ * b's new tokens are rows seq_start[b] .. seq_start[b+1]-1 of the row arrays,
+ * at positions pos_start[b] ..; rows at or past seq_start[n_reqs] belong to no
+ * request (a padded batch) and are neither read nor written.  Token p of
+ * request b is in page block_table[b * max_pages + p / page_tokens], slot
+ * p % page_tokens.
+ *
+ * dtype QSA_KV_FP16: k and v are FP16 [num_pages, page_tokens, hkv, head_dim]
+ * and the scales are NULL.  QSA_KV_E4M3: k and v hold E4M3 codes in that layout,
+ * k_scale and v_scale one byte per token and head, [num_pages, page_tokens,
+ * hkv]: a code stands for code * 2^(byte - 127).  qsa_kv_store picks, for each
+ * vector of head_dim values x, the least e in [-15, 8] with max |x| <= 448 *
+ * 2^e (8 if there is none) and stores the nearest E4M3 value of x * 2^-e (ties
+ * to even; at e = 8 at most 240 in magnitude) and the byte e + 127.  So every
+ * stored value is an FP16 number, and reading back loses nothing more; a value
+ * is off by at most 1/16 of itself or 2^(e - 10), whichever is larger.
+ * Infinities are stored as the largest value, a NaN as NaN (it does not count
+ * for the scale).  Codes written by others may use any byte in [1, 254]; values
+ * beyond FP16's range then become infinite or lose bits when they are read.
+ *
+ * head_dim 128 or 256, page_tokens a power of two in [8, 256], 1 <= hkv <= 1024
+ * (QSA_ERR_UNSUPPORTED otherwise); k and v 16-byte aligned; num_pages *
+ * page_tokens and max_pages * page_tokens below 2^31.  n_reqs <= num_reqs.
+ * Device-side problems are reported by qsa_get_device_status(): a request whose
+ * seq_start or pos_start is out of range (decreasing, past `rows`, negative,
+ * past the block table) is skipped, a token whose page id is outside the cache
+ * is not written, reads back as zeros, and counts as a zero key and value in the
+ * attention. */
+#define QSA_KV_FP16 0
+#define QSA_KV_E4M3 1
+typedef struct {
+    void          *k, *v;
+    uint8_t       *k_scale, *v_scale;
+    int32_t        dtype;
+    int32_t        num_pages, page_tokens, hkv, head_dim;
+    const int32_t *block_table;        /* device int32 [num_reqs, max_pages] */
+    int32_t        num_reqs, max_pages;
+} qsa_kv_cache;
+
+/* Writes the new tokens' keys and values into the cache.  k, v: FP16, row r at
+ * k + r * k_stride elements, hkv * head_dim contiguous values; the strides
+ * multiples of 8 and at least hkv * head_dim, so a slice of a fused projection
+ * can be passed as it is; both 16-byte aligned.  Two requests that share a
+ * page must not write the same slot in one call. */
+qsa_status qsa_kv_store(const void *k, int64_t k_stride, const void *v, int64_t v_stride, int32_t rows,
+                        int32_t n_reqs, const int32_t *seq_start, const int32_t *pos_start,
+                        const qsa_kv_cache *cache, void *stream);
+
+/* The reverse: copies tokens pos_start[b] .. of each request out of the cache
+ * as FP16, into rows seq_start[b] .. of k and v (strided as above). */
+qsa_status qsa_kv_load(void *k, int64_t k_stride, void *v, int64_t v_stride, int32_t rows, int32_t n_reqs,
+                       const int32_t *seq_start, const int32_t *pos_start, const qsa_kv_cache *cache, void *stream);
+
+/* Attention of the new tokens (a prefill chunk, single decode tokens, or both
+ * in one batch) over the cache, which already holds them: the row at position
+ * p of request b attends tokens max(0, p - window + 1) .. p (window 0: 0 .. p),
+ * query head h reads KV head h / (hq / hkv),
+ *   out[r, h, :] = sum_t softmax_t(scale * q[r, h, :] . k_t) * v_t
+ * q: FP16, row r at q + r * q_stride elements (a multiple of 8, at least hq *
+ * head_dim), out: FP16 [rows, hq, head_dim]; both 16-byte aligned.  hq / hkv <=
+ * 128.  Pages that no row attends are not read (their table entries may hold
+ * anything), and cache slots that no row of the request attends may hold
+ * anything, NaN included; keys and values that some row attends must be
+ * finite.  ws: qsa_chunk_attention_workspace_bytes(...) bytes, 256-byte
+ * aligned; calls that may overlap need workspaces of their own (two captured
+ * graphs replayed on different streams, too). */
+size_t qsa_chunk_attention_workspace_bytes(int32_t rows, int32_t hq, int32_t hkv, int32_t head_dim);
+qsa_status qsa_chunk_attention(const void *q, int64_t q_stride, int32_t rows, int32_t hq, int32_t n_reqs,
+                               const int32_t *seq_start, const int32_t *pos_start, const qsa_kv_cache *cache,
+                               int32_t window, float scale, void *out, void *ws, size_t ws_bytes, void *stream);
+
 /* Static, NUL-terminated description of a status code. */
 const char *qsa_status_string(qsa_status status);
 
