@@ -882,6 +882,23 @@ qsa_status check_cache(const qsa_kv_cache *c)
     return QSA_OK;
 }
 
+// A cache as [tokens][hkv * head_dim], boxes of 128 bytes x box tokens: FP16 in
+// the tensor cores' swizzled layout, codes as they are.
+qsa_status make_tmap_kv(CUtensorMap *tm, const qsa_kv_cache *c, const void *base, int32_t box)
+{
+    const bool q8 = c->dtype == QSA_KV_E4M3;
+    const cuuint64_t width = static_cast<cuuint64_t>(c->hkv) * c->head_dim;
+    cuuint64_t dims[2] = {width, static_cast<cuuint64_t>(c->num_pages) * c->page_tokens};
+    cuuint64_t strides[1] = {width * (q8 ? 1 : 2)};
+    cuuint32_t boxes[2] = {q8 ? 128u : 64u, static_cast<cuuint32_t>(box)};
+    cuuint32_t estr[2] = {1, 1};
+    const CUresult r = g_encode(tm, q8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+                                const_cast<void *>(base), dims, strides, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                                q8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? QSA_OK : QSA_ERR_INVALID_ARG;
+}
+
 // Checks shared by the three calls; `any` is false when there is nothing to do.
 qsa_status check_batch(int32_t rows, int32_t n_reqs, const int32_t *seq_start, const int32_t *pos_start,
                        const qsa_kv_cache *cache, bool *any)
@@ -966,11 +983,8 @@ qsa_status qsa_kv_load(void *k, int64_t k_stride, void *v, int64_t v_stride, int
 
 size_t qsa_chunk_attention_workspace_bytes(int32_t rows, int32_t hq, int32_t hkv, int32_t head_dim)
 {
-    (void)rows;
-    (void)hq;
-    (void)hkv;
-    (void)head_dim;
-    return 256;
+    if (rows <= 0 || hq <= 0 || hkv <= 0 || head_dim <= 0) return 256;
+    return up(chunk_workspace_bytes(rows, std::max(1, hq / hkv), head_dim), 256);
 }
 
 qsa_status qsa_chunk_attention(const void *q, int64_t q_stride, int32_t rows, int32_t hq, int32_t n_reqs,
@@ -1003,8 +1017,16 @@ qsa_status qsa_chunk_attention(const void *q, int64_t q_stride, int32_t rows, in
     p.window = window;
     p.scale = scale;
     p.ws = static_cast<uint8_t *>(ws);
+    p.ws_rows = chunk_part_rows(rows, p.group);
     p.wait_limit_ns = g_wait_ns;
-    return launch_rc(launch_chunk(p, d->sms, g_overlap, stream));
+    CUtensorMap tk, tv;
+    int32_t box_k, box_v;
+    chunk_boxes(cache->head_dim, cache->page_tokens, &box_k, &box_v);
+    if ((st = make_tmap_kv(&tk, cache, cache->k, box_k)) != QSA_OK) return st;
+    if ((st = make_tmap_kv(&tv, cache, cache->v, box_v)) != QSA_OK) return st;
+    st = launch_rc(launch_chunk(p, &tk, &tv, d->sms, g_overlap, stream));
+    if (st == QSA_OK) ++g_launches;                      // the join kernel
+    return st;
 }
 
 }  // extern "C"

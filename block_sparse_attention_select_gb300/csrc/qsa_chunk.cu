@@ -1,10 +1,45 @@
 // Dense attention of new tokens over the paged K/V cache.
 //
-// One warp per (row, query head): the lanes share the head dimension, walk the
-// row's visible tokens and keep the running maximum, the sum and the weighted
-// values in FP32 (o <- o * exp(m - m') + exp(s - m') * v).
+//   o = sum_t exp(s_t - m) v_t / sum_t exp(s_t - m),   s_t = scale * q . k_t
+//
+// in one pass over the visible tokens t, with the running maximum m and sum.
+// Both products run on the 5th-generation tensor cores (kind::f16, FP32
+// accumulators in TMEM), tile by tile of 128 tokens:
+//   S[row, token] = Q . K^T     M = 128 rows, N = 128 tokens, K = D
+//   O[row, dim]  += P . V       M = 128 rows, N = D, K = 128 tokens
+// A row of the tile is one (token, query head) pair: the query heads of a KV
+// head share its keys and values, so a unit of work is 128 consecutive pairs
+// (token * group + head) of one request and KV head; a decode token fills
+// `group` of them.
+//
+// Work: the units' tiles, in the order (request, rows, KV head), form one line
+// of W tiles that the CTAs (one per SM) share out evenly, so one row over a
+// long cache, a batch of unequal requests and a long prompt all fill the card.
+// A unit that lies across CTAs leaves unnormalised FP32 partial sums with their
+// maxima in the workspace (at most two per CTA), which a second kernel joins.
+// Every CTA finds its share itself from seq_start and pos_start: no plan kernel
+// and no host knowledge of the lengths.
+//
+// A CTA's warps: 0-7 softmax (warp w: TMEM lane quarter w % 4 = 32 rows, half
+// w / 4 of a tile's tokens and of the output's dimensions), 8 loads K and V by
+// TMA, one box per page piece, through the block table, 9 issues the MMAs,
+// 10-13 load the queries and, from the E4M3 cache, turn the loaded codes into
+// FP16 tiles.  The MMA warp runs one score product ahead (two S buffers):
+//   S(0) S(1) | O(0) S(2) | O(1) S(3) | ...
+// so the softmax of a tile overlaps the products of its neighbours.  P goes
+// back into its S buffer's columns as FP16 and is the A operand of the second
+// product from there.  K and V share a ring of 32-KB slots in the order of use.
+//
+// The accumulator is rescaled only when a row's maximum has grown by more than
+// 2^8 since the one in use: P is then at most 256, far inside FP16, and the sum
+// uses the same stale maximum, so the result is the same.  Rounding P to FP16
+// (2^-11 of each weight) is of the size of the output's own rounding.
+#include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+
+#include <algorithm>
+#include <mutex>
 
 #include "qsa_device.cuh"
 #include "qsa_internal.h"
@@ -13,121 +48,979 @@
 namespace qsa {
 namespace {
 
-constexpr int CH_WARPS = 8;
+constexpr int CH_ROWS = 128;                 // (token, head) rows of a unit: MMA M
+constexpr int CH_TILE = 128;                 // tokens of a tile
+constexpr int CH_SOFT = 8;                   // softmax warps
+constexpr int CH_LOAD = CH_SOFT, CH_MMA = CH_SOFT + 1, CH_HELP = CH_SOFT + 2;
+constexpr int CH_HELPERS = 4;
+constexpr int CH_WARPS = CH_HELP + CH_HELPERS;
+constexpr int CH_THREADS = 32 * CH_WARPS;
+constexpr uint32_t SLOT = 32768;             // FP16 slot: 128 x 128 values
+constexpr uint32_t RAW = 16384;              // the same values as codes
+constexpr int RAWS = 4;
+constexpr float RESCALE = 8.0f;              // log2 of the growth that rescales
+constexpr uint32_t TM_S = 0, TM_O = 256;     // TMEM columns: two S buffers of 128, O
+constexpr int BAR_PAIR = 1, BAR_HELP = 5;    // named barriers: four softmax warp pairs, the helpers
 
-// N consecutive cache values from `src` (FP16 or E4M3 with scale s) as FP32.
-template <int N, bool E4M3>
-__device__ __forceinline__ void cache_values(const uint8_t *src, float s, float (&x)[N])
+template <int D, bool Q8>
+struct Shape {
+    static constexpr int QB = CH_ROWS * D * 2;                         // bytes of Q
+    static constexpr int NS = (229376 - QB - (Q8 ? RAWS * RAW : 0)) / SLOT;   // FP16 slots
+    static constexpr int PARTS = D / 128;                              // slots per tile, K or V
+    // K slot: 128 dims (two chunks of 64) of 128 tokens; V slot: all dims of VTOK tokens
+    static constexpr int VTOK = CH_TILE / PARTS;
+    static constexpr int VCHUNK = VTOK * 128;                          // bytes of a V chunk of 64 dims
+};
+
+struct Ctrl {
+    uint64_t full[8], empty[8], raw_full[RAWS], raw_empty[RAWS];
+    uint64_t s_full[2], p_full[2], o_done, q_full, q_free, drain;
+    float xch[2][2][CH_ROWS];                // [tile parity][half][row]: row maxima, sums
+    uint16_t scale[2][CH_TILE];              // [slot parity][token]: FP16 scale (E4M3)
+    int64_t warp_work[CH_WARPS];
+    int64_t w0, w1, total;                   // this CTA's tiles, all tiles
+    int32_t ctas;                            // CTAs that have work
+    int32_t b, m, g, off;                    // the unit of tile w0, and w0's place in it
+    uint32_t tmem;
+    int32_t abort;
+};
+
+// A unit that lies across CTAs, as the join kernel needs it (written by the
+// CTA that holds the unit's first tile).
+struct Split {
+    int32_t parts;                           // 0: none
+    int32_t rows;                            // rows of the unit
+    int32_t s0, v0, g;                       // request's first row, unit's first (token, head) pair, KV head
+};
+
+// Workspace: a Split per CTA, then per place (two for each CTA) the rows'
+// (maximum in powers of two, sum), then their unnormalised outputs.
+constexpr size_t WS_ML = 4096;
+constexpr size_t WS_O = WS_ML + size_t{2} * CHUNK_MAX_CTAS * CH_ROWS * 8;
+static_assert(sizeof(Split) * CHUNK_MAX_CTAS <= WS_ML, "workspace header");
+
+// ------------------------------------------------------------- work sharing --
+
+struct Unit {
+    int32_t v0, rows;                        // first pair, pairs in use
+    int32_t lo_tok, hi_tok;                  // tokens that some row attends: lo_tok .. hi_tok
+    int32_t lo, hi;                          // tiles lo .. hi - 1
+};
+
+__device__ __forceinline__ int32_t units_of(const ChunkParams &p, const Seq &s)
 {
-    if constexpr (E4M3) {
+    return (s.n * p.group + CH_ROWS - 1) / CH_ROWS;
+}
+
+__device__ __forceinline__ Unit unit_of(const ChunkParams &p, const Seq &s, int32_t m)
+{
+    Unit u;
+    u.v0 = m * CH_ROWS;
+    const int32_t end = min(s.n * p.group, u.v0 + CH_ROWS);
+    u.rows = end - u.v0;
+    const int32_t first = s.p0 + u.v0 / p.group;
+    u.hi_tok = s.p0 + (end - 1) / p.group;
+    u.lo_tok = p.window > 0 ? max(0, first - p.window + 1) : 0;
+    u.lo = u.lo_tok / CH_TILE;
+    u.hi = u.hi_tok / CH_TILE + 1;
+    return u;
+}
+
+__device__ __forceinline__ int64_t warp_sum(int64_t x)
+{
 #pragma unroll
-        for (int i = 0; i < N; i += 4) {
-            const uint32_t u = __ldg(reinterpret_cast<const uint32_t *>(src + i));
-            uint32_t h[2];
-            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h[0]) : "h"(static_cast<uint16_t>(u & 0xffffu)));
-            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h[1]) : "h"(static_cast<uint16_t>(u >> 16)));
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+
+__device__ __forceinline__ int64_t warp_scan(int64_t x, int lane)      // inclusive
+{
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[c]));
-                x[i + 2 * c] = f.x * s;
-                x[i + 2 * c + 1] = f.y * s;
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    return x;
+}
+
+// Tiles of request b over all its units and KV heads, for the warp's 32
+// requests b (one per lane): long requests are summed by the whole warp.
+__device__ __forceinline__ int64_t request_tiles(const ChunkParams &p, int32_t b, int lane, bool flag)
+{
+    Seq s{0, 0, 0};
+    if (b < p.kv.n_reqs) {
+        bool bad;
+        s = seq_of(p.kv, b, &bad);
+        if (bad && flag) record_error(p.kv.status, ST_BAD_ROW);
+    }
+    const int32_t n = units_of(p, s);
+    int64_t tiles = 0;
+    if (n <= 4)
+        for (int32_t m = 0; m < n; ++m) {
+            const Unit u = unit_of(p, s, m);
+            tiles += u.hi - u.lo;
+        }
+    uint32_t big = __ballot_sync(0xffffffffu, n > 4);
+    while (big) {
+        const int src = __ffs(big) - 1;
+        big &= big - 1;
+        Seq t;
+        t.s0 = __shfl_sync(0xffffffffu, s.s0, src);
+        t.n = __shfl_sync(0xffffffffu, s.n, src);
+        t.p0 = __shfl_sync(0xffffffffu, s.p0, src);
+        const int32_t nu = units_of(p, t);
+        int64_t x = 0;
+        for (int32_t m = lane; m < nu; m += 32) {
+            const Unit u = unit_of(p, t, m);
+            x += u.hi - u.lo;
+        }
+        x = warp_sum(x);
+        if (lane == src) tiles = x;
+    }
+    return tiles * p.kv.hkv;
+}
+
+// Fills c.w0, c.w1 and, when there is work, the unit that w0 lies in.
+__device__ __forceinline__ void find_work(const ChunkParams &p, Ctrl &c, int warp, int lane)
+{
+    // requests in equal runs of whole warps
+    const int32_t run = (p.kv.n_reqs + CH_THREADS - 1) / CH_THREADS * 32;
+    const int32_t first = warp * run;
+    int64_t mine = 0;
+    for (int32_t b = first; b < first + run && b < p.kv.n_reqs; b += 32)
+        mine += warp_sum(request_tiles(p, b + lane, lane, blockIdx.x == 0));
+    if (lane == 0) c.warp_work[warp] = mine;
+    __syncthreads();
+    int64_t total = 0, before = 0;
+#pragma unroll
+    for (int w = 0; w < CH_WARPS; ++w) {
+        if (w == warp) before = total;
+        total += c.warp_work[w];
+    }
+    // one tile each at least, so that the CTAs with work are the first ones
+    const int32_t ctas = static_cast<int32_t>(min(total, static_cast<int64_t>(gridDim.x)));
+    const bool any = static_cast<int32_t>(blockIdx.x) < ctas;
+    const int64_t w0 = any ? total * blockIdx.x / ctas : 0, w1 = any ? total * (blockIdx.x + 1) / ctas : 0;
+    if (warp == 0 && lane == 0) {
+        c.w0 = w0;
+        c.w1 = w1;
+        c.total = total;
+        c.ctas = ctas;
+    }
+    if (w0 < w1 && before <= w0 && w0 < before + mine) {
+        int64_t at = before;
+        for (int32_t b0 = first;; b0 += 32) {
+            const int64_t tiles = request_tiles(p, b0 + lane, lane, false);
+            const int64_t scan = warp_scan(tiles, lane);
+            const uint32_t past = __ballot_sync(0xffffffffu, at + scan > w0);
+            if (past) {
+                const int src = __ffs(past) - 1;
+                at += __shfl_sync(0xffffffffu, scan - tiles, src);
+                const int32_t b = b0 + src;
+                bool bad;
+                const Seq s = seq_of(p.kv, b, &bad);
+                const int32_t n = units_of(p, s);
+                for (int32_t m0 = 0; m0 < n; m0 += 32) {
+                    int64_t x = 0;
+                    int32_t len = 0;
+                    if (m0 + lane < n) {
+                        const Unit u = unit_of(p, s, m0 + lane);
+                        len = u.hi - u.lo;
+                        x = static_cast<int64_t>(len) * p.kv.hkv;
+                    }
+                    const int64_t sc = warp_scan(x, lane);
+                    const uint32_t in = __ballot_sync(0xffffffffu, at + sc > w0);
+                    if (in) {
+                        if (lane == __ffs(in) - 1) {
+                            const int32_t rest = static_cast<int32_t>(w0 - (at + sc - x));
+                            c.b = b;
+                            c.m = m0 + lane;
+                            c.g = rest / len;
+                            c.off = rest % len;
+                        }
+                        break;
+                    }
+                    at += __shfl_sync(0xffffffffu, sc, 31);
+                }
+                break;
             }
+            at += __shfl_sync(0xffffffffu, scan, 31);
+            if (b0 + 32 >= first + run) break;
+        }
+    }
+    __syncthreads();
+}
+
+// The CTA's share as segments: a run of tiles of one unit.
+struct Walk {
+    int64_t left;
+    int32_t b, m, g, off, n_units;
+    Seq s;
+    Unit u;
+    int32_t j0, j1;                          // the segment's tiles
+    bool whole, head;                        // all of the unit; the unit's first tile is here
+
+    __device__ __forceinline__ Walk(const ChunkParams &p, const Ctrl &c)
+    {
+        left = c.w1 - c.w0;
+        b = c.b;
+        m = c.m;
+        g = c.g;
+        off = c.off;
+        if (left > 0) load(p);
+    }
+    __device__ __forceinline__ void load(const ChunkParams &p)
+    {
+        bool bad;
+        s = seq_of(p.kv, b, &bad);
+        n_units = units_of(p, s);
+    }
+    // the next segment, false at the end of the share
+    __device__ __forceinline__ bool next(const ChunkParams &p)
+    {
+        if (left <= 0) return false;
+        while (m >= n_units) {               // empty requests have no units
+            if (++b >= p.kv.n_reqs) return false;
+            m = 0;
+            load(p);
+        }
+        u = unit_of(p, s, m);
+        j0 = u.lo + off;
+        j1 = min(static_cast<int64_t>(u.hi), j0 + left);
+        head = off == 0;
+        whole = head && j1 == u.hi;
+        left -= j1 - j0;
+        return true;
+    }
+    __device__ __forceinline__ void done(const ChunkParams &p)
+    {
+        off = 0;
+        if (++g == p.kv.hkv) {
+            g = 0;
+            ++m;
+        }
+    }
+};
+
+// ------------------------------------------------------------------- pieces --
+
+// The FP16 / E4M3 slots of a segment in the order of use:
+// K(0) K(1) V(0) K(2) V(1) ... K(n-1) V(n-2) V(n-1), each in PARTS slots.
+template <int PARTS>
+struct Slots {
+    int32_t n, i;                            // tiles of the segment, step of the sequence
+    __device__ __forceinline__ Slots(int32_t tiles) : n(tiles), i(0) {}
+    __device__ __forceinline__ bool next(bool *is_v, int32_t *tile, int32_t *part)
+    {
+        const int32_t e = i / PARTS;
+        *part = i % PARTS;
+        if (e >= 2 * n) return false;
+        if (e == 0) {
+            *is_v = false;
+            *tile = 0;
+        } else if (e == 2 * n - 1) {
+            *is_v = true;
+            *tile = n - 1;
+        } else {
+            *is_v = (e & 1) == 0;            // e = 1: K(1); 2: V(0); 3: K(2); ...
+            *tile = *is_v ? e / 2 - 1 : (e + 1) / 2;
+        }
+        ++i;
+        return true;
+    }
+};
+
+__device__ __forceinline__ uint32_t sw128(uint32_t row, uint32_t c)
+{
+    return (row >> 3) * 1024u + (row & 7u) * 128u + ((c ^ (row & 7u)) << 4);
+}
+
+// V as the B operand [token (K)][dim (N)]: dims contiguous, 128-byte swizzle;
+// chunks of 64 dims `chunk` bytes apart, groups of 8 tokens 1024 bytes apart.
+__device__ __forceinline__ uint64_t sw128_mn_desc(uint32_t smem_addr, uint32_t chunk)
+{
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((smem_addr & 0x3FFFFu) >> 4);
+    d |= static_cast<uint64_t>(chunk >> 4) << 16;              // leading byte offset
+    d |= static_cast<uint64_t>(1024 >> 4) << 32;               // stride byte offset
+    d |= static_cast<uint64_t>(1) << 46;
+    d |= static_cast<uint64_t>(2) << 61;
+    return d;
+}
+
+// D[tmem] (+)= A[tmem] * B[smem desc], kind::f16.
+__device__ __forceinline__ void umma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const uint32_t (&v)[32])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
+        "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+        "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ float exp2_approx(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ void named_barrier(int id, int threads)
+{
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// A wait by a whole warp: true on every lane, or false on every lane.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort, uint64_t lim)
+{
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, lim));
+}
+
+// ------------------------------------------------------------------- kernel --
+
+template <int D, bool Q8>
+__global__ void __launch_bounds__(CH_THREADS, 1)
+chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const ChunkParams p)
+{
+    using Sh = Shape<D, Q8>;
+    constexpr int NS = Sh::NS, PARTS = Sh::PARTS;
+    static_assert(NS >= 3 && NS <= 8, "ring");
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint8_t *q_s = smem, *ring = smem + Sh::QB, *raw = ring + NS * SLOT;
+    Ctrl &c = *reinterpret_cast<Ctrl *>(smem + 229376);
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    volatile int *abort = &c.abort;
+    const uint64_t lim = p.wait_limit_ns;
+
+    if (t == 0) {
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(&c.full[i], Q8 ? CH_HELPERS : 1);
+            mbar_init(&c.empty[i], 1);
+        }
+        for (int i = 0; i < RAWS; ++i) {
+            mbar_init(&c.raw_full[i], 1);
+            mbar_init(&c.raw_empty[i], CH_HELPERS);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&c.s_full[i], 1);
+            mbar_init(&c.p_full[i], CH_SOFT);
+        }
+        mbar_init(&c.o_done, 1);
+        mbar_init(&c.q_full, CH_HELPERS);
+        mbar_init(&c.q_free, 1);
+        mbar_init(&c.drain, 1);
+        c.abort = 0;
+        fence_barrier_init();
+    }
+    if (warp == CH_MMA) {
+        tmem_alloc(&c.tmem, 512);
+        tmem_relinquish();
+    }
+    wait_prior_grid();
+    find_work(p, c, warp, lane);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = c.tmem;
+    const uint32_t ring_a = smem_u32(ring);
+    Walk w(p, c);
+
+    if (warp == CH_LOAD) {
+        // ---------------------------------------------------------- K, V loads
+        uint8_t *dst0 = Q8 ? raw : ring;
+        constexpr int NSL = Q8 ? RAWS : NS;
+        constexpr uint32_t BYTES = Q8 ? RAW : SLOT;
+        constexpr int CE = Q8 ? 128 : 64;                    // elements of a 128-byte chunk
+        uint64_t *full = Q8 ? c.raw_full : c.full, *empty = Q8 ? c.raw_empty : c.empty;
+        const int32_t P = p.kv.page_tokens;
+        const int32_t box_k = min(P, CH_TILE), box_v = min(P, Sh::VTOK);
+        const int sh_k = __ffs(box_k) - 1, sh_v = __ffs(box_v) - 1;
+        uint32_t slot = 0, phase = 0, used = 0;              // used: slots loaded at least once
+        bool ok = true;
+        while (ok && w.next(p)) {
+            const int32_t *bt = p.kv.block_table + static_cast<int64_t>(w.b) * p.kv.max_pages;
+            Slots<PARTS> seq(w.j1 - w.j0);
+            bool is_v, have, is_v2 = false;
+            int32_t tile, part;
+            // this lane's box of a slot: chunk and token, and the token's cache row
+            int32_t x = 0, y = 0;
+            uint32_t at = 0;
+            bool mine = false;
+            auto plan = [&](bool v, int32_t tl, int32_t pt) {
+                const int sh = v ? sh_v : sh_k;
+                const int32_t toks = v ? Sh::VTOK : CH_TILE;
+                const int32_t nb = toks >> sh;               // boxes of a chunk
+                const int32_t chunks = static_cast<int32_t>(BYTES) / (toks * 128);
+                const int32_t ch = lane / nb, i = lane - ch * nb;
+                mine = ch < chunks;
+                const int32_t tok = (w.j0 + tl) * CH_TILE + (v ? pt * Sh::VTOK : 0) + (i << sh);
+                x = w.g * D + (v ? 0 : pt * 128) + ch * CE;
+                at = static_cast<uint32_t>(ch * toks * 128 + (i << sh) * 128);
+                // boxes without a visible token read zeros (a row past the cache)
+                y = p.kv.num_pages << p.kv.page_shift;
+                if (mine && tok <= w.u.hi_tok && tok + (1 << sh) > w.u.lo_tok) {
+                    const int32_t page = __ldg(bt + (tok >> p.kv.page_shift));
+                    if (page >= 0 && page < p.kv.num_pages) y = (page << p.kv.page_shift) + (tok & (P - 1));
+                    else record_error(p.kv.status, ST_BAD_PAGE);
+                }
+            };
+            have = seq.next(&is_v2, &tile, &part);
+            if (have) plan(is_v2, tile, part);
+            while (have) {
+                is_v = is_v2;
+                const int32_t xx = x, yy = y;
+                const uint32_t aa = at;
+                const bool mm = mine;
+                // the next slot's page lookups run under the wait for this one
+                have = seq.next(&is_v2, &tile, &part);
+                if (have) plan(is_v2, tile, part);
+                if (!warp_wait(&empty[slot], phase ^ 1u, abort, lim)) {
+                    ok = false;
+                    break;
+                }
+                if (lane == 0) mbar_arrive_expect_tx(&full[slot], BYTES);
+                __syncwarp();
+                if (mm) tma_load_2d(dst0 + slot * BYTES + aa, is_v ? &tv : &tk, &full[slot], xx, yy);
+                used = (used & ~(256u << slot)) | (1u << slot) | (phase << (slot + 8));
+                if (++slot == NSL) {
+                    slot = 0;
+                    phase ^= 1u;
+                }
+            }
+            w.done(p);
+        }
+        // copies still in flight (only after an abort: otherwise they were waited for)
+        if (lane == 0)
+            for (int i = 0; i < NSL; ++i)
+                if (used & (1u << i)) mbar_wait_bounded(&full[i], (used >> (8 + i)) & 1u, lim);
+        __syncwarp();
+    } else if (warp == CH_MMA) {
+        // --------------------------------------------------------------- MMAs
+        constexpr uint32_t idesc_s = umma_idesc_f16_f32(CH_ROWS, CH_TILE);
+        constexpr uint32_t idesc_o = umma_idesc_f16_f32(CH_ROWS, D) | (1u << 16);   // B: dims contiguous
+        const uint64_t qd = sw128_kmajor_desc(smem_u32(q_s));
+        uint32_t slot = 0, phase = 0, it = 0, seg = 0;
+        bool ok = true;
+        auto advance = [&] {
+            if (++slot == NS) {
+                slot = 0;
+                phase ^= 1u;
+            }
+        };
+        // S(i) = Q . K(i)^T
+        auto scores = [&](uint32_t i, bool last) {
+#pragma unroll
+            for (int part = 0; part < PARTS; ++part) {
+                if (ok) ok = warp_wait(&c.full[slot], phase, abort, lim);
+                if (!ok) return;
+                if (lane == 0) {
+                    tc_fence_after();
+                    const uint64_t kd = sw128_kmajor_desc(ring_a + slot * SLOT);
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk) {
+                        const uint32_t ch = kk >> 2, in = (kk & 3) * 32;
+                        umma_f16(tmem + TM_S + (i & 1u) * 128u, qd + (((2 * part + ch) * (CH_ROWS * 128u) + in) >> 4),
+                                 kd + ((ch * (CH_TILE * 128u) + in) >> 4), idesc_s, part + kk > 0 ? 1u : 0u);
+                    }
+                    umma_commit(&c.empty[slot]);
+                    if (part == PARTS - 1) {
+                        umma_commit(&c.s_full[i & 1u]);
+                        if (last) umma_commit(&c.q_free);
+                    }
+                }
+                advance();
+            }
+        };
+        while (ok && w.next(p)) {
+            const int32_t n = w.j1 - w.j0;
+            ok = warp_wait(&c.q_full, seg & 1u, abort, lim);
+            if (ok) scores(it, n == 1);
+            if (n > 1) scores(it + 1, n == 2);
+            for (int32_t j = 0; ok && j < n; ++j) {
+                const uint32_t i = it + j;
+                ok = warp_wait(&c.p_full[i & 1u], (i >> 1) & 1u, abort, lim);
+                const int32_t tok0 = (w.j0 + j) * CH_TILE;
+#pragma unroll
+                for (int part = 0; part < PARTS; ++part) {
+                    if (ok) ok = warp_wait(&c.full[slot], phase, abort, lim);
+                    if (!ok) break;
+                    if constexpr (!Q8) {
+                        // rows of V that nothing attends may hold anything: zero
+                        // weights must meet zeros (the loaded pages' ends only)
+                        const int32_t a = w.u.lo_tok - (tok0 + part * Sh::VTOK);
+                        const int32_t z = w.u.hi_tok + 1 - (tok0 + part * Sh::VTOK);
+                        if (a > 0 || z < Sh::VTOK) {
+                            uint8_t *v = ring + slot * SLOT;
+                            constexpr int PER_TOK = D / 8;       // 16-byte pieces of a token
+                            for (int32_t e = lane; e < Sh::VTOK * PER_TOK; e += 32) {
+                                const int32_t tok = e / PER_TOK, pc = e % PER_TOK;
+                                if (tok < a || tok >= z)
+                                    *reinterpret_cast<uint4 *>(v + (pc >> 3) * Sh::VCHUNK + tok * 128 + (pc & 7) * 16) =
+                                        make_uint4(0u, 0u, 0u, 0u);
+                            }
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                        }
+                    }
+                    if (lane == 0) {
+                        tc_fence_after();
+                        const uint64_t vd = sw128_mn_desc(ring_a + slot * SLOT, Sh::VCHUNK);
+#pragma unroll
+                        for (int kk = 0; kk < Sh::VTOK / 16; ++kk)
+                            umma_f16_ta(tmem + TM_O, tmem + TM_S + (i & 1u) * 128u + (part * (Sh::VTOK / 16) + kk) * 8u,
+                                        vd + ((kk * 2048u) >> 4), idesc_o, j + part + kk > 0 ? 1u : 0u);
+                        umma_commit(&c.empty[slot]);
+                        if (part == PARTS - 1) umma_commit(&c.o_done);
+                    }
+                    advance();
+                }
+                if (j + 2 < n) scores(i + 2, j + 3 == n);
+            }
+            it += n;
+            ++seg;
+            w.done(p);
+        }
+        if (!ok) {                                            // products still running
+            if (lane == 0) {
+                umma_commit(&c.drain);
+                mbar_wait_bounded(&c.drain, 0, lim);
+            }
+            __syncwarp();
+        }
+    } else if (warp >= CH_HELP) {
+        // ------------------------------------------ queries, E4M3 to FP16 tiles
+        const int ht = t - CH_HELP * 32;                      // 0 .. 127
+        uint32_t seg = 0, slot = 0, phase = 0, rslot = 0, rphase = 0;
+        bool ok = true;                                       // false: keep to the barriers, do nothing
+        while (w.next(p)) {
+            if (ok && seg > 0) ok = warp_wait(&c.q_free, (seg - 1) & 1u, abort, lim);
+            if (ok) {
+                constexpr int PC = D / 8;                      // 16-byte pieces of a row
+                const uint8_t *q = static_cast<const uint8_t *>(p.q);
+                const uint32_t qa = smem_u32(q_s);
+#pragma unroll 4
+                for (int e = ht; e < CH_ROWS * PC; e += 32 * CH_HELPERS) {
+                    const int row = e / PC, pc = e % PC;
+                    const bool in = row < w.u.rows;
+                    const int32_t v = w.u.v0 + row, tok = v / p.group, h = v - tok * p.group;
+                    const uint8_t *src = in ? q + ((static_cast<int64_t>(w.s.s0) + tok) * p.q_stride +
+                                                   (w.g * p.group + h) * D + pc * 8) * 2 : q;
+                    const uint32_t dst = qa + (pc >> 3) * (CH_ROWS * 128u) + sw128(row, pc & 7);
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0)
+                                 : "memory");
+                }
+                asm volatile("cp.async.wait_all;" ::: "memory");
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&c.q_full);
+            }
+            ++seg;
+            if constexpr (Q8) {
+                const int32_t *bt = p.kv.block_table + static_cast<int64_t>(w.b) * p.kv.max_pages;
+                Slots<PARTS> seq(w.j1 - w.j0);
+                bool v, v2 = false;
+                int32_t tile = 0, part = 0, a = 0, z = 0;
+                // the slot's first token, and this thread's token's scale byte
+                int32_t tok0 = 0;
+                uint32_t byte = 127;
+                auto look = [&] {
+                    tok0 = (w.j0 + tile) * CH_TILE + (v2 ? part * Sh::VTOK : 0);
+                    const int32_t tok = tok0 + ht;
+                    byte = 127;
+                    if (tok >= w.u.lo_tok && tok <= w.u.hi_tok && ht < (v2 ? Sh::VTOK : CH_TILE)) {
+                        const int32_t page = __ldg(bt + (tok >> p.kv.page_shift));
+                        if (page >= 0 && page < p.kv.num_pages)
+                            byte = __ldg((v2 ? p.kv.v_scale : p.kv.k_scale) +
+                                         ((static_cast<int64_t>(page) << p.kv.page_shift) + (tok & (p.kv.page_tokens - 1))) * p.kv.hkv + w.g);
+                    }
+                };
+                bool have = seq.next(&v2, &tile, &part);
+                if (have) look();
+                uint32_t par = 0;
+                while (have) {
+                    v = v2;
+                    a = w.u.lo_tok - tok0;
+                    z = w.u.hi_tok + 1 - tok0;
+                    // 2^(byte - 127) as FP16 (2^-15 is subnormal)
+                    const int e = max(112, min(135, static_cast<int>(byte))) - 127;
+                    const uint32_t s16 = e >= -14 ? static_cast<uint32_t>(e + 15) << 10 : 0x200u;
+                    c.scale[par][ht] = static_cast<uint16_t>(s16);
+                    have = seq.next(&v2, &tile, &part);
+                    if (have) look();                          // in flight under this slot's conversion
+                    if (ok) ok = warp_wait(&c.raw_full[rslot], rphase, abort, lim);
+                    if (ok) ok = warp_wait(&c.empty[slot], phase ^ 1u, abort, lim);
+                    named_barrier(BAR_HELP, 32 * CH_HELPERS);  // the scales are in
+                    if (ok) {
+                        const int pc = ht & 7;                 // 16 codes of a 128-byte row
+                        const uint8_t *src = raw + rslot * RAW + pc * 16;
+                        uint8_t *dst = ring + slot * SLOT;
+                        const int32_t toks = v ? Sh::VTOK : CH_TILE;
+                        uint4 in[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            in[i] = *reinterpret_cast<const uint4 *>(src + ((ht >> 3) + 16 * i) * 128);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int rr = (ht >> 3) + 16 * i;
+                            const int half = rr / toks, tk2 = rr - half * toks;      // 128 dims, token
+                            const uint32_t sc = c.scale[par][tk2] * 0x10001u;
+                            const uint32_t cw[4] = {in[i].x, in[i].y, in[i].z, in[i].w};
+                            uint32_t o[8];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
+                                    "cvt.rn.f16x2.e4m3x2 %0, lo;\n\tcvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+                                    : "=r"(o[2 * k]), "=r"(o[2 * k + 1])
+                                    : "r"(cw[k]));
+                            }
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(o[k]) : "r"(sc));
+                            if (v && (tk2 < a || tk2 >= z)) {
+#pragma unroll
+                                for (int k = 0; k < 8; ++k) o[k] = 0u;
+                            }
+                            // dims 16 pc .. of this half: chunk pc / 4, pieces 2 (pc % 4) and + 1;
+                            // lanes of the upper four pieces store the odd one first, which
+                            // spreads a row's eight stores over all banks
+                            uint8_t *ck = dst + (2 * half + (pc >> 2)) * (toks * 128);
+                            const uint32_t p0 = 2 * (pc & 3), first = pc >> 2;
+                            const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
+                            *reinterpret_cast<uint4 *>(ck + sw128(tk2, p0 + first)) = first ? hi : lo;
+                            *reinterpret_cast<uint4 *>(ck + sw128(tk2, p0 + 1 - first)) = first ? lo : hi;
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(&c.raw_empty[rslot]);
+                            mbar_arrive(&c.full[slot]);
+                        }
+                    }
+                    par ^= 1u;
+                    if (++slot == NS) {
+                        slot = 0;
+                        phase ^= 1u;
+                    }
+                    if (++rslot == RAWS) {
+                        rslot = 0;
+                        rphase ^= 1u;
+                    }
+                }
+            }
+            w.done(p);
         }
     } else {
+        // ------------------------------------------------------------- softmax
+        constexpr int OC = D / 2;                              // output columns per thread
+        const int lq = warp & 3, half = warp >> 2, row = lq * 32 + lane;
+        const uint32_t lane_base = static_cast<uint32_t>(lq * 32) << 16;
+        const float cs = p.scale * 1.4426950408889634f;        // scores in powers of two
+        uint32_t it = 0;
+        bool ok = true;                                        // false: keep to the barriers, do nothing
+        Split split = {0, 0, 0, 0, 0};
+        while (w.next(p)) {
+            const int32_t n = w.j1 - w.j0;
+            // rows past the unit's last behave like it (their queries are zeros)
+            const int32_t vr = min(w.u.v0 + row, w.u.v0 + w.u.rows - 1);
+            const int32_t pos = w.s.p0 + vr / p.group;
+            const int32_t first = p.window > 0 ? max(0, pos - p.window + 1) : 0;
+            const bool live = lq * 32 < w.u.rows;              // some row of this warp is in use
+            float m = -INFINITY, l = 0.0f;
+            for (int32_t j = 0; j < n; ++j, ++it) {
+                const uint32_t buf = it & 1u;
+                const uint32_t ts = tmem + TM_S + buf * 128u + lane_base;
+                if (ok) ok = warp_wait(&c.s_full[buf], (it >> 1) & 1u, abort, lim);
+                float s[64];
+                float mx = -INFINITY;
+                if (ok && live) {
+                    tc_fence_after();
+                    uint32_t u[32];
 #pragma unroll
-        for (int i = 0; i < N; i += 4) {
-            const uint2 u = __ldg(reinterpret_cast<const uint2 *>(src + 2 * i));
-            const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&u.x));
-            const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&u.y));
-            x[i] = a.x;
-            x[i + 1] = a.y;
-            x[i + 2] = b.x;
-            x[i + 3] = b.y;
+                    for (int k = 0; k < 2; ++k) {
+                        tmem_ld_32x32b_x32(ts + half * 64u + k * 32u, u);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) s[32 * k + i] = __uint_as_float(u[i]);
+                    }
+                    const int32_t base = (w.j0 + j) * CH_TILE + half * 64;
+                    const int32_t hi = pos - base, lo = first - base;         // visible: lo <= i <= hi
+                    if (__any_sync(0xffffffffu, hi < 63 || lo > 0)) {
+#pragma unroll
+                        for (int i = 0; i < 64; ++i)
+                            if (i > hi || i < lo) s[i] = -INFINITY;
+                    }
+                    float a0 = s[0], a1 = s[1], a2 = s[2], a3 = s[3];
+#pragma unroll
+                    for (int i = 4; i < 64; i += 4) {
+                        a0 = fmaxf(a0, s[i]);
+                        a1 = fmaxf(a1, s[i + 1]);
+                        a2 = fmaxf(a2, s[i + 2]);
+                        a3 = fmaxf(a3, s[i + 3]);
+                    }
+                    mx = fmaxf(fmaxf(a0, a1), fmaxf(a2, a3));
+                    c.xch[buf][half][row] = mx;
+                }
+                // both halves have read their scores and left their maxima
+                named_barrier(BAR_PAIR + lq, 64);
+                if (ok && live) {
+                    mx = fmaxf(mx, c.xch[buf][half ^ 1][row]);
+                    const bool grow = (mx - m) * cs > RESCALE;  // the same in both halves
+                    float alpha = 1.0f;
+                    if (grow) {
+                        alpha = exp2_approx((m - mx) * cs);     // 0 at the first
+                        m = mx;
+                    }
+                    const float mc = m == -INFINITY ? 0.0f : m * cs;
+                    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    uint32_t u[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const float e0 = exp2_approx(fmaf(s[2 * i], cs, -mc));
+                        const float e1 = exp2_approx(fmaf(s[2 * i + 1], cs, -mc));
+                        sum[i & 3] += e0 + e1;
+                        const __half2 h = __floats2half2_rn(e0, e1);
+                        u[i] = *reinterpret_cast<const uint32_t *>(&h);
+                    }
+                    tmem_st_x32(ts + half * 32u, u);
+                    l = fmaf(l, alpha, (sum[0] + sum[1]) + (sum[2] + sum[3]));
+                    if (j > 0) ok = warp_wait(&c.o_done, (it - 1) & 1u, abort, lim);
+                    if (ok && j > 0 && __any_sync(0xffffffffu, grow)) {
+                        tc_fence_after();
+                        const uint32_t to = tmem + TM_O + lane_base + half * OC;
+#pragma unroll
+                        for (int k = 0; k < OC / 32; ++k) {
+                            tmem_ld_32x32b_x32(to + k * 32u, u);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(__uint_as_float(u[i]) * alpha);
+                            tmem_st_x32(to + k * 32u, u);
+                        }
+                    }
+                    tmem_st_wait();
+                } else if (ok && j > 0) {
+                    ok = warp_wait(&c.o_done, (it - 1) & 1u, abort, lim);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (ok && lane == 0) mbar_arrive(&c.p_full[buf]);
+            }
+            // the segment's sums: its rows' output, or its part of it
+            if (ok) ok = warp_wait(&c.o_done, (it - 1) & 1u, abort, lim);
+            float *lx = &c.xch[it & 1u][0][0];                 // not the last tile's buffer
+            if (ok && live) lx[half * CH_ROWS + row] = l;
+            named_barrier(BAR_PAIR + lq, 64);
+            if (ok && live) l += lx[(half ^ 1) * CH_ROWS + row];
+            named_barrier(BAR_PAIR + lq, 64);                  // read before the next tile's maxima
+            if (ok && live) {
+                tc_fence_after();
+                const uint32_t to = tmem + TM_O + lane_base + half * OC;
+                const bool in = row < w.u.rows;
+                uint32_t u[32];
+                if (w.whole) {
+                    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+                    const int32_t v = w.u.v0 + row, tok = v / p.group, h = v - tok * p.group;
+                    __half *out = static_cast<__half *>(p.out) +
+                                  ((static_cast<int64_t>(w.s.s0) + tok) * p.hq + w.g * p.group + h) * D + half * OC;
+#pragma unroll
+                    for (int k = 0; k < OC / 32; ++k) {
+                        tmem_ld_32x32b_x32(to + k * 32u, u);
+                        tmem_ld_wait();
+                        if (in) {
+#pragma unroll
+                            for (int i = 0; i < 32; i += 8) {
+                                uint32_t x[4];
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const __half2 hh = __floats2half2_rn(__uint_as_float(u[i + 2 * e]) * inv,
+                                                                         __uint_as_float(u[i + 2 * e + 1]) * inv);
+                                    x[e] = *reinterpret_cast<const uint32_t *>(&hh);
+                                }
+                                *reinterpret_cast<uint4 *>(out + 32 * k + i) = make_uint4(x[0], x[1], x[2], x[3]);
+                            }
+                        }
+                    }
+                } else {
+                    // two places per CTA: 0 for a unit begun before it, 1 for one that goes on after it
+                    const int64_t place = 2 * static_cast<int64_t>(blockIdx.x) + (w.head ? 1 : 0);
+                    float *ml = reinterpret_cast<float *>(p.ws + WS_ML) + (place * CH_ROWS + row) * 2;
+                    float *part = reinterpret_cast<float *>(p.ws + WS_O) + (place * p.ws_rows + row) * D + half * OC;
+                    if (in && half == 0) {
+                        ml[0] = m == -INFINITY ? -INFINITY : m * cs;
+                        ml[1] = l;
+                    }
+#pragma unroll
+                    for (int k = 0; k < OC / 32; ++k) {
+                        tmem_ld_32x32b_x32(to + k * 32u, u);
+                        tmem_ld_wait();
+                        if (in) {
+#pragma unroll
+                            for (int i = 0; i < 32; i += 4)
+                                *reinterpret_cast<uint4 *>(part + 32 * k + i) = make_uint4(u[i], u[i + 1], u[i + 2], u[i + 3]);
+                        }
+                    }
+                }
+                tc_fence_before();
+            }
+            if (t == 0 && w.head && !w.whole) {
+                // the unit's other tiles lie in the next CTAs' shares
+                const int64_t end = c.w1 + (w.u.hi - w.j1);
+                split.parts = 1;
+                while (c.total * (blockIdx.x + split.parts) / c.ctas < end) ++split.parts;
+                split.rows = w.u.rows;
+                split.s0 = w.s.s0;
+                split.v0 = w.u.v0;
+                split.g = w.g;
+            }
+            w.done(p);
+        }
+        if (t == 0) reinterpret_cast<Split *>(p.ws)[blockIdx.x] = split;
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (t == 0 && c.abort) record_error(p.kv.status, ST_TIMEOUT);
+    if (warp == CH_MMA) tmem_dealloc(tmem, 512);
+    allow_next_grid();
+}
+
+// Joins the parts of each split unit: block x the unit that CTA x began (part 0
+// in its second place, part i in the first place of the i-th CTA after it), a
+// warp per row.
+template <int D>
+__global__ void __launch_bounds__(256)
+chunk_join_kernel(const ChunkParams p)
+{
+    constexpr int N = D / 32;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    wait_prior_grid();
+    const Split sp = reinterpret_cast<const Split *>(p.ws)[blockIdx.x];
+    const int32_t n = sp.parts;
+    if (n == 0) return;
+    const float2 *ml = reinterpret_cast<const float2 *>(p.ws + WS_ML);
+    const float *po = reinterpret_cast<const float *>(p.ws + WS_O);
+    auto place = [&](int32_t i) { return 2 * (static_cast<int64_t>(blockIdx.x) + i) + (i == 0 ? 1 : 0); };
+    for (int32_t row = blockIdx.y * 8 + warp; row < sp.rows; row += 8 * gridDim.y) {
+        float mx = -INFINITY, sum = 0.0f;
+        for (int32_t i = lane; i < n; i += 32) mx = fmaxf(mx, ml[place(i) * CH_ROWS + row].x);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        float acc[N];
+#pragma unroll
+        for (int e = 0; e < N; ++e) acc[e] = 0.0f;
+        for (int32_t i0 = 0; i0 < n; i0 += 32) {
+            float wt = 0.0f;
+            if (i0 + lane < n) {
+                const float2 x = ml[place(i0 + lane) * CH_ROWS + row];
+                wt = x.x == -INFINITY ? 0.0f : exp2_approx(x.x - mx);      // a part in which the row saw nothing
+                sum = fmaf(x.y, wt, sum);
+            }
+            const int32_t k = min(32, n - i0);
+#pragma unroll 4
+            for (int32_t i = 0; i < k; ++i) {
+                const float f = __shfl_sync(0xffffffffu, wt, i);
+                const float4 *src = reinterpret_cast<const float4 *>(po + (place(i0 + i) * p.ws_rows + row) * D) + lane;
+#pragma unroll
+                for (int e = 0; e < N / 4; ++e) {
+                    const float4 x = src[32 * e];
+                    acc[4 * e] = fmaf(x.x, f, acc[4 * e]);
+                    acc[4 * e + 1] = fmaf(x.y, f, acc[4 * e + 1]);
+                    acc[4 * e + 2] = fmaf(x.z, f, acc[4 * e + 2]);
+                    acc[4 * e + 3] = fmaf(x.w, f, acc[4 * e + 3]);
+                }
+            }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+        const int32_t v = sp.v0 + row, tok = v / p.group, h = v - tok * p.group;
+        __half *out = static_cast<__half *>(p.out) +
+                      ((static_cast<int64_t>(sp.s0) + tok) * p.hq + sp.g * p.group + h) * D;
+#pragma unroll
+        for (int e = 0; e < N / 4; ++e) {
+            const __half2 a = __floats2half2_rn(acc[4 * e] * inv, acc[4 * e + 1] * inv);
+            const __half2 b = __floats2half2_rn(acc[4 * e + 2] * inv, acc[4 * e + 3] * inv);
+            uint2 u;
+            u.x = *reinterpret_cast<const uint32_t *>(&a);
+            u.y = *reinterpret_cast<const uint32_t *>(&b);
+            reinterpret_cast<uint2 *>(out)[32 * e + lane] = u;
         }
     }
 }
 
-template <int D, bool E4M3>
-__global__ void __launch_bounds__(CH_WARPS * 32)
-chunk_rows_kernel(const ChunkParams p)
-{
-    constexpr int N = D / 32, ES = E4M3 ? 1 : 2;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    wait_prior_grid();
-    if (blockIdx.x == 0) flag_bad_requests(p.kv);
-    const int64_t task = static_cast<int64_t>(blockIdx.x) * CH_WARPS + warp;
-    const int32_t row = static_cast<int32_t>(task / p.hq), h = static_cast<int32_t>(task % p.hq);
-    if (row >= p.kv.rows) return;
-    const int32_t b = find_request(p.kv, row, lane);
-    if (b < 0) return;
-    bool bad;
-    const Seq s = seq_of(p.kv, b, &bad);
-    if (row < s.s0 || row - s.s0 >= s.n) return;
-    const int32_t pos = s.p0 + (row - s.s0);
-    const int32_t first = p.window > 0 ? max(0, pos - p.window + 1) : 0;
-    const int32_t g = h / p.group;
-    const int32_t *bt = p.kv.block_table + static_cast<int64_t>(b) * p.kv.max_pages;
+constexpr size_t CH_SMEM = 229376 + sizeof(Ctrl);
+static_assert(CH_SMEM <= 232448, "shared memory budget");
 
-    float q[N], o[N];
-    cache_values<N, false>(static_cast<const uint8_t *>(p.q) + (row * p.q_stride + h * D + lane * N) * 2, 1.0f, q);
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        q[i] *= p.scale;
-        o[i] = 0.0f;
-    }
-    float m = -INFINITY, sum = 0.0f;
-    for (int32_t t = first; t <= pos; ++t) {
-        const int32_t page = __ldg(bt + (t >> p.kv.page_shift));
-        float k[N], v[N];
-        if (page >= 0 && page < p.kv.num_pages) {
-            const int64_t vec = (static_cast<int64_t>(page << p.kv.page_shift) + (t & (p.kv.page_tokens - 1))) * p.kv.hkv + g;
-            float ks = 1.0f, vs = 1.0f;
-            if (E4M3) {
-                ks = __uint_as_float(static_cast<uint32_t>(p.kv.k_scale[vec]) << 23);
-                vs = __uint_as_float(static_cast<uint32_t>(p.kv.v_scale[vec]) << 23);
-            }
-            cache_values<N, E4M3>(p.kv.k + (vec * D + lane * N) * ES, ks, k);
-            cache_values<N, E4M3>(p.kv.v + (vec * D + lane * N) * ES, vs, v);
-        } else {
-            if (lane == 0) record_error(p.kv.status, ST_BAD_PAGE);
-#pragma unroll
-            for (int i = 0; i < N; ++i) k[i] = v[i] = 0.0f;
+template <int D, bool Q8>
+int launch(const ChunkParams &p, const void *tk, const void *tv, int grid, bool overlap, cudaStream_t stream)
+{
+    static std::mutex mu;
+    static bool done[64] = {};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 0 || dev >= 64) return static_cast<int>(cudaErrorInvalidDevice);
+    {
+        std::lock_guard<std::mutex> lk(mu);
+        if (!done[dev]) {
+            const cudaError_t e = cudaFuncSetAttribute(chunk_kernel<D, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                       static_cast<int>(CH_SMEM));
+            if (e != cudaSuccess) return static_cast<int>(e);
+            done[dev] = true;
         }
-        float dot = 0.0f;
-#pragma unroll
-        for (int i = 0; i < N; ++i) dot = fmaf(q[i], k[i], dot);
-#pragma unroll
-        for (int x = 16; x > 0; x >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, x);
-        const float m2 = fmaxf(m, dot);
-        const float a = __expf(m - m2), e = __expf(dot - m2);
-        m = m2;
-        sum = fmaf(sum, a, e);
-#pragma unroll
-        for (int i = 0; i < N; ++i) o[i] = fmaf(o[i], a, e * v[i]);
     }
-    const float inv = 1.0f / sum;
-    __half *out = static_cast<__half *>(p.out) + (static_cast<int64_t>(row) * p.hq + h) * D + lane * N;
-#pragma unroll
-    for (int i = 0; i < N; ++i) out[i] = __float2half_rn(o[i] * inv);
+    void *args[] = {const_cast<void *>(tk), const_cast<void *>(tv), const_cast<ChunkParams *>(&p)};
+    const int rc = launch_kernel(reinterpret_cast<const void *>(&chunk_kernel<D, Q8>), dim3(grid), dim3(CH_THREADS),
+                                 CH_SMEM, stream, false, args);
+    if (rc != 0) return rc;
+    void *join[] = {const_cast<ChunkParams *>(&p)};
+    const unsigned rows8 = static_cast<unsigned>(std::min(4, (p.ws_rows + 7) / 8));
+    return launch_kernel(reinterpret_cast<const void *>(&chunk_join_kernel<D>), dim3(grid, rows8), dim3(256), 0, stream,
+                         overlap, join);
 }
 
 }  // namespace
 
-int launch_chunk(const ChunkParams &p, int sms, bool overlap, void *stream)
+int32_t chunk_part_rows(int32_t rows, int32_t group)
 {
-    (void)sms;
-    (void)overlap;
-    const int64_t tasks = static_cast<int64_t>(p.kv.rows) * p.hq;
-    const dim3 grid(static_cast<unsigned>((tasks + CH_WARPS - 1) / CH_WARPS));
-    void *args[] = {const_cast<ChunkParams *>(&p)};
-    const void *f;
+    return static_cast<int32_t>(std::min<int64_t>(CH_ROWS, static_cast<int64_t>(rows) * group));
+}
+
+size_t chunk_workspace_bytes(int32_t rows, int32_t group, int32_t head_dim)
+{
+    return WS_O + size_t{2} * CHUNK_MAX_CTAS * chunk_part_rows(rows, group) * head_dim * 4;
+}
+
+// tokens per box of the K and V tensor maps
+void chunk_boxes(int32_t head_dim, int32_t page_tokens, int32_t *box_k, int32_t *box_v)
+{
+    *box_k = std::min(page_tokens, CH_TILE);
+    *box_v = std::min(page_tokens, CH_TILE * 128 / head_dim);
+}
+
+int launch_chunk(const ChunkParams &p, const void *tk, const void *tv, int sms, bool overlap, void *stream)
+{
+    const int grid = std::min(sms, static_cast<int>(CHUNK_MAX_CTAS));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (p.kv.head_dim == 128)
-        f = p.kv.e4m3 ? reinterpret_cast<const void *>(&chunk_rows_kernel<128, true>)
-                      : reinterpret_cast<const void *>(&chunk_rows_kernel<128, false>);
-    else
-        f = p.kv.e4m3 ? reinterpret_cast<const void *>(&chunk_rows_kernel<256, true>)
-                      : reinterpret_cast<const void *>(&chunk_rows_kernel<256, false>);
-    return launch_kernel(f, grid, dim3(CH_WARPS * 32), 0, static_cast<cudaStream_t>(stream), false, args);
+        return p.kv.e4m3 ? launch<128, true>(p, tk, tv, grid, overlap, s) : launch<128, false>(p, tk, tv, grid, overlap, s);
+    return p.kv.e4m3 ? launch<256, true>(p, tk, tv, grid, overlap, s) : launch<256, false>(p, tk, tv, grid, overlap, s);
 }
 
 }  // namespace qsa

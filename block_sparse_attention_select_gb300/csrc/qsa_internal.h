@@ -196,6 +196,7 @@ struct ChunkParams {
     int32_t window;             // 0: none
     float scale;
     uint8_t *ws;
+    int32_t ws_rows;            // rows of a partial output in the workspace
     uint64_t wait_limit_ns;
 };
 
@@ -246,6 +247,12 @@ int launch_attend(const AttendParams &p, void *stream);
 int launch_kv_store(const KvParams &p, const void *k, int64_t k_stride, const void *v, int64_t v_stride, int sms,
                     void *stream);
 int launch_kv_load(const KvParams &p, void *k, int64_t k_stride, void *v, int64_t v_stride, int sms, void *stream);
-int launch_chunk(const ChunkParams &p, int sms, bool overlap, void *stream);
+// tk, tv: 2-D tensor maps of the caches [num_pages * page_tokens][hkv * head_dim]
+// with boxes of 128 bytes (FP16: 128-byte swizzle) x chunk_boxes() tokens
+constexpr int32_t CHUNK_MAX_CTAS = 160;
+int launch_chunk(const ChunkParams &p, const void *tk, const void *tv, int sms, bool overlap, void *stream);
+int32_t chunk_part_rows(int32_t rows, int32_t group);
+size_t chunk_workspace_bytes(int32_t rows, int32_t group, int32_t head_dim);
+void chunk_boxes(int32_t head_dim, int32_t page_tokens, int32_t *box_k, int32_t *box_v);
 
 }  // namespace qsa

@@ -142,9 +142,8 @@ kv_kernel(const KvParams p, uint8_t *kr, uint8_t *vr, int64_t k_stride, int64_t 
                 if (vec[j] == -1) continue;
                 uint4 o = x[j];
                 if (E4M3 && vec[j] >= 0) {
-                    // code * 2^(byte - 127): exact in FP16 for the bytes that
-                    // kv_store writes; the product is taken in FP32 for the rest
-                    const float s = __uint_as_float(static_cast<uint32_t>(sc[j]) << 23);
+                    // code * 2^(byte - 127), exact in FP16
+                    const float s = __uint_as_float(static_cast<uint32_t>(max(112, min(135, int(sc[j])))) << 23);
                     const uint32_t in[4] = {x[j].x & 0xffffu, x[j].x >> 16, x[j].y & 0xffffu, x[j].y >> 16};
                     uint32_t w[4];
 #pragma unroll

@@ -240,8 +240,8 @@ qsa_status qsa_block_select(const void *q, int32_t rows, int32_t H, const void *
  * stored value is an FP16 number, and reading back loses nothing more; a value
  * is off by at most 1/16 of itself or 2^(e - 10), whichever is larger.
  * Infinities are stored as the largest value, a NaN as NaN (it does not count
- * for the scale).  Codes written by others may use any byte in [1, 254]; values
- * beyond FP16's range then become infinite or lose bits when they are read.
+ * for the scale).  Scale bytes outside [112, 135] are read as the nearer of the
+ * two.
  *
  * head_dim 128 or 256, page_tokens a power of two in [8, 256], 1 <= hkv <= 1024
  * (QSA_ERR_UNSUPPORTED otherwise); k and v 16-byte aligned; num_pages *
