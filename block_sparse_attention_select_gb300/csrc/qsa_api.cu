@@ -882,15 +882,15 @@ qsa_status check_cache(const qsa_kv_cache *c)
     return QSA_OK;
 }
 
-// A cache as [tokens][hkv * head_dim], boxes of 128 bytes x box tokens: FP16 in
-// the tensor cores' swizzled layout, codes as they are.
-qsa_status make_tmap_kv(CUtensorMap *tm, const qsa_kv_cache *c, const void *base, int32_t box)
+// A cache as [tokens][hkv * head_dim], boxes of `bytes` x `box` tokens: FP16 in
+// the tensor cores' swizzled layout (128 bytes), codes as they are.
+qsa_status make_tmap_kv(CUtensorMap *tm, const qsa_kv_cache *c, const void *base, int32_t bytes, int32_t box)
 {
     const bool q8 = c->dtype == QSA_KV_E4M3;
     const cuuint64_t width = static_cast<cuuint64_t>(c->hkv) * c->head_dim;
     cuuint64_t dims[2] = {width, static_cast<cuuint64_t>(c->num_pages) * c->page_tokens};
     cuuint64_t strides[1] = {width * (q8 ? 1 : 2)};
-    cuuint32_t boxes[2] = {q8 ? 128u : 64u, static_cast<cuuint32_t>(box)};
+    cuuint32_t boxes[2] = {static_cast<cuuint32_t>(q8 ? bytes : bytes / 2), static_cast<cuuint32_t>(box)};
     cuuint32_t estr[2] = {1, 1};
     const CUresult r = g_encode(tm, q8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
                                 const_cast<void *>(base), dims, strides, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -1022,8 +1022,9 @@ qsa_status qsa_chunk_attention(const void *q, int64_t q_stride, int32_t rows, in
     CUtensorMap tk, tv;
     int32_t box_k, box_v;
     chunk_boxes(cache->head_dim, cache->page_tokens, &box_k, &box_v);
-    if ((st = make_tmap_kv(&tk, cache, cache->k, box_k)) != QSA_OK) return st;
-    if ((st = make_tmap_kv(&tv, cache, cache->v, box_v)) != QSA_OK) return st;
+    const int32_t v_bytes = p.kv.e4m3 ? cache->head_dim / 2 : 128;
+    if ((st = make_tmap_kv(&tk, cache, cache->k, 128, box_k)) != QSA_OK) return st;
+    if ((st = make_tmap_kv(&tv, cache, cache->v, v_bytes, box_v)) != QSA_OK) return st;
     st = launch_rc(launch_chunk(p, &tk, &tv, d->sms, g_overlap, stream));
     if (st == QSA_OK) ++g_launches;                      // the join kernel
     return st;

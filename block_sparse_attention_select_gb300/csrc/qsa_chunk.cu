@@ -4,31 +4,38 @@
 //
 // in one pass over the visible tokens t, with the running maximum m and sum.
 // Both products run on the 5th-generation tensor cores (kind::f16, FP32
-// accumulators in TMEM), tile by tile of 128 tokens:
-//   S[row, token] = Q . K^T     M = 128 rows, N = 128 tokens, K = D
-//   O[row, dim]  += P . V       M = 128 rows, N = D, K = 128 tokens
+// accumulators in TMEM), tile by tile of 128 tokens, each instruction spanning
+// a pair of SMs (cta_group::2), so a pair shares every key and value it loads:
+//   S[row, token] = Q . K^T     M = 256 rows, N = 128 tokens, K = D
+//   O[row, dim]  += P . V       M = 256 rows, N = D, K = 128 tokens
+// CTA r of the pair holds rows 128 r .. + 127 (Q, S, P, O), tokens 64 r .. + 63
+// of the key tile and dims r D / 2 .. of the value tile.  (With one CTA per
+// unit and M = 128, the ring held a quarter more than one tile of D = 256 and
+// the products waited for its copies: 1,021 us on the 1,616-row chunk over
+// 29,000 tokens, tensor pipe 46% busy.)
 // A row of the tile is one (token, query head) pair: the query heads of a KV
-// head share its keys and values, so a unit of work is 128 consecutive pairs
-// (token * group + head) of one request and KV head; a decode token fills
-// `group` of them.
+// head share its keys and values, so a unit of work is 256 consecutive pairs
+// (token * group + head) of one request and KV head.
 //
 // Work: the units' tiles, in the order (request, rows, KV head), form one line
-// of W tiles that the CTAs (one per SM) share out evenly, so one row over a
-// long cache, a batch of unequal requests and a long prompt all fill the card.
-// A unit that lies across CTAs leaves unnormalised FP32 partial sums with their
-// maxima in the workspace (at most two per CTA), which a second kernel joins.
-// Every CTA finds its share itself from seq_start and pos_start: no plan kernel
-// and no host knowledge of the lengths.
+// of W tiles that the CTA pairs share out evenly, so one row over a long cache,
+// a batch of unequal requests and a long prompt all fill the card.  A unit that
+// lies across pairs leaves unnormalised FP32 partial sums with their maxima in
+// the workspace (at most two per pair), which a second kernel joins.  Every
+// pair finds its share itself from seq_start and pos_start: no plan kernel and
+// no host knowledge of the lengths.
 //
 // A CTA's warps: 0-7 softmax (warp w: TMEM lane quarter w % 4 = 32 rows, half
 // w / 4 of a tile's tokens and of the output's dimensions), 8 loads K and V by
-// TMA, one box per page piece, through the block table, 9 issues the MMAs,
-// 10-13 load the queries and, from the E4M3 cache, turn the loaded codes into
-// FP16 tiles.  The MMA warp runs one score product ahead (two S buffers):
+// TMA, one box per page piece, through the block table, 9 issues the MMAs (in
+// the first CTA of the pair), 12-15 load the queries, clear the value rows that
+// nothing attends and, from the E4M3 cache, turn the loaded codes into FP16
+// tiles; 10 and 11 only give their registers to the softmax.  The MMA warp runs
+// one score product ahead (two S buffers):
 //   S(0) S(1) | O(0) S(2) | O(1) S(3) | ...
 // so the softmax of a tile overlaps the products of its neighbours.  P goes
 // back into its S buffer's columns as FP16 and is the A operand of the second
-// product from there.  K and V share a ring of 32-KB slots in the order of use.
+// product from there.  K and V share a ring of slots in the order of use.
 //
 // The accumulator is rescaled only when a row's maximum has grown by more than
 // 2^8 since the one in use: P is then at most 256, far inside FP16, and the sum
@@ -48,56 +55,54 @@
 namespace qsa {
 namespace {
 
-constexpr int CH_ROWS = 128;                 // (token, head) rows of a unit: MMA M
+constexpr int CH_HALF = 128;                 // rows of one CTA: TMEM lanes
+constexpr int CH_ROWS = 256;                 // (token, head) rows of a unit: MMA M
 constexpr int CH_TILE = 128;                 // tokens of a tile
 constexpr int CH_SOFT = 8;                   // softmax warps
-constexpr int CH_LOAD = CH_SOFT, CH_MMA = CH_SOFT + 1, CH_HELP = CH_SOFT + 2;
+constexpr int CH_LOAD = 8, CH_MMA = 9, CH_HELP = 12;
 constexpr int CH_HELPERS = 4;
 constexpr int CH_WARPS = CH_HELP + CH_HELPERS;
 constexpr int CH_THREADS = 32 * CH_WARPS;
-constexpr uint32_t SLOT = 32768;             // FP16 slot: 128 x 128 values
-constexpr uint32_t RAW = 16384;              // the same values as codes
-constexpr int RAWS = 4;
+constexpr int RAWS = 4;                      // slots of loaded codes (E4M3)
+constexpr uint32_t RING = 229376;            // bytes for Q and the ring
 constexpr float RESCALE = 8.0f;              // log2 of the growth that rescales
 constexpr uint32_t TM_S = 0, TM_O = 256;     // TMEM columns: two S buffers of 128, O
 constexpr int BAR_PAIR = 1, BAR_HELP = 5;    // named barriers: four softmax warp pairs, the helpers
 
 template <int D, bool Q8>
 struct Shape {
-    static constexpr int QB = CH_ROWS * D * 2;                         // bytes of Q
-    static constexpr int NS = (229376 - QB - (Q8 ? RAWS * RAW : 0)) / SLOT;   // FP16 slots
-    static constexpr int PARTS = D / 128;                              // slots per tile, K or V
-    // K slot: 128 dims (two chunks of 64) of 128 tokens; V slot: all dims of VTOK tokens
-    static constexpr int VTOK = CH_TILE / PARTS;
-    static constexpr int VCHUNK = VTOK * 128;                          // bytes of a V chunk of 64 dims
+    static constexpr uint32_t QB = CH_HALF * D * 2;                    // bytes of Q
+    // a CTA's half of a K tile: 64 tokens, or of a V tile: D / 2 dims of 128 tokens
+    static constexpr uint32_t SLOT = 128 * D, RAW = SLOT / 2;
+    static constexpr int KTOK = 64, VTOK = CH_TILE;
+    static constexpr int NS = (RING - QB - (Q8 ? RAWS * RAW : 0)) / SLOT;
 };
 
 struct Ctrl {
-    uint64_t full[8], empty[8], raw_full[RAWS], raw_empty[RAWS];
+    uint64_t full[12], empty[12], raw_full[RAWS], raw_empty[RAWS], bnd[8];
     uint64_t s_full[2], p_full[2], o_done, q_full, q_free, drain;
-    float xch[2][2][CH_ROWS];                // [tile parity][half][row]: row maxima, sums
+    alignas(8) float xch[2][2][CH_HALF];                // [tile parity][half][row]: row maxima, sums
     uint16_t scale[2][CH_TILE];              // [slot parity][token]: FP16 scale (E4M3)
-    int64_t warp_work[CH_WARPS];
-    int64_t w0, w1, total;                   // this CTA's tiles, all tiles
-    int32_t ctas;                            // CTAs that have work
+    int64_t w0, w1, total;                   // this pair's tiles, all tiles
+    int32_t pairs;                           // pairs that have work
     int32_t b, m, g, off;                    // the unit of tile w0, and w0's place in it
     uint32_t tmem;
     int32_t abort;
 };
 
-// A unit that lies across CTAs, as the join kernel needs it (written by the
-// CTA that holds the unit's first tile).
+// A unit that lies across pairs, as the join kernel needs it (written by the
+// pair that holds the unit's first tile).
 struct Split {
     int32_t parts;                           // 0: none
     int32_t rows;                            // rows of the unit
     int32_t s0, v0, g;                       // request's first row, unit's first (token, head) pair, KV head
 };
 
-// Workspace: a Split per CTA, then per place (two for each CTA) the rows'
+// Workspace: a Split per pair, then per place (two for each pair) the rows'
 // (maximum in powers of two, sum), then their unnormalised outputs.
 constexpr size_t WS_ML = 4096;
-constexpr size_t WS_O = WS_ML + size_t{2} * CHUNK_MAX_CTAS * CH_ROWS * 8;
-static_assert(sizeof(Split) * CHUNK_MAX_CTAS <= WS_ML, "workspace header");
+constexpr size_t WS_O = WS_ML + size_t{2} * CHUNK_MAX_PAIRS * CH_ROWS * 8;
+static_assert(sizeof(Split) * CHUNK_MAX_PAIRS <= WS_ML, "workspace header");
 
 // ------------------------------------------------------------- work sharing --
 
@@ -180,7 +185,8 @@ __device__ __forceinline__ int64_t request_tiles(const ChunkParams &p, int32_t b
     return tiles * p.kv.hkv;
 }
 
-// Fills c.w0, c.w1 and, when there is work, the unit that w0 lies in.
+// Fills c.w0, c.w1 and, when there is work, the unit that w0 lies in (both CTAs
+// of a pair do, alike).
 __device__ __forceinline__ void find_work(const ChunkParams &p, Ctrl &c, int warp, int lane)
 {
     // requests in equal runs of whole warps
@@ -189,23 +195,24 @@ __device__ __forceinline__ void find_work(const ChunkParams &p, Ctrl &c, int war
     int64_t mine = 0;
     for (int32_t b = first; b < first + run && b < p.kv.n_reqs; b += 32)
         mine += warp_sum(request_tiles(p, b + lane, lane, blockIdx.x == 0));
-    if (lane == 0) c.warp_work[warp] = mine;
+    int64_t *warp_work = reinterpret_cast<int64_t *>(&c.xch[0][0][0]);    // free until the first tile
+    if (lane == 0) warp_work[warp] = mine;
     __syncthreads();
     int64_t total = 0, before = 0;
 #pragma unroll
     for (int w = 0; w < CH_WARPS; ++w) {
         if (w == warp) before = total;
-        total += c.warp_work[w];
+        total += warp_work[w];
     }
-    // one tile each at least, so that the CTAs with work are the first ones
-    const int32_t ctas = static_cast<int32_t>(min(total, static_cast<int64_t>(gridDim.x)));
-    const bool any = static_cast<int32_t>(blockIdx.x) < ctas;
-    const int64_t w0 = any ? total * blockIdx.x / ctas : 0, w1 = any ? total * (blockIdx.x + 1) / ctas : 0;
+    // one tile each at least, so that the pairs with work are the first ones
+    const int32_t pairs = static_cast<int32_t>(min(total, static_cast<int64_t>(gridDim.x >> 1)));
+    const int32_t me = blockIdx.x >> 1;
+    const int64_t w0 = me < pairs ? total * me / pairs : 0, w1 = me < pairs ? total * (me + 1) / pairs : 0;
     if (warp == 0 && lane == 0) {
         c.w0 = w0;
         c.w1 = w1;
         c.total = total;
-        c.ctas = ctas;
+        c.pairs = pairs;
     }
     if (w0 < w1 && before <= w0 && w0 < before + mine) {
         int64_t at = before;
@@ -251,7 +258,7 @@ __device__ __forceinline__ void find_work(const ChunkParams &p, Ctrl &c, int war
     __syncthreads();
 }
 
-// The CTA's share as segments: a run of tiles of one unit.
+// The pair's share as segments: a run of tiles of one unit.
 struct Walk {
     int64_t left;
     int32_t b, m, g, off, n_units;
@@ -292,6 +299,12 @@ struct Walk {
         left -= j1 - j0;
         return true;
     }
+    // whether tile j0 + k holds tokens that no row attends
+    __device__ __forceinline__ bool cut(int32_t k) const
+    {
+        const int32_t t0 = (j0 + k) * CH_TILE;
+        return t0 < u.lo_tok || t0 + CH_TILE - 1 > u.hi_tok;
+    }
     __device__ __forceinline__ void done(const ChunkParams &p)
     {
         off = 0;
@@ -304,31 +317,13 @@ struct Walk {
 
 // ------------------------------------------------------------------- pieces --
 
-// The FP16 / E4M3 slots of a segment in the order of use:
-// K(0) K(1) V(0) K(2) V(1) ... K(n-1) V(n-2) V(n-1), each in PARTS slots.
-template <int PARTS>
-struct Slots {
-    int32_t n, i;                            // tiles of the segment, step of the sequence
-    __device__ __forceinline__ Slots(int32_t tiles) : n(tiles), i(0) {}
-    __device__ __forceinline__ bool next(bool *is_v, int32_t *tile, int32_t *part)
-    {
-        const int32_t e = i / PARTS;
-        *part = i % PARTS;
-        if (e >= 2 * n) return false;
-        if (e == 0) {
-            *is_v = false;
-            *tile = 0;
-        } else if (e == 2 * n - 1) {
-            *is_v = true;
-            *tile = n - 1;
-        } else {
-            *is_v = (e & 1) == 0;            // e = 1: K(1); 2: V(0); 3: K(2); ...
-            *tile = *is_v ? e / 2 - 1 : (e + 1) / 2;
-        }
-        ++i;
-        return true;
-    }
-};
+// Slot e of a segment of n tiles, in the order of use:
+// K(0) K(1) V(0) K(2) V(1) ... K(n-1) V(n-2) V(n-1).
+__device__ __forceinline__ void slot_at(int32_t e, int32_t n, bool *is_v, int32_t *tile)
+{
+    *is_v = e > 0 && ((e & 1) == 0 || e == 2 * n - 1);
+    *tile = e == 2 * n - 1 ? n - 1 : *is_v ? e / 2 - 1 : (e + 1) / 2;
+}
 
 __device__ __forceinline__ uint32_t sw128(uint32_t row, uint32_t c)
 {
@@ -348,15 +343,70 @@ __device__ __forceinline__ uint64_t sw128_mn_desc(uint32_t smem_addr, uint32_t c
     return d;
 }
 
-// D[tmem] (+)= A[tmem] * B[smem desc], kind::f16.
-__device__ __forceinline__ void umma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                            uint32_t accumulate)
+// D[tmem] (+)= A * B over the CTA pair, kind::f16; A in shared memory, or in TMEM.
+__device__ __forceinline__ void umma2_f16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate)
 {
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void umma2_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
         "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Arrive once on `bar` of both CTAs when every tcgen05 op issued so far is done.
+__device__ __forceinline__ void umma2_commit(uint64_t *bar)
+{
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+}
+
+// The first CTA's copy of a shared-memory address.
+__device__ __forceinline__ uint32_t of_first(const void *p)
+{
+    uint32_t a;
+    asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_u32(p)));
+    return a;
+}
+
+__device__ __forceinline__ void cluster_arrive(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void cluster_arrive_expect_tx(uint32_t bar, uint32_t bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+                 : "memory");
+}
+
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// 2-D tiled load into this CTA, completing on a barrier of either CTA of the pair.
+__device__ __forceinline__ void tma_load_2d_pair(void *dst_smem, const void *tmap, uint32_t bar, int32_t x, int32_t y)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst_smem)),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(x), "r"(y)
         : "memory");
 }
 
@@ -396,109 +446,133 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volati
 // ------------------------------------------------------------------- kernel --
 
 template <int D, bool Q8>
-__global__ void __launch_bounds__(CH_THREADS, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(CH_THREADS, 1)
 chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const ChunkParams p)
 {
     using Sh = Shape<D, Q8>;
-    constexpr int NS = Sh::NS, PARTS = Sh::PARTS;
-    static_assert(NS >= 3 && NS <= 8, "ring");
+    constexpr int NS = Sh::NS;
+    constexpr uint32_t SLOT = Sh::SLOT, RAW = Sh::RAW;
+    static_assert(NS >= 3 && NS <= 12, "ring: 12 slots hold at most 7 value tiles, fewer than the cut tiles' barriers");
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t *q_s = smem, *ring = smem + Sh::QB, *raw = ring + NS * SLOT;
-    Ctrl &c = *reinterpret_cast<Ctrl *>(smem + 229376);
+    Ctrl &c = *reinterpret_cast<Ctrl *>(smem + RING);
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    const int rank = blockIdx.x & 1;                         // in the pair
     volatile int *abort = &c.abort;
     const uint64_t lim = p.wait_limit_ns;
 
     if (t == 0) {
+        // full, p_full and q_full count in the first CTA, for both
         for (int i = 0; i < NS; ++i) {
-            mbar_init(&c.full[i], Q8 ? CH_HELPERS : 1);
+            mbar_init(&c.full[i], Q8 ? 2 * CH_HELPERS : 2);
             mbar_init(&c.empty[i], 1);
         }
         for (int i = 0; i < RAWS; ++i) {
             mbar_init(&c.raw_full[i], 1);
             mbar_init(&c.raw_empty[i], CH_HELPERS);
         }
+        for (int i = 0; i < 8; ++i) mbar_init(&c.bnd[i], 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&c.s_full[i], 1);
-            mbar_init(&c.p_full[i], CH_SOFT);
+            mbar_init(&c.p_full[i], 2 * CH_SOFT);
         }
         mbar_init(&c.o_done, 1);
-        mbar_init(&c.q_full, CH_HELPERS);
+        mbar_init(&c.q_full, 2 * CH_HELPERS);
         mbar_init(&c.q_free, 1);
         mbar_init(&c.drain, 1);
         c.abort = 0;
         fence_barrier_init();
     }
     if (warp == CH_MMA) {
-        tmem_alloc(&c.tmem, 512);
-        tmem_relinquish();
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&c.tmem)), "r"(512)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
     wait_prior_grid();
     find_work(p, c, warp, lane);
     tc_fence_before();
     __syncthreads();
+    cluster_sync();                                          // the pair's barriers and TMEM are ready
     tc_fence_after();
     const uint32_t tmem = c.tmem;
     const uint32_t ring_a = smem_u32(ring);
     Walk w(p, c);
-
+    // registers after the split: 8 x 32 x 168 + 8 x 32 x 88 = 65,536
+    if (warp >= CH_LOAD && warp < CH_HELP) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == CH_LOAD) {
         // ---------------------------------------------------------- K, V loads
         uint8_t *dst0 = Q8 ? raw : ring;
         constexpr int NSL = Q8 ? RAWS : NS;
         constexpr uint32_t BYTES = Q8 ? RAW : SLOT;
-        constexpr int CE = Q8 ? 128 : 64;                    // elements of a 128-byte chunk
-        uint64_t *full = Q8 ? c.raw_full : c.full, *empty = Q8 ? c.raw_empty : c.empty;
+        // elements of a box row: 128 bytes, or half a 128-wide head's 64 codes
+        constexpr int CK = Q8 ? 128 : 64, CV = Q8 ? D / 2 : 64;
+        constexpr int KCH = D / CK, VCH = D / 2 / CV;         // boxes across
+        uint64_t *empty = Q8 ? c.raw_empty : c.empty;
         const int32_t P = p.kv.page_tokens;
-        const int32_t box_k = min(P, CH_TILE), box_v = min(P, Sh::VTOK);
-        const int sh_k = __ffs(box_k) - 1, sh_v = __ffs(box_v) - 1;
-        uint32_t slot = 0, phase = 0, used = 0;              // used: slots loaded at least once
+        const int sh_k = __ffs(min(P, Sh::KTOK)) - 1, sh_v = __ffs(min(P, Sh::VTOK)) - 1;
+        uint32_t slot = 0, phase = 0, used = 0, last = 0;     // slots loaded at least once, their latest phases
+        uint32_t nb = 0;                                      // boundary tiles so far
         bool ok = true;
+        // this lane's box of a slot: place in the tensor and in the slot
+        int32_t x = 0, y = 0;
+        uint32_t at = 0;
+        bool mine = false;
+        const int32_t *bt = nullptr;
+        auto plan = [&](int32_t e) {
+            bool v;
+            int32_t tile;
+            slot_at(e, w.j1 - w.j0, &v, &tile);
+            const int sh = v ? sh_v : sh_k;
+            const int32_t toks = v ? Sh::VTOK : Sh::KTOK;
+            const int lb = __ffs(toks) - 1 - sh;              // log2 of the boxes down
+            const int32_t ch = lane >> lb, i = lane & ((1 << lb) - 1);
+            mine = ch < (v ? VCH : KCH);
+            const int32_t tok = (w.j0 + tile) * CH_TILE + (v ? 0 : rank * Sh::KTOK) + (i << sh);
+            x = w.g * D + (v ? rank * (D / 2) + ch * CV : ch * CK);
+            const int32_t row_bytes = v && Q8 ? CV : 128;
+            at = static_cast<uint32_t>((ch * toks + (i << sh)) * row_bytes);
+            // boxes without a visible token read zeros (a row past the cache)
+            y = p.kv.num_pages << p.kv.page_shift;
+            if (mine && tok <= w.u.hi_tok && tok + (1 << sh) > w.u.lo_tok) {
+                const int32_t page = __ldg(bt + (tok >> p.kv.page_shift));
+                if (page >= 0 && page < p.kv.num_pages) y = (page << p.kv.page_shift) + (tok & (P - 1));
+                else record_error(p.kv.status, ST_BAD_PAGE);
+            }
+        };
         while (ok && w.next(p)) {
-            const int32_t *bt = p.kv.block_table + static_cast<int64_t>(w.b) * p.kv.max_pages;
-            Slots<PARTS> seq(w.j1 - w.j0);
-            bool is_v, have, is_v2 = false;
-            int32_t tile, part;
-            // this lane's box of a slot: chunk and token, and the token's cache row
-            int32_t x = 0, y = 0;
-            uint32_t at = 0;
-            bool mine = false;
-            auto plan = [&](bool v, int32_t tl, int32_t pt) {
-                const int sh = v ? sh_v : sh_k;
-                const int32_t toks = v ? Sh::VTOK : CH_TILE;
-                const int32_t nb = toks >> sh;               // boxes of a chunk
-                const int32_t chunks = static_cast<int32_t>(BYTES) / (toks * 128);
-                const int32_t ch = lane / nb, i = lane - ch * nb;
-                mine = ch < chunks;
-                const int32_t tok = (w.j0 + tl) * CH_TILE + (v ? pt * Sh::VTOK : 0) + (i << sh);
-                x = w.g * D + (v ? 0 : pt * 128) + ch * CE;
-                at = static_cast<uint32_t>(ch * toks * 128 + (i << sh) * 128);
-                // boxes without a visible token read zeros (a row past the cache)
-                y = p.kv.num_pages << p.kv.page_shift;
-                if (mine && tok <= w.u.hi_tok && tok + (1 << sh) > w.u.lo_tok) {
-                    const int32_t page = __ldg(bt + (tok >> p.kv.page_shift));
-                    if (page >= 0 && page < p.kv.num_pages) y = (page << p.kv.page_shift) + (tok & (P - 1));
-                    else record_error(p.kv.status, ST_BAD_PAGE);
-                }
-            };
-            have = seq.next(&is_v2, &tile, &part);
-            if (have) plan(is_v2, tile, part);
-            while (have) {
-                is_v = is_v2;
+            bt = p.kv.block_table + static_cast<int64_t>(w.b) * p.kv.max_pages;
+            const int32_t n = w.j1 - w.j0;
+            plan(0);
+            for (int32_t e = 0; e < 2 * n; ++e) {
+                bool v;
+                int32_t tile;
+                slot_at(e, n, &v, &tile);
                 const int32_t xx = x, yy = y;
                 const uint32_t aa = at;
                 const bool mm = mine;
-                // the next slot's page lookups run under the wait for this one
-                have = seq.next(&is_v2, &tile, &part);
-                if (have) plan(is_v2, tile, part);
+                if (e + 1 < 2 * n) plan(e + 1);               // page lookups run under this slot's wait
                 if (!warp_wait(&empty[slot], phase ^ 1u, abort, lim)) {
                     ok = false;
                     break;
                 }
-                if (lane == 0) mbar_arrive_expect_tx(&full[slot], BYTES);
+                uint32_t bar;
+                if constexpr (Q8) {
+                    bar = smem_u32(&c.raw_full[slot]);
+                    if (lane == 0) mbar_arrive_expect_tx(&c.raw_full[slot], BYTES);
+                } else if (v && w.cut(tile)) {
+                    // the helpers clear rows of this one before the products see it
+                    bar = smem_u32(&c.bnd[nb & 7u]);
+                    if (lane == 0) mbar_arrive_expect_tx(&c.bnd[nb & 7u], BYTES);
+                    ++nb;
+                } else {
+                    bar = of_first(&c.full[slot]);
+                    if (lane == 0) cluster_arrive_expect_tx(bar, BYTES);
+                }
                 __syncwarp();
-                if (mm) tma_load_2d(dst0 + slot * BYTES + aa, is_v ? &tv : &tk, &full[slot], xx, yy);
-                used = (used & ~(256u << slot)) | (1u << slot) | (phase << (slot + 8));
+                if (mm) tma_load_2d_pair(dst0 + slot * BYTES + aa, v ? &tv : &tk, bar, xx, yy);
+                used |= 1u << slot;
+                last = (last & ~(1u << slot)) | (phase << slot);
                 if (++slot == NSL) {
                     slot = 0;
                     phase ^= 1u;
@@ -506,12 +580,17 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
             }
             w.done(p);
         }
-        // copies still in flight (only after an abort: otherwise they were waited for)
-        if (lane == 0)
-            for (int i = 0; i < NSL; ++i)
-                if (used & (1u << i)) mbar_wait_bounded(&full[i], (used >> (8 + i)) & 1u, lim);
+        // after an abort copies may be in flight: let them land (their barriers
+        // may be the other CTA's, so give them the time instead)
+        if (!ok && lane == 0) {
+            if (Q8)
+                for (int i = 0; i < NSL; ++i)
+                    if (used & (1u << i)) mbar_wait_bounded(&c.raw_full[i], (last >> i) & 1u, lim);
+            const long long t0 = clock64();
+            while (clock64() - t0 < 4000000) {}
+        }
         __syncwarp();
-    } else if (warp == CH_MMA) {
+    } else if (warp == CH_MMA && rank == 0) {
         // --------------------------------------------------------------- MMAs
         constexpr uint32_t idesc_s = umma_idesc_f16_f32(CH_ROWS, CH_TILE);
         constexpr uint32_t idesc_o = umma_idesc_f16_f32(CH_ROWS, D) | (1u << 16);   // B: dims contiguous
@@ -526,71 +605,46 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
         };
         // S(i) = Q . K(i)^T
         auto scores = [&](uint32_t i, bool last) {
+            ok = ok && warp_wait(&c.full[slot], phase, abort, lim);
+            if (!ok) return;
+            if (lane == 0) {
+                tc_fence_after();
+                const uint64_t kd = sw128_kmajor_desc(ring_a + slot * SLOT);
 #pragma unroll
-            for (int part = 0; part < PARTS; ++part) {
-                if (ok) ok = warp_wait(&c.full[slot], phase, abort, lim);
-                if (!ok) return;
-                if (lane == 0) {
-                    tc_fence_after();
-                    const uint64_t kd = sw128_kmajor_desc(ring_a + slot * SLOT);
-#pragma unroll
-                    for (int kk = 0; kk < 8; ++kk) {
-                        const uint32_t ch = kk >> 2, in = (kk & 3) * 32;
-                        umma_f16(tmem + TM_S + (i & 1u) * 128u, qd + (((2 * part + ch) * (CH_ROWS * 128u) + in) >> 4),
-                                 kd + ((ch * (CH_TILE * 128u) + in) >> 4), idesc_s, part + kk > 0 ? 1u : 0u);
-                    }
-                    umma_commit(&c.empty[slot]);
-                    if (part == PARTS - 1) {
-                        umma_commit(&c.s_full[i & 1u]);
-                        if (last) umma_commit(&c.q_free);
-                    }
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t ch = kk >> 2, in = (kk & 3) * 32;
+                    umma2_f16(tmem + TM_S + (i & 1u) * 128u, qd + ((ch * (CH_HALF * 128u) + in) >> 4),
+                              kd + ((ch * (Sh::KTOK * 128u) + in) >> 4), idesc_s, kk > 0 ? 1u : 0u);
                 }
-                advance();
+                umma2_commit(&c.empty[slot]);
+                umma2_commit(&c.s_full[i & 1u]);
+                if (last) umma2_commit(&c.q_free);
             }
+            __syncwarp();
+            advance();
         };
         while (ok && w.next(p)) {
             const int32_t n = w.j1 - w.j0;
             ok = warp_wait(&c.q_full, seg & 1u, abort, lim);
-            if (ok) scores(it, n == 1);
+            scores(it, n == 1);
             if (n > 1) scores(it + 1, n == 2);
             for (int32_t j = 0; ok && j < n; ++j) {
                 const uint32_t i = it + j;
                 ok = warp_wait(&c.p_full[i & 1u], (i >> 1) & 1u, abort, lim);
-                const int32_t tok0 = (w.j0 + j) * CH_TILE;
+                ok = ok && warp_wait(&c.full[slot], phase, abort, lim);
+                if (!ok) break;
+                if (lane == 0) {
+                    tc_fence_after();
+                    const uint64_t vd = sw128_mn_desc(ring_a + slot * SLOT, Sh::VTOK * 128);
 #pragma unroll
-                for (int part = 0; part < PARTS; ++part) {
-                    if (ok) ok = warp_wait(&c.full[slot], phase, abort, lim);
-                    if (!ok) break;
-                    if constexpr (!Q8) {
-                        // rows of V that nothing attends may hold anything: zero
-                        // weights must meet zeros (the loaded pages' ends only)
-                        const int32_t a = w.u.lo_tok - (tok0 + part * Sh::VTOK);
-                        const int32_t z = w.u.hi_tok + 1 - (tok0 + part * Sh::VTOK);
-                        if (a > 0 || z < Sh::VTOK) {
-                            uint8_t *v = ring + slot * SLOT;
-                            constexpr int PER_TOK = D / 8;       // 16-byte pieces of a token
-                            for (int32_t e = lane; e < Sh::VTOK * PER_TOK; e += 32) {
-                                const int32_t tok = e / PER_TOK, pc = e % PER_TOK;
-                                if (tok < a || tok >= z)
-                                    *reinterpret_cast<uint4 *>(v + (pc >> 3) * Sh::VCHUNK + tok * 128 + (pc & 7) * 16) =
-                                        make_uint4(0u, 0u, 0u, 0u);
-                            }
-                            fence_proxy_async_smem();
-                            __syncwarp();
-                        }
-                    }
-                    if (lane == 0) {
-                        tc_fence_after();
-                        const uint64_t vd = sw128_mn_desc(ring_a + slot * SLOT, Sh::VCHUNK);
-#pragma unroll
-                        for (int kk = 0; kk < Sh::VTOK / 16; ++kk)
-                            umma_f16_ta(tmem + TM_O, tmem + TM_S + (i & 1u) * 128u + (part * (Sh::VTOK / 16) + kk) * 8u,
-                                        vd + ((kk * 2048u) >> 4), idesc_o, j + part + kk > 0 ? 1u : 0u);
-                        umma_commit(&c.empty[slot]);
-                        if (part == PARTS - 1) umma_commit(&c.o_done);
-                    }
-                    advance();
+                    for (int kk = 0; kk < CH_TILE / 16; ++kk)
+                        umma2_f16_ta(tmem + TM_O, tmem + TM_S + (i & 1u) * 128u + kk * 8u, vd + ((kk * 2048u) >> 4),
+                                     idesc_o, j + kk > 0 ? 1u : 0u);
+                    umma2_commit(&c.empty[slot]);
+                    umma2_commit(&c.o_done);
                 }
+                __syncwarp();
+                advance();
                 if (j + 2 < n) scores(i + 2, j + 3 == n);
             }
             it += n;
@@ -599,108 +653,144 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
         }
         if (!ok) {                                            // products still running
             if (lane == 0) {
-                umma_commit(&c.drain);
+                umma2_commit(&c.drain);
                 mbar_wait_bounded(&c.drain, 0, lim);
             }
             __syncwarp();
         }
+    }
     } else if (warp >= CH_HELP) {
-        // ------------------------------------------ queries, E4M3 to FP16 tiles
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        // --------------------- queries, cut value tiles, E4M3 codes to FP16 tiles
         const int ht = t - CH_HELP * 32;                      // 0 .. 127
-        uint32_t seg = 0, slot = 0, phase = 0, rslot = 0, rphase = 0;
+        uint32_t seg = 0, slot = 0, phase = 0, rslot = 0, rphase = 0, ring0 = 0, nb = 0;
         bool ok = true;                                       // false: keep to the barriers, do nothing
         while (w.next(p)) {
+            const int32_t n = w.j1 - w.j0;
             if (ok && seg > 0) ok = warp_wait(&c.q_free, (seg - 1) & 1u, abort, lim);
             if (ok) {
                 constexpr int PC = D / 8;                      // 16-byte pieces of a row
                 const uint8_t *q = static_cast<const uint8_t *>(p.q);
                 const uint32_t qa = smem_u32(q_s);
 #pragma unroll 4
-                for (int e = ht; e < CH_ROWS * PC; e += 32 * CH_HELPERS) {
-                    const int row = e / PC, pc = e % PC;
-                    const bool in = row < w.u.rows;
-                    const int32_t v = w.u.v0 + row, tok = v / p.group, h = v - tok * p.group;
+                for (int e = ht; e < CH_HALF * PC; e += 32 * CH_HELPERS) {
+                    const int row = e / PC, pc = e % PC, ur = rank * CH_HALF + row;
+                    const bool in = ur < w.u.rows;
+                    const int32_t v = w.u.v0 + ur, tok = v / p.group, h = v - tok * p.group;
                     const uint8_t *src = in ? q + ((static_cast<int64_t>(w.s.s0) + tok) * p.q_stride +
                                                    (w.g * p.group + h) * D + pc * 8) * 2 : q;
-                    const uint32_t dst = qa + (pc >> 3) * (CH_ROWS * 128u) + sw128(row, pc & 7);
+                    const uint32_t dst = qa + (pc >> 3) * (CH_HALF * 128u) + sw128(row, pc & 7);
                     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0)
                                  : "memory");
                 }
                 asm volatile("cp.async.wait_all;" ::: "memory");
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&c.q_full);
+                if (lane == 0) cluster_arrive(of_first(&c.q_full));
             }
             ++seg;
-            if constexpr (Q8) {
-                const int32_t *bt = p.kv.block_table + static_cast<int64_t>(w.b) * p.kv.max_pages;
-                Slots<PARTS> seq(w.j1 - w.j0);
-                bool v, v2 = false;
-                int32_t tile = 0, part = 0, a = 0, z = 0;
-                // the slot's first token, and this thread's token's scale byte
-                int32_t tok0 = 0;
-                uint32_t byte = 127;
-                auto look = [&] {
-                    tok0 = (w.j0 + tile) * CH_TILE + (v2 ? part * Sh::VTOK : 0);
-                    const int32_t tok = tok0 + ht;
-                    byte = 127;
-                    if (tok >= w.u.lo_tok && tok <= w.u.hi_tok && ht < (v2 ? Sh::VTOK : CH_TILE)) {
-                        const int32_t page = __ldg(bt + (tok >> p.kv.page_shift));
-                        if (page >= 0 && page < p.kv.num_pages)
-                            byte = __ldg((v2 ? p.kv.v_scale : p.kv.k_scale) +
-                                         ((static_cast<int64_t>(page) << p.kv.page_shift) + (tok & (p.kv.page_tokens - 1))) * p.kv.hkv + w.g);
+            if constexpr (!Q8) {
+                // Rows of V that nothing attends may hold anything (the ends of
+                // loaded pages): zero weights must meet zeros.
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int32_t tile = k == 0 ? 0 : n - 1;
+                    if ((k == 1 && n == 1) || !w.cut(tile)) continue;
+                    if (ok) ok = warp_wait(&c.bnd[nb & 7u], (nb >> 3) & 1u, abort, lim);
+                    ++nb;
+                    const uint32_t vs = (ring0 + (tile < n - 1 ? 2 * (tile + 1) : 2 * n - 1)) % NS;
+                    if (ok) {
+                        uint8_t *v = ring + vs * SLOT;
+                        const int32_t a = w.u.lo_tok - (w.j0 + tile) * CH_TILE, z = w.u.hi_tok + 1 - (w.j0 + tile) * CH_TILE;
+                        if (ht < a || ht >= z) {
+#pragma unroll
+                            for (int ch = 0; ch < D / 128; ++ch)
+#pragma unroll
+                                for (int i = 0; i < 8; ++i)
+                                    *reinterpret_cast<uint4 *>(v + (ch * CH_TILE + ht) * 128 + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+                        }
+                        fence_proxy_async_smem();
                     }
+                    named_barrier(BAR_HELP, 32 * CH_HELPERS);
+                    if (ok && ht == 0) cluster_arrive(of_first(&c.full[vs]));
+                }
+                ring0 = (ring0 + 2 * n) % NS;
+            } else {
+                const int32_t *bt = p.kv.block_table + static_cast<int64_t>(w.b) * p.kv.max_pages;
+                // scale bytes of the slot's tokens, one per thread, looked up two
+                // slots ahead: first the page, then the byte
+                auto token = [&](int32_t e) -> int32_t {       // this thread's token of slot e, -1: none
+                    bool v;
+                    int32_t tile;
+                    if (e >= 2 * n) return -1;
+                    slot_at(e, n, &v, &tile);
+                    const int32_t tok = (w.j0 + tile) * CH_TILE + (v ? 0 : rank * Sh::KTOK) + ht;
+                    return ht < (v ? Sh::VTOK : Sh::KTOK) && tok >= w.u.lo_tok && tok <= w.u.hi_tok ? tok : -1;
                 };
-                bool have = seq.next(&v2, &tile, &part);
-                if (have) look();
+                auto page_of = [&](int32_t tok) -> int32_t { return tok >= 0 ? __ldg(bt + (tok >> p.kv.page_shift)) : -1; };
+                auto byte_of = [&](int32_t e, int32_t tok, int32_t page) -> uint32_t {
+                    if (page < 0 || page >= p.kv.num_pages) return 127u;
+                    bool v;
+                    int32_t tile;
+                    slot_at(e, n, &v, &tile);
+                    return __ldg((v ? p.kv.v_scale : p.kv.k_scale) +
+                                 ((static_cast<int64_t>(page) << p.kv.page_shift) + (tok & (p.kv.page_tokens - 1))) * p.kv.hkv + w.g);
+                };
+                int32_t tok1 = token(0), page1 = page_of(tok1);
+                uint32_t byte = byte_of(0, tok1, page1);
+                tok1 = token(1);
+                page1 = page_of(tok1);
                 uint32_t par = 0;
-                while (have) {
-                    v = v2;
-                    a = w.u.lo_tok - tok0;
-                    z = w.u.hi_tok + 1 - tok0;
+                for (int32_t e = 0; e < 2 * n; ++e) {
+                    bool v;
+                    int32_t tile;
+                    slot_at(e, n, &v, &tile);
+                    const int32_t tok0 = (w.j0 + tile) * CH_TILE;      // V: rows outside lo_tok .. hi_tok are cleared
+                    const int32_t a = v ? w.u.lo_tok - tok0 : 0, z = v ? w.u.hi_tok + 1 - tok0 : CH_TILE;
                     // 2^(byte - 127) as FP16 (2^-15 is subnormal)
-                    const int e = max(112, min(135, static_cast<int>(byte))) - 127;
-                    const uint32_t s16 = e >= -14 ? static_cast<uint32_t>(e + 15) << 10 : 0x200u;
-                    c.scale[par][ht] = static_cast<uint16_t>(s16);
-                    have = seq.next(&v2, &tile, &part);
-                    if (have) look();                          // in flight under this slot's conversion
+                    const int x = max(112, min(135, static_cast<int>(byte))) - 127;
+                    c.scale[par][ht] = static_cast<uint16_t>(x >= -14 ? (x + 15) << 10 : 0x200);
+                    byte = byte_of(e + 1, tok1, page1);                // in flight under the conversion
+                    tok1 = token(e + 2);
+                    page1 = page_of(tok1);
                     if (ok) ok = warp_wait(&c.raw_full[rslot], rphase, abort, lim);
                     if (ok) ok = warp_wait(&c.empty[slot], phase ^ 1u, abort, lim);
-                    named_barrier(BAR_HELP, 32 * CH_HELPERS);  // the scales are in
+                    named_barrier(BAR_HELP, 32 * CH_HELPERS);          // the scales are in
                     if (ok) {
-                        const int pc = ht & 7;                 // 16 codes of a 128-byte row
-                        const uint8_t *src = raw + rslot * RAW + pc * 16;
+                        constexpr int N = RAW / 16 / (32 * CH_HELPERS); // 16-code pieces per thread
+                        // a row of codes: 128 bytes, 64 for V of a 128-wide head
+                        const int sh = v && D == 128 ? 2 : 3;           // log2 of its pieces
+                        const int pc = ht & ((1 << sh) - 1);
+                        const int toks = v ? Sh::VTOK : Sh::KTOK;
+                        const uint8_t *src = raw + rslot * RAW + ht * 16;
                         uint8_t *dst = ring + slot * SLOT;
-                        const int32_t toks = v ? Sh::VTOK : CH_TILE;
-                        uint4 in[8];
+                        uint4 in[N];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            in[i] = *reinterpret_cast<const uint4 *>(src + ((ht >> 3) + 16 * i) * 128);
+                        for (int i = 0; i < N; ++i) in[i] = *reinterpret_cast<const uint4 *>(src + i * (16 * 32 * CH_HELPERS));
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int rr = (ht >> 3) + 16 * i;
-                            const int half = rr / toks, tk2 = rr - half * toks;      // 128 dims, token
+                        for (int i = 0; i < N; ++i) {
+                            const int rr = (ht >> sh) + i * ((32 * CH_HELPERS) >> sh);
+                            const int blk = rr / toks, tk2 = rr & (toks - 1);      // 128 dims, token
                             const uint32_t sc = c.scale[par][tk2] * 0x10001u;
                             const uint32_t cw[4] = {in[i].x, in[i].y, in[i].z, in[i].w};
                             uint32_t o[8];
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
+                            for (int k = 0; k < 4; ++k)
                                 asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
                                     "cvt.rn.f16x2.e4m3x2 %0, lo;\n\tcvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
                                     : "=r"(o[2 * k]), "=r"(o[2 * k + 1])
                                     : "r"(cw[k]));
-                            }
 #pragma unroll
                             for (int k = 0; k < 8; ++k)
                                 asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(o[k]) : "r"(sc));
-                            if (v && (tk2 < a || tk2 >= z)) {
+                            if (tk2 < a || tk2 >= z) {
 #pragma unroll
                                 for (int k = 0; k < 8; ++k) o[k] = 0u;
                             }
-                            // dims 16 pc .. of this half: chunk pc / 4, pieces 2 (pc % 4) and + 1;
+                            // dims 16 pc .. of the row: chunk pc / 4, pieces 2 (pc % 4) and + 1;
                             // lanes of the upper four pieces store the odd one first, which
                             // spreads a row's eight stores over all banks
-                            uint8_t *ck = dst + (2 * half + (pc >> 2)) * (toks * 128);
+                            uint8_t *ck = dst + (2 * blk + (pc >> 2)) * (toks * 128);
                             const uint32_t p0 = 2 * (pc & 3), first = pc >> 2;
                             const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
                             *reinterpret_cast<uint4 *>(ck + sw128(tk2, p0 + first)) = first ? hi : lo;
@@ -710,7 +800,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                         __syncwarp();
                         if (lane == 0) {
                             mbar_arrive(&c.raw_empty[rslot]);
-                            mbar_arrive(&c.full[slot]);
+                            cluster_arrive(of_first(&c.full[slot]));
                         }
                     }
                     par ^= 1u;
@@ -727,21 +817,24 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
             w.done(p);
         }
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
         // ------------------------------------------------------------- softmax
         constexpr int OC = D / 2;                              // output columns per thread
         const int lq = warp & 3, half = warp >> 2, row = lq * 32 + lane;
         const uint32_t lane_base = static_cast<uint32_t>(lq * 32) << 16;
         const float cs = p.scale * 1.4426950408889634f;        // scores in powers of two
+        const uint32_t p_full0 = of_first(&c.p_full[0]);
         uint32_t it = 0;
         bool ok = true;                                        // false: keep to the barriers, do nothing
         Split split = {0, 0, 0, 0, 0};
         while (w.next(p)) {
             const int32_t n = w.j1 - w.j0;
             // rows past the unit's last behave like it (their queries are zeros)
-            const int32_t vr = min(w.u.v0 + row, w.u.v0 + w.u.rows - 1);
+            const int32_t mine = w.u.rows - rank * CH_HALF;    // rows in use here, if positive
+            const int32_t vr = w.u.v0 + min(rank * CH_HALF + row, w.u.rows - 1);
             const int32_t pos = w.s.p0 + vr / p.group;
             const int32_t first = p.window > 0 ? max(0, pos - p.window + 1) : 0;
-            const bool live = lq * 32 < w.u.rows;              // some row of this warp is in use
+            const bool live = lq * 32 < mine;                  // some row of this warp is in use
             float m = -INFINITY, l = 0.0f;
             for (int32_t j = 0; j < n; ++j, ++it) {
                 const uint32_t buf = it & 1u;
@@ -819,23 +912,23 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (ok && lane == 0) mbar_arrive(&c.p_full[buf]);
+                if (ok && lane == 0) cluster_arrive(p_full0 + buf * 8u);
             }
             // the segment's sums: its rows' output, or its part of it
             if (ok) ok = warp_wait(&c.o_done, (it - 1) & 1u, abort, lim);
             float *lx = &c.xch[it & 1u][0][0];                 // not the last tile's buffer
-            if (ok && live) lx[half * CH_ROWS + row] = l;
+            if (ok && live) lx[half * CH_HALF + row] = l;
             named_barrier(BAR_PAIR + lq, 64);
-            if (ok && live) l += lx[(half ^ 1) * CH_ROWS + row];
+            if (ok && live) l += lx[(half ^ 1) * CH_HALF + row];
             named_barrier(BAR_PAIR + lq, 64);                  // read before the next tile's maxima
             if (ok && live) {
                 tc_fence_after();
                 const uint32_t to = tmem + TM_O + lane_base + half * OC;
-                const bool in = row < w.u.rows;
+                const bool in = row < mine;
                 uint32_t u[32];
                 if (w.whole) {
                     const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-                    const int32_t v = w.u.v0 + row, tok = v / p.group, h = v - tok * p.group;
+                    const int32_t v = w.u.v0 + rank * CH_HALF + row, tok = v / p.group, h = v - tok * p.group;
                     __half *out = static_cast<__half *>(p.out) +
                                   ((static_cast<int64_t>(w.s.s0) + tok) * p.hq + w.g * p.group + h) * D + half * OC;
 #pragma unroll
@@ -857,10 +950,11 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                         }
                     }
                 } else {
-                    // two places per CTA: 0 for a unit begun before it, 1 for one that goes on after it
-                    const int64_t place = 2 * static_cast<int64_t>(blockIdx.x) + (w.head ? 1 : 0);
-                    float *ml = reinterpret_cast<float *>(p.ws + WS_ML) + (place * CH_ROWS + row) * 2;
-                    float *part = reinterpret_cast<float *>(p.ws + WS_O) + (place * p.ws_rows + row) * D + half * OC;
+                    // two places per pair: 0 for a unit begun before it, 1 for one that goes on after it
+                    const int64_t place = 2 * static_cast<int64_t>(blockIdx.x >> 1) + (w.head ? 1 : 0);
+                    const int ur = rank * CH_HALF + row;
+                    float *ml = reinterpret_cast<float *>(p.ws + WS_ML) + (place * CH_ROWS + ur) * 2;
+                    float *part = reinterpret_cast<float *>(p.ws + WS_O) + (place * p.ws_rows + ur) * D + half * OC;
                     if (in && half == 0) {
                         ml[0] = m == -INFINITY ? -INFINITY : m * cs;
                         ml[1] = l;
@@ -879,10 +973,10 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                 tc_fence_before();
             }
             if (t == 0 && w.head && !w.whole) {
-                // the unit's other tiles lie in the next CTAs' shares
+                // the unit's other tiles lie in the next pairs' shares
                 const int64_t end = c.w1 + (w.u.hi - w.j1);
                 split.parts = 1;
-                while (c.total * (blockIdx.x + split.parts) / c.ctas < end) ++split.parts;
+                while (c.total * ((blockIdx.x >> 1) + split.parts) / c.pairs < end) ++split.parts;
                 split.rows = w.u.rows;
                 split.s0 = w.s.s0;
                 split.v0 = w.u.v0;
@@ -890,19 +984,21 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
             }
             w.done(p);
         }
-        if (t == 0) reinterpret_cast<Split *>(p.ws)[blockIdx.x] = split;
+        if (t == 0 && rank == 0) reinterpret_cast<Split *>(p.ws)[blockIdx.x >> 1] = split;
     }
 
     tc_fence_before();
     __syncthreads();
+    cluster_sync();                                          // nothing of the pair reaches into the other any more
     tc_fence_after();
     if (t == 0 && c.abort) record_error(p.kv.status, ST_TIMEOUT);
-    if (warp == CH_MMA) tmem_dealloc(tmem, 512);
+    if (warp == CH_MMA)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
     allow_next_grid();
 }
 
-// Joins the parts of each split unit: block x the unit that CTA x began (part 0
-// in its second place, part i in the first place of the i-th CTA after it), a
+// Joins the parts of each split unit: block x the unit that pair x began (part 0
+// in its second place, part i in the first place of the i-th pair after it), a
 // warp per row.
 template <int D>
 __global__ void __launch_bounds__(256)
@@ -965,7 +1061,7 @@ chunk_join_kernel(const ChunkParams p)
     }
 }
 
-constexpr size_t CH_SMEM = 229376 + sizeof(Ctrl);
+constexpr size_t CH_SMEM = RING + sizeof(Ctrl);
 static_assert(CH_SMEM <= 232448, "shared memory budget");
 
 template <int D, bool Q8>
@@ -990,8 +1086,8 @@ int launch(const ChunkParams &p, const void *tk, const void *tv, int grid, bool 
                                  CH_SMEM, stream, false, args);
     if (rc != 0) return rc;
     void *join[] = {const_cast<ChunkParams *>(&p)};
-    const unsigned rows8 = static_cast<unsigned>(std::min(4, (p.ws_rows + 7) / 8));
-    return launch_kernel(reinterpret_cast<const void *>(&chunk_join_kernel<D>), dim3(grid, rows8), dim3(256), 0, stream,
+    const unsigned rows8 = static_cast<unsigned>(std::min(8, (p.ws_rows + 7) / 8));
+    return launch_kernel(reinterpret_cast<const void *>(&chunk_join_kernel<D>), dim3(grid / 2, rows8), dim3(256), 0, stream,
                          overlap, join);
 }
 
@@ -1004,19 +1100,20 @@ int32_t chunk_part_rows(int32_t rows, int32_t group)
 
 size_t chunk_workspace_bytes(int32_t rows, int32_t group, int32_t head_dim)
 {
-    return WS_O + size_t{2} * CHUNK_MAX_CTAS * chunk_part_rows(rows, group) * head_dim * 4;
+    return WS_O + size_t{2} * CHUNK_MAX_PAIRS * chunk_part_rows(rows, group) * head_dim * 4;
 }
 
 // tokens per box of the K and V tensor maps
 void chunk_boxes(int32_t head_dim, int32_t page_tokens, int32_t *box_k, int32_t *box_v)
 {
-    *box_k = std::min(page_tokens, CH_TILE);
-    *box_v = std::min(page_tokens, CH_TILE * 128 / head_dim);
+    (void)head_dim;
+    *box_k = std::min(page_tokens, CH_TILE / 2);
+    *box_v = std::min(page_tokens, CH_TILE);
 }
 
 int launch_chunk(const ChunkParams &p, const void *tk, const void *tv, int sms, bool overlap, void *stream)
 {
-    const int grid = std::min(sms, static_cast<int>(CHUNK_MAX_CTAS));
+    const int grid = 2 * std::min(sms / 2, static_cast<int>(CHUNK_MAX_PAIRS));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (p.kv.head_dim == 128)
         return p.kv.e4m3 ? launch<128, true>(p, tk, tv, grid, overlap, s) : launch<128, false>(p, tk, tv, grid, overlap, s);

@@ -248,8 +248,9 @@ int launch_kv_store(const KvParams &p, const void *k, int64_t k_stride, const vo
                     void *stream);
 int launch_kv_load(const KvParams &p, void *k, int64_t k_stride, void *v, int64_t v_stride, int sms, void *stream);
 // tk, tv: 2-D tensor maps of the caches [num_pages * page_tokens][hkv * head_dim]
-// with boxes of 128 bytes (FP16: 128-byte swizzle) x chunk_boxes() tokens
-constexpr int32_t CHUNK_MAX_CTAS = 160;
+// with boxes of 128 bytes (FP16: 128-byte swizzle; the codes of half a 128-wide
+// head: 64 bytes) x chunk_boxes() tokens
+constexpr int32_t CHUNK_MAX_PAIRS = 80;
 int launch_chunk(const ChunkParams &p, const void *tk, const void *tv, int sms, bool overlap, void *stream);
 int32_t chunk_part_rows(int32_t rows, int32_t group);
 size_t chunk_workspace_bytes(int32_t rows, int32_t group, int32_t head_dim);

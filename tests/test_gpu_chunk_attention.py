@@ -217,6 +217,63 @@ def test_dense_equals_sparse_when_everything_is_selected():
     assert torch.all((dense.float() - sparse).abs() <= tol)
 
 
+def reference64(q, k, v, lens, window=0):
+    """Attention of contiguous [tokens, heads, dim] requests on the GPU in 64 bits."""
+    outs, mags, at, row = [], [], 0, 0
+    for n, c in lens:
+        kk, vv = k[at:at + c].double(), v[at:at + c].double()
+        group = q.shape[1] // k.shape[1]
+        kk, vv = (x.repeat_interleave(group, 1).transpose(0, 1) for x in (kk, vv))
+        s = torch.matmul(q[row:row + n].double().transpose(0, 1), kk.transpose(1, 2)) * q.shape[2] ** -0.5
+        p = torch.arange(c - n, c, device="cuda")[:, None]
+        t = torch.arange(c, device="cuda")
+        hide = (t > p) | ((t <= p - window) if window else (t > p))
+        w = torch.softmax(s.masked_fill(hide, -float("inf")), -1)
+        outs.append(torch.matmul(w, vv).transpose(0, 1))
+        mags.append(torch.matmul(w, vv.abs()).transpose(0, 1))
+        at, row = at + c, row + n
+    return torch.cat(outs), torch.cat(mags)
+
+
+@pytest.mark.parametrize("quantised", [False, True])
+@pytest.mark.parametrize("D,hkv,group,page,lens,window", [
+    (128, 8, 4, 128, [(2048, 2048), (1000, 1500)], 0),            # many units of few tiles, ends cut
+    (128, 4, 5, 16, [(3001, 3001), (70, 70)], 60),                # one tile or two in every unit
+    (256, 2, 12, 64, [(701, 4000), (1, 3500), (300, 300)], 0),
+    (256, 4, 3, 8, [(1500, 1500)] * 2, 40),
+    (128, 1, 128, 64, [(60, 1000), (1, 1), (2, 129)], 0),         # two query tokens fill a unit
+    (256, 8, 1, 256, [(1, 300 + 61 * i) for i in range(50)], 0),  # more requests than a warp
+    (128, 2, 7, 32, [(1 + i % 3, 5 + 37 * i) for i in range(70)], 0),
+])
+def test_many_units(D, hkv, group, page, lens, window, quantised):
+    g = torch.Generator(device="cuda").manual_seed(40)
+    T, C = sum(n for n, _ in lens), sum(c for _, c in lens)
+    need = [-(-c // page) for _, c in lens]
+    table = torch.full((len(lens), max(need)), -1, dtype=torch.int32)
+    perm, at = torch.randperm(sum(need), generator=torch.Generator().manual_seed(41)).to(torch.int32), 0
+    for b, m in enumerate(need):
+        table[b, :m] = perm[at:at + m]
+        at += m
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    cache = qsa.KVCache.empty(sum(need), page, hkv, D, table.cuda(), quantised=quantised)
+    for t in (cache.k, cache.v):
+        t.view(torch.uint8).fill_(0x7F)                               # NaN in both formats
+    kv = torch.randn(C, 2 * hkv, D, generator=g, device="cuda", dtype=torch.float16)
+    starts = i32(np.concatenate([[0], np.cumsum([c for _, c in lens])]).tolist())
+    zero = torch.zeros(len(lens), dtype=torch.int32, device="cuda")
+    qsa.kv_store(kv[:, :hkv], kv[:, hkv:], starts, zero, cache)
+    k, v = qsa.kv_load(starts, zero, C, cache)
+    q = torch.randn(T, hkv * group, D, generator=g, device="cuda", dtype=torch.float16)
+    ss = i32(np.concatenate([[0], np.cumsum([n for n, _ in lens])]).tolist())
+    out = qsa.chunk_attention(q, ss, i32([c - n for n, c in lens]), cache, window=window)
+    ok()
+    want, mag = reference64(q, k, v, lens, window)
+    n = max(c for _, c in lens) if not window else window
+    tol = 2.0 ** -11 * want.abs() + 2.0 ** -10 * mag + n * 2.0 ** -25 * 6.0 + 2.0 ** -25
+    off = (out.double() - want).abs()
+    assert torch.all(off <= tol), float((off / tol).max())
+
+
 def test_binding_refuses():
     b = Batch(39, [(4, 9)], hkv=2, group=2, head_dim=128, page=8, quantised=False)
     cache = device_cache(b, b.stored())
