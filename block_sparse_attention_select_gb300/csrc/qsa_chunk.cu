@@ -25,17 +25,22 @@
 // pair finds its share itself from seq_start and pos_start: no plan kernel and
 // no host knowledge of the lengths.
 //
-// A CTA's warps: 0-7 softmax (warp w: TMEM lane quarter w % 4 = 32 rows, half
-// w / 4 of a tile's tokens and of the output's dimensions), 8 loads K and V by
-// TMA, one box per page piece, through the block table, 9 issues the MMAs (in
-// the first CTA of the pair), 12-15 load the queries, clear the value rows that
-// nothing attends and, from the E4M3 cache, turn the loaded codes into FP16
-// tiles; 10 and 11 only give their registers to the softmax.  The MMA warp runs
-// one score product ahead (two S buffers):
+// A CTA's warps: 0-7 softmax, 8 loads K and V by TMA, one box per page piece,
+// through the block table, 9 issues the MMAs (in the first CTA of the pair),
+// 10-13 load the queries, clear the value rows that nothing attends and, from
+// the E4M3 cache, turn the loaded codes into FP16 tiles.  The MMA warp runs one
+// score product ahead (two S buffers):
 //   S(0) S(1) | O(0) S(2) | O(1) S(3) | ...
 // so the softmax of a tile overlaps the products of its neighbours.  P goes
 // back into its S buffer's columns as FP16 and is the A operand of the second
 // product from there.  K and V share a ring of slots in the order of use.
+//
+// Softmax warps 0-3 take the even tiles and 4-7 the odd ones (warp w: TMEM lane
+// quarter w % 4, a row per thread), so that one group's exponentials run beside
+// the other's loads, maxima and waits.  A row's running maximum passes from
+// tile to tile, from one group to the other, before the exponentials start;
+// each group keeps its own sum.  The scores are read from TMEM twice (maximum,
+// exponentials) in pieces of 32, which needs fewer registers than holding them.
 //
 // The accumulator is rescaled only when a row's maximum has grown by more than
 // 2^8 since the one in use: P is then at most 256, far inside FP16, and the sum
@@ -59,7 +64,7 @@ constexpr int CH_HALF = 128;                 // rows of one CTA: TMEM lanes
 constexpr int CH_ROWS = 256;                 // (token, head) rows of a unit: MMA M
 constexpr int CH_TILE = 128;                 // tokens of a tile
 constexpr int CH_SOFT = 8;                   // softmax warps
-constexpr int CH_LOAD = 8, CH_MMA = 9, CH_HELP = 12;
+constexpr int CH_LOAD = 8, CH_MMA = 9, CH_HELP = 10;
 constexpr int CH_HELPERS = 4;
 constexpr int CH_WARPS = CH_HELP + CH_HELPERS;
 constexpr int CH_THREADS = 32 * CH_WARPS;
@@ -80,8 +85,9 @@ struct Shape {
 
 struct Ctrl {
     uint64_t full[12], empty[12], raw_full[RAWS], raw_empty[RAWS], bnd[8];
-    uint64_t s_full[2], p_full[2], o_done, q_full, q_free, drain;
-    alignas(8) float xch[2][2][CH_HALF];                // [tile parity][half][row]: row maxima, sums
+    uint64_t s_full[2], p_full[2], o_done[2], m_out[2][4], q_full, q_free, drain;
+    alignas(8) float mrow[2][CH_HALF];       // [tile parity][row]: maximum in use at the group's last tile
+    float lrow[2][CH_HALF];                  // [tile parity][row]: sums of a segment
     uint16_t scale[2][CH_TILE];              // [slot parity][token]: FP16 scale (E4M3)
     int64_t w0, w1, total;                   // this pair's tiles, all tiles
     int32_t pairs;                           // pairs that have work
@@ -195,7 +201,7 @@ __device__ __forceinline__ void find_work(const ChunkParams &p, Ctrl &c, int war
     int64_t mine = 0;
     for (int32_t b = first; b < first + run && b < p.kv.n_reqs; b += 32)
         mine += warp_sum(request_tiles(p, b + lane, lane, blockIdx.x == 0));
-    int64_t *warp_work = reinterpret_cast<int64_t *>(&c.xch[0][0][0]);    // free until the first tile
+    int64_t *warp_work = reinterpret_cast<int64_t *>(&c.mrow[0][0]);    // free until the first tile
     if (lane == 0) warp_work[warp] = mine;
     __syncthreads();
     int64_t total = 0, before = 0;
@@ -423,6 +429,16 @@ __device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const uint32_t (&v)[
         : "memory");
 }
 
+__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&v)[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ float exp2_approx(float x)
@@ -430,6 +446,27 @@ __device__ __forceinline__ float exp2_approx(float x)
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// two FP32 lanes at once
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tadd.rn.f32x2 d, a, b;\n\t"
+        "mov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
 }
 
 __device__ __forceinline__ void named_barrier(int id, int threads)
@@ -474,9 +511,10 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
         for (int i = 0; i < 8; ++i) mbar_init(&c.bnd[i], 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&c.s_full[i], 1);
-            mbar_init(&c.p_full[i], 2 * CH_SOFT);
+            mbar_init(&c.p_full[i], CH_SOFT);                // four warps of each CTA
+            mbar_init(&c.o_done[i], 1);
+            for (int k = 0; k < 4; ++k) mbar_init(&c.m_out[i][k], 1);
         }
-        mbar_init(&c.o_done, 1);
         mbar_init(&c.q_full, 2 * CH_HELPERS);
         mbar_init(&c.q_free, 1);
         mbar_init(&c.drain, 1);
@@ -497,9 +535,6 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
     const uint32_t tmem = c.tmem;
     const uint32_t ring_a = smem_u32(ring);
     Walk w(p, c);
-    // registers after the split: 8 x 32 x 168 + 8 x 32 x 88 = 65,536
-    if (warp >= CH_LOAD && warp < CH_HELP) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == CH_LOAD) {
         // ---------------------------------------------------------- K, V loads
         uint8_t *dst0 = Q8 ? raw : ring;
@@ -641,7 +676,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                         umma2_f16_ta(tmem + TM_O, tmem + TM_S + (i & 1u) * 128u + kk * 8u, vd + ((kk * 2048u) >> 4),
                                      idesc_o, j + kk > 0 ? 1u : 0u);
                     umma2_commit(&c.empty[slot]);
-                    umma2_commit(&c.o_done);
+                    umma2_commit(&c.o_done[i & 1u]);
                 }
                 __syncwarp();
                 advance();
@@ -658,9 +693,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
             }
             __syncwarp();
         }
-    }
     } else if (warp >= CH_HELP) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         // --------------------- queries, cut value tiles, E4M3 codes to FP16 tiles
         const int ht = t - CH_HELP * 32;                      // 0 .. 127
         uint32_t seg = 0, slot = 0, phase = 0, rslot = 0, rphase = 0, ring0 = 0, nb = 0;
@@ -816,15 +849,15 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
             }
             w.done(p);
         }
-    } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+    } else if (warp < CH_SOFT) {
         // ------------------------------------------------------------- softmax
         constexpr int OC = D / 2;                              // output columns per thread
-        const int lq = warp & 3, half = warp >> 2, row = lq * 32 + lane;
+        const int lq = warp & 3, grp = warp >> 2, row = lq * 32 + lane;
         const uint32_t lane_base = static_cast<uint32_t>(lq * 32) << 16;
+        const uint32_t ts = tmem + TM_S + grp * 128u + lane_base;
         const float cs = p.scale * 1.4426950408889634f;        // scores in powers of two
-        const uint32_t p_full0 = of_first(&c.p_full[0]);
-        uint32_t it = 0;
+        const uint32_t p_full0 = of_first(&c.p_full[grp]);
+        uint32_t it = 0;                                       // tiles before the segment
         bool ok = true;                                        // false: keep to the barriers, do nothing
         Split split = {0, 0, 0, 0, 0};
         while (w.next(p)) {
@@ -836,101 +869,116 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
             const int32_t first = p.window > 0 ? max(0, pos - p.window + 1) : 0;
             const bool live = lq * 32 < mine;                  // some row of this warp is in use
             float m = -INFINITY, l = 0.0f;
-            for (int32_t j = 0; j < n; ++j, ++it) {
-                const uint32_t buf = it & 1u;
-                const uint32_t ts = tmem + TM_S + buf * 128u + lane_base;
-                if (ok) ok = warp_wait(&c.s_full[buf], (it >> 1) & 1u, abort, lim);
-                float s[64];
+            for (int32_t j = (grp - it) & 1; ok && j < n; j += 2) {
+                const uint32_t i = it + j;                     // tile i & 1 == grp
+                ok = warp_wait(&c.s_full[grp], (i >> 1) & 1u, abort, lim);
+                const int32_t base = (w.j0 + j) * CH_TILE;
+                const int32_t hi = pos - base, lo = first - base;              // visible: lo <= column <= hi
+                const bool masked = __any_sync(0xffffffffu, hi < CH_TILE - 1 || lo > 0);
+                auto hide = [&](uint32_t (&u)[32], int k) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (32 * k + e > hi || 32 * k + e < lo) u[e] = 0xff800000u;   // -inf
+                };
                 float mx = -INFINITY;
                 if (ok && live) {
                     tc_fence_after();
+                    uint32_t u[2][32];
+                    tmem_ld_32x32b_x32(ts, u[0]);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        tmem_ld_wait();
+                        if (k < 3) tmem_ld_32x32b_x32(ts + (k + 1) * 32u, u[(k + 1) & 1]);
+                        uint32_t (&x)[32] = u[k & 1];
+                        if (masked) hide(x, k);
+                        float a[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) a[e] = fmaxf(__uint_as_float(x[e]), __uint_as_float(x[e + 4]));
+#pragma unroll
+                        for (int e = 8; e < 32; e += 8)
+#pragma unroll
+                            for (int f = 0; f < 4; ++f)
+                                a[f] = fmaxf(fmaxf(a[f], __uint_as_float(x[e + f])), __uint_as_float(x[e + f + 4]));
+                        mx = fmaxf(fmaxf(mx, fmaxf(a[0], a[1])), fmaxf(a[2], a[3]));
+                    }
+                }
+                // the maximum in use at the tile before, and the one for this tile
+                if (ok && i > 0) ok = warp_wait(&c.m_out[grp ^ 1][lq], ((i - 1) >> 1) & 1u, abort, lim);
+                float mp = j > 0 ? c.mrow[grp ^ 1][row] : -INFINITY;
+                const bool grow = (mx - mp) * cs > RESCALE;
+                const float mi = grow ? mx : mp;
+                c.mrow[grp][row] = mi;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&c.m_out[grp][lq]);
+                if (ok && live) {
+                    const float mc = mi == -INFINITY ? 0.0f : mi * cs;
+                    if (m != mi) l *= exp2_approx(m * cs - mc);                // 0 at the first
+                    m = mi;
+                    float2 sum[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
+                    const float2 c2 = make_float2(cs, cs), mc2 = make_float2(-mc, -mc);
+                    uint32_t u[2][32];
+                    tmem_ld_32x32b_x32(ts, u[0]);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        tmem_ld_wait();
+                        if (k < 3) tmem_ld_32x32b_x32(ts + (k + 1) * 32u, u[(k + 1) & 1]);
+                        uint32_t (&x)[32] = u[k & 1];
+                        if (masked) hide(x, k);
+                        uint32_t o[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const float2 y = fma2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), c2, mc2);
+                            const float2 z = make_float2(exp2_approx(y.x), exp2_approx(y.y));
+                            sum[e & 1] = add2(sum[e & 1], z);
+                            const __half2 h = __floats2half2_rn(z.x, z.y);
+                            o[e] = *reinterpret_cast<const uint32_t *>(&h);
+                        }
+                        // columns 16 k .. of P over scores that have been read
+                        tmem_st_x16(ts + k * 16u, o);
+                    }
+                    l += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
+                }
+                if (ok && i > 0) ok = warp_wait(&c.o_done[grp ^ 1], ((i - 1) >> 1) & 1u, abort, lim);
+                if (ok && live && j > 0 && __any_sync(0xffffffffu, grow)) {
+                    tc_fence_after();
+                    const float alpha = grow ? exp2_approx((mp - mi) * cs) : 1.0f;
                     uint32_t u[32];
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        tmem_ld_32x32b_x32(ts + half * 64u + k * 32u, u);
+                    for (int k = 0; k < D / 32; ++k) {
+                        tmem_ld_32x32b_x32(tmem + TM_O + lane_base + k * 32u, u);
                         tmem_ld_wait();
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) s[32 * k + i] = __uint_as_float(u[i]);
+                        for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * alpha);
+                        tmem_st_x32(tmem + TM_O + lane_base + k * 32u, u);
                     }
-                    const int32_t base = (w.j0 + j) * CH_TILE + half * 64;
-                    const int32_t hi = pos - base, lo = first - base;         // visible: lo <= i <= hi
-                    if (__any_sync(0xffffffffu, hi < 63 || lo > 0)) {
-#pragma unroll
-                        for (int i = 0; i < 64; ++i)
-                            if (i > hi || i < lo) s[i] = -INFINITY;
-                    }
-                    float a0 = s[0], a1 = s[1], a2 = s[2], a3 = s[3];
-#pragma unroll
-                    for (int i = 4; i < 64; i += 4) {
-                        a0 = fmaxf(a0, s[i]);
-                        a1 = fmaxf(a1, s[i + 1]);
-                        a2 = fmaxf(a2, s[i + 2]);
-                        a3 = fmaxf(a3, s[i + 3]);
-                    }
-                    mx = fmaxf(fmaxf(a0, a1), fmaxf(a2, a3));
-                    c.xch[buf][half][row] = mx;
                 }
-                // both halves have read their scores and left their maxima
-                named_barrier(BAR_PAIR + lq, 64);
-                if (ok && live) {
-                    mx = fmaxf(mx, c.xch[buf][half ^ 1][row]);
-                    const bool grow = (mx - m) * cs > RESCALE;  // the same in both halves
-                    float alpha = 1.0f;
-                    if (grow) {
-                        alpha = exp2_approx((m - mx) * cs);     // 0 at the first
-                        m = mx;
-                    }
-                    const float mc = m == -INFINITY ? 0.0f : m * cs;
-                    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                    uint32_t u[32];
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const float e0 = exp2_approx(fmaf(s[2 * i], cs, -mc));
-                        const float e1 = exp2_approx(fmaf(s[2 * i + 1], cs, -mc));
-                        sum[i & 3] += e0 + e1;
-                        const __half2 h = __floats2half2_rn(e0, e1);
-                        u[i] = *reinterpret_cast<const uint32_t *>(&h);
-                    }
-                    tmem_st_x32(ts + half * 32u, u);
-                    l = fmaf(l, alpha, (sum[0] + sum[1]) + (sum[2] + sum[3]));
-                    if (j > 0) ok = warp_wait(&c.o_done, (it - 1) & 1u, abort, lim);
-                    if (ok && j > 0 && __any_sync(0xffffffffu, grow)) {
-                        tc_fence_after();
-                        const uint32_t to = tmem + TM_O + lane_base + half * OC;
-#pragma unroll
-                        for (int k = 0; k < OC / 32; ++k) {
-                            tmem_ld_32x32b_x32(to + k * 32u, u);
-                            tmem_ld_wait();
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(__uint_as_float(u[i]) * alpha);
-                            tmem_st_x32(to + k * 32u, u);
-                        }
-                    }
-                    tmem_st_wait();
-                } else if (ok && j > 0) {
-                    ok = warp_wait(&c.o_done, (it - 1) & 1u, abort, lim);
-                }
+                tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (ok && lane == 0) cluster_arrive(p_full0 + buf * 8u);
+                if (ok && lane == 0) cluster_arrive(p_full0);
             }
+            it += n;
             // the segment's sums: its rows' output, or its part of it
-            if (ok) ok = warp_wait(&c.o_done, (it - 1) & 1u, abort, lim);
-            float *lx = &c.xch[it & 1u][0][0];                 // not the last tile's buffer
-            if (ok && live) lx[half * CH_HALF + row] = l;
+            if (ok) ok = warp_wait(&c.o_done[(it - 1) & 1u], ((it - 1) >> 1) & 1u, abort, lim);
+            c.lrow[grp][row] = l;
             named_barrier(BAR_PAIR + lq, 64);
-            if (ok && live) l += lx[(half ^ 1) * CH_HALF + row];
+            {
+                // both groups' sums at the last tile's maximum
+                const float ml = c.mrow[(it - 1) & 1u][row], lo = c.lrow[grp ^ 1][row], mo = c.mrow[grp ^ 1][row];
+                l = (l > 0.0f ? l * exp2_approx((m - ml) * cs) : 0.0f) + (lo > 0.0f ? lo * exp2_approx((mo - ml) * cs) : 0.0f);
+                m = ml;
+            }
             named_barrier(BAR_PAIR + lq, 64);                  // read before the next tile's maxima
             if (ok && live) {
                 tc_fence_after();
-                const uint32_t to = tmem + TM_O + lane_base + half * OC;
+                const uint32_t to = tmem + TM_O + lane_base + grp * OC;
                 const bool in = row < mine;
                 uint32_t u[32];
                 if (w.whole) {
                     const float inv = l > 0.0f ? 1.0f / l : 0.0f;
                     const int32_t v = w.u.v0 + rank * CH_HALF + row, tok = v / p.group, h = v - tok * p.group;
                     __half *out = static_cast<__half *>(p.out) +
-                                  ((static_cast<int64_t>(w.s.s0) + tok) * p.hq + w.g * p.group + h) * D + half * OC;
+                                  ((static_cast<int64_t>(w.s.s0) + tok) * p.hq + w.g * p.group + h) * D + grp * OC;
 #pragma unroll
                     for (int k = 0; k < OC / 32; ++k) {
                         tmem_ld_32x32b_x32(to + k * 32u, u);
@@ -954,8 +1002,8 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                     const int64_t place = 2 * static_cast<int64_t>(blockIdx.x >> 1) + (w.head ? 1 : 0);
                     const int ur = rank * CH_HALF + row;
                     float *ml = reinterpret_cast<float *>(p.ws + WS_ML) + (place * CH_ROWS + ur) * 2;
-                    float *part = reinterpret_cast<float *>(p.ws + WS_O) + (place * p.ws_rows + ur) * D + half * OC;
-                    if (in && half == 0) {
+                    float *part = reinterpret_cast<float *>(p.ws + WS_O) + (place * p.ws_rows + ur) * D + grp * OC;
+                    if (in && grp == 0) {
                         ml[0] = m == -INFINITY ? -INFINITY : m * cs;
                         ml[1] = l;
                     }
