@@ -18,7 +18,9 @@
 // (token * group + head) of one request and KV head.
 //
 // Work: the units' tiles, in the order (request, rows, KV head), form one line
-// of W tiles that the CTA pairs share out evenly, so one row over a long cache,
+// that the CTA pairs share out evenly (each unit a little longer than its tiles
+// for what it costs besides them: without that, pairs with many short units
+// ended last, 1,019 us against 8xx us on four prompts of 4,096 tokens), so one row over a long cache,
 // a batch of unequal requests and a long prompt all fill the card.  A unit that
 // lies across pairs leaves unnormalised FP32 partial sums with their maxima in
 // the workspace (at most two per pair), which a second kernel joins.  Every
@@ -27,20 +29,21 @@
 //
 // A CTA's warps: 0-7 softmax, 8 loads K and V by TMA, one box per page piece,
 // through the block table, 9 issues the MMAs (in the first CTA of the pair),
-// 10-13 load the queries, clear the value rows that nothing attends and, from
-// the E4M3 cache, turn the loaded codes into FP16 tiles.  The MMA warp runs one
-// score product ahead (two S buffers):
-//   S(0) S(1) | O(0) S(2) | O(1) S(3) | ...
-// so the softmax of a tile overlaps the products of its neighbours.  P goes
-// back into its S buffer's columns as FP16 and is the A operand of the second
-// product from there.  K and V share a ring of slots in the order of use.
+// 12-15 load the queries, clear the value rows that nothing attends and, from
+// the E4M3 cache, turn the loaded codes into FP16 tiles; 10 and 11 only give
+// their registers away.  K and V share a ring of slots in the order of use.
 //
 // Softmax warps 0-3 take the even tiles and 4-7 the odd ones (warp w: TMEM lane
 // quarter w % 4, a row per thread), so that one group's exponentials run beside
-// the other's loads, maxima and waits.  A row's running maximum passes from
-// tile to tile, from one group to the other, before the exponentials start;
-// each group keeps its own sum.  The scores are read from TMEM twice (maximum,
-// exponentials) in pieces of 32, which needs fewer registers than holding them.
+// the other's waits; S has a buffer for each.  A thread takes its 128 scores
+// into registers, its row's running maximum passes on from tile to tile, from
+// one group to the other, before the exponentials start, and each group keeps
+// its own sum.  P goes to TMEM as FP16 and is the A operand of the second
+// product from there.  With D = 128, P has columns of its own, so the score
+// product of the tile after next starts as soon as the scores are in registers:
+//   S(0) S(1) | S(2) O(0) | S(3) O(1) | ...
+// With D = 256, TMEM is full (2 x 128 for S, 256 for O): P overwrites its
+// scores and the order is S(0) S(1) | O(0) S(2) | O(1) S(3) | ...
 //
 // The accumulator is rescaled only when a row's maximum has grown by more than
 // 2^8 since the one in use: P is then at most 256, far inside FP16, and the sum
@@ -64,14 +67,16 @@ constexpr int CH_HALF = 128;                 // rows of one CTA: TMEM lanes
 constexpr int CH_ROWS = 256;                 // (token, head) rows of a unit: MMA M
 constexpr int CH_TILE = 128;                 // tokens of a tile
 constexpr int CH_SOFT = 8;                   // softmax warps
-constexpr int CH_LOAD = 8, CH_MMA = 9, CH_HELP = 10;
+constexpr int CH_LOAD = 8, CH_MMA = 9, CH_HELP = 12;
 constexpr int CH_HELPERS = 4;
 constexpr int CH_WARPS = CH_HELP + CH_HELPERS;
 constexpr int CH_THREADS = 32 * CH_WARPS;
 constexpr int RAWS = 4;                      // slots of loaded codes (E4M3)
+constexpr int MAX_SLOTS = 10;                // slots of the ring at most
 constexpr uint32_t RING = 229376;            // bytes for Q and the ring
 constexpr float RESCALE = 8.0f;              // log2 of the growth that rescales
 constexpr uint32_t TM_S = 0, TM_O = 256;     // TMEM columns: two S buffers of 128, O
+constexpr int UNIT_COST = 4;                 // tiles' worth of time that a unit costs besides its tiles
 constexpr int BAR_PAIR = 1, BAR_HELP = 5;    // named barriers: four softmax warp pairs, the helpers
 
 template <int D, bool Q8>
@@ -80,18 +85,21 @@ struct Shape {
     // a CTA's half of a K tile: 64 tokens, or of a V tile: D / 2 dims of 128 tokens
     static constexpr uint32_t SLOT = 128 * D, RAW = SLOT / 2;
     static constexpr int KTOK = 64, VTOK = CH_TILE;
-    static constexpr int NS = (RING - QB - (Q8 ? RAWS * RAW : 0)) / SLOT;
+    static constexpr int FIT = (RING - QB - (Q8 ? RAWS * RAW : 0)) / SLOT, NS = FIT < MAX_SLOTS ? FIT : MAX_SLOTS;
+    static constexpr bool OWN_P = D == 128;                            // P beside S, not over it
+    static constexpr uint32_t TM_P = OWN_P ? 384 : TM_S, P_STRIDE = OWN_P ? 64 : 128;
+    static constexpr int LEAD = OWN_P ? 3 : 2;                         // key tiles loaded before the first value tile
 };
 
 struct Ctrl {
-    uint64_t full[12], empty[12], raw_full[RAWS], raw_empty[RAWS], bnd[8];
-    uint64_t s_full[2], p_full[2], o_done[2], m_out[2][4], q_full, q_free, drain;
+    uint64_t full[MAX_SLOTS], empty[MAX_SLOTS], raw_full[RAWS], raw_empty[RAWS], bnd[8];
+    uint64_t s_full[2], s_free[2], p_full[2], o_done[2], m_out[2][4], q_full, q_free, drain;
     alignas(8) float mrow[2][CH_HALF];       // [tile parity][row]: maximum in use at the group's last tile
     float lrow[2][CH_HALF];                  // [tile parity][row]: sums of a segment
     uint16_t scale[2][CH_TILE];              // [slot parity][token]: FP16 scale (E4M3)
-    int64_t w0, w1, total;                   // this pair's tiles, all tiles
+    int64_t w0, w1, total;                   // this pair's share of the line, the line's length
     int32_t pairs;                           // pairs that have work
-    int32_t b, m, g, off;                    // the unit of tile w0, and w0's place in it
+    int32_t b, m, g, off;                    // the unit that w0 lies in, and w0's place in it
     uint32_t tmem;
     int32_t abort;
 };
@@ -137,128 +145,112 @@ __device__ __forceinline__ Unit unit_of(const ChunkParams &p, const Seq &s, int3
     return u;
 }
 
-__device__ __forceinline__ int64_t warp_sum(int64_t x)
-{
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    return x;
-}
-
-__device__ __forceinline__ int64_t warp_scan(int64_t x, int lane)      // inclusive
+template <typename T>
+__device__ __forceinline__ T warp_scan(T x, int lane)      // inclusive
 {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+        const T y = __shfl_up_sync(0xffffffffu, x, o);
         if (lane >= o) x += y;
     }
     return x;
 }
 
-// Tiles of request b over all its units and KV heads, for the warp's 32
-// requests b (one per lane): long requests are summed by the whole warp.
-__device__ __forceinline__ int64_t request_tiles(const ChunkParams &p, int32_t b, int lane, bool flag)
+// The sum of x over the threads before this one, and over all of them.
+template <typename T>
+__device__ __forceinline__ T block_scan(T x, T *warp_total, int warp, int lane, T *total)
 {
-    Seq s{0, 0, 0};
-    if (b < p.kv.n_reqs) {
-        bool bad;
-        s = seq_of(p.kv, b, &bad);
-        if (bad && flag) record_error(p.kv.status, ST_BAD_ROW);
-    }
-    const int32_t n = units_of(p, s);
-    int64_t tiles = 0;
-    if (n <= 4)
-        for (int32_t m = 0; m < n; ++m) {
-            const Unit u = unit_of(p, s, m);
-            tiles += u.hi - u.lo;
-        }
-    uint32_t big = __ballot_sync(0xffffffffu, n > 4);
-    while (big) {
-        const int src = __ffs(big) - 1;
-        big &= big - 1;
-        Seq t;
-        t.s0 = __shfl_sync(0xffffffffu, s.s0, src);
-        t.n = __shfl_sync(0xffffffffu, s.n, src);
-        t.p0 = __shfl_sync(0xffffffffu, s.p0, src);
-        const int32_t nu = units_of(p, t);
-        int64_t x = 0;
-        for (int32_t m = lane; m < nu; m += 32) {
-            const Unit u = unit_of(p, t, m);
-            x += u.hi - u.lo;
-        }
-        x = warp_sum(x);
-        if (lane == src) tiles = x;
-    }
-    return tiles * p.kv.hkv;
-}
-
-// Fills c.w0, c.w1 and, when there is work, the unit that w0 lies in (both CTAs
-// of a pair do, alike).
-__device__ __forceinline__ void find_work(const ChunkParams &p, Ctrl &c, int warp, int lane)
-{
-    // requests in equal runs of whole warps
-    const int32_t run = (p.kv.n_reqs + CH_THREADS - 1) / CH_THREADS * 32;
-    const int32_t first = warp * run;
-    int64_t mine = 0;
-    for (int32_t b = first; b < first + run && b < p.kv.n_reqs; b += 32)
-        mine += warp_sum(request_tiles(p, b + lane, lane, blockIdx.x == 0));
-    int64_t *warp_work = reinterpret_cast<int64_t *>(&c.mrow[0][0]);    // free until the first tile
-    if (lane == 0) warp_work[warp] = mine;
+    const T sc = warp_scan(x, lane);
+    if (lane == 31) warp_total[warp] = sc;
     __syncthreads();
-    int64_t total = 0, before = 0;
+    T before = 0, all = 0;
 #pragma unroll
     for (int w = 0; w < CH_WARPS; ++w) {
-        if (w == warp) before = total;
-        total += warp_work[w];
+        if (w == warp) before = all;
+        all += warp_total[w];
     }
-    // one tile each at least, so that the pairs with work are the first ones
+    *total = all;
+    return before + sc - x;
+}
+
+// Finds this pair's share of the line, c.w0 .. c.w1, and the unit that w0 lies
+// in (both CTAs of a pair do, alike).  Each thread counts the units of a run of
+// requests, then adds up the lengths of an equal run of units.
+__device__ __forceinline__ void find_work(const ChunkParams &p, Ctrl &c, int warp, int lane)
+{
+    const int t = threadIdx.x;
+    // free until the first tile
+    int32_t *prefix = reinterpret_cast<int32_t *>(&c.mrow[0][0]);
+    int32_t *wt32 = reinterpret_cast<int32_t *>(&c.scale[0][0]);
+    int64_t *wt64 = reinterpret_cast<int64_t *>(&c.scale[1][0]);
+    const int32_t run = (p.kv.n_reqs + CH_THREADS - 1) / CH_THREADS;
+    const int32_t r0 = min(t * run, p.kv.n_reqs), r1 = min(r0 + run, p.kv.n_reqs);
+    int32_t mine = 0, units;
+    for (int32_t b = r0; b < r1; ++b) {
+        bool bad;
+        mine += units_of(p, seq_of(p.kv, b, &bad));
+        if (bad && blockIdx.x == 0) record_error(p.kv.status, ST_BAD_ROW);
+    }
+    prefix[t] = block_scan(mine, wt32, warp, lane, &units);
+    __syncthreads();
+    const int32_t u0 = static_cast<int32_t>(static_cast<int64_t>(units) * t / CH_THREADS);
+    const int32_t u1 = static_cast<int32_t>(static_cast<int64_t>(units) * (t + 1) / CH_THREADS);
+    int32_t b0 = 0, m0 = 0;
+    Seq s0{0, 0, 0};
+    int64_t cost = 0, total;
+    if (u0 < u1) {
+        int lo = 0;                                          // the last run that starts at or before u0
+#pragma unroll
+        for (int step = CH_THREADS / 2; step > 0; step >>= 1)
+            if (prefix[lo + step] <= u0) lo += step;
+        b0 = lo * run;
+        m0 = u0 - prefix[lo];
+        bool bad;
+        s0 = seq_of(p.kv, b0, &bad);
+        for (int32_t n = units_of(p, s0); m0 >= n; n = units_of(p, s0)) {
+            m0 -= n;
+            s0 = seq_of(p.kv, ++b0, &bad);
+        }
+        int32_t b = b0, m = m0;
+        Seq s = s0;
+        for (int32_t u = u0; u < u1; ++u, ++m) {
+            while (m >= units_of(p, s)) {
+                s = seq_of(p.kv, ++b, &bad);
+                m = 0;
+            }
+            const Unit un = unit_of(p, s, m);
+            cost += UNIT_COST + un.hi - un.lo;
+        }
+        cost *= p.kv.hkv;
+    }
+    int64_t at = block_scan(cost, wt64, warp, lane, &total);
+    // one place each at least, so that the pairs with work are the first ones
     const int32_t pairs = static_cast<int32_t>(min(total, static_cast<int64_t>(gridDim.x >> 1)));
     const int32_t me = blockIdx.x >> 1;
     const int64_t w0 = me < pairs ? total * me / pairs : 0, w1 = me < pairs ? total * (me + 1) / pairs : 0;
-    if (warp == 0 && lane == 0) {
+    if (t == 0) {
         c.w0 = w0;
         c.w1 = w1;
         c.total = total;
         c.pairs = pairs;
     }
-    if (w0 < w1 && before <= w0 && w0 < before + mine) {
-        int64_t at = before;
-        for (int32_t b0 = first;; b0 += 32) {
-            const int64_t tiles = request_tiles(p, b0 + lane, lane, false);
-            const int64_t scan = warp_scan(tiles, lane);
-            const uint32_t past = __ballot_sync(0xffffffffu, at + scan > w0);
-            if (past) {
-                const int src = __ffs(past) - 1;
-                at += __shfl_sync(0xffffffffu, scan - tiles, src);
-                const int32_t b = b0 + src;
+    if (w0 < w1 && at <= w0 && w0 < at + cost) {
+        for (;; ++m0) {
+            while (m0 >= units_of(p, s0)) {
                 bool bad;
-                const Seq s = seq_of(p.kv, b, &bad);
-                const int32_t n = units_of(p, s);
-                for (int32_t m0 = 0; m0 < n; m0 += 32) {
-                    int64_t x = 0;
-                    int32_t len = 0;
-                    if (m0 + lane < n) {
-                        const Unit u = unit_of(p, s, m0 + lane);
-                        len = u.hi - u.lo;
-                        x = static_cast<int64_t>(len) * p.kv.hkv;
-                    }
-                    const int64_t sc = warp_scan(x, lane);
-                    const uint32_t in = __ballot_sync(0xffffffffu, at + sc > w0);
-                    if (in) {
-                        if (lane == __ffs(in) - 1) {
-                            const int32_t rest = static_cast<int32_t>(w0 - (at + sc - x));
-                            c.b = b;
-                            c.m = m0 + lane;
-                            c.g = rest / len;
-                            c.off = rest % len;
-                        }
-                        break;
-                    }
-                    at += __shfl_sync(0xffffffffu, sc, 31);
-                }
+                s0 = seq_of(p.kv, ++b0, &bad);
+                m0 = 0;
+            }
+            const Unit un = unit_of(p, s0, m0);
+            const int32_t len = UNIT_COST + un.hi - un.lo;
+            if (w0 < at + static_cast<int64_t>(len) * p.kv.hkv) {
+                c.b = b0;
+                c.m = m0;
+                c.g = static_cast<int32_t>(w0 - at) / len;
+                c.off = static_cast<int32_t>(w0 - at) % len;
                 break;
             }
-            at += __shfl_sync(0xffffffffu, scan, 31);
-            if (b0 + 32 >= first + run) break;
+            at += static_cast<int64_t>(len) * p.kv.hkv;
         }
     }
     __syncthreads();
@@ -298,12 +290,15 @@ struct Walk {
             load(p);
         }
         u = unit_of(p, s, m);
-        j0 = u.lo + off;
-        j1 = min(static_cast<int64_t>(u.hi), j0 + left);
-        head = off == 0;
+        // a unit's place in the line: UNIT_COST, then its tiles
+        const int32_t len = UNIT_COST + u.hi - u.lo;
+        const int32_t end = static_cast<int32_t>(min(static_cast<int64_t>(len), off + left));
+        left -= end - off;
+        j0 = u.lo + max(0, off - UNIT_COST);
+        j1 = u.lo + max(0, end - UNIT_COST);
+        head = j0 == u.lo;
         whole = head && j1 == u.hi;
-        left -= j1 - j0;
-        return true;
+        return j0 < j1;                      // false: the share ends before the unit's first tile
     }
     // whether tile j0 + k holds tokens that no row attends
     __device__ __forceinline__ bool cut(int32_t k) const
@@ -323,12 +318,22 @@ struct Walk {
 
 // ------------------------------------------------------------------- pieces --
 
-// Slot e of a segment of n tiles, in the order of use:
-// K(0) K(1) V(0) K(2) V(1) ... K(n-1) V(n-2) V(n-1).
+// Slot e of a segment of n tiles, in the order of use: LEAD key tiles, then
+// value and key tiles in turn, then the value tiles left,
+// e.g. K(0) K(1) V(0) K(2) V(1) ... K(n-1) V(n-2) V(n-1).
+template <int LEAD>
 __device__ __forceinline__ void slot_at(int32_t e, int32_t n, bool *is_v, int32_t *tile)
 {
-    *is_v = e > 0 && ((e & 1) == 0 || e == 2 * n - 1);
-    *tile = e == 2 * n - 1 ? n - 1 : *is_v ? e / 2 - 1 : (e + 1) / 2;
+    const int32_t lead = min(LEAD, n), r = e - lead, turns = 2 * (n - lead);
+    *is_v = r >= 0 && (r >= turns || (r & 1) == 0);
+    *tile = r < 0 ? e : r >= turns ? r - (n - lead) : (r >> 1) + ((r & 1) ? lead : 0);
+}
+
+template <int LEAD>
+__device__ __forceinline__ int32_t slot_of_v(int32_t tile, int32_t n)
+{
+    const int32_t lead = min(LEAD, n);
+    return lead + (tile < n - lead ? 2 * tile : n - lead + tile);
 }
 
 __device__ __forceinline__ uint32_t sw128(uint32_t row, uint32_t c)
@@ -489,7 +494,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
     using Sh = Shape<D, Q8>;
     constexpr int NS = Sh::NS;
     constexpr uint32_t SLOT = Sh::SLOT, RAW = Sh::RAW;
-    static_assert(NS >= 3 && NS <= 12, "ring: 12 slots hold at most 7 value tiles, fewer than the cut tiles' barriers");
+    static_assert(NS >= 3 && NS <= 10, "10 slots hold fewer value tiles than there are barriers for cut ones");
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t *q_s = smem, *ring = smem + Sh::QB, *raw = ring + NS * SLOT;
     Ctrl &c = *reinterpret_cast<Ctrl *>(smem + RING);
@@ -499,7 +504,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
     const uint64_t lim = p.wait_limit_ns;
 
     if (t == 0) {
-        // full, p_full and q_full count in the first CTA, for both
+        // full, s_free, p_full and q_full count in the first CTA, for both
         for (int i = 0; i < NS; ++i) {
             mbar_init(&c.full[i], Q8 ? 2 * CH_HELPERS : 2);
             mbar_init(&c.empty[i], 1);
@@ -512,6 +517,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
         for (int i = 0; i < 2; ++i) {
             mbar_init(&c.s_full[i], 1);
             mbar_init(&c.p_full[i], CH_SOFT);                // four warps of each CTA
+            mbar_init(&c.s_free[i], CH_SOFT);
             mbar_init(&c.o_done[i], 1);
             for (int k = 0; k < 4; ++k) mbar_init(&c.m_out[i][k], 1);
         }
@@ -535,6 +541,9 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
     const uint32_t tmem = c.tmem;
     const uint32_t ring_a = smem_u32(ring);
     Walk w(p, c);
+    // registers after the split: 8 x 32 x 200 + 8 x 32 x 56 = 65,536
+    if (warp >= CH_LOAD && warp < CH_HELP) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == CH_LOAD) {
         // ---------------------------------------------------------- K, V loads
         uint8_t *dst0 = Q8 ? raw : ring;
@@ -557,7 +566,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
         auto plan = [&](int32_t e) {
             bool v;
             int32_t tile;
-            slot_at(e, w.j1 - w.j0, &v, &tile);
+            slot_at<Sh::LEAD>(e, w.j1 - w.j0, &v, &tile);
             const int sh = v ? sh_v : sh_k;
             const int32_t toks = v ? Sh::VTOK : Sh::KTOK;
             const int lb = __ffs(toks) - 1 - sh;              // log2 of the boxes down
@@ -582,7 +591,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
             for (int32_t e = 0; e < 2 * n; ++e) {
                 bool v;
                 int32_t tile;
-                slot_at(e, n, &v, &tile);
+                slot_at<Sh::LEAD>(e, n, &v, &tile);
                 const int32_t xx = x, yy = y;
                 const uint32_t aa = at;
                 const bool mm = mine;
@@ -626,74 +635,75 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
         }
         __syncwarp();
     } else if (warp == CH_MMA && rank == 0) {
-        // --------------------------------------------------------------- MMAs
-        constexpr uint32_t idesc_s = umma_idesc_f16_f32(CH_ROWS, CH_TILE);
-        constexpr uint32_t idesc_o = umma_idesc_f16_f32(CH_ROWS, D) | (1u << 16);   // B: dims contiguous
-        const uint64_t qd = sw128_kmajor_desc(smem_u32(q_s));
-        uint32_t slot = 0, phase = 0, it = 0, seg = 0;
-        bool ok = true;
-        auto advance = [&] {
-            if (++slot == NS) {
-                slot = 0;
-                phase ^= 1u;
-            }
-        };
-        // S(i) = Q . K(i)^T
-        auto scores = [&](uint32_t i, bool last) {
-            ok = ok && warp_wait(&c.full[slot], phase, abort, lim);
-            if (!ok) return;
-            if (lane == 0) {
+        // ------------------------------------------------- MMAs, by one thread
+        if (lane == 0) {
+            constexpr uint32_t idesc_s = umma_idesc_f16_f32(CH_ROWS, CH_TILE);
+            constexpr uint32_t idesc_o = umma_idesc_f16_f32(CH_ROWS, D) | (1u << 16);   // B: dims contiguous
+            const uint64_t qd = sw128_kmajor_desc(smem_u32(q_s));
+            const uint64_t kd0 = sw128_kmajor_desc(ring_a), vd0 = sw128_mn_desc(ring_a, Sh::VTOK * 128);
+            uint32_t slot = 0, phase = 0, it = 0, seg = 0;
+            bool ok = true;
+            auto advance = [&] {
+                if (++slot == NS) {
+                    slot = 0;
+                    phase ^= 1u;
+                }
+            };
+            // S(i) = Q . K(i)^T
+            auto scores = [&](uint32_t i, bool last) {
+                ok = ok && mbar_wait(&c.full[slot], phase, abort, lim);
+                if (!ok) return;
                 tc_fence_after();
-                const uint64_t kd = sw128_kmajor_desc(ring_a + slot * SLOT);
+                const uint64_t kd = kd0 + slot * (SLOT >> 4);
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                     const uint32_t ch = kk >> 2, in = (kk & 3) * 32;
                     umma2_f16(tmem + TM_S + (i & 1u) * 128u, qd + ((ch * (CH_HALF * 128u) + in) >> 4),
                               kd + ((ch * (Sh::KTOK * 128u) + in) >> 4), idesc_s, kk > 0 ? 1u : 0u);
                 }
-                umma2_commit(&c.empty[slot]);
                 umma2_commit(&c.s_full[i & 1u]);
+                umma2_commit(&c.empty[slot]);
                 if (last) umma2_commit(&c.q_free);
-            }
-            __syncwarp();
-            advance();
-        };
-        while (ok && w.next(p)) {
-            const int32_t n = w.j1 - w.j0;
-            ok = warp_wait(&c.q_full, seg & 1u, abort, lim);
-            scores(it, n == 1);
-            if (n > 1) scores(it + 1, n == 2);
-            for (int32_t j = 0; ok && j < n; ++j) {
-                const uint32_t i = it + j;
-                ok = warp_wait(&c.p_full[i & 1u], (i >> 1) & 1u, abort, lim);
-                ok = ok && warp_wait(&c.full[slot], phase, abort, lim);
-                if (!ok) break;
-                if (lane == 0) {
+                advance();
+            };
+            while (ok && w.next(p)) {
+                const int32_t n = w.j1 - w.j0;
+                ok = mbar_wait(&c.q_full, seg & 1u, abort, lim);
+                scores(it, n == 1);
+                if (n > 1) scores(it + 1, n == 2);
+                for (int32_t j = 0; ok && j < n; ++j) {
+                    const uint32_t i = it + j;
+                    if (Sh::OWN_P && j + 2 < n) {
+                        ok = mbar_wait(&c.s_free[i & 1u], (i >> 1) & 1u, abort, lim);
+                        scores(i + 2, j + 3 == n);
+                    }
+                    ok = ok && mbar_wait(&c.full[slot], phase, abort, lim);
+                    ok = ok && mbar_wait(&c.p_full[i & 1u], (i >> 1) & 1u, abort, lim);
+                    if (!ok) break;
                     tc_fence_after();
-                    const uint64_t vd = sw128_mn_desc(ring_a + slot * SLOT, Sh::VTOK * 128);
+                    const uint64_t vd = vd0 + slot * (SLOT >> 4);
 #pragma unroll
                     for (int kk = 0; kk < CH_TILE / 16; ++kk)
-                        umma2_f16_ta(tmem + TM_O, tmem + TM_S + (i & 1u) * 128u + kk * 8u, vd + ((kk * 2048u) >> 4),
-                                     idesc_o, j + kk > 0 ? 1u : 0u);
-                    umma2_commit(&c.empty[slot]);
+                        umma2_f16_ta(tmem + TM_O, tmem + Sh::TM_P + (i & 1u) * Sh::P_STRIDE + kk * 8u,
+                                     vd + ((kk * 2048u) >> 4), idesc_o, j + kk > 0 ? 1u : 0u);
                     umma2_commit(&c.o_done[i & 1u]);
+                    umma2_commit(&c.empty[slot]);
+                    advance();
+                    if (!Sh::OWN_P && j + 2 < n) scores(i + 2, j + 3 == n);
                 }
-                __syncwarp();
-                advance();
-                if (j + 2 < n) scores(i + 2, j + 3 == n);
+                it += n;
+                ++seg;
+                w.done(p);
             }
-            it += n;
-            ++seg;
-            w.done(p);
-        }
-        if (!ok) {                                            // products still running
-            if (lane == 0) {
+            if (!ok) {                                        // products still running
                 umma2_commit(&c.drain);
                 mbar_wait_bounded(&c.drain, 0, lim);
             }
-            __syncwarp();
         }
+        __syncwarp();
+    }
     } else if (warp >= CH_HELP) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         // --------------------- queries, cut value tiles, E4M3 codes to FP16 tiles
         const int ht = t - CH_HELP * 32;                      // 0 .. 127
         uint32_t seg = 0, slot = 0, phase = 0, rslot = 0, rphase = 0, ring0 = 0, nb = 0;
@@ -702,18 +712,22 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
             const int32_t n = w.j1 - w.j0;
             if (ok && seg > 0) ok = warp_wait(&c.q_free, (seg - 1) & 1u, abort, lim);
             if (ok) {
-                constexpr int PC = D / 8;                      // 16-byte pieces of a row
-                const uint8_t *q = static_cast<const uint8_t *>(p.q);
-                const uint32_t qa = smem_u32(q_s);
-#pragma unroll 4
-                for (int e = ht; e < CH_HALF * PC; e += 32 * CH_HELPERS) {
-                    const int row = e / PC, pc = e % PC, ur = rank * CH_HALF + row;
-                    const bool in = ur < w.u.rows;
-                    const int32_t v = w.u.v0 + ur, tok = v / p.group, h = v - tok * p.group;
-                    const uint8_t *src = in ? q + ((static_cast<int64_t>(w.s.s0) + tok) * p.q_stride +
-                                                   (w.g * p.group + h) * D + pc * 8) * 2 : q;
-                    const uint32_t dst = qa + (pc >> 3) * (CH_HALF * 128u) + sw128(row, pc & 7);
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0)
+                // the warp's 32 rows: a lane finds one row's queries, then
+                // all lanes copy the rows, 512 bytes at a time
+                constexpr int RPI = 256 / D;                   // rows per copy instruction
+                const int r0 = (ht >> 5) * 32, ur = rank * CH_HALF + r0 + lane;
+                const int32_t v = w.u.v0 + ur, tok = v / p.group, h = v - tok * p.group;
+                const bool in = ur < w.u.rows;
+                const uint64_t mine = in ? reinterpret_cast<uint64_t>(p.q) +
+                    ((static_cast<int64_t>(w.s.s0) + tok) * p.q_stride + (w.g * p.group + h) * D) * 2 : 0;
+                const int pc = lane & (D / 8 - 1);
+                const uint32_t dst = smem_u32(q_s) + (pc >> 3) * (CH_HALF * 128u);
+#pragma unroll 8
+                for (int i = 0; i < 32 / RPI; ++i) {
+                    const int k = i * RPI + lane / (D / 8);
+                    const uint64_t src = __shfl_sync(0xffffffffu, mine, k);
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + sw128(r0 + k, pc & 7)),
+                                 "l"((src ? src : reinterpret_cast<uint64_t>(p.q)) + (src ? pc * 16 : 0)), "r"(src ? 16 : 0)
                                  : "memory");
                 }
                 asm volatile("cp.async.wait_all;" ::: "memory");
@@ -731,7 +745,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                     if ((k == 1 && n == 1) || !w.cut(tile)) continue;
                     if (ok) ok = warp_wait(&c.bnd[nb & 7u], (nb >> 3) & 1u, abort, lim);
                     ++nb;
-                    const uint32_t vs = (ring0 + (tile < n - 1 ? 2 * (tile + 1) : 2 * n - 1)) % NS;
+                    const uint32_t vs = (ring0 + slot_of_v<Sh::LEAD>(tile, n)) % NS;
                     if (ok) {
                         uint8_t *v = ring + vs * SLOT;
                         const int32_t a = w.u.lo_tok - (w.j0 + tile) * CH_TILE, z = w.u.hi_tok + 1 - (w.j0 + tile) * CH_TILE;
@@ -756,7 +770,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                     bool v;
                     int32_t tile;
                     if (e >= 2 * n) return -1;
-                    slot_at(e, n, &v, &tile);
+                    slot_at<Sh::LEAD>(e, n, &v, &tile);
                     const int32_t tok = (w.j0 + tile) * CH_TILE + (v ? 0 : rank * Sh::KTOK) + ht;
                     return ht < (v ? Sh::VTOK : Sh::KTOK) && tok >= w.u.lo_tok && tok <= w.u.hi_tok ? tok : -1;
                 };
@@ -765,7 +779,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                     if (page < 0 || page >= p.kv.num_pages) return 127u;
                     bool v;
                     int32_t tile;
-                    slot_at(e, n, &v, &tile);
+                    slot_at<Sh::LEAD>(e, n, &v, &tile);
                     return __ldg((v ? p.kv.v_scale : p.kv.k_scale) +
                                  ((static_cast<int64_t>(page) << p.kv.page_shift) + (tok & (p.kv.page_tokens - 1))) * p.kv.hkv + w.g);
                 };
@@ -777,7 +791,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                 for (int32_t e = 0; e < 2 * n; ++e) {
                     bool v;
                     int32_t tile;
-                    slot_at(e, n, &v, &tile);
+                    slot_at<Sh::LEAD>(e, n, &v, &tile);
                     const int32_t tok0 = (w.j0 + tile) * CH_TILE;      // V: rows outside lo_tok .. hi_tok are cleared
                     const int32_t a = v ? w.u.lo_tok - tok0 : 0, z = v ? w.u.hi_tok + 1 - tok0 : CH_TILE;
                     // 2^(byte - 127) as FP16 (2^-15 is subnormal)
@@ -849,14 +863,16 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
             }
             w.done(p);
         }
-    } else if (warp < CH_SOFT) {
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         // ------------------------------------------------------------- softmax
         constexpr int OC = D / 2;                              // output columns per thread
         const int lq = warp & 3, grp = warp >> 2, row = lq * 32 + lane;
         const uint32_t lane_base = static_cast<uint32_t>(lq * 32) << 16;
         const uint32_t ts = tmem + TM_S + grp * 128u + lane_base;
+        const uint32_t tp = tmem + Sh::TM_P + grp * Sh::P_STRIDE + lane_base;
         const float cs = p.scale * 1.4426950408889634f;        // scores in powers of two
-        const uint32_t p_full0 = of_first(&c.p_full[grp]);
+        const uint32_t p_full0 = of_first(&c.p_full[grp]), s_free0 = of_first(&c.s_free[grp]);
         uint32_t it = 0;                                       // tiles before the segment
         bool ok = true;                                        // false: keep to the barriers, do nothing
         Split split = {0, 0, 0, 0, 0};
@@ -875,66 +891,64 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                 const int32_t base = (w.j0 + j) * CH_TILE;
                 const int32_t hi = pos - base, lo = first - base;              // visible: lo <= column <= hi
                 const bool masked = __any_sync(0xffffffffu, hi < CH_TILE - 1 || lo > 0);
-                auto hide = [&](uint32_t (&u)[32], int k) {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (32 * k + e > hi || 32 * k + e < lo) u[e] = 0xff800000u;   // -inf
-                };
+                uint32_t s[4][32];
                 float mx = -INFINITY;
                 if (ok && live) {
                     tc_fence_after();
-                    uint32_t u[2][32];
-                    tmem_ld_32x32b_x32(ts, u[0]);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        tmem_ld_wait();
-                        if (k < 3) tmem_ld_32x32b_x32(ts + (k + 1) * 32u, u[(k + 1) & 1]);
-                        uint32_t (&x)[32] = u[k & 1];
-                        if (masked) hide(x, k);
-                        float a[4];
+                    for (int k = 0; k < 4; ++k) tmem_ld_32x32b_x32(ts + k * 32u, s[k]);
+                    tmem_ld_wait();
+                }
+                if constexpr (Sh::OWN_P) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (ok && lane == 0) cluster_arrive(s_free0);
+                }
+                if (ok && live) {
+                    if (masked) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) a[e] = fmaxf(__uint_as_float(x[e]), __uint_as_float(x[e + 4]));
-#pragma unroll
-                        for (int e = 8; e < 32; e += 8)
-#pragma unroll
-                            for (int f = 0; f < 4; ++f)
-                                a[f] = fmaxf(fmaxf(a[f], __uint_as_float(x[e + f])), __uint_as_float(x[e + f + 4]));
-                        mx = fmaxf(fmaxf(mx, fmaxf(a[0], a[1])), fmaxf(a[2], a[3]));
+                        for (int e = 0; e < CH_TILE; ++e)
+                            if (e > hi || e < lo) s[e >> 5][e & 31] = 0xff800000u;       // -inf
                     }
+                    float a[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) a[e] = fmaxf(__uint_as_float(s[0][e]), __uint_as_float(s[0][e + 4]));
+#pragma unroll
+                    for (int e = 8; e < CH_TILE; e += 8)
+#pragma unroll
+                        for (int f = 0; f < 4; ++f)
+                            a[f] = fmaxf(fmaxf(a[f], __uint_as_float(s[e >> 5][(e & 31) + f])),
+                                         __uint_as_float(s[e >> 5][(e & 31) + f + 4]));
+                    mx = fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3]));
                 }
                 // the maximum in use at the tile before, and the one for this tile
                 if (ok && i > 0) ok = warp_wait(&c.m_out[grp ^ 1][lq], ((i - 1) >> 1) & 1u, abort, lim);
-                float mp = j > 0 ? c.mrow[grp ^ 1][row] : -INFINITY;
+                const float mp = j > 0 ? c.mrow[grp ^ 1][row] : -INFINITY;
                 const bool grow = (mx - mp) * cs > RESCALE;
                 const float mi = grow ? mx : mp;
                 c.mrow[grp][row] = mi;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&c.m_out[grp][lq]);
+                // P's columns are free when the tile before last is done with them
+                if (Sh::OWN_P && ok && i > 1) ok = warp_wait(&c.o_done[grp], ((i - 2) >> 1) & 1u, abort, lim);
                 if (ok && live) {
                     const float mc = mi == -INFINITY ? 0.0f : mi * cs;
                     if (m != mi) l *= exp2_approx(m * cs - mc);                // 0 at the first
                     m = mi;
                     float2 sum[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
                     const float2 c2 = make_float2(cs, cs), mc2 = make_float2(-mc, -mc);
-                    uint32_t u[2][32];
-                    tmem_ld_32x32b_x32(ts, u[0]);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        tmem_ld_wait();
-                        if (k < 3) tmem_ld_32x32b_x32(ts + (k + 1) * 32u, u[(k + 1) & 1]);
-                        uint32_t (&x)[32] = u[k & 1];
-                        if (masked) hide(x, k);
                         uint32_t o[16];
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
-                            const float2 y = fma2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), c2, mc2);
+                            const float2 y = fma2(make_float2(__uint_as_float(s[k][2 * e]), __uint_as_float(s[k][2 * e + 1])), c2, mc2);
                             const float2 z = make_float2(exp2_approx(y.x), exp2_approx(y.y));
                             sum[e & 1] = add2(sum[e & 1], z);
                             const __half2 h = __floats2half2_rn(z.x, z.y);
                             o[e] = *reinterpret_cast<const uint32_t *>(&h);
                         }
-                        // columns 16 k .. of P over scores that have been read
-                        tmem_st_x16(ts + k * 16u, o);
+                        tmem_st_x16(tp + k * 16u, o);
                     }
                     l += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
                 }
