@@ -387,6 +387,17 @@ __device__ __forceinline__ void umma2_commit(uint64_t *bar)
         : "memory");
 }
 
+// One thread of the (converged) warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t x;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(x));
+    return x != 0;
+}
+
+// A value that is the same in every lane, told to the compiler.
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+
 // The first CTA's copy of a shared-memory address.
 __device__ __forceinline__ uint32_t of_first(const void *p)
 {
@@ -635,72 +646,84 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
         }
         __syncwarp();
     } else if (warp == CH_MMA && rank == 0) {
-        // ------------------------------------------------- MMAs, by one thread
-        if (lane == 0) {
-            constexpr uint32_t idesc_s = umma_idesc_f16_f32(CH_ROWS, CH_TILE);
-            constexpr uint32_t idesc_o = umma_idesc_f16_f32(CH_ROWS, D) | (1u << 16);   // B: dims contiguous
-            const uint64_t qd = sw128_kmajor_desc(smem_u32(q_s));
-            const uint64_t kd0 = sw128_kmajor_desc(ring_a), vd0 = sw128_mn_desc(ring_a, Sh::VTOK * 128);
-            uint32_t slot = 0, phase = 0, it = 0, seg = 0;
-            bool ok = true;
-            auto advance = [&] {
-                if (++slot == NS) {
-                    slot = 0;
-                    phase ^= 1u;
-                }
-            };
-            // S(i) = Q . K(i)^T
-            auto scores = [&](uint32_t i, bool last) {
-                ok = ok && mbar_wait(&c.full[slot], phase, abort, lim);
-                if (!ok) return;
-                tc_fence_after();
-                const uint64_t kd = kd0 + slot * (SLOT >> 4);
+        // --------------------------------------------------------------- MMAs
+        // The warp runs as one and elects the issuing thread at each batch;
+        // descriptors pass through a broadcast, so that their arithmetic is
+        // uniform.
+        constexpr uint32_t idesc_s = umma_idesc_f16_f32(CH_ROWS, CH_TILE);
+        constexpr uint32_t idesc_o = umma_idesc_f16_f32(CH_ROWS, D) | (1u << 16);   // B: dims contiguous
+        const uint64_t qd = sw128_kmajor_desc(uniform(smem_u32(q_s)));
+        const uint64_t kd0 = sw128_kmajor_desc(0), vd0 = sw128_mn_desc(0, Sh::VTOK * 128);
+        const uint32_t tm = uniform(tmem);
+        uint32_t slot = 0, phase = 0, it = 0, seg = 0;
+        bool ok = true;
+        auto advance = [&] {
+            if (++slot == NS) {
+                slot = 0;
+                phase ^= 1u;
+            }
+        };
+        // S(i) = Q . K(i)^T
+        auto scores = [&](uint32_t i, bool last) {
+            ok = ok && warp_wait(&c.full[slot], phase, abort, lim);
+            if (!ok) return;
+            tc_fence_after();
+            const uint64_t kd = kd0 | (uniform(ring_a + slot * SLOT) >> 4);
+            const uint32_t d = tm + TM_S + uniform(i & 1u) * 128u;
+            if (elect_one()) {
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                     const uint32_t ch = kk >> 2, in = (kk & 3) * 32;
-                    umma2_f16(tmem + TM_S + (i & 1u) * 128u, qd + ((ch * (CH_HALF * 128u) + in) >> 4),
-                              kd + ((ch * (Sh::KTOK * 128u) + in) >> 4), idesc_s, kk > 0 ? 1u : 0u);
+                    umma2_f16(d, qd + ((ch * (CH_HALF * 128u) + in) >> 4), kd + ((ch * (Sh::KTOK * 128u) + in) >> 4),
+                              idesc_s, kk > 0 ? 1u : 0u);
                 }
                 umma2_commit(&c.s_full[i & 1u]);
                 umma2_commit(&c.empty[slot]);
                 if (last) umma2_commit(&c.q_free);
-                advance();
-            };
-            while (ok && w.next(p)) {
-                const int32_t n = w.j1 - w.j0;
-                ok = mbar_wait(&c.q_full, seg & 1u, abort, lim);
-                scores(it, n == 1);
-                if (n > 1) scores(it + 1, n == 2);
-                for (int32_t j = 0; ok && j < n; ++j) {
-                    const uint32_t i = it + j;
-                    if (Sh::OWN_P && j + 2 < n) {
-                        ok = mbar_wait(&c.s_free[i & 1u], (i >> 1) & 1u, abort, lim);
-                        scores(i + 2, j + 3 == n);
-                    }
-                    ok = ok && mbar_wait(&c.full[slot], phase, abort, lim);
-                    ok = ok && mbar_wait(&c.p_full[i & 1u], (i >> 1) & 1u, abort, lim);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint64_t vd = vd0 + slot * (SLOT >> 4);
+            }
+            __syncwarp();
+            advance();
+        };
+        while (ok && w.next(p)) {
+            const int32_t n = w.j1 - w.j0;
+            ok = warp_wait(&c.q_full, seg & 1u, abort, lim);
+            scores(it, n == 1);
+            if (n > 1) scores(it + 1, n == 2);
+            for (int32_t j = 0; ok && j < n; ++j) {
+                const uint32_t i = it + j;
+                if (Sh::OWN_P && j + 2 < n) {
+                    ok = warp_wait(&c.s_free[i & 1u], (i >> 1) & 1u, abort, lim);
+                    scores(i + 2, j + 3 == n);
+                }
+                ok = ok && warp_wait(&c.full[slot], phase, abort, lim);
+                ok = ok && warp_wait(&c.p_full[i & 1u], (i >> 1) & 1u, abort, lim);
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t vd = vd0 | (uniform(ring_a + slot * SLOT) >> 4);
+                const uint32_t pa = tm + Sh::TM_P + uniform(i & 1u) * Sh::P_STRIDE;
+                const uint32_t fresh = uniform(j > 0 ? 1u : 0u);
+                if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < CH_TILE / 16; ++kk)
-                        umma2_f16_ta(tmem + TM_O, tmem + Sh::TM_P + (i & 1u) * Sh::P_STRIDE + kk * 8u,
-                                     vd + ((kk * 2048u) >> 4), idesc_o, j + kk > 0 ? 1u : 0u);
+                        umma2_f16_ta(tm + TM_O, pa + kk * 8u, vd + ((kk * 2048u) >> 4), idesc_o, kk > 0 ? 1u : fresh);
                     umma2_commit(&c.o_done[i & 1u]);
                     umma2_commit(&c.empty[slot]);
-                    advance();
-                    if (!Sh::OWN_P && j + 2 < n) scores(i + 2, j + 3 == n);
                 }
-                it += n;
-                ++seg;
-                w.done(p);
+                __syncwarp();
+                advance();
+                if (!Sh::OWN_P && j + 2 < n) scores(i + 2, j + 3 == n);
             }
-            if (!ok) {                                        // products still running
+            it += n;
+            ++seg;
+            w.done(p);
+        }
+        if (!ok) {                                            // products still running
+            if (elect_one()) {
                 umma2_commit(&c.drain);
                 mbar_wait_bounded(&c.drain, 0, lim);
             }
+            __syncwarp();
         }
-        __syncwarp();
     }
     } else if (warp >= CH_HELP) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
