@@ -1014,6 +1014,9 @@ qsa_status qsa_chunk_attention(const void *q, int64_t q_stride, int32_t rows, in
     p.out = out;
     p.hq = hq;
     p.group = hq / cache->hkv;
+    p.group_shift = 31;
+    while ((1 << (p.group_shift - 31)) < p.group) ++p.group_shift;
+    p.group_mul = static_cast<uint32_t>(((uint64_t{1} << p.group_shift) + p.group - 1) / p.group);
     p.window = window;
     p.scale = scale;
     p.ws = static_cast<uint8_t *>(ws);

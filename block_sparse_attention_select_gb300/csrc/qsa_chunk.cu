@@ -67,7 +67,9 @@ constexpr int CH_HALF = 128;                 // rows of one CTA: TMEM lanes
 constexpr int CH_ROWS = 256;                 // (token, head) rows of a unit: MMA M
 constexpr int CH_TILE = 128;                 // tokens of a tile
 constexpr int CH_SOFT = 8;                   // softmax warps
-constexpr int CH_LOAD = 8, CH_MMA = 9, CH_HELP = 12;
+constexpr int CH_LOAD = 8, CH_MMA = 9, CH_SCHED = 10, CH_MMA2 = 11, CH_HELP = 12;
+constexpr int CH_ROLES = 15;                 // warps that read the segments: all but the scheduler
+
 constexpr int CH_HELPERS = 4;
 constexpr int CH_WARPS = CH_HELP + CH_HELPERS;
 constexpr int CH_THREADS = 32 * CH_WARPS;
@@ -81,22 +83,43 @@ constexpr int BAR_PAIR = 1, BAR_HELP = 5;    // named barriers: four softmax war
 
 template <int D, bool Q8>
 struct Shape {
-    static constexpr uint32_t QB = CH_HALF * D * 2;                    // bytes of Q
+    static constexpr int QBUFS = D == 128 ? 2 : 1;                     // buffers of Q
+    static constexpr uint32_t QB = CH_HALF * D * 2;                    // bytes of one
     // a CTA's half of a K tile: 64 tokens, or of a V tile: D / 2 dims of 128 tokens
     static constexpr uint32_t SLOT = 128 * D, RAW = SLOT / 2;
     static constexpr int KTOK = 64, VTOK = CH_TILE;
-    static constexpr int FIT = (RING - QB - (Q8 ? RAWS * RAW : 0)) / SLOT, NS = FIT < MAX_SLOTS ? FIT : MAX_SLOTS;
+    static constexpr int FIT = (RING - QBUFS * QB - (Q8 ? RAWS * RAW : 0)) / SLOT, NS = FIT < MAX_SLOTS ? FIT : MAX_SLOTS;
     static constexpr bool OWN_P = D == 128;                            // P beside S, not over it
     static constexpr uint32_t TM_P = OWN_P ? 384 : TM_S, P_STRIDE = OWN_P ? 64 : 128;
     static constexpr int LEAD = OWN_P ? 3 : 2;                         // key tiles loaded before the first value tile
 };
 
+// A run of tiles of one unit, a pair's next piece of work.
+struct alignas(16) Seg {
+    int32_t n, j0;                           // tiles j0 .. j0 + n - 1; n = 0: no more work
+    int32_t b, g;                            // request, KV head
+    int32_t s0, p0, v0, rows;                // request's first row and position, unit's first (token, head) pair, pairs in use
+    int32_t lo_tok, hi_tok;                  // tokens that some row attends: lo_tok .. hi_tok
+    int32_t place;                           // workspace place of the partial result, -1: this is the whole unit
+    int32_t pad;
+
+    // whether tile j0 + k holds tokens that no row attends
+    __device__ __forceinline__ bool cut(int32_t k) const
+    {
+        const int32_t t0 = (j0 + k) * CH_TILE;
+        return t0 < lo_tok || t0 + CH_TILE - 1 > hi_tok;
+    }
+};
+constexpr int SEGS = 4;                      // segments the scheduler may be ahead
+constexpr uint64_t SEG_WAIT_NS = 10000000000ull;
+
 struct Ctrl {
+    Seg seg[SEGS];
+    uint64_t seg_full[SEGS], seg_empty[SEGS];
     uint64_t full[MAX_SLOTS], empty[MAX_SLOTS], raw_full[RAWS], raw_empty[RAWS], bnd[8];
-    uint64_t s_full[2], s_free[2], p_full[2], o_done[2], m_out[2][4], q_full, q_free, drain;
-    alignas(8) float mrow[2][CH_HALF];       // [tile parity][row]: maximum in use at the group's last tile
-    float lrow[2][CH_HALF];                  // [tile parity][row]: sums of a segment
-    uint16_t scale[2][CH_TILE];              // [slot parity][token]: FP16 scale (E4M3)
+    uint64_t s_full[2], s_free[2], p_full[2], o_done[2], m_out[2][4], q_full[2], q_free[2], drain;
+    alignas(8) float mrow[2][CH_HALF];       // [tile parity][row]: maximum in use at the group's last tile; sums at a segment's end
+    alignas(8) uint16_t scale[2][CH_TILE];   // [slot parity][token]: FP16 scale (E4M3)
     int64_t w0, w1, total;                   // this pair's share of the line, the line's length
     int32_t pairs;                           // pairs that have work
     int32_t b, m, g, off;                    // the unit that w0 lies in, and w0's place in it
@@ -121,10 +144,17 @@ static_assert(sizeof(Split) * CHUNK_MAX_PAIRS <= WS_ML, "workspace header");
 // ------------------------------------------------------------- work sharing --
 
 struct Unit {
-    int32_t v0, rows;                        // first pair, pairs in use
-    int32_t lo_tok, hi_tok;                  // tokens that some row attends: lo_tok .. hi_tok
+    int32_t v0, rows, lo_tok, hi_tok;        // as in Seg
     int32_t lo, hi;                          // tiles lo .. hi - 1
 };
+
+// v / p.group for 0 <= v < 2^31: with s = ceil(log2 group) and group_mul =
+// ceil(2^(31 + s) / group), the error of v * group_mul against v * 2^(31 + s) /
+// group is below 2^31 * 2^s / group, less than one unit of the quotient's grid.
+__device__ __forceinline__ int32_t by_group(const ChunkParams &p, int32_t v)
+{
+    return static_cast<int32_t>((static_cast<uint64_t>(static_cast<uint32_t>(v)) * p.group_mul) >> p.group_shift);
+}
 
 __device__ __forceinline__ int32_t units_of(const ChunkParams &p, const Seq &s)
 {
@@ -137,8 +167,8 @@ __device__ __forceinline__ Unit unit_of(const ChunkParams &p, const Seq &s, int3
     u.v0 = m * CH_ROWS;
     const int32_t end = min(s.n * p.group, u.v0 + CH_ROWS);
     u.rows = end - u.v0;
-    const int32_t first = s.p0 + u.v0 / p.group;
-    u.hi_tok = s.p0 + (end - 1) / p.group;
+    const int32_t first = s.p0 + by_group(p, u.v0);
+    u.hi_tok = s.p0 + by_group(p, end - 1);
     u.lo_tok = p.window > 0 ? max(0, first - p.window + 1) : 0;
     u.lo = u.lo_tok / CH_TILE;
     u.hi = u.hi_tok / CH_TILE + 1;
@@ -173,16 +203,21 @@ __device__ __forceinline__ T block_scan(T x, T *warp_total, int warp, int lane, 
     return before + sc - x;
 }
 
+// Shared memory of find_work: the queries' place, which is free until then.
+struct FindScratch {
+    int32_t prefix[CH_THREADS];
+    int32_t units[CH_WARPS];
+    int64_t costs[CH_WARPS];
+};
+static_assert(sizeof(FindScratch) <= Shape<128, false>::QB, "scratch");
+
 // Finds this pair's share of the line, c.w0 .. c.w1, and the unit that w0 lies
 // in (both CTAs of a pair do, alike).  Each thread counts the units of a run of
 // requests, then adds up the lengths of an equal run of units.
-__device__ __forceinline__ void find_work(const ChunkParams &p, Ctrl &c, int warp, int lane)
+__device__ __forceinline__ void find_work(const ChunkParams &p, Ctrl &c, FindScratch &s, int warp, int lane)
 {
     const int t = threadIdx.x;
-    // free until the first tile
-    int32_t *prefix = reinterpret_cast<int32_t *>(&c.mrow[0][0]);
-    int32_t *wt32 = reinterpret_cast<int32_t *>(&c.scale[0][0]);
-    int64_t *wt64 = reinterpret_cast<int64_t *>(&c.scale[1][0]);
+    int32_t *prefix = s.prefix;
     const int32_t run = (p.kv.n_reqs + CH_THREADS - 1) / CH_THREADS;
     const int32_t r0 = min(t * run, p.kv.n_reqs), r1 = min(r0 + run, p.kv.n_reqs);
     int32_t mine = 0, units;
@@ -191,7 +226,7 @@ __device__ __forceinline__ void find_work(const ChunkParams &p, Ctrl &c, int war
         mine += units_of(p, seq_of(p.kv, b, &bad));
         if (bad && blockIdx.x == 0) record_error(p.kv.status, ST_BAD_ROW);
     }
-    prefix[t] = block_scan(mine, wt32, warp, lane, &units);
+    prefix[t] = block_scan(mine, s.units, warp, lane, &units);
     __syncthreads();
     const int32_t u0 = static_cast<int32_t>(static_cast<int64_t>(units) * t / CH_THREADS);
     const int32_t u1 = static_cast<int32_t>(static_cast<int64_t>(units) * (t + 1) / CH_THREADS);
@@ -212,18 +247,18 @@ __device__ __forceinline__ void find_work(const ChunkParams &p, Ctrl &c, int war
             s0 = seq_of(p.kv, ++b0, &bad);
         }
         int32_t b = b0, m = m0;
-        Seq s = s0;
+        Seq sb = s0;
         for (int32_t u = u0; u < u1; ++u, ++m) {
-            while (m >= units_of(p, s)) {
-                s = seq_of(p.kv, ++b, &bad);
+            while (m >= units_of(p, sb)) {
+                sb = seq_of(p.kv, ++b, &bad);
                 m = 0;
             }
-            const Unit un = unit_of(p, s, m);
+            const Unit un = unit_of(p, sb, m);
             cost += UNIT_COST + un.hi - un.lo;
         }
         cost *= p.kv.hkv;
     }
-    int64_t at = block_scan(cost, wt64, warp, lane, &total);
+    int64_t at = block_scan(cost, s.costs, warp, lane, &total);
     // one place each at least, so that the pairs with work are the first ones
     const int32_t pairs = static_cast<int32_t>(min(total, static_cast<int64_t>(gridDim.x >> 1)));
     const int32_t me = blockIdx.x >> 1;
@@ -256,14 +291,11 @@ __device__ __forceinline__ void find_work(const ChunkParams &p, Ctrl &c, int war
     __syncthreads();
 }
 
-// The pair's share as segments: a run of tiles of one unit.
+// The pair's share as segments.
 struct Walk {
     int64_t left;
     int32_t b, m, g, off, n_units;
     Seq s;
-    Unit u;
-    int32_t j0, j1;                          // the segment's tiles
-    bool whole, head;                        // all of the unit; the unit's first tile is here
 
     __device__ __forceinline__ Walk(const ChunkParams &p, const Ctrl &c)
     {
@@ -280,39 +312,40 @@ struct Walk {
         s = seq_of(p.kv, b, &bad);
         n_units = units_of(p, s);
     }
-    // the next segment, false at the end of the share
-    __device__ __forceinline__ bool next(const ChunkParams &p)
+    // the next segment (n = 0 at the end of the share); *rest: tiles of the unit after it
+    __device__ __forceinline__ Seg next(const ChunkParams &p, bool *head, int32_t *rest)
     {
-        if (left <= 0) return false;
+        Seg x;
+        x.n = 0;
+        if (left <= 0) return x;
         while (m >= n_units) {               // empty requests have no units
-            if (++b >= p.kv.n_reqs) return false;
+            if (++b >= p.kv.n_reqs) return x;
             m = 0;
             load(p);
         }
-        u = unit_of(p, s, m);
+        const Unit u = unit_of(p, s, m);
         // a unit's place in the line: UNIT_COST, then its tiles
         const int32_t len = UNIT_COST + u.hi - u.lo;
         const int32_t end = static_cast<int32_t>(min(static_cast<int64_t>(len), off + left));
         left -= end - off;
-        j0 = u.lo + max(0, off - UNIT_COST);
-        j1 = u.lo + max(0, end - UNIT_COST);
-        head = j0 == u.lo;
-        whole = head && j1 == u.hi;
-        return j0 < j1;                      // false: the share ends before the unit's first tile
-    }
-    // whether tile j0 + k holds tokens that no row attends
-    __device__ __forceinline__ bool cut(int32_t k) const
-    {
-        const int32_t t0 = (j0 + k) * CH_TILE;
-        return t0 < u.lo_tok || t0 + CH_TILE - 1 > u.hi_tok;
-    }
-    __device__ __forceinline__ void done(const ChunkParams &p)
-    {
+        x.j0 = u.lo + max(0, off - UNIT_COST);
+        x.n = u.lo + max(0, end - UNIT_COST) - x.j0;      // 0: the share ends before the unit's first tile
+        x.b = b;
+        x.g = g;
+        x.s0 = s.s0;
+        x.p0 = s.p0;
+        x.v0 = u.v0;
+        x.rows = u.rows;
+        x.lo_tok = u.lo_tok;
+        x.hi_tok = u.hi_tok;
+        *head = x.j0 == u.lo;
+        *rest = u.hi - x.j0 - x.n;
         off = 0;
         if (++g == p.kv.hkv) {
             g = 0;
             ++m;
         }
+        return x;
     }
 };
 
@@ -505,9 +538,9 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
     using Sh = Shape<D, Q8>;
     constexpr int NS = Sh::NS;
     constexpr uint32_t SLOT = Sh::SLOT, RAW = Sh::RAW;
-    static_assert(NS >= 3 && NS <= 10, "10 slots hold fewer value tiles than there are barriers for cut ones");
+    static_assert(NS >= 3 && NS <= MAX_SLOTS, "10 slots hold fewer value tiles than there are barriers for cut ones");
     extern __shared__ __align__(1024) uint8_t smem[];
-    uint8_t *q_s = smem, *ring = smem + Sh::QB, *raw = ring + NS * SLOT;
+    uint8_t *q_s = smem, *ring = smem + Sh::QBUFS * Sh::QB, *raw = ring + NS * SLOT;
     Ctrl &c = *reinterpret_cast<Ctrl *>(smem + RING);
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     const int rank = blockIdx.x & 1;                         // in the pair
@@ -532,8 +565,14 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
             mbar_init(&c.o_done[i], 1);
             for (int k = 0; k < 4; ++k) mbar_init(&c.m_out[i][k], 1);
         }
-        mbar_init(&c.q_full, 2 * CH_HELPERS);
-        mbar_init(&c.q_free, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&c.q_full[i], 2 * CH_HELPERS);
+            mbar_init(&c.q_free[i], 1);
+        }
+        for (int i = 0; i < SEGS; ++i) {
+            mbar_init(&c.seg_full[i], 1);
+            mbar_init(&c.seg_empty[i], CH_ROLES);
+        }
         mbar_init(&c.drain, 1);
         c.abort = 0;
         fence_barrier_init();
@@ -544,14 +583,28 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
     wait_prior_grid();
-    find_work(p, c, warp, lane);
+    find_work(p, c, *reinterpret_cast<FindScratch *>(q_s), warp, lane);
     tc_fence_before();
     __syncthreads();
     cluster_sync();                                          // the pair's barriers and TMEM are ready
     tc_fence_after();
     const uint32_t tmem = c.tmem;
     const uint32_t ring_a = smem_u32(ring);
-    Walk w(p, c);
+    // The next segment, false at the end.  Its wait ignores the abort flag: after
+    // a time-out every role still walks through all segments, keeps to its named
+    // barriers and does nothing else.
+    uint32_t segs = 0;
+    Seg w;
+    auto next_segment = [&]() -> bool {
+        const uint32_t k = segs % SEGS;
+        bool got = mbar_wait_bounded(&c.seg_full[k], (segs / SEGS) & 1u, SEG_WAIT_NS);
+        got = __all_sync(0xffffffffu, got);
+        w = c.seg[k];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&c.seg_empty[k]);
+        ++segs;
+        return got && w.n > 0;
+    };
     // registers after the split: 8 x 32 x 200 + 8 x 32 x 56 = 65,536
     if (warp >= CH_LOAD && warp < CH_HELP) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
@@ -577,7 +630,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
         auto plan = [&](int32_t e) {
             bool v;
             int32_t tile;
-            slot_at<Sh::LEAD>(e, w.j1 - w.j0, &v, &tile);
+            slot_at<Sh::LEAD>(e, w.n, &v, &tile);
             const int sh = v ? sh_v : sh_k;
             const int32_t toks = v ? Sh::VTOK : Sh::KTOK;
             const int lb = __ffs(toks) - 1 - sh;              // log2 of the boxes down
@@ -589,15 +642,16 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
             at = static_cast<uint32_t>((ch * toks + (i << sh)) * row_bytes);
             // boxes without a visible token read zeros (a row past the cache)
             y = p.kv.num_pages << p.kv.page_shift;
-            if (mine && tok <= w.u.hi_tok && tok + (1 << sh) > w.u.lo_tok) {
+            if (mine && tok <= w.hi_tok && tok + (1 << sh) > w.lo_tok) {
                 const int32_t page = __ldg(bt + (tok >> p.kv.page_shift));
                 if (page >= 0 && page < p.kv.num_pages) y = (page << p.kv.page_shift) + (tok & (P - 1));
                 else record_error(p.kv.status, ST_BAD_PAGE);
             }
         };
-        while (ok && w.next(p)) {
+        while (next_segment()) {
+            if (!ok) continue;
             bt = p.kv.block_table + static_cast<int64_t>(w.b) * p.kv.max_pages;
-            const int32_t n = w.j1 - w.j0;
+            const int32_t n = w.n;
             plan(0);
             for (int32_t e = 0; e < 2 * n; ++e) {
                 bool v;
@@ -633,7 +687,6 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                     phase ^= 1u;
                 }
             }
-            w.done(p);
         }
         // after an abort copies may be in flight: let them land (their barriers
         // may be the other CTA's, so give them the time instead)
@@ -645,21 +698,53 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
             while (clock64() - t0 < 4000000) {}
         }
         __syncwarp();
-    } else if (warp == CH_MMA && rank == 0) {
+    } else if (warp == CH_SCHED) {
+        // ----------------------------------------------------------- segments
+        Walk walk(p, c);
+        Split split = {0, 0, 0, 0, 0};
+        for (uint32_t i = 0;; ++i) {
+            bool head = false;
+            int32_t rest = 0;
+            Seg x = walk.next(p, &head, &rest);
+            x.place = head && rest == 0 ? -1 : 2 * static_cast<int32_t>(blockIdx.x >> 1) + (head ? 1 : 0);
+            if (x.n > 0 && head && rest > 0) {
+                // the unit's other tiles lie in the next pairs' shares
+                split.parts = 1;
+                while (c.total * ((blockIdx.x >> 1) + split.parts) / c.pairs < c.w1 + rest) ++split.parts;
+                split.rows = x.rows;
+                split.s0 = x.s0;
+                split.v0 = x.v0;
+                split.g = x.g;
+            }
+            const uint32_t k = i % SEGS;
+            if (i >= SEGS) mbar_wait_bounded(&c.seg_empty[k], (i / SEGS - 1) & 1u, SEG_WAIT_NS);
+            __syncwarp();
+            if (lane == 0) {
+                c.seg[k] = x;
+                mbar_arrive(&c.seg_full[k]);
+            }
+            if (x.n == 0) break;
+        }
+        if (lane == 0 && rank == 0) reinterpret_cast<Split *>(p.ws)[blockIdx.x >> 1] = split;
+        __syncwarp();
+    } else {
         // --------------------------------------------------------------- MMAs
         // The warp runs as one and elects the issuing thread at each batch;
         // descriptors pass through a broadcast, so that their arithmetic is
-        // uniform.
+        // uniform.  With P beside S, one warp issues the score products and the
+        // other the second ones, so that neither waits for what the other needs;
+        // else the first warp issues both.
+        const bool do_s = rank == 0 && warp == CH_MMA, do_o = rank == 0 && (Sh::OWN_P ? warp == CH_MMA2 : warp == CH_MMA);
         constexpr uint32_t idesc_s = umma_idesc_f16_f32(CH_ROWS, CH_TILE);
         constexpr uint32_t idesc_o = umma_idesc_f16_f32(CH_ROWS, D) | (1u << 16);   // B: dims contiguous
-        const uint64_t qd = sw128_kmajor_desc(uniform(smem_u32(q_s)));
         const uint64_t kd0 = sw128_kmajor_desc(0), vd0 = sw128_mn_desc(0, Sh::VTOK * 128);
         const uint32_t tm = uniform(tmem);
         uint32_t slot = 0, phase = 0, it = 0, seg = 0;
         bool ok = true;
-        auto advance = [&] {
-            if (++slot == NS) {
-                slot = 0;
+        auto advance = [&](int32_t by) {
+            slot += by;
+            if (slot >= NS) {
+                slot -= NS;
                 phase ^= 1u;
             }
         };
@@ -668,6 +753,8 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
             ok = ok && warp_wait(&c.full[slot], phase, abort, lim);
             if (!ok) return;
             tc_fence_after();
+            const uint32_t qb = Sh::QBUFS == 2 ? uniform(seg & 1u) : 0u;
+            const uint64_t qd = kd0 | (uniform(smem_u32(q_s) + qb * Sh::QB) >> 4);
             const uint64_t kd = kd0 | (uniform(ring_a + slot * SLOT) >> 4);
             const uint32_t d = tm + TM_S + uniform(i & 1u) * 128u;
             if (elect_one()) {
@@ -679,43 +766,67 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                 }
                 umma2_commit(&c.s_full[i & 1u]);
                 umma2_commit(&c.empty[slot]);
-                if (last) umma2_commit(&c.q_free);
+                if (last) umma2_commit(&c.q_free[qb]);
             }
             __syncwarp();
-            advance();
         };
-        while (ok && w.next(p)) {
-            const int32_t n = w.j1 - w.j0;
-            ok = warp_wait(&c.q_full, seg & 1u, abort, lim);
-            scores(it, n == 1);
-            if (n > 1) scores(it + 1, n == 2);
-            for (int32_t j = 0; ok && j < n; ++j) {
-                const uint32_t i = it + j;
-                if (Sh::OWN_P && j + 2 < n) {
-                    ok = warp_wait(&c.s_free[i & 1u], (i >> 1) & 1u, abort, lim);
-                    scores(i + 2, j + 3 == n);
-                }
-                ok = ok && warp_wait(&c.full[slot], phase, abort, lim);
-                ok = ok && warp_wait(&c.p_full[i & 1u], (i >> 1) & 1u, abort, lim);
-                if (!ok) break;
-                tc_fence_after();
-                const uint64_t vd = vd0 | (uniform(ring_a + slot * SLOT) >> 4);
-                const uint32_t pa = tm + Sh::TM_P + uniform(i & 1u) * Sh::P_STRIDE;
-                const uint32_t fresh = uniform(j > 0 ? 1u : 0u);
-                if (elect_one()) {
+        // O (+)= P(i) . V(i)
+        auto values = [&](uint32_t i, bool first) {
+            ok = ok && warp_wait(&c.full[slot], phase, abort, lim);
+            ok = ok && warp_wait(&c.p_full[i & 1u], (i >> 1) & 1u, abort, lim);
+            if (!ok) return;
+            tc_fence_after();
+            const uint64_t vd = vd0 | (uniform(ring_a + slot * SLOT) >> 4);
+            const uint32_t pa = tm + Sh::TM_P + uniform(i & 1u) * Sh::P_STRIDE;
+            const uint32_t add = uniform(first ? 0u : 1u);
+            if (elect_one()) {
 #pragma unroll
-                    for (int kk = 0; kk < CH_TILE / 16; ++kk)
-                        umma2_f16_ta(tm + TM_O, pa + kk * 8u, vd + ((kk * 2048u) >> 4), idesc_o, kk > 0 ? 1u : fresh);
-                    umma2_commit(&c.o_done[i & 1u]);
-                    umma2_commit(&c.empty[slot]);
+                for (int kk = 0; kk < CH_TILE / 16; ++kk)
+                    umma2_f16_ta(tm + TM_O, pa + kk * 8u, vd + ((kk * 2048u) >> 4), idesc_o, kk > 0 ? 1u : add);
+                umma2_commit(&c.o_done[i & 1u]);
+                umma2_commit(&c.empty[slot]);
+            }
+            __syncwarp();
+        };
+        while (next_segment()) {
+            if (!ok || !(do_s || do_o)) continue;
+            const int32_t n = w.n, lead = min(Sh::LEAD, n);
+            if (do_s) ok = warp_wait(&c.q_full[Sh::QBUFS == 2 ? seg & 1u : 0u], (Sh::QBUFS == 2 ? seg >> 1 : seg) & 1u, abort, lim);
+            if constexpr (Sh::OWN_P) {
+                // this warp's slots of the segment's 2 n: where they are is given by slot_at
+                int32_t at = 0;
+                for (int32_t j = 0; ok && j < n; ++j) {
+                    const int32_t e = do_s ? (j < lead ? j : 2 * j - lead + 1) : slot_of_v<Sh::LEAD>(j, n);
+                    advance(e - at);
+                    at = e;
+                    const uint32_t i = it + j;
+                    if (do_s) {
+                        // the scores two tiles before are in registers (the first two tiles of a segment: those of the one before)
+                        if (i > 1) ok = warp_wait(&c.s_free[i & 1u], ((i - 2) >> 1) & 1u, abort, lim);
+                        scores(i, j == n - 1);
+                    } else {
+                        values(i, j == 0);
+                    }
                 }
-                __syncwarp();
-                advance();
-                if (!Sh::OWN_P && j + 2 < n) scores(i + 2, j + 3 == n);
+                advance(2 * n - at);
+            } else {
+                scores(it, n == 1);
+                advance(1);
+                if (n > 1) {
+                    scores(it + 1, n == 2);
+                    advance(1);
+                }
+                for (int32_t j = 0; ok && j < n; ++j) {
+                    values(it + j, j == 0);
+                    advance(1);
+                    if (j + 2 < n) {
+                        scores(it + j + 2, j + 3 == n);
+                        advance(1);
+                    }
+                }
             }
             it += n;
             ++seg;
-            w.done(p);
         }
         if (!ok) {                                            // products still running
             if (elect_one()) {
@@ -731,20 +842,21 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
         const int ht = t - CH_HELP * 32;                      // 0 .. 127
         uint32_t seg = 0, slot = 0, phase = 0, rslot = 0, rphase = 0, ring0 = 0, nb = 0;
         bool ok = true;                                       // false: keep to the barriers, do nothing
-        while (w.next(p)) {
-            const int32_t n = w.j1 - w.j0;
-            if (ok && seg > 0) ok = warp_wait(&c.q_free, (seg - 1) & 1u, abort, lim);
+        while (next_segment()) {
+            const int32_t n = w.n;
+            const uint32_t qb = Sh::QBUFS == 2 ? seg & 1u : 0u, quse = Sh::QBUFS == 2 ? seg >> 1 : seg;   // buffer, its uses before
+            if (ok && quse > 0) ok = warp_wait(&c.q_free[qb], (quse - 1) & 1u, abort, lim);
             if (ok) {
                 // the warp's 32 rows: a lane finds one row's queries, then
                 // all lanes copy the rows, 512 bytes at a time
                 constexpr int RPI = 256 / D;                   // rows per copy instruction
                 const int r0 = (ht >> 5) * 32, ur = rank * CH_HALF + r0 + lane;
-                const int32_t v = w.u.v0 + ur, tok = v / p.group, h = v - tok * p.group;
-                const bool in = ur < w.u.rows;
+                const int32_t v = w.v0 + ur, tok = by_group(p, v), h = v - tok * p.group;
+                const bool in = ur < w.rows;
                 const uint64_t mine = in ? reinterpret_cast<uint64_t>(p.q) +
-                    ((static_cast<int64_t>(w.s.s0) + tok) * p.q_stride + (w.g * p.group + h) * D) * 2 : 0;
+                    ((static_cast<int64_t>(w.s0) + tok) * p.q_stride + (w.g * p.group + h) * D) * 2 : 0;
                 const int pc = lane & (D / 8 - 1);
-                const uint32_t dst = smem_u32(q_s) + (pc >> 3) * (CH_HALF * 128u);
+                const uint32_t dst = smem_u32(q_s) + qb * Sh::QB + (pc >> 3) * (CH_HALF * 128u);
 #pragma unroll 8
                 for (int i = 0; i < 32 / RPI; ++i) {
                     const int k = i * RPI + lane / (D / 8);
@@ -756,7 +868,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                 asm volatile("cp.async.wait_all;" ::: "memory");
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) cluster_arrive(of_first(&c.q_full));
+                if (lane == 0) cluster_arrive(of_first(&c.q_full[qb]));
             }
             ++seg;
             if constexpr (!Q8) {
@@ -771,7 +883,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                     const uint32_t vs = (ring0 + slot_of_v<Sh::LEAD>(tile, n)) % NS;
                     if (ok) {
                         uint8_t *v = ring + vs * SLOT;
-                        const int32_t a = w.u.lo_tok - (w.j0 + tile) * CH_TILE, z = w.u.hi_tok + 1 - (w.j0 + tile) * CH_TILE;
+                        const int32_t a = w.lo_tok - (w.j0 + tile) * CH_TILE, z = w.hi_tok + 1 - (w.j0 + tile) * CH_TILE;
                         if (ht < a || ht >= z) {
 #pragma unroll
                             for (int ch = 0; ch < D / 128; ++ch)
@@ -795,7 +907,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                     if (e >= 2 * n) return -1;
                     slot_at<Sh::LEAD>(e, n, &v, &tile);
                     const int32_t tok = (w.j0 + tile) * CH_TILE + (v ? 0 : rank * Sh::KTOK) + ht;
-                    return ht < (v ? Sh::VTOK : Sh::KTOK) && tok >= w.u.lo_tok && tok <= w.u.hi_tok ? tok : -1;
+                    return ht < (v ? Sh::VTOK : Sh::KTOK) && tok >= w.lo_tok && tok <= w.hi_tok ? tok : -1;
                 };
                 auto page_of = [&](int32_t tok) -> int32_t { return tok >= 0 ? __ldg(bt + (tok >> p.kv.page_shift)) : -1; };
                 auto byte_of = [&](int32_t e, int32_t tok, int32_t page) -> uint32_t {
@@ -816,7 +928,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                     int32_t tile;
                     slot_at<Sh::LEAD>(e, n, &v, &tile);
                     const int32_t tok0 = (w.j0 + tile) * CH_TILE;      // V: rows outside lo_tok .. hi_tok are cleared
-                    const int32_t a = v ? w.u.lo_tok - tok0 : 0, z = v ? w.u.hi_tok + 1 - tok0 : CH_TILE;
+                    const int32_t a = v ? w.lo_tok - tok0 : 0, z = v ? w.hi_tok + 1 - tok0 : CH_TILE;
                     // 2^(byte - 127) as FP16 (2^-15 is subnormal)
                     const int x = max(112, min(135, static_cast<int>(byte))) - 127;
                     c.scale[par][ht] = static_cast<uint16_t>(x >= -14 ? (x + 15) << 10 : 0x200);
@@ -884,7 +996,6 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                     }
                 }
             }
-            w.done(p);
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
@@ -898,13 +1009,12 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
         const uint32_t p_full0 = of_first(&c.p_full[grp]), s_free0 = of_first(&c.s_free[grp]);
         uint32_t it = 0;                                       // tiles before the segment
         bool ok = true;                                        // false: keep to the barriers, do nothing
-        Split split = {0, 0, 0, 0, 0};
-        while (w.next(p)) {
-            const int32_t n = w.j1 - w.j0;
+        while (next_segment()) {
+            const int32_t n = w.n;
             // rows past the unit's last behave like it (their queries are zeros)
-            const int32_t mine = w.u.rows - rank * CH_HALF;    // rows in use here, if positive
-            const int32_t vr = w.u.v0 + min(rank * CH_HALF + row, w.u.rows - 1);
-            const int32_t pos = w.s.p0 + vr / p.group;
+            const int32_t mine = w.rows - rank * CH_HALF;      // rows in use here, if positive
+            const int32_t vr = w.v0 + min(rank * CH_HALF + row, w.rows - 1);
+            const int32_t tok = by_group(p, vr), pos = w.p0 + tok;
             const int32_t first = p.window > 0 ? max(0, pos - p.window + 1) : 0;
             const bool live = lq * 32 < mine;                  // some row of this warp is in use
             float m = -INFINITY, l = 0.0f;
@@ -980,7 +1090,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                     tc_fence_after();
                     const float alpha = grow ? exp2_approx((mp - mi) * cs) : 1.0f;
                     uint32_t u[32];
-#pragma unroll
+#pragma unroll 1
                     for (int k = 0; k < D / 32; ++k) {
                         tmem_ld_32x32b_x32(tmem + TM_O + lane_base + k * 32u, u);
                         tmem_ld_wait();
@@ -997,79 +1107,59 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
             it += n;
             // the segment's sums: its rows' output, or its part of it
             if (ok) ok = warp_wait(&c.o_done[(it - 1) & 1u], ((it - 1) >> 1) & 1u, abort, lim);
-            c.lrow[grp][row] = l;
             named_barrier(BAR_PAIR + lq, 64);
-            {
-                // both groups' sums at the last tile's maximum
-                const float ml = c.mrow[(it - 1) & 1u][row], lo = c.lrow[grp ^ 1][row], mo = c.mrow[grp ^ 1][row];
-                l = (l > 0.0f ? l * exp2_approx((m - ml) * cs) : 0.0f) + (lo > 0.0f ? lo * exp2_approx((mo - ml) * cs) : 0.0f);
-                m = ml;
-            }
-            named_barrier(BAR_PAIR + lq, 64);                  // read before the next tile's maxima
+            // both groups' sums at the last tile's maximum, exchanged in place of the maxima
+            const float mlast = c.mrow[(it - 1) & 1u][row];
+            l = l > 0.0f ? l * exp2_approx((m - mlast) * cs) : 0.0f;
+            named_barrier(BAR_PAIR + lq, 64);
+            c.mrow[grp][row] = l;
+            named_barrier(BAR_PAIR + lq, 64);
+            l += c.mrow[grp ^ 1][row];
             if (ok && live) {
                 tc_fence_after();
                 const uint32_t to = tmem + TM_O + lane_base + grp * OC;
-                const bool in = row < mine;
-                uint32_t u[32];
-                if (w.whole) {
-                    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-                    const int32_t v = w.u.v0 + rank * CH_HALF + row, tok = v / p.group, h = v - tok * p.group;
-                    __half *out = static_cast<__half *>(p.out) +
-                                  ((static_cast<int64_t>(w.s.s0) + tok) * p.hq + w.g * p.group + h) * D + grp * OC;
+                const bool in = row < mine, whole = w.place < 0;
+                const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+                const int32_t h = vr - tok * p.group, ur = rank * CH_HALF + row;
+                __half *out = static_cast<__half *>(p.out) +
+                              ((static_cast<int64_t>(w.s0) + tok) * p.hq + w.g * p.group + h) * D + grp * OC;
+                float *part = nullptr;
+                if (!whole) {
+                    part = reinterpret_cast<float *>(p.ws + WS_O) + (static_cast<int64_t>(w.place) * p.ws_rows + ur) * D + grp * OC;
+                    if (in && grp == 0)
+                        *reinterpret_cast<float2 *>(p.ws + WS_ML + (static_cast<int64_t>(w.place) * CH_ROWS + ur) * 8) =
+                            make_float2(mlast == -INFINITY ? -INFINITY : mlast * cs, l);
+                }
+                // rolled: a unit's end is code that has left the instruction cache
+#pragma unroll 1
+                for (int k = 0; k < OC / 32; ++k) {
+                    uint32_t u[32];
+                    tmem_ld_32x32b_x32(to + k * 32u, u);
+                    tmem_ld_wait();
+                    if (!in) continue;
+                    if (whole) {
 #pragma unroll
-                    for (int k = 0; k < OC / 32; ++k) {
-                        tmem_ld_32x32b_x32(to + k * 32u, u);
-                        tmem_ld_wait();
-                        if (in) {
+                        for (int i = 0; i < 32; i += 8) {
+                            uint32_t x[4];
 #pragma unroll
-                            for (int i = 0; i < 32; i += 8) {
-                                uint32_t x[4];
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    const __half2 hh = __floats2half2_rn(__uint_as_float(u[i + 2 * e]) * inv,
-                                                                         __uint_as_float(u[i + 2 * e + 1]) * inv);
-                                    x[e] = *reinterpret_cast<const uint32_t *>(&hh);
-                                }
-                                *reinterpret_cast<uint4 *>(out + 32 * k + i) = make_uint4(x[0], x[1], x[2], x[3]);
+                            for (int e = 0; e < 4; ++e) {
+                                const __half2 hh = __floats2half2_rn(__uint_as_float(u[i + 2 * e]) * inv,
+                                                                     __uint_as_float(u[i + 2 * e + 1]) * inv);
+                                x[e] = *reinterpret_cast<const uint32_t *>(&hh);
                             }
+                            *reinterpret_cast<uint4 *>(out + 32 * k + i) = make_uint4(x[0], x[1], x[2], x[3]);
                         }
-                    }
-                } else {
-                    // two places per pair: 0 for a unit begun before it, 1 for one that goes on after it
-                    const int64_t place = 2 * static_cast<int64_t>(blockIdx.x >> 1) + (w.head ? 1 : 0);
-                    const int ur = rank * CH_HALF + row;
-                    float *ml = reinterpret_cast<float *>(p.ws + WS_ML) + (place * CH_ROWS + ur) * 2;
-                    float *part = reinterpret_cast<float *>(p.ws + WS_O) + (place * p.ws_rows + ur) * D + grp * OC;
-                    if (in && grp == 0) {
-                        ml[0] = m == -INFINITY ? -INFINITY : m * cs;
-                        ml[1] = l;
-                    }
+                    } else {
 #pragma unroll
-                    for (int k = 0; k < OC / 32; ++k) {
-                        tmem_ld_32x32b_x32(to + k * 32u, u);
-                        tmem_ld_wait();
-                        if (in) {
-#pragma unroll
-                            for (int i = 0; i < 32; i += 4)
-                                *reinterpret_cast<uint4 *>(part + 32 * k + i) = make_uint4(u[i], u[i + 1], u[i + 2], u[i + 3]);
-                        }
+                        for (int i = 0; i < 32; i += 4)
+                            *reinterpret_cast<uint4 *>(part + 32 * k + i) = make_uint4(u[i], u[i + 1], u[i + 2], u[i + 3]);
                     }
                 }
                 tc_fence_before();
             }
-            if (t == 0 && w.head && !w.whole) {
-                // the unit's other tiles lie in the next pairs' shares
-                const int64_t end = c.w1 + (w.u.hi - w.j1);
-                split.parts = 1;
-                while (c.total * ((blockIdx.x >> 1) + split.parts) / c.pairs < end) ++split.parts;
-                split.rows = w.u.rows;
-                split.s0 = w.s.s0;
-                split.v0 = w.u.v0;
-                split.g = w.g;
-            }
-            w.done(p);
+            // sums and O are read: the other group may go on to the next tile
+            named_barrier(BAR_PAIR + lq, 64);
         }
-        if (t == 0 && rank == 0) reinterpret_cast<Split *>(p.ws)[blockIdx.x >> 1] = split;
     }
 
     tc_fence_before();

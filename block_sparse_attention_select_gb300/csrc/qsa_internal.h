@@ -193,6 +193,8 @@ struct ChunkParams {
     int64_t q_stride;           // elements
     void *out;                  // FP16 [rows, hq, D]
     int32_t hq, group;          // query heads, query heads per KV head
+    uint32_t group_mul;         // v / group = (v * group_mul) >> group_shift for 0 <= v < 2^31
+    int32_t group_shift;
     int32_t window;             // 0: none
     float scale;
     uint8_t *ws;
