@@ -18,9 +18,9 @@ ROOT = os.path.dirname(HERE)
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libqsa.so")
-SOURCES = ["qsa_api.cu", "qsa_attend.cu", "qsa_chunk.cu", "qsa_kv.cu", "qsa_plan.cu", "qsa_produce.cu", "qsa_score.cu",
-           "qsa_select.cu"]
-HEADERS = ["qsa_device.cuh", "qsa_internal.h", "qsa_seq.cuh"]
+SOURCES = ["qsa_api.cu", "qsa_attend.cu", "qsa_chunk.cu", "qsa_chunk_rows.cu", "qsa_kv.cu", "qsa_plan.cu",
+           "qsa_produce.cu", "qsa_score.cu", "qsa_select.cu"]
+HEADERS = ["qsa_chunk.cuh", "qsa_device.cuh", "qsa_internal.h", "qsa_seq.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "--expt-relaxed-constexpr", f"-I{INCLUDE}", f"-I{CSRC}"]

@@ -882,9 +882,9 @@ qsa_status check_cache(const qsa_kv_cache *c)
     return QSA_OK;
 }
 
-// A cache as [tokens][hkv * head_dim], boxes of `bytes` x `box` tokens: FP16 in
-// the tensor cores' swizzled layout (128 bytes), codes as they are.
-qsa_status make_tmap_kv(CUtensorMap *tm, const qsa_kv_cache *c, const void *base, int32_t bytes, int32_t box)
+// A cache as [tokens][hkv * head_dim], boxes of `bytes` x `box` tokens, in the
+// 128-byte swizzled layout or as they are.
+qsa_status make_tmap_kv(CUtensorMap *tm, const qsa_kv_cache *c, const void *base, int32_t bytes, int32_t box, bool swizzle)
 {
     const bool q8 = c->dtype == QSA_KV_E4M3;
     const cuuint64_t width = static_cast<cuuint64_t>(c->hkv) * c->head_dim;
@@ -894,7 +894,7 @@ qsa_status make_tmap_kv(CUtensorMap *tm, const qsa_kv_cache *c, const void *base
     cuuint32_t estr[2] = {1, 1};
     const CUresult r = g_encode(tm, q8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
                                 const_cast<void *>(base), dims, strides, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                                q8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+                                swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
                                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? QSA_OK : QSA_ERR_INVALID_ARG;
 }
@@ -913,6 +913,14 @@ qsa_status check_batch(int32_t rows, int32_t n_reqs, const int32_t *seq_start, c
     if (!aligned(seq_start, 4) || !aligned(pos_start, 4)) return QSA_ERR_INVALID_ARG;
     *any = true;
     return QSA_OK;
+}
+
+// Which attention kernel: units of 16 (token, query head) pairs read straight
+// from the cache's bytes while requests have no more than that on average, the
+// tensor-core pairs of SMs above.
+bool few_rows(int32_t rows, int32_t group, int32_t n_reqs)
+{
+    return static_cast<int64_t>(rows) * group <= int64_t{16} * n_reqs;
 }
 
 // A row array of `width` contiguous FP16 values per row.
@@ -984,7 +992,8 @@ qsa_status qsa_kv_load(void *k, int64_t k_stride, void *v, int64_t v_stride, int
 size_t qsa_chunk_attention_workspace_bytes(int32_t rows, int32_t hq, int32_t hkv, int32_t head_dim)
 {
     if (rows <= 0 || hq <= 0 || hkv <= 0 || head_dim <= 0) return 256;
-    return up(chunk_workspace_bytes(rows, std::max(1, hq / hkv), head_dim), 256);
+    const int32_t group = std::max(1, hq / hkv);
+    return up(std::max(chunk_workspace_bytes(rows, group, head_dim), chunk_rows_workspace_bytes(rows, group, head_dim)), 256);
 }
 
 qsa_status qsa_chunk_attention(const void *q, int64_t q_stride, int32_t rows, int32_t hq, int32_t n_reqs,
@@ -1020,15 +1029,23 @@ qsa_status qsa_chunk_attention(const void *q, int64_t q_stride, int32_t rows, in
     p.window = window;
     p.scale = scale;
     p.ws = static_cast<uint8_t *>(ws);
-    p.ws_rows = chunk_part_rows(rows, p.group);
     p.wait_limit_ns = g_wait_ns;
     CUtensorMap tk, tv;
-    int32_t box_k, box_v;
-    chunk_boxes(cache->head_dim, cache->page_tokens, &box_k, &box_v);
-    const int32_t v_bytes = p.kv.e4m3 ? cache->head_dim / 2 : 128;
-    if ((st = make_tmap_kv(&tk, cache, cache->k, 128, box_k)) != QSA_OK) return st;
-    if ((st = make_tmap_kv(&tv, cache, cache->v, v_bytes, box_v)) != QSA_OK) return st;
-    st = launch_rc(launch_chunk(p, &tk, &tv, d->sms, g_overlap, stream));
+    if (few_rows(rows, p.group, n_reqs)) {
+        p.ws_rows = chunk_rows_part_rows(rows, p.group);
+        const int32_t box = chunk_rows_box(cache->page_tokens);
+        if ((st = make_tmap_kv(&tk, cache, cache->k, 128, box, true)) != QSA_OK) return st;
+        if ((st = make_tmap_kv(&tv, cache, cache->v, 128, box, true)) != QSA_OK) return st;
+        st = launch_rc(launch_chunk_rows(p, &tk, &tv, d->sms, g_overlap, stream));
+    } else {
+        p.ws_rows = chunk_part_rows(rows, p.group);
+        int32_t box_k, box_v;
+        chunk_boxes(cache->head_dim, cache->page_tokens, &box_k, &box_v);
+        const int32_t v_bytes = p.kv.e4m3 ? cache->head_dim / 2 : 128;
+        if ((st = make_tmap_kv(&tk, cache, cache->k, 128, box_k, !p.kv.e4m3)) != QSA_OK) return st;
+        if ((st = make_tmap_kv(&tv, cache, cache->v, v_bytes, box_v, !p.kv.e4m3)) != QSA_OK) return st;
+        st = launch_rc(launch_chunk(p, &tk, &tv, d->sms, g_overlap, stream));
+    }
     if (st == QSA_OK) ++g_launches;                      // the join kernel
     return st;
 }

@@ -56,9 +56,7 @@
 #include <algorithm>
 #include <mutex>
 
-#include "qsa_device.cuh"
-#include "qsa_internal.h"
-#include "qsa_seq.cuh"
+#include "qsa_chunk.cuh"
 
 namespace qsa {
 namespace {
@@ -69,7 +67,6 @@ constexpr int CH_TILE = 128;                 // tokens of a tile
 constexpr int CH_SOFT = 8;                   // softmax warps
 constexpr int CH_LOAD = 8, CH_MMA = 9, CH_SCHED = 10, CH_MMA2 = 11, CH_HELP = 12;
 constexpr int CH_ROLES = 15;                 // warps that read the segments: all but the scheduler
-
 constexpr int CH_HELPERS = 4;
 constexpr int CH_WARPS = CH_HELP + CH_HELPERS;
 constexpr int CH_THREADS = 32 * CH_WARPS;
@@ -78,8 +75,13 @@ constexpr int MAX_SLOTS = 10;                // slots of the ring at most
 constexpr uint32_t RING = 229376;            // bytes for Q and the ring
 constexpr float RESCALE = 8.0f;              // log2 of the growth that rescales
 constexpr uint32_t TM_S = 0, TM_O = 256;     // TMEM columns: two S buffers of 128, O
-constexpr int UNIT_COST = 4;                 // tiles' worth of time that a unit costs besides its tiles
 constexpr int BAR_PAIR = 1, BAR_HELP = 5;    // named barriers: four softmax warp pairs, the helpers
+
+struct PairGeometry {
+    static constexpr int ROWS = CH_ROWS, TILE = CH_TILE, UNIT_COST = 4, THREADS = CH_THREADS, WARPS = CH_WARPS,
+                         WORKERS = CHUNK_MAX_PAIRS;
+};
+using G = PairGeometry;
 
 template <int D, bool Q8>
 struct Shape {
@@ -94,259 +96,15 @@ struct Shape {
     static constexpr int LEAD = OWN_P ? 3 : 2;                         // key tiles loaded before the first value tile
 };
 
-// A run of tiles of one unit, a pair's next piece of work.
-struct alignas(16) Seg {
-    int32_t n, j0;                           // tiles j0 .. j0 + n - 1; n = 0: no more work
-    int32_t b, g;                            // request, KV head
-    int32_t s0, p0, v0, rows;                // request's first row and position, unit's first (token, head) pair, pairs in use
-    int32_t lo_tok, hi_tok;                  // tokens that some row attends: lo_tok .. hi_tok
-    int32_t place;                           // workspace place of the partial result, -1: this is the whole unit
-    int32_t pad;
-
-    // whether tile j0 + k holds tokens that no row attends
-    __device__ __forceinline__ bool cut(int32_t k) const
-    {
-        const int32_t t0 = (j0 + k) * CH_TILE;
-        return t0 < lo_tok || t0 + CH_TILE - 1 > hi_tok;
-    }
-};
-constexpr int SEGS = 4;                      // segments the scheduler may be ahead
-constexpr uint64_t SEG_WAIT_NS = 10000000000ull;
-
 struct Ctrl {
-    Seg seg[SEGS];
-    uint64_t seg_full[SEGS], seg_empty[SEGS];
+    SegRing segs;
     uint64_t full[MAX_SLOTS], empty[MAX_SLOTS], raw_full[RAWS], raw_empty[RAWS], bnd[8];
     uint64_t s_full[2], s_free[2], p_full[2], o_done[2], m_out[2][4], q_full[2], q_free[2], drain;
     alignas(8) float mrow[2][CH_HALF];       // [tile parity][row]: maximum in use at the group's last tile; sums at a segment's end
     alignas(8) uint16_t scale[2][CH_TILE];   // [slot parity][token]: FP16 scale (E4M3)
-    int64_t w0, w1, total;                   // this pair's share of the line, the line's length
-    int32_t pairs;                           // pairs that have work
-    int32_t b, m, g, off;                    // the unit that w0 lies in, and w0's place in it
+    Share share;
     uint32_t tmem;
     int32_t abort;
-};
-
-// A unit that lies across pairs, as the join kernel needs it (written by the
-// pair that holds the unit's first tile).
-struct Split {
-    int32_t parts;                           // 0: none
-    int32_t rows;                            // rows of the unit
-    int32_t s0, v0, g;                       // request's first row, unit's first (token, head) pair, KV head
-};
-
-// Workspace: a Split per pair, then per place (two for each pair) the rows'
-// (maximum in powers of two, sum), then their unnormalised outputs.
-constexpr size_t WS_ML = 4096;
-constexpr size_t WS_O = WS_ML + size_t{2} * CHUNK_MAX_PAIRS * CH_ROWS * 8;
-static_assert(sizeof(Split) * CHUNK_MAX_PAIRS <= WS_ML, "workspace header");
-
-// ------------------------------------------------------------- work sharing --
-
-struct Unit {
-    int32_t v0, rows, lo_tok, hi_tok;        // as in Seg
-    int32_t lo, hi;                          // tiles lo .. hi - 1
-};
-
-// v / p.group for 0 <= v < 2^31: with s = ceil(log2 group) and group_mul =
-// ceil(2^(31 + s) / group), the error of v * group_mul against v * 2^(31 + s) /
-// group is below 2^31 * 2^s / group, less than one unit of the quotient's grid.
-__device__ __forceinline__ int32_t by_group(const ChunkParams &p, int32_t v)
-{
-    return static_cast<int32_t>((static_cast<uint64_t>(static_cast<uint32_t>(v)) * p.group_mul) >> p.group_shift);
-}
-
-__device__ __forceinline__ int32_t units_of(const ChunkParams &p, const Seq &s)
-{
-    return (s.n * p.group + CH_ROWS - 1) / CH_ROWS;
-}
-
-__device__ __forceinline__ Unit unit_of(const ChunkParams &p, const Seq &s, int32_t m)
-{
-    Unit u;
-    u.v0 = m * CH_ROWS;
-    const int32_t end = min(s.n * p.group, u.v0 + CH_ROWS);
-    u.rows = end - u.v0;
-    const int32_t first = s.p0 + by_group(p, u.v0);
-    u.hi_tok = s.p0 + by_group(p, end - 1);
-    u.lo_tok = p.window > 0 ? max(0, first - p.window + 1) : 0;
-    u.lo = u.lo_tok / CH_TILE;
-    u.hi = u.hi_tok / CH_TILE + 1;
-    return u;
-}
-
-template <typename T>
-__device__ __forceinline__ T warp_scan(T x, int lane)      // inclusive
-{
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const T y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-    }
-    return x;
-}
-
-// The sum of x over the threads before this one, and over all of them.
-template <typename T>
-__device__ __forceinline__ T block_scan(T x, T *warp_total, int warp, int lane, T *total)
-{
-    const T sc = warp_scan(x, lane);
-    if (lane == 31) warp_total[warp] = sc;
-    __syncthreads();
-    T before = 0, all = 0;
-#pragma unroll
-    for (int w = 0; w < CH_WARPS; ++w) {
-        if (w == warp) before = all;
-        all += warp_total[w];
-    }
-    *total = all;
-    return before + sc - x;
-}
-
-// Shared memory of find_work: the queries' place, which is free until then.
-struct FindScratch {
-    int32_t prefix[CH_THREADS];
-    int32_t units[CH_WARPS];
-    int64_t costs[CH_WARPS];
-};
-static_assert(sizeof(FindScratch) <= Shape<128, false>::QB, "scratch");
-
-// Finds this pair's share of the line, c.w0 .. c.w1, and the unit that w0 lies
-// in (both CTAs of a pair do, alike).  Each thread counts the units of a run of
-// requests, then adds up the lengths of an equal run of units.
-__device__ __forceinline__ void find_work(const ChunkParams &p, Ctrl &c, FindScratch &s, int warp, int lane)
-{
-    const int t = threadIdx.x;
-    int32_t *prefix = s.prefix;
-    const int32_t run = (p.kv.n_reqs + CH_THREADS - 1) / CH_THREADS;
-    const int32_t r0 = min(t * run, p.kv.n_reqs), r1 = min(r0 + run, p.kv.n_reqs);
-    int32_t mine = 0, units;
-    for (int32_t b = r0; b < r1; ++b) {
-        bool bad;
-        mine += units_of(p, seq_of(p.kv, b, &bad));
-        if (bad && blockIdx.x == 0) record_error(p.kv.status, ST_BAD_ROW);
-    }
-    prefix[t] = block_scan(mine, s.units, warp, lane, &units);
-    __syncthreads();
-    const int32_t u0 = static_cast<int32_t>(static_cast<int64_t>(units) * t / CH_THREADS);
-    const int32_t u1 = static_cast<int32_t>(static_cast<int64_t>(units) * (t + 1) / CH_THREADS);
-    int32_t b0 = 0, m0 = 0;
-    Seq s0{0, 0, 0};
-    int64_t cost = 0, total;
-    if (u0 < u1) {
-        int lo = 0;                                          // the last run that starts at or before u0
-#pragma unroll
-        for (int step = CH_THREADS / 2; step > 0; step >>= 1)
-            if (prefix[lo + step] <= u0) lo += step;
-        b0 = lo * run;
-        m0 = u0 - prefix[lo];
-        bool bad;
-        s0 = seq_of(p.kv, b0, &bad);
-        for (int32_t n = units_of(p, s0); m0 >= n; n = units_of(p, s0)) {
-            m0 -= n;
-            s0 = seq_of(p.kv, ++b0, &bad);
-        }
-        int32_t b = b0, m = m0;
-        Seq sb = s0;
-        for (int32_t u = u0; u < u1; ++u, ++m) {
-            while (m >= units_of(p, sb)) {
-                sb = seq_of(p.kv, ++b, &bad);
-                m = 0;
-            }
-            const Unit un = unit_of(p, sb, m);
-            cost += UNIT_COST + un.hi - un.lo;
-        }
-        cost *= p.kv.hkv;
-    }
-    int64_t at = block_scan(cost, s.costs, warp, lane, &total);
-    // one place each at least, so that the pairs with work are the first ones
-    const int32_t pairs = static_cast<int32_t>(min(total, static_cast<int64_t>(gridDim.x >> 1)));
-    const int32_t me = blockIdx.x >> 1;
-    const int64_t w0 = me < pairs ? total * me / pairs : 0, w1 = me < pairs ? total * (me + 1) / pairs : 0;
-    if (t == 0) {
-        c.w0 = w0;
-        c.w1 = w1;
-        c.total = total;
-        c.pairs = pairs;
-    }
-    if (w0 < w1 && at <= w0 && w0 < at + cost) {
-        for (;; ++m0) {
-            while (m0 >= units_of(p, s0)) {
-                bool bad;
-                s0 = seq_of(p.kv, ++b0, &bad);
-                m0 = 0;
-            }
-            const Unit un = unit_of(p, s0, m0);
-            const int32_t len = UNIT_COST + un.hi - un.lo;
-            if (w0 < at + static_cast<int64_t>(len) * p.kv.hkv) {
-                c.b = b0;
-                c.m = m0;
-                c.g = static_cast<int32_t>(w0 - at) / len;
-                c.off = static_cast<int32_t>(w0 - at) % len;
-                break;
-            }
-            at += static_cast<int64_t>(len) * p.kv.hkv;
-        }
-    }
-    __syncthreads();
-}
-
-// The pair's share as segments.
-struct Walk {
-    int64_t left;
-    int32_t b, m, g, off, n_units;
-    Seq s;
-
-    __device__ __forceinline__ Walk(const ChunkParams &p, const Ctrl &c)
-    {
-        left = c.w1 - c.w0;
-        b = c.b;
-        m = c.m;
-        g = c.g;
-        off = c.off;
-        if (left > 0) load(p);
-    }
-    __device__ __forceinline__ void load(const ChunkParams &p)
-    {
-        bool bad;
-        s = seq_of(p.kv, b, &bad);
-        n_units = units_of(p, s);
-    }
-    // the next segment (n = 0 at the end of the share); *rest: tiles of the unit after it
-    __device__ __forceinline__ Seg next(const ChunkParams &p, bool *head, int32_t *rest)
-    {
-        Seg x;
-        x.n = 0;
-        if (left <= 0) return x;
-        while (m >= n_units) {               // empty requests have no units
-            if (++b >= p.kv.n_reqs) return x;
-            m = 0;
-            load(p);
-        }
-        const Unit u = unit_of(p, s, m);
-        // a unit's place in the line: UNIT_COST, then its tiles
-        const int32_t len = UNIT_COST + u.hi - u.lo;
-        const int32_t end = static_cast<int32_t>(min(static_cast<int64_t>(len), off + left));
-        left -= end - off;
-        x.j0 = u.lo + max(0, off - UNIT_COST);
-        x.n = u.lo + max(0, end - UNIT_COST) - x.j0;      // 0: the share ends before the unit's first tile
-        x.b = b;
-        x.g = g;
-        x.s0 = s.s0;
-        x.p0 = s.p0;
-        x.v0 = u.v0;
-        x.rows = u.rows;
-        x.lo_tok = u.lo_tok;
-        x.hi_tok = u.hi_tok;
-        *head = x.j0 == u.lo;
-        *rest = u.hi - x.j0 - x.n;
-        off = 0;
-        if (++g == p.kv.hkv) {
-            g = 0;
-            ++m;
-        }
-        return x;
-    }
 };
 
 // ------------------------------------------------------------------- pieces --
@@ -367,11 +125,6 @@ __device__ __forceinline__ int32_t slot_of_v(int32_t tile, int32_t n)
 {
     const int32_t lead = min(LEAD, n);
     return lead + (tile < n - lead ? 2 * tile : n - lead + tile);
-}
-
-__device__ __forceinline__ uint32_t sw128(uint32_t row, uint32_t c)
-{
-    return (row >> 3) * 1024u + (row & 7u) * 128u + ((c ^ (row & 7u)) << 4);
 }
 
 // V as the B operand [token (K)][dim (N)]: dims contiguous, 128-byte swizzle;
@@ -490,13 +243,6 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&v)[
 
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-__device__ __forceinline__ float exp2_approx(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // two FP32 lanes at once
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
 {
@@ -516,17 +262,6 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b)
         : "=f"(d.x), "=f"(d.y)
         : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return d;
-}
-
-__device__ __forceinline__ void named_barrier(int id, int threads)
-{
-    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
-
-// A wait by a whole warp: true on every lane, or false on every lane.
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort, uint64_t lim)
-{
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, lim));
 }
 
 // ------------------------------------------------------------------- kernel --
@@ -570,8 +305,8 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
             mbar_init(&c.q_free[i], 1);
         }
         for (int i = 0; i < SEGS; ++i) {
-            mbar_init(&c.seg_full[i], 1);
-            mbar_init(&c.seg_empty[i], CH_ROLES);
+            mbar_init(&c.segs.full[i], 1);
+            mbar_init(&c.segs.empty[i], CH_ROLES);
         }
         mbar_init(&c.drain, 1);
         c.abort = 0;
@@ -583,28 +318,18 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
     wait_prior_grid();
-    find_work(p, c, *reinterpret_cast<FindScratch *>(q_s), warp, lane);
+    // (the queries' place is free until the segments are known)
+    static_assert(sizeof(FindScratch<G>) <= Sh::QB, "scratch");
+    find_work<G>(p, c.share, *reinterpret_cast<FindScratch<G> *>(q_s), blockIdx.x >> 1, gridDim.x >> 1, warp, lane);
     tc_fence_before();
     __syncthreads();
     cluster_sync();                                          // the pair's barriers and TMEM are ready
     tc_fence_after();
     const uint32_t tmem = c.tmem;
     const uint32_t ring_a = smem_u32(ring);
-    // The next segment, false at the end.  Its wait ignores the abort flag: after
-    // a time-out every role still walks through all segments, keeps to its named
-    // barriers and does nothing else.
     uint32_t segs = 0;
     Seg w;
-    auto next_segment = [&]() -> bool {
-        const uint32_t k = segs % SEGS;
-        bool got = mbar_wait_bounded(&c.seg_full[k], (segs / SEGS) & 1u, SEG_WAIT_NS);
-        got = __all_sync(0xffffffffu, got);
-        w = c.seg[k];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&c.seg_empty[k]);
-        ++segs;
-        return got && w.n > 0;
-    };
+    auto next_segment = [&]() -> bool { return qsa::next_segment(c.segs, &segs, &w, lane); };
     // registers after the split: 8 x 32 x 200 + 8 x 32 x 56 = 65,536
     if (warp >= CH_LOAD && warp < CH_HELP) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
@@ -669,7 +394,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                 if constexpr (Q8) {
                     bar = smem_u32(&c.raw_full[slot]);
                     if (lane == 0) mbar_arrive_expect_tx(&c.raw_full[slot], BYTES);
-                } else if (v && w.cut(tile)) {
+                } else if (v && w.cut(tile, CH_TILE)) {
                     // the helpers clear rows of this one before the products see it
                     bar = smem_u32(&c.bnd[nb & 7u]);
                     if (lane == 0) mbar_arrive_expect_tx(&c.bnd[nb & 7u], BYTES);
@@ -700,33 +425,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
         __syncwarp();
     } else if (warp == CH_SCHED) {
         // ----------------------------------------------------------- segments
-        Walk walk(p, c);
-        Split split = {0, 0, 0, 0, 0};
-        for (uint32_t i = 0;; ++i) {
-            bool head = false;
-            int32_t rest = 0;
-            Seg x = walk.next(p, &head, &rest);
-            x.place = head && rest == 0 ? -1 : 2 * static_cast<int32_t>(blockIdx.x >> 1) + (head ? 1 : 0);
-            if (x.n > 0 && head && rest > 0) {
-                // the unit's other tiles lie in the next pairs' shares
-                split.parts = 1;
-                while (c.total * ((blockIdx.x >> 1) + split.parts) / c.pairs < c.w1 + rest) ++split.parts;
-                split.rows = x.rows;
-                split.s0 = x.s0;
-                split.v0 = x.v0;
-                split.g = x.g;
-            }
-            const uint32_t k = i % SEGS;
-            if (i >= SEGS) mbar_wait_bounded(&c.seg_empty[k], (i / SEGS - 1) & 1u, SEG_WAIT_NS);
-            __syncwarp();
-            if (lane == 0) {
-                c.seg[k] = x;
-                mbar_arrive(&c.seg_full[k]);
-            }
-            if (x.n == 0) break;
-        }
-        if (lane == 0 && rank == 0) reinterpret_cast<Split *>(p.ws)[blockIdx.x >> 1] = split;
-        __syncwarp();
+        schedule<G>(p, c.share, c.segs, blockIdx.x >> 1, rank == 0, lane);
     } else {
         // --------------------------------------------------------------- MMAs
         // The warp runs as one and elects the issuing thread at each batch;
@@ -877,7 +576,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     const int32_t tile = k == 0 ? 0 : n - 1;
-                    if ((k == 1 && n == 1) || !w.cut(tile)) continue;
+                    if ((k == 1 && n == 1) || !w.cut(tile, CH_TILE)) continue;
                     if (ok) ok = warp_wait(&c.bnd[nb & 7u], (nb >> 3) & 1u, abort, lim);
                     ++nb;
                     const uint32_t vs = (ring0 + slot_of_v<Sh::LEAD>(tile, n)) % NS;
@@ -1125,7 +824,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                               ((static_cast<int64_t>(w.s0) + tok) * p.hq + w.g * p.group + h) * D + grp * OC;
                 float *part = nullptr;
                 if (!whole) {
-                    part = reinterpret_cast<float *>(p.ws + WS_O) + (static_cast<int64_t>(w.place) * p.ws_rows + ur) * D + grp * OC;
+                    part = reinterpret_cast<float *>(p.ws + ws_o<CH_ROWS, CHUNK_MAX_PAIRS>()) + (static_cast<int64_t>(w.place) * p.ws_rows + ur) * D + grp * OC;
                     if (in && grp == 0)
                         *reinterpret_cast<float2 *>(p.ws + WS_ML + (static_cast<int64_t>(w.place) * CH_ROWS + ur) * 8) =
                             make_float2(mlast == -INFINITY ? -INFINITY : mlast * cs, l);
@@ -1172,70 +871,6 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
     allow_next_grid();
 }
 
-// Joins the parts of each split unit: block x the unit that pair x began (part 0
-// in its second place, part i in the first place of the i-th pair after it), a
-// warp per row.
-template <int D>
-__global__ void __launch_bounds__(256)
-chunk_join_kernel(const ChunkParams p)
-{
-    constexpr int N = D / 32;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    wait_prior_grid();
-    const Split sp = reinterpret_cast<const Split *>(p.ws)[blockIdx.x];
-    const int32_t n = sp.parts;
-    if (n == 0) return;
-    const float2 *ml = reinterpret_cast<const float2 *>(p.ws + WS_ML);
-    const float *po = reinterpret_cast<const float *>(p.ws + WS_O);
-    auto place = [&](int32_t i) { return 2 * (static_cast<int64_t>(blockIdx.x) + i) + (i == 0 ? 1 : 0); };
-    for (int32_t row = blockIdx.y * 8 + warp; row < sp.rows; row += 8 * gridDim.y) {
-        float mx = -INFINITY, sum = 0.0f;
-        for (int32_t i = lane; i < n; i += 32) mx = fmaxf(mx, ml[place(i) * CH_ROWS + row].x);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        float acc[N];
-#pragma unroll
-        for (int e = 0; e < N; ++e) acc[e] = 0.0f;
-        for (int32_t i0 = 0; i0 < n; i0 += 32) {
-            float wt = 0.0f;
-            if (i0 + lane < n) {
-                const float2 x = ml[place(i0 + lane) * CH_ROWS + row];
-                wt = x.x == -INFINITY ? 0.0f : exp2_approx(x.x - mx);      // a part in which the row saw nothing
-                sum = fmaf(x.y, wt, sum);
-            }
-            const int32_t k = min(32, n - i0);
-#pragma unroll 4
-            for (int32_t i = 0; i < k; ++i) {
-                const float f = __shfl_sync(0xffffffffu, wt, i);
-                const float4 *src = reinterpret_cast<const float4 *>(po + (place(i0 + i) * p.ws_rows + row) * D) + lane;
-#pragma unroll
-                for (int e = 0; e < N / 4; ++e) {
-                    const float4 x = src[32 * e];
-                    acc[4 * e] = fmaf(x.x, f, acc[4 * e]);
-                    acc[4 * e + 1] = fmaf(x.y, f, acc[4 * e + 1]);
-                    acc[4 * e + 2] = fmaf(x.z, f, acc[4 * e + 2]);
-                    acc[4 * e + 3] = fmaf(x.w, f, acc[4 * e + 3]);
-                }
-            }
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-        const int32_t v = sp.v0 + row, tok = v / p.group, h = v - tok * p.group;
-        __half *out = static_cast<__half *>(p.out) +
-                      ((static_cast<int64_t>(sp.s0) + tok) * p.hq + sp.g * p.group + h) * D;
-#pragma unroll
-        for (int e = 0; e < N / 4; ++e) {
-            const __half2 a = __floats2half2_rn(acc[4 * e] * inv, acc[4 * e + 1] * inv);
-            const __half2 b = __floats2half2_rn(acc[4 * e + 2] * inv, acc[4 * e + 3] * inv);
-            uint2 u;
-            u.x = *reinterpret_cast<const uint32_t *>(&a);
-            u.y = *reinterpret_cast<const uint32_t *>(&b);
-            reinterpret_cast<uint2 *>(out)[32 * e + lane] = u;
-        }
-    }
-}
-
 constexpr size_t CH_SMEM = RING + sizeof(Ctrl);
 static_assert(CH_SMEM <= 232448, "shared memory budget");
 
@@ -1262,7 +897,7 @@ int launch(const ChunkParams &p, const void *tk, const void *tv, int grid, bool 
     if (rc != 0) return rc;
     void *join[] = {const_cast<ChunkParams *>(&p)};
     const unsigned rows8 = static_cast<unsigned>(std::min(8, (p.ws_rows + 7) / 8));
-    return launch_kernel(reinterpret_cast<const void *>(&chunk_join_kernel<D>), dim3(grid / 2, rows8), dim3(256), 0, stream,
+    return launch_kernel(reinterpret_cast<const void *>(&chunk_join_kernel<G, D>), dim3(grid / 2, rows8), dim3(256), 0, stream,
                          overlap, join);
 }
 
@@ -1275,7 +910,7 @@ int32_t chunk_part_rows(int32_t rows, int32_t group)
 
 size_t chunk_workspace_bytes(int32_t rows, int32_t group, int32_t head_dim)
 {
-    return WS_O + size_t{2} * CHUNK_MAX_PAIRS * chunk_part_rows(rows, group) * head_dim * 4;
+    return ws_o<CH_ROWS, CHUNK_MAX_PAIRS>() + size_t{2} * CHUNK_MAX_PAIRS * chunk_part_rows(rows, group) * head_dim * 4;
 }
 
 // tokens per box of the K and V tensor maps

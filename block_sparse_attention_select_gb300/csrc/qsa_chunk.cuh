@@ -1,0 +1,418 @@
+// Dense attention over the paged cache: what its two kernels share, the line of
+// work and its segments, and the kernel that joins partial results.
+#pragma once
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "qsa_device.cuh"
+#include "qsa_internal.h"
+#include "qsa_seq.cuh"
+
+namespace qsa {
+namespace {
+
+// A kernel's geometry G gives ROWS ((token, query head) pairs of a unit), TILE
+// (tokens of a tile), UNIT_COST (tiles' worth of time that a unit costs besides
+// its tiles), THREADS and WARPS of a CTA, WORKERS (at most; a worker is a CTA or
+// a pair of them).
+
+// A run of tiles of one unit, a worker's next piece of work.
+struct alignas(16) Seg {
+    int32_t n, j0;                           // tiles j0 .. j0 + n - 1; n = 0: no more work
+    int32_t b, g;                            // request, KV head
+    int32_t s0, p0, v0, rows;                // request's first row and position, unit's first (token, head) pair, pairs in use
+    int32_t lo_tok, hi_tok;                  // tokens that some row attends: lo_tok .. hi_tok
+    int32_t place;                           // workspace place of the partial result, -1: this is the whole unit
+    int32_t pad;
+
+    // whether tile j0 + k holds tokens that no row attends
+    __device__ __forceinline__ bool cut(int32_t k, int32_t tile) const
+    {
+        const int32_t t0 = (j0 + k) * tile;
+        return t0 < lo_tok || t0 + tile - 1 > hi_tok;
+    }
+};
+// A unit that lies across workers, as the join kernel needs it (written by the
+// worker that holds the unit's first tile).
+struct Split {
+    int32_t parts;                           // 0: none
+    int32_t rows;                            // rows of the unit
+    int32_t s0, v0, g;                       // request's first row, unit's first (token, head) pair, KV head
+};
+
+// Workspace: a Split per worker, then per place (two for each worker: 0 for a
+// unit begun before its share, 1 for one that goes on after it) the rows'
+// (maximum in powers of two, sum), then their unnormalised outputs.
+constexpr size_t WS_ML = 4096;
+template <int ROWS, int WORKERS>
+constexpr size_t ws_o() { return WS_ML + size_t{2} * WORKERS * ROWS * 8; }
+
+// ------------------------------------------------------------- work sharing --
+
+struct Unit {
+    int32_t v0, rows, lo_tok, hi_tok;        // as in Seg
+    int32_t lo, hi;                          // tiles lo .. hi - 1
+};
+
+// v / p.group for 0 <= v < 2^31: with s = ceil(log2 group) and group_mul =
+// ceil(2^(31 + s) / group), the error of v * group_mul against v * 2^(31 + s) /
+// group is below 2^31 * 2^s / group, less than one unit of the quotient's grid.
+__device__ __forceinline__ int32_t by_group(const ChunkParams &p, int32_t v)
+{
+    return static_cast<int32_t>((static_cast<uint64_t>(static_cast<uint32_t>(v)) * p.group_mul) >> p.group_shift);
+}
+
+template <typename G>
+__device__ __forceinline__ int32_t units_of(const ChunkParams &p, const Seq &s)
+{
+    return (s.n * p.group + G::ROWS - 1) / G::ROWS;
+}
+
+template <typename G>
+__device__ __forceinline__ Unit unit_of(const ChunkParams &p, const Seq &s, int32_t m)
+{
+    Unit u;
+    u.v0 = m * G::ROWS;
+    const int32_t end = min(s.n * p.group, u.v0 + G::ROWS);
+    u.rows = end - u.v0;
+    const int32_t first = s.p0 + by_group(p, u.v0);
+    u.hi_tok = s.p0 + by_group(p, end - 1);
+    u.lo_tok = p.window > 0 ? max(0, first - p.window + 1) : 0;
+    u.lo = u.lo_tok / G::TILE;
+    u.hi = u.hi_tok / G::TILE + 1;
+    return u;
+}
+
+template <typename T>
+__device__ __forceinline__ T warp_scan(T x, int lane)      // inclusive
+{
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const T y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    return x;
+}
+
+// The sum of x over the threads before this one, and over all of them.
+template <typename G, typename T>
+__device__ __forceinline__ T block_scan(T x, T *warp_total, int warp, int lane, T *total)
+{
+    const T sc = warp_scan(x, lane);
+    if (lane == 31) warp_total[warp] = sc;
+    __syncthreads();
+    T before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < G::WARPS; ++w) {
+        if (w == warp) before = all;
+        all += warp_total[w];
+    }
+    *total = all;
+    return before + sc - x;
+}
+
+// A worker's share of the line.
+struct Share {
+    int64_t w0, w1, total;                   // w0 .. w1, the line's length
+    int32_t workers;                         // those that have work
+    int32_t b, m, g, off;                    // the unit that w0 lies in, and w0's place in it
+};
+
+// Shared memory that find_work needs.
+template <typename G>
+struct FindScratch {
+    int32_t prefix[G::THREADS];
+    int32_t units[G::WARPS];
+    int64_t costs[G::WARPS];
+};
+
+// Finds worker `me`'s share of the line (of `n_workers`), by the whole CTA.  Each
+// thread counts the units of a run of requests, then adds up the lengths of an
+// equal run of units.
+template <typename G>
+__device__ __forceinline__ void find_work(const ChunkParams &p, Share &c, FindScratch<G> &s, int32_t me,
+                                          int32_t n_workers, int warp, int lane)
+{
+    const int t = threadIdx.x;
+    int32_t *prefix = s.prefix;
+    const int32_t run = (p.kv.n_reqs + G::THREADS - 1) / G::THREADS;
+    const int32_t r0 = min(t * run, p.kv.n_reqs), r1 = min(r0 + run, p.kv.n_reqs);
+    int32_t mine = 0, units;
+    for (int32_t b = r0; b < r1; ++b) {
+        bool bad;
+        mine += units_of<G>(p, seq_of(p.kv, b, &bad));
+        if (bad && blockIdx.x == 0) record_error(p.kv.status, ST_BAD_ROW);
+    }
+    prefix[t] = block_scan<G>(mine, s.units, warp, lane, &units);
+    __syncthreads();
+    const int32_t u0 = static_cast<int32_t>(static_cast<int64_t>(units) * t / G::THREADS);
+    const int32_t u1 = static_cast<int32_t>(static_cast<int64_t>(units) * (t + 1) / G::THREADS);
+    int32_t b0 = 0, m0 = 0;
+    Seq s0{0, 0, 0};
+    int64_t cost = 0, total;
+    if (u0 < u1) {
+        int lo = 0;                                          // the last run that starts at or before u0
+#pragma unroll
+        for (int step = 256; step > 0; step >>= 1)
+            if (lo + step < G::THREADS && prefix[lo + step] <= u0) lo += step;
+        b0 = lo * run;
+        m0 = u0 - prefix[lo];
+        bool bad;
+        s0 = seq_of(p.kv, b0, &bad);
+        for (int32_t n = units_of<G>(p, s0); m0 >= n; n = units_of<G>(p, s0)) {
+            m0 -= n;
+            s0 = seq_of(p.kv, ++b0, &bad);
+        }
+        int32_t b = b0, m = m0;
+        Seq sb = s0;
+        for (int32_t u = u0; u < u1; ++u, ++m) {
+            while (m >= units_of<G>(p, sb)) {
+                sb = seq_of(p.kv, ++b, &bad);
+                m = 0;
+            }
+            const Unit un = unit_of<G>(p, sb, m);
+            cost += G::UNIT_COST + un.hi - un.lo;
+        }
+        cost *= p.kv.hkv;
+    }
+    int64_t at = block_scan<G>(cost, s.costs, warp, lane, &total);
+    // one place each at least, so that the workers with work are the first ones
+    const int32_t workers = static_cast<int32_t>(min(total, static_cast<int64_t>(n_workers)));
+    const int64_t w0 = me < workers ? total * me / workers : 0, w1 = me < workers ? total * (me + 1) / workers : 0;
+    if (t == 0) {
+        c.w0 = w0;
+        c.w1 = w1;
+        c.total = total;
+        c.workers = workers;
+    }
+    if (w0 < w1 && at <= w0 && w0 < at + cost) {
+        for (;; ++m0) {
+            while (m0 >= units_of<G>(p, s0)) {
+                bool bad;
+                s0 = seq_of(p.kv, ++b0, &bad);
+                m0 = 0;
+            }
+            const Unit un = unit_of<G>(p, s0, m0);
+            const int32_t len = G::UNIT_COST + un.hi - un.lo;
+            if (w0 < at + static_cast<int64_t>(len) * p.kv.hkv) {
+                c.b = b0;
+                c.m = m0;
+                c.g = static_cast<int32_t>(w0 - at) / len;
+                c.off = static_cast<int32_t>(w0 - at) % len;
+                break;
+            }
+            at += static_cast<int64_t>(len) * p.kv.hkv;
+        }
+    }
+    __syncthreads();
+}
+
+// The share as segments.
+template <typename G>
+struct Walk {
+    int64_t left;
+    int32_t b, m, g, off, n_units;
+    Seq s;
+
+    __device__ __forceinline__ Walk(const ChunkParams &p, const Share &c)
+    {
+        left = c.w1 - c.w0;
+        b = c.b;
+        m = c.m;
+        g = c.g;
+        off = c.off;
+        if (left > 0) load(p);
+    }
+    __device__ __forceinline__ void load(const ChunkParams &p)
+    {
+        bool bad;
+        s = seq_of(p.kv, b, &bad);
+        n_units = units_of<G>(p, s);
+    }
+    // the next segment (n = 0 at the end of the share); *rest: tiles of the unit after it
+    __device__ __forceinline__ Seg next(const ChunkParams &p, bool *head, int32_t *rest)
+    {
+        Seg x;
+        x.n = 0;
+        if (left <= 0) return x;
+        while (m >= n_units) {               // empty requests have no units
+            if (++b >= p.kv.n_reqs) return x;
+            m = 0;
+            load(p);
+        }
+        const Unit u = unit_of<G>(p, s, m);
+        // a unit's place in the line: G::UNIT_COST, then its tiles
+        const int32_t len = G::UNIT_COST + u.hi - u.lo;
+        const int32_t end = static_cast<int32_t>(min(static_cast<int64_t>(len), off + left));
+        left -= end - off;
+        x.j0 = u.lo + max(0, off - G::UNIT_COST);
+        x.n = u.lo + max(0, end - G::UNIT_COST) - x.j0;      // 0: the share ends before the unit's first tile
+        x.b = b;
+        x.g = g;
+        x.s0 = s.s0;
+        x.p0 = s.p0;
+        x.v0 = u.v0;
+        x.rows = u.rows;
+        x.lo_tok = u.lo_tok;
+        x.hi_tok = u.hi_tok;
+        *head = x.j0 == u.lo;
+        *rest = u.hi - x.j0 - x.n;
+        off = 0;
+        if (++g == p.kv.hkv) {
+            g = 0;
+            ++m;
+        }
+        return x;
+    }
+};
+
+
+// The scheduler warp: walks through the share and hands out its segments
+// through a ring; `me` writes its split unit, if any, for the join kernel.
+constexpr int SEGS = 4;                      // segments it may be ahead
+constexpr uint64_t SEG_WAIT_NS = 10000000000ull;
+struct SegRing {
+    Seg seg[SEGS];
+    uint64_t full[SEGS], empty[SEGS];
+};
+
+template <typename G>
+__device__ __forceinline__ void schedule(const ChunkParams &p, const Share &c, SegRing &ring, int32_t me, bool tell, int lane)
+{
+    Walk<G> walk(p, c);
+    Split split = {0, 0, 0, 0, 0};
+    for (uint32_t i = 0;; ++i) {
+        bool head = false;
+        int32_t rest = 0;
+        Seg x = walk.next(p, &head, &rest);
+        x.place = head && rest == 0 ? -1 : 2 * me + (head ? 1 : 0);
+        if (x.n > 0 && head && rest > 0) {
+            // the unit's other tiles lie in the next workers' shares
+            split.parts = 1;
+            while (c.total * (me + split.parts) / c.workers < c.w1 + rest) ++split.parts;
+            split.rows = x.rows;
+            split.s0 = x.s0;
+            split.v0 = x.v0;
+            split.g = x.g;
+        }
+        const uint32_t k = i % SEGS;
+        if (i >= SEGS) mbar_wait_bounded(&ring.empty[k], (i / SEGS - 1) & 1u, SEG_WAIT_NS);
+        __syncwarp();
+        if (lane == 0) {
+            ring.seg[k] = x;
+            mbar_arrive(&ring.full[k]);
+        }
+        if (x.n == 0) break;
+    }
+    if (lane == 0 && tell) reinterpret_cast<Split *>(p.ws)[me] = split;
+    __syncwarp();
+}
+
+// Segment number *i of the ring, false at the end.  The wait ignores the abort
+// flag: after a time-out every role still walks through all segments, keeps to
+// its named barriers and does nothing else.
+__device__ __forceinline__ bool next_segment(SegRing &ring, uint32_t *i, Seg *w, int lane)
+{
+    const uint32_t k = *i % SEGS;
+    bool got = mbar_wait_bounded(&ring.full[k], (*i / SEGS) & 1u, SEG_WAIT_NS);
+    got = __all_sync(0xffffffffu, got);
+    *w = ring.seg[k];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&ring.empty[k]);
+    ++*i;
+    return got && w->n > 0;
+}
+
+// ------------------------------------------------------------------- pieces --
+
+__device__ __forceinline__ uint32_t sw128(uint32_t row, uint32_t c)
+{
+    return (row >> 3) * 1024u + (row & 7u) * 128u + ((c ^ (row & 7u)) << 4);
+}
+
+__device__ __forceinline__ float exp2_approx(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ void named_barrier(int id, int threads)
+{
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// A wait by a whole warp: true on every lane, or false on every lane.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort, uint64_t lim)
+{
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, lim));
+}
+
+// --------------------------------------------------------------------- join --
+
+// Joins the parts of each split unit: block x the unit that worker x began (part
+// 0 in its second place, part i in the first place of the i-th worker after it),
+// a warp per row.  G: the geometry of the kernel that left the parts.
+template <typename G, int D>
+__global__ void __launch_bounds__(256)
+chunk_join_kernel(const ChunkParams p)
+{
+    constexpr int N = D / 32;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    wait_prior_grid();
+    const Split sp = reinterpret_cast<const Split *>(p.ws)[blockIdx.x];
+    const int32_t n = sp.parts;
+    if (n == 0) return;
+    const float2 *ml = reinterpret_cast<const float2 *>(p.ws + WS_ML);
+    const float *po = reinterpret_cast<const float *>(p.ws + ws_o<G::ROWS, G::WORKERS>());
+    auto place = [&](int32_t i) { return 2 * (static_cast<int64_t>(blockIdx.x) + i) + (i == 0 ? 1 : 0); };
+    for (int32_t row = blockIdx.y * 8 + warp; row < sp.rows; row += 8 * gridDim.y) {
+        float mx = -INFINITY, sum = 0.0f;
+        for (int32_t i = lane; i < n; i += 32) mx = fmaxf(mx, ml[place(i) * G::ROWS + row].x);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        float acc[N];
+#pragma unroll
+        for (int e = 0; e < N; ++e) acc[e] = 0.0f;
+        for (int32_t i0 = 0; i0 < n; i0 += 32) {
+            float wt = 0.0f;
+            if (i0 + lane < n) {
+                const float2 x = ml[place(i0 + lane) * G::ROWS + row];
+                wt = x.x == -INFINITY ? 0.0f : exp2_approx(x.x - mx);      // a part in which the row saw nothing
+                sum = fmaf(x.y, wt, sum);
+            }
+            const int32_t k = min(32, n - i0);
+#pragma unroll 4
+            for (int32_t i = 0; i < k; ++i) {
+                const float f = __shfl_sync(0xffffffffu, wt, i);
+                const float4 *src = reinterpret_cast<const float4 *>(po + (place(i0 + i) * p.ws_rows + row) * D) + lane;
+#pragma unroll
+                for (int e = 0; e < N / 4; ++e) {
+                    const float4 x = src[32 * e];
+                    acc[4 * e] = fmaf(x.x, f, acc[4 * e]);
+                    acc[4 * e + 1] = fmaf(x.y, f, acc[4 * e + 1]);
+                    acc[4 * e + 2] = fmaf(x.z, f, acc[4 * e + 2]);
+                    acc[4 * e + 3] = fmaf(x.w, f, acc[4 * e + 3]);
+                }
+            }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+        const int32_t v = sp.v0 + row, tok = v / p.group, h = v - tok * p.group;
+        __half *out = static_cast<__half *>(p.out) +
+                      ((static_cast<int64_t>(sp.s0) + tok) * p.hq + sp.g * p.group + h) * D;
+#pragma unroll
+        for (int e = 0; e < N / 4; ++e) {
+            const __half2 a = __floats2half2_rn(acc[4 * e] * inv, acc[4 * e + 1] * inv);
+            const __half2 b = __floats2half2_rn(acc[4 * e + 2] * inv, acc[4 * e + 3] * inv);
+            uint2 u;
+            u.x = *reinterpret_cast<const uint32_t *>(&a);
+            u.y = *reinterpret_cast<const uint32_t *>(&b);
+            reinterpret_cast<uint2 *>(out)[32 * e + lane] = u;
+        }
+    }
+}
+
+}  // namespace
+}  // namespace qsa

@@ -257,5 +257,12 @@ int launch_chunk(const ChunkParams &p, const void *tk, const void *tv, int sms, 
 int32_t chunk_part_rows(int32_t rows, int32_t group);
 size_t chunk_workspace_bytes(int32_t rows, int32_t group, int32_t head_dim);
 void chunk_boxes(int32_t head_dim, int32_t page_tokens, int32_t *box_k, int32_t *box_v);
+// The kernel for few rows (units of 16 pairs); tk, tv: boxes of 128 bytes x
+// chunk_rows_box() tokens, 128-byte swizzle for both cache types.
+constexpr int32_t CHUNK_MAX_CTAS = 160;
+int launch_chunk_rows(const ChunkParams &p, const void *tk, const void *tv, int sms, bool overlap, void *stream);
+int32_t chunk_rows_part_rows(int32_t rows, int32_t group);
+size_t chunk_rows_workspace_bytes(int32_t rows, int32_t group, int32_t head_dim);
+int32_t chunk_rows_box(int32_t page_tokens);
 
 }  // namespace qsa
