@@ -896,8 +896,8 @@ int launch(const ChunkParams &p, const void *tk, const void *tv, int grid, bool 
                                  CH_SMEM, stream, false, args);
     if (rc != 0) return rc;
     void *join[] = {const_cast<ChunkParams *>(&p)};
-    const unsigned rows8 = static_cast<unsigned>(std::min(8, (p.ws_rows + 7) / 8));
-    return launch_kernel(reinterpret_cast<const void *>(&chunk_join_kernel<G, D>), dim3(grid / 2, rows8), dim3(256), 0, stream,
+    const unsigned y = static_cast<unsigned>(std::min(8, (p.ws_rows + 7) / 8));
+    return launch_kernel(reinterpret_cast<const void *>(&chunk_join_kernel<G, D>), dim3(grid / 2, y), dim3(256), 0, stream,
                          overlap, join);
 }
 

@@ -351,13 +351,20 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volati
 // --------------------------------------------------------------------- join --
 
 // Joins the parts of each split unit: block x the unit that worker x began (part
-// 0 in its second place, part i in the first place of the i-th worker after it),
-// a warp per row.  G: the geometry of the kernel that left the parts.
+// 0 in its second place, part i in the first place of the i-th worker after it).
+// A warp takes a row; with many parts (one row over a long cache) the warps of a
+// CTA share the parts of a row instead and add up through shared memory, for the
+// loads of one warp would come one after another.  G: the geometry of the kernel
+// that left the parts.
+constexpr int JOIN_WARPS = 8;
+constexpr int JOIN_PARTS = 6;                // parts that one warp takes
+
 template <typename G, int D>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(32 * JOIN_WARPS)
 chunk_join_kernel(const ChunkParams p)
 {
     constexpr int N = D / 32;
+    __shared__ float part_sum[JOIN_WARPS][D];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     wait_prior_grid();
     const Split sp = reinterpret_cast<const Split *>(p.ws)[blockIdx.x];
@@ -366,14 +373,16 @@ chunk_join_kernel(const ChunkParams p)
     const float2 *ml = reinterpret_cast<const float2 *>(p.ws + WS_ML);
     const float *po = reinterpret_cast<const float *>(p.ws + ws_o<G::ROWS, G::WORKERS>());
     auto place = [&](int32_t i) { return 2 * (static_cast<int64_t>(blockIdx.x) + i) + (i == 0 ? 1 : 0); };
-    for (int32_t row = blockIdx.y * 8 + warp; row < sp.rows; row += 8 * gridDim.y) {
+    const bool shared_row = n > JOIN_PARTS;
+    const int32_t step = shared_row ? gridDim.y : JOIN_WARPS * gridDim.y;
+    for (int32_t row = shared_row ? blockIdx.y : blockIdx.y * JOIN_WARPS + warp; row < sp.rows; row += step) {
         float mx = -INFINITY, sum = 0.0f;
         for (int32_t i = lane; i < n; i += 32) mx = fmaxf(mx, ml[place(i) * G::ROWS + row].x);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        float acc[N];
+        float4 acc[N / 4];
 #pragma unroll
-        for (int e = 0; e < N; ++e) acc[e] = 0.0f;
+        for (int e = 0; e < N / 4; ++e) acc[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         for (int32_t i0 = 0; i0 < n; i0 += 32) {
             float wt = 0.0f;
             if (i0 + lane < n) {
@@ -383,29 +392,48 @@ chunk_join_kernel(const ChunkParams p)
             }
             const int32_t k = min(32, n - i0);
 #pragma unroll 4
-            for (int32_t i = 0; i < k; ++i) {
+            for (int32_t i = shared_row ? warp : 0; i < k; i += shared_row ? JOIN_WARPS : 1) {
                 const float f = __shfl_sync(0xffffffffu, wt, i);
                 const float4 *src = reinterpret_cast<const float4 *>(po + (place(i0 + i) * p.ws_rows + row) * D) + lane;
 #pragma unroll
                 for (int e = 0; e < N / 4; ++e) {
                     const float4 x = src[32 * e];
-                    acc[4 * e] = fmaf(x.x, f, acc[4 * e]);
-                    acc[4 * e + 1] = fmaf(x.y, f, acc[4 * e + 1]);
-                    acc[4 * e + 2] = fmaf(x.z, f, acc[4 * e + 2]);
-                    acc[4 * e + 3] = fmaf(x.w, f, acc[4 * e + 3]);
+                    acc[e].x = fmaf(x.x, f, acc[e].x);
+                    acc[e].y = fmaf(x.y, f, acc[e].y);
+                    acc[e].z = fmaf(x.z, f, acc[e].z);
+                    acc[e].w = fmaf(x.w, f, acc[e].w);
                 }
             }
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (shared_row) {                    // uniform: n and the rows are the block's
+#pragma unroll
+            for (int e = 0; e < N / 4; ++e) reinterpret_cast<float4 *>(part_sum[warp])[32 * e + lane] = acc[e];
+            __syncthreads();
+            if (warp == 0) {
+#pragma unroll
+                for (int e = 0; e < N / 4; ++e)
+#pragma unroll
+                    for (int k = 1; k < JOIN_WARPS; ++k) {
+                        const float4 x = reinterpret_cast<const float4 *>(part_sum[k])[32 * e + lane];
+                        acc[e].x += x.x;
+                        acc[e].y += x.y;
+                        acc[e].z += x.z;
+                        acc[e].w += x.w;
+                    }
+            }
+            __syncthreads();
+            if (warp != 0) continue;
+        }
         const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-        const int32_t v = sp.v0 + row, tok = v / p.group, h = v - tok * p.group;
+        const int32_t v = sp.v0 + row, tok = by_group(p, v), h = v - tok * p.group;
         __half *out = static_cast<__half *>(p.out) +
                       ((static_cast<int64_t>(sp.s0) + tok) * p.hq + sp.g * p.group + h) * D;
 #pragma unroll
         for (int e = 0; e < N / 4; ++e) {
-            const __half2 a = __floats2half2_rn(acc[4 * e] * inv, acc[4 * e + 1] * inv);
-            const __half2 b = __floats2half2_rn(acc[4 * e + 2] * inv, acc[4 * e + 3] * inv);
+            const __half2 a = __floats2half2_rn(acc[e].x * inv, acc[e].y * inv);
+            const __half2 b = __floats2half2_rn(acc[e].z * inv, acc[e].w * inv);
             uint2 u;
             u.x = *reinterpret_cast<const uint32_t *>(&a);
             u.y = *reinterpret_cast<const uint32_t *>(&b);

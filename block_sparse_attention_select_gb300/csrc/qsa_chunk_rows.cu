@@ -59,7 +59,8 @@ struct RowShape {
     static constexpr uint32_t SUM = CR_ROWS * D * 4;                       // outputs added up
     // an even number of stages: a stage then belongs to one group of warps, which
     // waits for each of its phases (a parity wait must not skip one)
-    static constexpr int FIT = (227 * 1024 - 8192 - SUM) / STAGE, NS = (FIT < CR_MAX_STAGES ? FIT : CR_MAX_STAGES) & ~1;
+    static constexpr uint32_t QF = CR_ROWS * D * 2;                        // queries as A operands
+    static constexpr int FIT = (227 * 1024 - 8192 - SUM - QF) / STAGE, NS = (FIT < CR_MAX_STAGES ? FIT : CR_MAX_STAGES) & ~1;
     static constexpr int CHUNKS = D * ES / 128;                            // 128-byte chunks of a vector
     static constexpr int PD = 16 / ES;                                     // dims of a 16-byte piece
 };
@@ -73,12 +74,12 @@ struct RowCtrl {
     int32_t abort;
 };
 
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint4 &a, uint32_t b0, uint32_t b1)
 {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
 }
 
 // four codes -> two pairs of FP16
@@ -98,12 +99,7 @@ __device__ __forceinline__ uint32_t half2_mul(uint32_t a, uint32_t b)
 
 __device__ __forceinline__ uint32_t word(const uint4 &v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
-__device__ __forceinline__ uint4 lds128(uint32_t a)
-{
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-    return v;
-}
+__device__ __forceinline__ uint4 lds128(const uint8_t *a) { return *reinterpret_cast<const uint4 *>(a); }
 
 template <int D, bool Q8>
 __global__ void __launch_bounds__(CR_THREADS, 1)
@@ -115,7 +111,8 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
     static_assert(NS >= 2 && NS % 2 == 0, "ring");
     extern __shared__ __align__(1024) uint8_t smem[];
     float4 *sum = reinterpret_cast<float4 *>(smem + NS * STAGE);
-    RowCtrl &c = *reinterpret_cast<RowCtrl *>(smem + NS * STAGE + Sh::SUM);
+    uint4 *qf = reinterpret_cast<uint4 *>(smem + NS * STAGE + Sh::SUM);      // [product over D][lane]
+    RowCtrl &c = *reinterpret_cast<RowCtrl *>(smem + NS * STAGE + Sh::SUM + Sh::QF);
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     volatile int *abort = &c.abort;
     const uint64_t lim = p.wait_limit_ns;
@@ -239,37 +236,34 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
         constexpr int VI = Sh::CHUNKS;
         const int r = lane >> 2, q = lane & 3;
         const int grp = warp >> 2, sub = (warp & 3) * 16;          // stages of this parity, tokens sub .. + 15
-        const uint32_t ring = smem_u32(smem);
         const float cs = p.scale * 1.4426950408889634f;            // scores in powers of two
         uint32_t slot = 0, phase = 0, it = 0;
         bool ok = true;
         while (next_segment(c.segs, &segs, &w, lane)) {
-            // queries as A operands; rows r and r + 8 of the unit
-            uint32_t qa[KS][4];
             int32_t pos[2], first[2];
+            const uint8_t *qrow[2];                                // rows r and r + 8 of the unit
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int row = r + 8 * e;
                 const int32_t v = w.v0 + min(row, w.rows - 1), tok = by_group(p, v), h = v - tok * p.group;
                 pos[e] = w.p0 + tok;
                 first[e] = p.window > 0 ? max(0, pos[e] - p.window + 1) : 0;
-                const uint8_t *src = static_cast<const uint8_t *>(p.q) +
-                                     ((static_cast<int64_t>(w.s0) + tok) * p.q_stride + (w.g * p.group + h) * D) * 2;
-#pragma unroll
-                for (int i = 0; i < KI; ++i)
-#pragma unroll
-                    for (int j = 0; j < PD / 4; j += 2) {
-                        // dims 8 PD (i / 2) + PD (2 q + i % 2) + 4 j .. + 7
-                        uint4 x = make_uint4(0u, 0u, 0u, 0u);
-                        if (row < w.rows)
-                            x = __ldg(reinterpret_cast<const uint4 *>(src + (8 * PD * (i >> 1) + PD * (2 * q + (i & 1)) + 4 * j) * 2));
-                        uint32_t (&a)[4] = qa[i * (PD / 4) + j], (&b)[4] = qa[i * (PD / 4) + j + 1];
-                        a[e] = x.x;
-                        a[e + 2] = x.y;
-                        b[e] = x.z;
-                        b[e + 2] = x.w;
-                    }
+                qrow[e] = row >= w.rows ? nullptr : static_cast<const uint8_t *>(p.q) +
+                          ((static_cast<int64_t>(w.s0) + tok) * p.q_stride + (w.g * p.group + h) * D) * 2;
             }
+            // The queries as A operands, in shared memory (in registers they
+            // spilled: 294 us on the 64-request E4M3 step).  Product k of
+            // piece i takes dims 8 PD (i / 2) + PD (2 q + i % 2) + 4 k .. + 3.
+            for (int k = warp; k < KS; k += CR_COMP) {
+                const int i = k / (PD / 4), j = k % (PD / 4);
+                const int dim = 8 * PD * (i >> 1) + PD * (2 * q + (i & 1)) + 4 * j;
+                uint2 x[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    x[e] = qrow[e] ? __ldg(reinterpret_cast<const uint2 *>(qrow[e] + dim * 2)) : make_uint2(0u, 0u);
+                qf[k * 32 + lane] = make_uint4(x[0].x, x[1].x, x[0].y, x[1].y);
+            }
+            named_barrier(BAR_COMP, 32 * CR_COMP);
             float o[VI][PD][4];
 #pragma unroll
             for (int i = 0; i < VI; ++i)
@@ -289,7 +283,7 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
                 ok = warp_wait(&c.full[sl], ph, abort, lim);
                 const int32_t tok0 = (w.j0 + j) * CR_TILE + sub;
                 if (ok && tok0 <= w.hi_tok && tok0 + 15 >= w.lo_tok) {
-                    const uint32_t ka = ring + sl * STAGE, va = ka + HALF;
+                    const uint8_t *ka = smem + sl * STAGE, *va = ka + HALF;
                     // ---- scores of tokens sub + 8 n + 2 q + {0, 1}
                     float s[2][4] = {};
 #pragma unroll
@@ -300,7 +294,8 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
                             x[n] = lds128(ka + (i >> 1) * (CR_TILE * 128) + (sub + 8 * n + r) * 128 +
                                           (((2 * q + (i & 1)) ^ r) << 4));
 #pragma unroll
-                        for (int k = 0; k < PD / 4; ++k)
+                        for (int k = 0; k < PD / 4; ++k) {
+                            const uint4 a = qf[(i * (PD / 4) + k) * 32 + lane];
 #pragma unroll
                             for (int n = 0; n < 2; ++n) {
                                 uint32_t b0, b1;
@@ -310,8 +305,9 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
                                     b0 = word(x[n], 2 * (k & 1));
                                     b1 = word(x[n], 2 * (k & 1) + 1);
                                 }
-                                mma16816(s[n], qa[i * (PD / 4) + k], b0, b1);
+                                mma16816(s[n], a, b0, b1);
                             }
+                        }
                     }
                     // ---- softmax, in powers of two
                     const bool edge = tok0 < w.lo_tok || tok0 + 15 > w.hi_tok;      // some token that no row attends
@@ -355,7 +351,7 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
                                 o[i][d][3] *= a1;
                             }
                     }
-                    uint32_t pa[4];
+                    uint32_t pw[4];
 #pragma unroll
                     for (int n = 0; n < 2; ++n)
 #pragma unroll
@@ -364,8 +360,9 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
                             const float x = exp2_approx(s[n][2 * e] - mm), y = exp2_approx(s[n][2 * e + 1] - mm);
                             l[e] += x + y;
                             const __half2 hh = __floats2half2_rn(x, y);
-                            pa[2 * n + e] = *reinterpret_cast<const uint32_t *>(&hh);
+                            pw[2 * n + e] = *reinterpret_cast<const uint32_t *>(&hh);
                         }
+                    const uint4 pa = make_uint4(pw[0], pw[1], pw[2], pw[3]);
                     // ---- O += P . V; tokens 2 q, 2 q + 1 (x), 2 q + 8, 2 q + 9 (y)
                     uint32_t fx = 0, fy = 0;
                     if (Q8) {
@@ -493,7 +490,7 @@ template <int D, bool Q8>
 int launch(const ChunkParams &p, const void *tk, const void *tv, int grid, bool overlap, cudaStream_t stream)
 {
     using Sh = RowShape<D, Q8>;
-    constexpr size_t SMEM = Sh::NS * Sh::STAGE + Sh::SUM + sizeof(RowCtrl);
+    constexpr size_t SMEM = Sh::NS * Sh::STAGE + Sh::SUM + Sh::QF + sizeof(RowCtrl);
     static_assert(SMEM <= 232448, "shared memory budget");
     static std::mutex mu;
     static bool done[64] = {};
@@ -514,8 +511,8 @@ int launch(const ChunkParams &p, const void *tk, const void *tv, int grid, bool 
                                  stream, false, args);
     if (rc != 0) return rc;
     void *join[] = {const_cast<ChunkParams *>(&p)};
-    const unsigned rows8 = static_cast<unsigned>((p.ws_rows + 7) / 8);
-    return launch_kernel(reinterpret_cast<const void *>(&chunk_join_kernel<G, D>), dim3(grid, rows8), dim3(256), 0, stream,
+    const unsigned y = static_cast<unsigned>(p.ws_rows);
+    return launch_kernel(reinterpret_cast<const void *>(&chunk_join_kernel<G, D>), dim3(grid, y), dim3(256), 0, stream,
                          overlap, join);
 }
 
