@@ -38,11 +38,10 @@ namespace {
 constexpr int CR_ROWS = 16;
 constexpr int CR_TILE = 64;                  // tokens of a stage
 constexpr int CR_COMP = 8;                   // computing warps
-constexpr int CR_LOAD = 8, CR_SCHED = 9;
+constexpr int CR_LOAD = 8, CR_SCHED = 9, CR_SCALE = 10;   // CR_SCALE: K's scales, the next warp V's (E4M3)
 constexpr int CR_WARPS = 12;
 constexpr int CR_THREADS = 32 * CR_WARPS;
 constexpr int CR_MAX_STAGES = 8;
-constexpr int CR_ROLES = CR_COMP + 1;
 constexpr int BAR_COMP = 1;
 constexpr float CR_RESCALE = 8.0f;           // log2 of the growth of a maximum that rescales
 
@@ -119,12 +118,12 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
 
     if (t == 0) {
         for (int i = 0; i < NS; ++i) {
-            mbar_init(&c.full[i], 1);
+            mbar_init(&c.full[i], Q8 ? 3 : 1);                 // the copies, and the two scale warps
             mbar_init(&c.empty[i], CR_COMP / 2);
         }
         for (int i = 0; i < SEGS; ++i) {
             mbar_init(&c.segs.full[i], 1);
-            mbar_init(&c.segs.empty[i], CR_ROLES);
+            mbar_init(&c.segs.empty[i], CR_COMP + (Q8 ? 3 : 1));
         }
         c.abort = 0;
         fence_barrier_init();
@@ -151,8 +150,8 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
             while (next_segment(c.segs, &segs, &w, lane)) {
                 if (!ok) continue;
                 const int32_t *bt = p.kv.block_table + static_cast<int64_t>(w.b) * p.kv.max_pages;
-                // a lane looks up tokens lane and lane + 32 of each stage: the cache
-                // row two stages ahead, the scales one stage ahead
+                // a lane looks up the cache rows of tokens lane and lane + 32, two
+                // stages ahead
                 const int32_t nowhere = p.kv.num_pages << p.kv.page_shift;       // past the cache: reads zeros
                 auto row_of = [&](int32_t j, int k) -> int32_t {
                     const int32_t tok = (w.j0 + j) * CR_TILE + lane + 32 * k;
@@ -163,34 +162,17 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
                     record_error(p.kv.status, ST_BAD_PAGE);
                     return nowhere;
                 };
-                auto byte_of = [&](const uint8_t *scale, int32_t row) -> uint32_t {
-                    return row < nowhere ? __ldg(scale + static_cast<int64_t>(row) * p.kv.hkv + w.g) : 127u;
-                };
                 int32_t row[2], row1[2];
-                uint32_t ks[2] = {0, 0}, vs[2] = {0, 0};
-#pragma unroll
-                for (int k = 0; k < 2; ++k) row[k] = row_of(0, k);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
+                    row[k] = row_of(0, k);
                     row1[k] = row_of(1, k);
-                    if (Q8) {
-                        ks[k] = byte_of(p.kv.k_scale, row[k]);
-                        vs[k] = byte_of(p.kv.v_scale, row[k]);
-                    }
                 }
                 for (int32_t j = 0; j < w.n; ++j) {
                     if (!warp_wait(&c.empty[slot], phase ^ 1u, abort, lim)) {
                         ok = false;
                         break;
                     }
-                    if (Q8) {
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            c.scale[slot][0][lane + 32 * k] = __uint_as_float(max(112u, min(135u, ks[k])) << 23);
-                            c.scale[slot][1][lane + 32 * k] = __uint_as_float(max(112u, min(135u, vs[k])) << 23);
-                        }
-                    }
-                    __syncwarp();
                     if (lane == 0) mbar_arrive_expect_tx(&c.full[slot], STAGE);
                     __syncwarp();
                     uint8_t *dst = smem + slot * STAGE;
@@ -214,10 +196,6 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         row[k] = row1[k];
-                        if (Q8) {
-                            ks[k] = byte_of(p.kv.k_scale, row[k]);
-                            vs[k] = byte_of(p.kv.v_scale, row[k]);
-                        }
                         row1[k] = row_of(j + 2, k);
                     }
                 }
@@ -227,6 +205,71 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
                 for (int i = 0; i < NS; ++i)
                     if (used & (1u << i)) mbar_wait_bounded(&c.full[i], (last >> i) & 1u, lim);
             __syncwarp();
+        } else if (Q8) {
+            // ---------------------------------------------------------- scales
+            // Bytes that no one else reads come from HBM: four stages' loads go
+            // out together, while the four before are written (one stage ahead,
+            // each stage waited for a memory latency: 217 us on the 64-request
+            // step).
+            const uint8_t *scale = warp == CR_SCALE ? p.kv.k_scale : p.kv.v_scale;
+            const int which = warp - CR_SCALE;
+            uint32_t slot = 0, phase = 0;
+            bool ok = true;
+            while (next_segment(c.segs, &segs, &w, lane)) {
+                if (!ok) continue;
+                const int32_t *bt = p.kv.block_table + static_cast<int64_t>(w.b) * p.kv.max_pages;
+                auto page_of = [&](int32_t j, int k) -> int32_t {
+                    const int32_t tok = (w.j0 + j) * CR_TILE + lane + 32 * k;
+                    return j < w.n && tok >= w.lo_tok && tok <= w.hi_tok ? __ldg(bt + (tok >> p.kv.page_shift)) : -1;
+                };
+                auto byte_of = [&](int32_t j, int k, int32_t page) -> uint32_t {
+                    if (page < 0 || page >= p.kv.num_pages) return 127u;
+                    const int32_t tok = (w.j0 + j) * CR_TILE + lane + 32 * k;
+                    return __ldg(scale + ((static_cast<int64_t>(page) << p.kv.page_shift) + (tok & (p.kv.page_tokens - 1))) * p.kv.hkv + w.g);
+                };
+                int32_t page[4][2];
+                uint32_t byte[4][2];
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) page[u][k] = page_of(u, k);
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        byte[u][k] = byte_of(u, k, page[u][k]);
+                        page[u][k] = page_of(u + 4, k);
+                    }
+                for (int32_t j = 0; ok && j < w.n; j += 4) {
+                    uint32_t next[4][2];
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            next[u][k] = byte_of(j + 4 + u, k, page[u][k]);
+                            page[u][k] = page_of(j + 8 + u, k);
+                        }
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        if (!ok || j + u >= w.n) break;
+                        ok = warp_wait(&c.empty[slot], phase ^ 1u, abort, lim);
+                        if (!ok) break;
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+                            c.scale[slot][which][lane + 32 * k] = __uint_as_float(max(112u, min(135u, byte[u][k])) << 23);
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&c.full[slot]);
+                        if (++slot == NS) {
+                            slot = 0;
+                            phase ^= 1u;
+                        }
+                    }
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) byte[u][k] = next[u][k];
+                }
+            }
         }
     } else {
         // -------------------------------------------------------------- compute
