@@ -55,7 +55,7 @@ template <int D, bool Q8>
 struct RowShape {
     static constexpr int ES = Q8 ? 1 : 2;
     static constexpr uint32_t HALF = CR_TILE * D * ES, STAGE = 2 * HALF;   // K, then V
-    static constexpr uint32_t SUM = CR_ROWS * D * 4;                       // outputs added up
+    static constexpr uint32_t SUM = CR_ROWS * D * 4;                       // an eighth of the eight warps' outputs
     // an even number of stages: a stage then belongs to one group of warps, which
     // waits for each of its phases (a parity wait must not skip one)
     static constexpr uint32_t QF = CR_ROWS * D * 2;                        // queries as A operands
@@ -447,7 +447,7 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
                 __syncwarp();
                 if (ok && lane == 0) mbar_arrive(&c.empty[sl]);
             }
-            // ---- the eight warps' sums: at the largest maximum, added up in order
+            // ---- the eight warps' sums, at the largest maximum
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
@@ -464,35 +464,45 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
                 f[e] = m[e] == -INFINITY ? 0.0f : exp2_approx(m[e] - mt[e]);
                 if (q == 0) c.l[warp][r + 8 * e] = l[e] * f[e];
             }
-            for (int k = 0; k < CR_COMP; ++k) {
-                if (warp == k) {
+            // Eight steps; in each every warp lays down PD / 8 dims of each chunk, and
+            // thread t adds up the eight warps' values of place t: chunk i, row
+            // r' + 8 (e / 2), dims 8 PD i + PD (2 q' + e % 2) .., where t = (i, lane', e).
+            constexpr int DS = PD / 8, OWN = (VI * 128 + 255) / 256;    // dims per step, places per thread
+            float x[OWN][PD];
 #pragma unroll
-                    for (int i = 0; i < VI; ++i)
+            for (int st = 0; st < 8; ++st) {
 #pragma unroll
-                        for (int d = 0; d < PD; ++d) {
-                            float4 x = k == 0 ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : sum[(i * PD + d) * 32 + lane];
-                            x.x = fmaf(o[i][d][0], f[0], x.x);
-                            x.y = fmaf(o[i][d][1], f[0], x.y);
-                            x.z = fmaf(o[i][d][2], f[1], x.z);
-                            x.w = fmaf(o[i][d][3], f[1], x.w);
-                            sum[(i * PD + d) * 32 + lane] = x;
+                for (int i = 0; i < VI; ++i)
+#pragma unroll
+                    for (int d = 0; d < DS; ++d) {
+                        const float (&v)[4] = o[i][st * DS + d];
+                        sum[((warp * DS + d) * VI + i) * 32 + lane] = make_float4(v[0] * f[0], v[1] * f[0], v[2] * f[1], v[3] * f[1]);
+                    }
+                named_barrier(BAR_COMP, 32 * CR_COMP);
+                const float *src = reinterpret_cast<const float *>(sum);
+#pragma unroll
+                for (int k = 0; k < OWN; ++k)
+#pragma unroll
+                    for (int d = 0; d < DS; ++d) {
+                        float v = 0.0f;
+                        if (t + 256 * k < VI * 128) {
+#pragma unroll
+                            for (int j = 0; j < CR_COMP; ++j) v += src[(j * DS + d) * VI * 128 + t + 256 * k];
                         }
-                }
+                        x[k][st * DS + d] = v;
+                    }
                 named_barrier(BAR_COMP, 32 * CR_COMP);
             }
-            // piece (i, e): row r + 8 (e / 2), dims 8 PD i + PD (2 q + e % 2) ..
-            for (int pc = warp; ok && pc < 4 * VI; pc += CR_COMP) {
-                const int i = pc >> 2, e = pc & 3, row = r + 8 * (e >> 1), dim = 8 * PD * i + PD * (2 * q + (e & 1));
-                if (row >= w.rows) continue;
+#pragma unroll
+            for (int k = 0; k < OWN; ++k) {
+                const int at = t + 256 * k, i = at >> 7, ln = (at >> 2) & 31, e = at & 3;
+                const int row = (ln >> 2) + 8 * (e >> 1), dim = 8 * PD * i + PD * (2 * (ln & 3) + (e & 1));
+                if (!ok || at >= VI * 128 || row >= w.rows) continue;
                 float lt = 0.0f;
 #pragma unroll
-                for (int k = 0; k < CR_COMP; ++k) lt += c.l[k][row];
-                const float inv = w.place < 0 ? (lt > 0.0f ? 1.0f / lt : 0.0f) : 1.0f;
-                float x[PD];
-                const float *src = reinterpret_cast<const float *>(sum + (i * PD) * 32 + lane) + e;
-#pragma unroll
-                for (int d = 0; d < PD; ++d) x[d] = src[d * 128] * inv;
+                for (int j = 0; j < CR_COMP; ++j) lt += c.l[j][row];
                 if (w.place < 0) {
+                    const float inv = lt > 0.0f ? 1.0f / lt : 0.0f;
                     const int32_t v = w.v0 + row, tok = by_group(p, v), h = v - tok * p.group;
                     __half *out = static_cast<__half *>(p.out) +
                                   ((static_cast<int64_t>(w.s0) + tok) * p.hq + w.g * p.group + h) * D + dim;
@@ -500,9 +510,9 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
                     for (int d = 0; d < PD; d += 8) {
                         uint32_t u[4];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const __half2 hh = __floats2half2_rn(x[d + 2 * k], x[d + 2 * k + 1]);
-                            u[k] = *reinterpret_cast<const uint32_t *>(&hh);
+                        for (int j = 0; j < 4; ++j) {
+                            const __half2 hh = __floats2half2_rn(x[k][d + 2 * j] * inv, x[k][d + 2 * j + 1] * inv);
+                            u[j] = *reinterpret_cast<const uint32_t *>(&hh);
                         }
                         *reinterpret_cast<uint4 *>(out + d) = make_uint4(u[0], u[1], u[2], u[3]);
                     }
@@ -511,11 +521,11 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
                                  (static_cast<int64_t>(w.place) * p.ws_rows + row) * D + dim;
 #pragma unroll
                     for (int d = 0; d < PD; d += 4)
-                        *reinterpret_cast<float4 *>(out + d) = make_float4(x[d], x[d + 1], x[d + 2], x[d + 3]);
-                    if (i == 0 && q == 0 && (e & 1) == 0) {
+                        *reinterpret_cast<float4 *>(out + d) = make_float4(x[k][d], x[k][d + 1], x[k][d + 2], x[k][d + 3]);
+                    if (dim == 0) {
                         float ma = c.m[0][row];
 #pragma unroll
-                        for (int k = 1; k < CR_COMP; ++k) ma = fmaxf(ma, c.m[k][row]);
+                        for (int j = 1; j < CR_COMP; ++j) ma = fmaxf(ma, c.m[j][row]);
                         *reinterpret_cast<float2 *>(p.ws + WS_ML + (static_cast<int64_t>(w.place) * CR_ROWS + row) * 8) =
                             make_float2(ma, lt);
                     }

@@ -12,9 +12,11 @@
 //
 // Both are bound by memory: each vector is read once and written once.  A
 // vector belongs to head_dim / 8 lanes, 16 bytes of FP16 in each; the lanes
-// reduce the maximum by shuffles.  A CTA takes a few consecutive rows: its
-// warps first look up the rows' cache lines, then every thread issues its loads
-// (KV_BATCH vectors of one row set) before it uses the first.
+// reduce the maximum by shuffles.  A warp takes up to 16 consecutive rows: its
+// lanes look up one row's cache line each (request, page), then the warp walks
+// through the rows' vectors, KV_BATCH of them in flight.  (With the lookups by a
+// CTA for 8 rows at a time, each CTA waited for three memory latencies to move
+// 12 KB: 122 us to read a 184,320-token E4M3 context back, 4.65 TB/s.)
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
@@ -28,35 +30,28 @@ namespace qsa {
 namespace {
 
 constexpr int KV_THREADS = 256;
-constexpr int KV_BATCH = 4;        // vectors in flight per thread
-constexpr int KV_MAX_ROWS = 32;    // rows per CTA
+constexpr int KV_BATCH = 8;        // vectors in flight per thread
+constexpr int KV_MAX_ROWS = 16;    // rows per warp
 
-// Cache line (page * page_tokens + slot) of each of the CTA's rows: -1 no
+// Cache line (page * page_tokens + slot) of `row`, a row per lane: -1 no
 // request or skipped, -2 a page outside the cache.
-__device__ __forceinline__ void find_lines(const KvParams &p, int32_t row0, int32_t rows_per_cta, int32_t *line)
+__device__ __forceinline__ int32_t find_line(const KvParams &p, int32_t row)
 {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int32_t i = warp; i < rows_per_cta; i += KV_THREADS / 32) {
-        const int32_t row = row0 + i;
-        int32_t l = -1;
-        const int32_t b = row < p.rows ? find_request(p, row, lane) : -1;
-        if (b >= 0) {
-            bool bad;
-            const Seq s = seq_of(p, b, &bad);
-            if (row >= s.s0 && row - s.s0 < s.n) {
-                const int32_t pos = s.p0 + (row - s.s0);
-                const int32_t page = __ldg(p.block_table + static_cast<int64_t>(b) * p.max_pages + (pos >> p.page_shift));
-                if (page >= 0 && page < p.num_pages) {
-                    l = (page << p.page_shift) + (pos & (p.page_tokens - 1));
-                } else {
-                    l = -2;
-                    if (lane == 0) record_error(p.status, ST_BAD_PAGE);
-                }
-            }
-        }
-        if (lane == 0) line[i] = l;
+    // the last request that starts at or before the row
+    int32_t lo = 0, hi = p.n_reqs;
+    while (hi - lo > 1) {
+        const int32_t mid = (lo + hi) >> 1;
+        if (__ldg(p.seq_start + mid) <= row) lo = mid;
+        else hi = mid;
     }
-    __syncthreads();
+    bool bad;
+    const Seq s = seq_of(p, lo, &bad);
+    if (row < s.s0 || row - s.s0 >= s.n) return -1;
+    const int32_t pos = s.p0 + (row - s.s0);
+    const int32_t page = __ldg(p.block_table + static_cast<int64_t>(lo) * p.max_pages + (pos >> p.page_shift));
+    if (page >= 0 && page < p.num_pages) return (page << p.page_shift) + (pos & (p.page_tokens - 1));
+    record_error(p.status, ST_BAD_PAGE);
+    return -2;
 }
 
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d)
@@ -86,22 +81,26 @@ __device__ __forceinline__ int scale_exponent(float a)
 
 // LOAD false: rows k, v -> cache; true: cache -> rows.
 template <int D, bool E4M3, bool LOAD>
-__global__ void __launch_bounds__(KV_THREADS)
-kv_kernel(const KvParams p, uint8_t *kr, uint8_t *vr, int64_t k_stride, int64_t v_stride, int32_t rows_per_cta)
+__global__ void __launch_bounds__(KV_THREADS, 3)
+kv_kernel(const KvParams p, uint8_t *kr, uint8_t *vr, int64_t k_stride, int64_t v_stride, int32_t rows_per_warp)
 {
     constexpr int LPV = D / 8;                     // lanes per vector
-    constexpr int VPP = KV_THREADS / LPV;           // vectors per pass of the CTA
+    constexpr int VPP = 32 / LPV;                   // vectors per pass of the warp
     constexpr int ES = E4M3 ? 1 : 2;                // bytes of a cache element
-    __shared__ int32_t line[KV_MAX_ROWS];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     wait_prior_grid();
     if (blockIdx.x == 0) flag_bad_requests(p);
-    const int32_t row0 = blockIdx.x * rows_per_cta;
-    find_lines(p, row0, rows_per_cta, line);
+    const int64_t first = (static_cast<int64_t>(blockIdx.x) * (KV_THREADS / 32) + warp) * rows_per_warp;
+    if (first >= p.rows) return;
+    const int32_t row0 = static_cast<int32_t>(first), n_rows = min(rows_per_warp, p.rows - row0);
+    const int32_t mine = lane < n_rows ? find_line(p, row0 + lane) : -1;
 
-    const int sub = threadIdx.x / LPV, l = threadIdx.x % LPV;
+    const int sub = lane / LPV, l = lane % LPV;
     const int32_t per_row = 2 * p.hkv;              // vectors of a row: K heads, then V heads
-    const int32_t n = rows_per_cta * per_row;
-    for (int32_t base = sub; base < n + sub; base += VPP * KV_BATCH) {     // the same trips for every thread
+    const int32_t n = n_rows * per_row;
+    // the lane's next vector as row and head, advanced without divisions
+    int32_t r = sub / per_row, hv = sub - r * per_row;
+    for (int32_t base = 0; base < n; base += VPP * KV_BATCH) {
         uint4 x[KV_BATCH];
         int64_t vec[KV_BATCH];                      // (line, head) vector of the cache, negative: none
         uint8_t *row[KV_BATCH];                     // this lane's 16 bytes of the row array
@@ -109,13 +108,11 @@ kv_kernel(const KvParams p, uint8_t *kr, uint8_t *vr, int64_t k_stride, int64_t 
         bool is_v[KV_BATCH];
 #pragma unroll
         for (int j = 0; j < KV_BATCH; ++j) {
-            const int32_t i = base + j * VPP;
             vec[j] = -1;
             x[j] = make_uint4(0u, 0u, 0u, 0u);
             sc[j] = 0;
-            if (i < n) {
-                const int32_t r = i / per_row, hv = i - r * per_row;
-                const int32_t ln = line[r];
+            const int32_t ln = __shfl_sync(0xffffffffu, mine, r & 31);
+            if (r < n_rows) {
                 is_v[j] = hv >= p.hkv;
                 const int32_t h = is_v[j] ? hv - p.hkv : hv;
                 row[j] = (is_v[j] ? vr + (static_cast<int64_t>(row0) + r) * v_stride * 2
@@ -134,6 +131,11 @@ kv_kernel(const KvParams p, uint8_t *kr, uint8_t *vr, int64_t k_stride, int64_t 
                         x[j] = *reinterpret_cast<const uint4 *>(src);
                     }
                 }
+            }
+            hv += VPP;
+            while (hv >= per_row) {
+                hv -= per_row;
+                ++r;
             }
         }
 #pragma unroll
@@ -192,15 +194,14 @@ kv_kernel(const KvParams p, uint8_t *kr, uint8_t *vr, int64_t k_stride, int64_t 
 template <bool LOAD>
 int launch(const KvParams &p, void *k, int64_t k_stride, void *v, int64_t v_stride, int sms, void *stream)
 {
-    // enough rows to fill the batch of loads once, but no fewer CTAs than SMs
-    const int vectors = KV_THREADS / (p.head_dim / 8) * KV_BATCH;
-    int rows_per_cta = std::max(1, std::min(KV_MAX_ROWS, vectors / (2 * p.hkv)));
-    rows_per_cta = std::max(1, std::min(rows_per_cta, p.rows / sms));
-    const dim3 grid((p.rows + rows_per_cta - 1) / rows_per_cta);
+    // 16 rows per warp where that still gives every SM two CTAs, fewer below
+    constexpr int WARPS = KV_THREADS / 32;
+    const int rows_per_warp = std::max(1, std::min(KV_MAX_ROWS, p.rows / (2 * sms * WARPS)));
+    const dim3 grid((p.rows + rows_per_warp * WARPS - 1) / (rows_per_warp * WARPS));
     KvParams pp = p;
     uint8_t *kr = static_cast<uint8_t *>(k), *vr = static_cast<uint8_t *>(v);
-    int32_t rpc = rows_per_cta;
-    void *args[] = {&pp, &kr, &vr, &k_stride, &v_stride, &rpc};
+    int32_t rpw = rows_per_warp;
+    void *args[] = {&pp, &kr, &vr, &k_stride, &v_stride, &rpw};
     const void *f;
     if (p.head_dim == 128)
         f = p.e4m3 ? reinterpret_cast<const void *>(&kv_kernel<128, true, LOAD>)
