@@ -264,6 +264,57 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b)
     return d;
 }
 
+// A slot of loaded codes as the FP16 tile that the products read, by 128
+// threads: 16 codes at a time, times the token's scale; tokens outside a .. z - 1
+// become zeros.  Codes lie in rows of 128 bytes (V of a 128-wide head: 64), one
+// token's 128 (64) dims; a thread keeps its place in the row and steps over rows,
+// so that all its addresses are one base and constants.
+template <int D, bool V>
+__device__ __forceinline__ void codes_to_half(const uint8_t *src, uint8_t *dst, const uint16_t *scale, int ht, int a, int z)
+{
+    constexpr int SH = V && D == 128 ? 2 : 3;                 // log2 of a row's 16-code pieces
+    constexpr int TOKS = V ? CH_TILE : 64, STEP = 128 >> SH;  // tokens of the slot, rows per pass
+    constexpr int N = 128 * D / 2 / 16 / 128;                 // pieces per thread
+    const int pc = ht & ((1 << SH) - 1), r0 = ht >> SH;
+    const uint8_t *in = src + ht * 16;
+    // dims 16 pc .. of the row: chunk pc / 4, pieces 2 (pc % 4) and + 1; lanes of
+    // the upper four pieces store the odd one first, which spreads a row's eight
+    // stores over all banks
+    const uint32_t first = pc >> 2, p0 = 2 * (pc & 3) + first;
+    uint8_t *out = dst + first * (TOKS * 128) + r0 * 128;
+    const uint32_t o0 = (p0 ^ (r0 & 7)) << 4, o1 = ((p0 ^ 1u) ^ (r0 & 7)) << 4;
+    const bool cut = a > 0 || z < TOKS;
+#pragma unroll
+    for (int i0 = 0; i0 < N; i0 += 4) {
+        uint4 x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const uint4 *>(in + (i0 + i) * (16 * 128));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int blk = (STEP * (i0 + i)) / TOKS, tk = (STEP * (i0 + i)) % TOKS;     // 128 dims, token - r0
+            const uint32_t sc = scale[r0 + tk] * 0x10001u;
+            const uint32_t cw[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+            uint32_t o[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
+                    "cvt.rn.f16x2.e4m3x2 %0, lo;\n\tcvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+                    : "=r"(o[2 * k]), "=r"(o[2 * k + 1])
+                    : "r"(cw[k]));
+#pragma unroll
+            for (int k = 0; k < 8; ++k) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(o[k]) : "r"(sc));
+            if (cut && (r0 + tk < a || r0 + tk >= z)) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) o[k] = 0u;
+            }
+            const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
+            uint8_t *at = out + (2 * blk * TOKS + tk) * 128;
+            *reinterpret_cast<uint4 *>(at + o0) = first ? hi : lo;
+            *reinterpret_cast<uint4 *>(at + o1) = first ? lo : hi;
+        }
+    }
+}
+
 // ------------------------------------------------------------------- kernel --
 
 template <int D, bool Q8>
@@ -638,45 +689,10 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                     if (ok) ok = warp_wait(&c.empty[slot], phase ^ 1u, abort, lim);
                     named_barrier(BAR_HELP, 32 * CH_HELPERS);          // the scales are in
                     if (ok) {
-                        constexpr int N = RAW / 16 / (32 * CH_HELPERS); // 16-code pieces per thread
-                        // a row of codes: 128 bytes, 64 for V of a 128-wide head
-                        const int sh = v && D == 128 ? 2 : 3;           // log2 of its pieces
-                        const int pc = ht & ((1 << sh) - 1);
-                        const int toks = v ? Sh::VTOK : Sh::KTOK;
-                        const uint8_t *src = raw + rslot * RAW + ht * 16;
+                        const uint8_t *src = raw + rslot * RAW;
                         uint8_t *dst = ring + slot * SLOT;
-                        uint4 in[N];
-#pragma unroll
-                        for (int i = 0; i < N; ++i) in[i] = *reinterpret_cast<const uint4 *>(src + i * (16 * 32 * CH_HELPERS));
-#pragma unroll
-                        for (int i = 0; i < N; ++i) {
-                            const int rr = (ht >> sh) + i * ((32 * CH_HELPERS) >> sh);
-                            const int blk = rr / toks, tk2 = rr & (toks - 1);      // 128 dims, token
-                            const uint32_t sc = c.scale[par][tk2] * 0x10001u;
-                            const uint32_t cw[4] = {in[i].x, in[i].y, in[i].z, in[i].w};
-                            uint32_t o[8];
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
-                                    "cvt.rn.f16x2.e4m3x2 %0, lo;\n\tcvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
-                                    : "=r"(o[2 * k]), "=r"(o[2 * k + 1])
-                                    : "r"(cw[k]));
-#pragma unroll
-                            for (int k = 0; k < 8; ++k)
-                                asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(o[k]) : "r"(sc));
-                            if (tk2 < a || tk2 >= z) {
-#pragma unroll
-                                for (int k = 0; k < 8; ++k) o[k] = 0u;
-                            }
-                            // dims 16 pc .. of the row: chunk pc / 4, pieces 2 (pc % 4) and + 1;
-                            // lanes of the upper four pieces store the odd one first, which
-                            // spreads a row's eight stores over all banks
-                            uint8_t *ck = dst + (2 * blk + (pc >> 2)) * (toks * 128);
-                            const uint32_t p0 = 2 * (pc & 3), first = pc >> 2;
-                            const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
-                            *reinterpret_cast<uint4 *>(ck + sw128(tk2, p0 + first)) = first ? hi : lo;
-                            *reinterpret_cast<uint4 *>(ck + sw128(tk2, p0 + 1 - first)) = first ? lo : hi;
-                        }
+                        if (v) codes_to_half<D, true>(src, dst, c.scale[par], ht, a, z);
+                        else codes_to_half<D, false>(src, dst, c.scale[par], ht, 0, Sh::KTOK);
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0) {
