@@ -275,14 +275,14 @@ __device__ __forceinline__ void codes_to_half(const uint8_t *src, uint8_t *dst, 
     constexpr int SH = V && D == 128 ? 2 : 3;                 // log2 of a row's 16-code pieces
     constexpr int TOKS = V ? CH_TILE : 64, STEP = 128 >> SH;  // tokens of the slot, rows per pass
     constexpr int N = 128 * D / 2 / 16 / 128;                 // pieces per thread
-    const int pc = ht & ((1 << SH) - 1), r0 = ht >> SH;
-    const uint8_t *in = src + ht * 16;
-    // dims 16 pc .. of the row: chunk pc / 4, pieces 2 (pc % 4) and + 1; lanes of
-    // the upper four pieces store the odd one first, which spreads a row's eight
-    // stores over all banks
-    const uint32_t first = pc >> 2, p0 = 2 * (pc & 3) + first;
-    uint8_t *out = dst + first * (TOKS * 128) + r0 * 128;
-    const uint32_t o0 = (p0 ^ (r0 & 7)) << 4, o1 = ((p0 ^ 1u) ^ (r0 & 7)) << 4;
+    const int pc = ht & ((1 << SH) - 1);
+    // Dims 16 pc .. of the row go to chunk pc / 4, pieces 2 (pc % 4) and + 1.  With
+    // eight pieces to a row, lanes of the upper four take the neighbouring row:
+    // the eight stores then meet all banks.
+    const int r0 = SH == 3 ? (ht >> 3) ^ (pc >> 2) : ht >> 2;
+    const uint8_t *in = src + (r0 << (SH + 4)) + pc * 16;
+    uint8_t *out = dst + (pc >> 2) * (TOKS * 128) + r0 * 128;
+    const uint32_t p0 = 2 * (pc & 3), o0 = (p0 ^ (r0 & 7)) << 4, o1 = ((p0 + 1) ^ (r0 & 7)) << 4;
     const bool cut = a > 0 || z < TOKS;
 #pragma unroll
     for (int i0 = 0; i0 < N; i0 += 4) {
@@ -307,10 +307,9 @@ __device__ __forceinline__ void codes_to_half(const uint8_t *src, uint8_t *dst, 
 #pragma unroll
                 for (int k = 0; k < 8; ++k) o[k] = 0u;
             }
-            const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
             uint8_t *at = out + (2 * blk * TOKS + tk) * 128;
-            *reinterpret_cast<uint4 *>(at + o0) = first ? hi : lo;
-            *reinterpret_cast<uint4 *>(at + o1) = first ? lo : hi;
+            *reinterpret_cast<uint4 *>(at + o0) = make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4 *>(at + o1) = make_uint4(o[4], o[5], o[6], o[7]);
         }
     }
 }
@@ -649,44 +648,43 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                 ring0 = (ring0 + 2 * n) % NS;
             } else {
                 const int32_t *bt = p.kv.block_table + static_cast<int64_t>(w.b) * p.kv.max_pages;
-                // scale bytes of the slot's tokens, one per thread, looked up two
-                // slots ahead: first the page, then the byte
-                auto token = [&](int32_t e) -> int32_t {       // this thread's token of slot e, -1: none
+                // Scale bytes of the slot's tokens, one per thread, looked up ahead:
+                // the page two slots, the byte one.
+                struct Look {
                     bool v;
-                    int32_t tile;
-                    if (e >= 2 * n) return -1;
-                    slot_at<Sh::LEAD>(e, n, &v, &tile);
-                    const int32_t tok = (w.j0 + tile) * CH_TILE + (v ? 0 : rank * Sh::KTOK) + ht;
-                    return ht < (v ? Sh::VTOK : Sh::KTOK) && tok >= w.lo_tok && tok <= w.hi_tok ? tok : -1;
+                    int32_t tile, tok, page;                   // page: -1 none
                 };
-                auto page_of = [&](int32_t tok) -> int32_t { return tok >= 0 ? __ldg(bt + (tok >> p.kv.page_shift)) : -1; };
-                auto byte_of = [&](int32_t e, int32_t tok, int32_t page) -> uint32_t {
-                    if (page < 0 || page >= p.kv.num_pages) return 127u;
-                    bool v;
-                    int32_t tile;
-                    slot_at<Sh::LEAD>(e, n, &v, &tile);
-                    return __ldg((v ? p.kv.v_scale : p.kv.k_scale) +
-                                 ((static_cast<int64_t>(page) << p.kv.page_shift) + (tok & (p.kv.page_tokens - 1))) * p.kv.hkv + w.g);
+                auto look = [&](int32_t e) {
+                    Look k{false, 0, 0, -1};
+                    if (e < 2 * n) {
+                        slot_at<Sh::LEAD>(e, n, &k.v, &k.tile);
+                        k.tok = (w.j0 + k.tile) * CH_TILE + (k.v ? 0 : rank * Sh::KTOK) + ht;
+                        if (ht < (k.v ? Sh::VTOK : Sh::KTOK) && k.tok >= w.lo_tok && k.tok <= w.hi_tok)
+                            k.page = __ldg(bt + (k.tok >> p.kv.page_shift));
+                    }
+                    return k;
                 };
-                int32_t tok1 = token(0), page1 = page_of(tok1);
-                uint32_t byte = byte_of(0, tok1, page1);
-                tok1 = token(1);
-                page1 = page_of(tok1);
+                auto byte_of = [&](const Look &k) -> uint32_t {
+                    if (k.page < 0 || k.page >= p.kv.num_pages) return 127u;
+                    return __ldg((k.v ? p.kv.v_scale : p.kv.k_scale) +
+                                 ((static_cast<int64_t>(k.page) << p.kv.page_shift) + (k.tok & (p.kv.page_tokens - 1))) * p.kv.hkv + w.g);
+                };
+                Look now = look(0), next = look(1);
+                uint32_t byte = byte_of(now);
                 uint32_t par = 0;
                 for (int32_t e = 0; e < 2 * n; ++e) {
-                    bool v;
-                    int32_t tile;
-                    slot_at<Sh::LEAD>(e, n, &v, &tile);
-                    const int32_t tok0 = (w.j0 + tile) * CH_TILE;      // V: rows outside lo_tok .. hi_tok are cleared
-                    const int32_t a = v ? w.lo_tok - tok0 : 0, z = v ? w.hi_tok + 1 - tok0 : CH_TILE;
+                    const bool v = now.v;
+                    const int32_t tok0 = (w.j0 + now.tile) * CH_TILE;  // V: rows outside lo_tok .. hi_tok are cleared
+                    const int32_t a = w.lo_tok - tok0, z = w.hi_tok + 1 - tok0;
                     // 2^(byte - 127) as FP16 (2^-15 is subnormal)
                     const int x = max(112, min(135, static_cast<int>(byte))) - 127;
                     c.scale[par][ht] = static_cast<uint16_t>(x >= -14 ? (x + 15) << 10 : 0x200);
-                    byte = byte_of(e + 1, tok1, page1);                // in flight under the conversion
-                    tok1 = token(e + 2);
-                    page1 = page_of(tok1);
-                    if (ok) ok = warp_wait(&c.raw_full[rslot], rphase, abort, lim);
-                    if (ok) ok = warp_wait(&c.empty[slot], phase ^ 1u, abort, lim);
+                    byte = byte_of(next);                              // in flight under the conversion
+                    now = next;
+                    next = look(e + 2);
+                    if (ok)
+                        ok = __all_sync(0xffffffffu, mbar_wait(&c.raw_full[rslot], rphase, abort, lim) &&
+                                                         mbar_wait(&c.empty[slot], phase ^ 1u, abort, lim));
                     named_barrier(BAR_HELP, 32 * CH_HELPERS);          // the scales are in
                     if (ok) {
                         const uint8_t *src = raw + rslot * RAW;
