@@ -92,8 +92,32 @@ struct Shape {
     static constexpr int KTOK = 64, VTOK = CH_TILE;
     static constexpr int FIT = (RING - QBUFS * QB - (Q8 ? RAWS * RAW : 0)) / SLOT, NS = FIT < MAX_SLOTS ? FIT : MAX_SLOTS;
     static constexpr bool OWN_P = D == 128;                            // P beside S, not over it
+    // With two issuing warps, keys and values have rings of their own, so that
+    // each warp waits for every phase of its slots in turn.
+    static constexpr int NK = OWN_P ? NS / 2 : NS, NV = OWN_P ? NS - NK : 1;   // slots 0 .. NK - 1, then the values'
     static constexpr uint32_t TM_P = OWN_P ? 384 : TM_S, P_STRIDE = OWN_P ? 64 : 128;
     static constexpr int LEAD = OWN_P ? 3 : 2;                         // key tiles loaded before the first value tile
+};
+
+// A role's place in the ring of slots (one ring, or one for keys and one for
+// values), and the parity of the use it is at.
+template <typename Sh>
+struct RingPos {
+    uint32_t k = 0, kp = 0, v = 0, vp = 0;
+    __device__ __forceinline__ uint32_t slot(bool is_v) const { return Sh::OWN_P && is_v ? Sh::NK + v : k; }
+    __device__ __forceinline__ uint32_t phase(bool is_v) const { return Sh::OWN_P && is_v ? vp : kp; }
+    __device__ __forceinline__ void next(bool is_v)
+    {
+        if (Sh::OWN_P && is_v) {
+            if (++v == Sh::NV) {
+                v = 0;
+                vp ^= 1u;
+            }
+        } else if (++k == Sh::NK) {
+            k = 0;
+            kp ^= 1u;
+        }
+    }
 };
 
 struct Ctrl {
@@ -386,7 +410,6 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
     if (warp == CH_LOAD) {
         // ---------------------------------------------------------- K, V loads
         uint8_t *dst0 = Q8 ? raw : ring;
-        constexpr int NSL = Q8 ? RAWS : NS;
         constexpr uint32_t BYTES = Q8 ? RAW : SLOT;
         // elements of a box row: 128 bytes, or half a 128-wide head's 64 codes
         constexpr int CK = Q8 ? 128 : 64, CV = Q8 ? D / 2 : 64;
@@ -394,7 +417,8 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
         uint64_t *empty = Q8 ? c.raw_empty : c.empty;
         const int32_t P = p.kv.page_tokens;
         const int sh_k = __ffs(min(P, Sh::KTOK)) - 1, sh_v = __ffs(min(P, Sh::VTOK)) - 1;
-        uint32_t slot = 0, phase = 0, used = 0, last = 0;     // slots loaded at least once, their latest phases
+        RingPos<Sh> pos;
+        uint32_t rslot = 0, rphase = 0, used = 0, last = 0;   // raw slots; those loaded at least once, their latest phases
         uint32_t nb = 0;                                      // boundary tiles so far
         bool ok = true;
         // this lane's box of a slot: place in the tensor and in the slot
@@ -436,6 +460,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                 const uint32_t aa = at;
                 const bool mm = mine;
                 if (e + 1 < 2 * n) plan(e + 1);               // page lookups run under this slot's wait
+                const uint32_t slot = Q8 ? rslot : pos.slot(v), phase = Q8 ? rphase : pos.phase(v);
                 if (!warp_wait(&empty[slot], phase ^ 1u, abort, lim)) {
                     ok = false;
                     break;
@@ -455,11 +480,15 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                 }
                 __syncwarp();
                 if (mm) tma_load_2d_pair(dst0 + slot * BYTES + aa, v ? &tv : &tk, bar, xx, yy);
-                used |= 1u << slot;
-                last = (last & ~(1u << slot)) | (phase << slot);
-                if (++slot == NSL) {
-                    slot = 0;
-                    phase ^= 1u;
+                if (Q8) {
+                    used |= 1u << rslot;
+                    last = (last & ~(1u << rslot)) | (rphase << rslot);
+                    if (++rslot == RAWS) {
+                        rslot = 0;
+                        rphase ^= 1u;
+                    }
+                } else {
+                    pos.next(v);
                 }
             }
         }
@@ -467,7 +496,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
         // may be the other CTA's, so give them the time instead)
         if (!ok && lane == 0) {
             if (Q8)
-                for (int i = 0; i < NSL; ++i)
+                for (int i = 0; i < RAWS; ++i)
                     if (used & (1u << i)) mbar_wait_bounded(&c.raw_full[i], (last >> i) & 1u, lim);
             const long long t0 = clock64();
             while (clock64() - t0 < 4000000) {}
@@ -488,19 +517,15 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
         constexpr uint32_t idesc_o = umma_idesc_f16_f32(CH_ROWS, D) | (1u << 16);   // B: dims contiguous
         const uint64_t kd0 = sw128_kmajor_desc(0), vd0 = sw128_mn_desc(0, Sh::VTOK * 128);
         const uint32_t tm = uniform(tmem);
-        uint32_t slot = 0, phase = 0, it = 0, seg = 0;
+        RingPos<Sh> ringpos;
+        uint32_t it = 0, seg = 0;
         bool ok = true;
-        auto advance = [&](int32_t by) {
-            slot += by;
-            if (slot >= NS) {
-                slot -= NS;
-                phase ^= 1u;
-            }
-        };
         // S(i) = Q . K(i)^T
         auto scores = [&](uint32_t i, bool last) {
-            ok = ok && warp_wait(&c.full[slot], phase, abort, lim);
+            const uint32_t slot = ringpos.slot(false);
+            ok = ok && warp_wait(&c.full[slot], ringpos.phase(false), abort, lim);
             if (!ok) return;
+            ringpos.next(false);
             tc_fence_after();
             const uint32_t qb = Sh::QBUFS == 2 ? uniform(seg & 1u) : 0u;
             const uint64_t qd = kd0 | (uniform(smem_u32(q_s) + qb * Sh::QB) >> 4);
@@ -521,9 +546,11 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
         };
         // O (+)= P(i) . V(i)
         auto values = [&](uint32_t i, bool first) {
-            ok = ok && warp_wait(&c.full[slot], phase, abort, lim);
+            const uint32_t slot = ringpos.slot(true);
+            ok = ok && warp_wait(&c.full[slot], ringpos.phase(true), abort, lim);
             ok = ok && warp_wait(&c.p_full[i & 1u], (i >> 1) & 1u, abort, lim);
             if (!ok) return;
+            ringpos.next(true);
             tc_fence_after();
             const uint64_t vd = vd0 | (uniform(ring_a + slot * SLOT) >> 4);
             const uint32_t pa = tm + Sh::TM_P + uniform(i & 1u) * Sh::P_STRIDE;
@@ -539,39 +566,25 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
         };
         while (next_segment()) {
             if (!ok || !(do_s || do_o)) continue;
-            const int32_t n = w.n, lead = min(Sh::LEAD, n);
+            const int32_t n = w.n;
             if (do_s) ok = warp_wait(&c.q_full[Sh::QBUFS == 2 ? seg & 1u : 0u], (Sh::QBUFS == 2 ? seg >> 1 : seg) & 1u, abort, lim);
             if constexpr (Sh::OWN_P) {
-                // this warp's slots of the segment's 2 n: where they are is given by slot_at
-                int32_t at = 0;
                 for (int32_t j = 0; ok && j < n; ++j) {
-                    const int32_t e = do_s ? (j < lead ? j : 2 * j - lead + 1) : slot_of_v<Sh::LEAD>(j, n);
-                    advance(e - at);
-                    at = e;
                     const uint32_t i = it + j;
                     if (do_s) {
-                        // the scores two tiles before are in registers (the first two tiles of a segment: those of the one before)
+                        // the scores two tiles before are in registers
                         if (i > 1) ok = warp_wait(&c.s_free[i & 1u], ((i - 2) >> 1) & 1u, abort, lim);
                         scores(i, j == n - 1);
                     } else {
                         values(i, j == 0);
                     }
                 }
-                advance(2 * n - at);
             } else {
                 scores(it, n == 1);
-                advance(1);
-                if (n > 1) {
-                    scores(it + 1, n == 2);
-                    advance(1);
-                }
+                if (n > 1) scores(it + 1, n == 2);
                 for (int32_t j = 0; ok && j < n; ++j) {
                     values(it + j, j == 0);
-                    advance(1);
-                    if (j + 2 < n) {
-                        scores(it + j + 2, j + 3 == n);
-                        advance(1);
-                    }
+                    if (j + 2 < n) scores(it + j + 2, j + 3 == n);
                 }
             }
             it += n;
@@ -589,7 +602,8 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
         asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         // --------------------- queries, cut value tiles, E4M3 codes to FP16 tiles
         const int ht = t - CH_HELP * 32;                      // 0 .. 127
-        uint32_t seg = 0, slot = 0, phase = 0, rslot = 0, rphase = 0, ring0 = 0, nb = 0;
+        RingPos<Sh> pos;
+        uint32_t seg = 0, rslot = 0, rphase = 0, ring0 = 0, nb = 0;         // ring0: the segment's first slot (OWN_P: value slot)
         bool ok = true;                                       // false: keep to the barriers, do nothing
         while (next_segment()) {
             const int32_t n = w.n;
@@ -629,7 +643,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                     if ((k == 1 && n == 1) || !w.cut(tile, CH_TILE)) continue;
                     if (ok) ok = warp_wait(&c.bnd[nb & 7u], (nb >> 3) & 1u, abort, lim);
                     ++nb;
-                    const uint32_t vs = (ring0 + slot_of_v<Sh::LEAD>(tile, n)) % NS;
+                    const uint32_t vs = Sh::OWN_P ? Sh::NK + (ring0 + tile) % Sh::NV : (ring0 + slot_of_v<Sh::LEAD>(tile, n)) % NS;
                     if (ok) {
                         uint8_t *v = ring + vs * SLOT;
                         const int32_t a = w.lo_tok - (w.j0 + tile) * CH_TILE, z = w.hi_tok + 1 - (w.j0 + tile) * CH_TILE;
@@ -645,7 +659,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                     named_barrier(BAR_HELP, 32 * CH_HELPERS);
                     if (ok && ht == 0) cluster_arrive(of_first(&c.full[vs]));
                 }
-                ring0 = (ring0 + 2 * n) % NS;
+                ring0 = Sh::OWN_P ? (ring0 + n) % Sh::NV : (ring0 + 2 * n) % NS;
             } else {
                 const int32_t *bt = p.kv.block_table + static_cast<int64_t>(w.b) * p.kv.max_pages;
                 // Scale bytes of the slot's tokens, one per thread, looked up ahead:
@@ -682,9 +696,10 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                     byte = byte_of(next);                              // in flight under the conversion
                     now = next;
                     next = look(e + 2);
+                    const uint32_t slot = pos.slot(v);
                     if (ok)
                         ok = __all_sync(0xffffffffu, mbar_wait(&c.raw_full[rslot], rphase, abort, lim) &&
-                                                         mbar_wait(&c.empty[slot], phase ^ 1u, abort, lim));
+                                                         mbar_wait(&c.empty[slot], pos.phase(v) ^ 1u, abort, lim));
                     named_barrier(BAR_HELP, 32 * CH_HELPERS);          // the scales are in
                     if (ok) {
                         const uint8_t *src = raw + rslot * RAW;
@@ -699,10 +714,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                         }
                     }
                     par ^= 1u;
-                    if (++slot == NS) {
-                        slot = 0;
-                        phase ^= 1u;
-                    }
+                    pos.next(v);
                     if (++rslot == RAWS) {
                         rslot = 0;
                         rphase ^= 1u;
