@@ -78,7 +78,7 @@ constexpr uint32_t TM_S = 0, TM_O = 256;     // TMEM columns: two S buffers of 1
 constexpr int BAR_PAIR = 1, BAR_HELP = 5;    // named barriers: four softmax warp pairs, the helpers
 
 struct PairGeometry {
-    static constexpr int ROWS = CH_ROWS, TILE = CH_TILE, UNIT_COST = 4, THREADS = CH_THREADS, WARPS = CH_WARPS,
+    static constexpr int ROWS = CH_ROWS, TILE = CH_TILE, UNIT_COST = 4, MIN_SHARE = 1, THREADS = CH_THREADS, WARPS = CH_WARPS,
                          WORKERS = CHUNK_MAX_PAIRS;
 };
 using G = PairGeometry;

@@ -176,8 +176,9 @@ __device__ __forceinline__ void find_work(const ChunkParams &p, Share &c, FindSc
         cost *= p.kv.hkv;
     }
     int64_t at = block_scan<G>(cost, s.costs, warp, lane, &total);
-    // one place each at least, so that the workers with work are the first ones
-    const int32_t workers = static_cast<int32_t>(min(total, static_cast<int64_t>(n_workers)));
+    // MIN_SHARE each at least: a smaller share costs more in the join than it
+    // saves here; and the workers with work are the first ones
+    const int32_t workers = static_cast<int32_t>(min((total + G::MIN_SHARE - 1) / G::MIN_SHARE, static_cast<int64_t>(n_workers)));
     const int64_t w0 = me < workers ? total * me / workers : 0, w1 = me < workers ? total * (me + 1) / workers : 0;
     if (t == 0) {
         c.w0 = w0;

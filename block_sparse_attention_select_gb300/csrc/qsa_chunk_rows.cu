@@ -46,7 +46,7 @@ constexpr int BAR_COMP = 1;
 constexpr float CR_RESCALE = 8.0f;           // log2 of the growth of a maximum that rescales
 
 struct RowsGeometry {
-    static constexpr int ROWS = CR_ROWS, TILE = CR_TILE, UNIT_COST = 4, THREADS = CR_THREADS, WARPS = CR_WARPS,
+    static constexpr int ROWS = CR_ROWS, TILE = CR_TILE, UNIT_COST = 4, MIN_SHARE = 3, THREADS = CR_THREADS, WARPS = CR_WARPS,
                          WORKERS = CHUNK_MAX_CTAS;
 };
 using G = RowsGeometry;

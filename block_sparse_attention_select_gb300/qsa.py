@@ -351,7 +351,7 @@ class KVCache:
         if any(t is not None and t.device != k.device for t in (v, block_table, k_scale, v_scale)):
             raise ValueError("the tensors of a cache must be on one device")
         self.k, self.v, self.block_table, self.k_scale, self.v_scale = k, v, block_table, k_scale, v_scale
-        self.device = k.device
+        self.device, self.index = k.device, k.device.index
         npg, pt, self.hkv, self.head_dim = (int(x) for x in k.shape)
         self.c = KVCacheC(k.data_ptr(), v.data_ptr(), 0 if k_scale is None else k_scale.data_ptr(),
                           0 if v_scale is None else v_scale.data_ptr(), QSA_KV_E4M3 if quantised else QSA_KV_FP16,
@@ -376,11 +376,11 @@ class KVCache:
 def _row_stride(t, cache: KVCache, heads: int, name: str) -> int:
     """Checks an FP16 row array [rows, heads, head_dim] and returns its row
     stride: rows may be slices of wider ones, a row itself is contiguous."""
-    if t.dtype != torch.float16:
+    shape, stride = t.shape, t.stride()
+    if t.dtype is not torch.float16:
         raise TypeError(f"{name} must be {torch.float16}, got {t.dtype}")
     if t.device != cache.device:
         raise ValueError(f"{name} must be on the cache's device")
-    shape, stride = t.shape, t.stride()
     if len(shape) != 3 or shape[1] != heads or shape[2] != cache.head_dim:
         raise ValueError(f"{name} must be [rows, {heads}, {cache.head_dim}], got {list(shape)}")
     if stride[2] != 1 or (heads > 1 and stride[1] != cache.head_dim):
@@ -389,12 +389,15 @@ def _row_stride(t, cache: KVCache, heads: int, name: str) -> int:
 
 
 def _requests(seq_start, pos_start, cache: KVCache) -> int:
-    _need(seq_start, torch.int32, "seq_start"), _need(pos_start, torch.int32, "pos_start")
-    n = pos_start.shape[0]
-    if seq_start.dim() != 1 or pos_start.dim() != 1 or seq_start.shape[0] != n + 1:
+    """Checks the two arrays that describe a batch; the number of requests."""
+    dev, n = cache.device, pos_start.shape[0] if pos_start.dim() == 1 else -1
+    if not (seq_start.dtype is torch.int32 and pos_start.dtype is torch.int32 and seq_start.shape == (n + 1,)
+            and seq_start.device == dev and pos_start.device == dev and seq_start.is_contiguous()
+            and pos_start.is_contiguous()):
+        _need(seq_start, torch.int32, "seq_start"), _need(pos_start, torch.int32, "pos_start")
+        if seq_start.device != dev or pos_start.device != dev:
+            raise ValueError("seq_start and pos_start must be on the cache's device")
         raise ValueError("seq_start must be int32 [n + 1] and pos_start int32 [n]")
-    if seq_start.device != cache.device or pos_start.device != cache.device:
-        raise ValueError("seq_start and pos_start must be on the cache's device")
     return n
 
 
@@ -402,22 +405,23 @@ def _call(cache: KVCache, stream, fn, *args, made=()):
     """fn(*args, stream) on the cache's device.  `made`: tensors that the call
     allocated itself, on the current stream: their memory must not be handed out
     again before the work on another stream is done."""
-    dev = cache.device
+    index = cache.index
     if stream is None:
-        handle = torch.cuda.current_stream(dev).cuda_stream
+        # (the raw handle: building a Stream object costs as much as the launch)
+        handle = torch._C._cuda_getCurrentRawStream(index)
     else:
         if not hasattr(stream, "cuda_stream"):
-            stream = torch.cuda.ExternalStream(int(stream), device=dev)
+            stream = torch.cuda.ExternalStream(int(stream), device=cache.device)
         handle = stream.cuda_stream
-        current = torch.cuda.current_stream(dev)
-        if handle != current.cuda_stream and made:
+        current = torch.cuda.current_stream(cache.device)
+        if made and handle != current.cuda_stream:
             stream.wait_stream(current)
             for t in made:
                 t.record_stream(stream)
-    if torch.cuda.current_device() == dev.index:
+    if torch._C._cuda_getDevice() == index:
         status = fn(*args, handle)
     else:
-        with torch.cuda.device(dev):
+        with torch.cuda.device(index):
             status = fn(*args, handle)
     if status != QSA_OK:
         raise QSAError(status, fn.__name__)
@@ -482,7 +486,8 @@ def chunk_attention(q, seq_start, pos_start, cache: KVCache, window: int = 0, sc
         made.append(out)
     elif out.shape != q.shape or out.device != cache.device:
         raise ValueError("out must have q's shape and device")
-    _need(out, torch.float16, "out")
+    else:
+        _need(out, torch.float16, "out")
     if ws is None:
         ws = alloc_chunk_attention_workspace(cache, rows, hq)
         made.append(ws)
