@@ -78,7 +78,7 @@ constexpr uint32_t TM_S = 0, TM_O = 256;     // TMEM columns: two S buffers of 1
 constexpr int BAR_PAIR = 1, BAR_HELP = 5;    // named barriers: four softmax warp pairs, the helpers
 
 struct PairGeometry {
-    static constexpr int ROWS = CH_ROWS, TILE = CH_TILE, UNIT_COST = 4, MIN_SHARE = 1, THREADS = CH_THREADS, WARPS = CH_WARPS,
+    static constexpr int ROWS = CH_ROWS, TILE = CH_TILE, UNIT_COST = 4, MIN_SHARE = 4, THREADS = CH_THREADS, WARPS = CH_WARPS,
                          WORKERS = CHUNK_MAX_PAIRS;
 };
 using G = PairGeometry;
@@ -922,7 +922,7 @@ int launch(const ChunkParams &p, const void *tk, const void *tv, int grid, bool 
                                  CH_SMEM, stream, false, args);
     if (rc != 0) return rc;
     void *join[] = {const_cast<ChunkParams *>(&p)};
-    const unsigned y = static_cast<unsigned>(std::min(8, (p.ws_rows + 7) / 8));
+    const unsigned y = static_cast<unsigned>(std::min(CH_ROWS / JOIN_WARPS, p.ws_rows));
     return launch_kernel(reinterpret_cast<const void *>(&chunk_join_kernel<G, D>), dim3(grid / 2, y), dim3(256), 0, stream,
                          overlap, join);
 }

@@ -353,10 +353,10 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volati
 
 // Joins the parts of each split unit: block x the unit that worker x began (part
 // 0 in its second place, part i in the first place of the i-th worker after it).
-// A warp takes a row; with many parts (one row over a long cache) the warps of a
-// CTA share the parts of a row instead and add up through shared memory, for the
-// loads of one warp would come one after another.  G: the geometry of the kernel
-// that left the parts.
+// A warp takes a row; with many parts and few rows (no more than blocks along y)
+// the warps of a CTA share the parts of a row instead and add up through shared
+// memory, for the loads of one warp would come one after another.  G: the
+// geometry of the kernel that left the parts.
 constexpr int JOIN_WARPS = 8;
 constexpr int JOIN_PARTS = 6;                // parts that one warp takes
 
@@ -374,7 +374,7 @@ chunk_join_kernel(const ChunkParams p)
     const float2 *ml = reinterpret_cast<const float2 *>(p.ws + WS_ML);
     const float *po = reinterpret_cast<const float *>(p.ws + ws_o<G::ROWS, G::WORKERS>());
     auto place = [&](int32_t i) { return 2 * (static_cast<int64_t>(blockIdx.x) + i) + (i == 0 ? 1 : 0); };
-    const bool shared_row = n > JOIN_PARTS;
+    const bool shared_row = n > JOIN_PARTS && sp.rows <= static_cast<int32_t>(gridDim.y);
     const int32_t step = shared_row ? gridDim.y : JOIN_WARPS * gridDim.y;
     for (int32_t row = shared_row ? blockIdx.y : blockIdx.y * JOIN_WARPS + warp; row < sp.rows; row += step) {
         float mx = -INFINITY, sum = 0.0f;
@@ -392,7 +392,7 @@ chunk_join_kernel(const ChunkParams p)
                 sum = fmaf(x.y, wt, sum);
             }
             const int32_t k = min(32, n - i0);
-#pragma unroll 4
+#pragma unroll 8
             for (int32_t i = shared_row ? warp : 0; i < k; i += shared_row ? JOIN_WARPS : 1) {
                 const float f = __shfl_sync(0xffffffffu, wt, i);
                 const float4 *src = reinterpret_cast<const float4 *>(po + (place(i0 + i) * p.ws_rows + row) * D) + lane;
