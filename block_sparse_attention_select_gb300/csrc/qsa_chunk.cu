@@ -55,6 +55,7 @@
 
 #include <algorithm>
 #include <mutex>
+#include <type_traits>
 
 #include "qsa_chunk.cuh"
 
@@ -417,69 +418,67 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
         uint64_t *empty = Q8 ? c.raw_empty : c.empty;
         const int32_t P = p.kv.page_tokens;
         const int sh_k = __ffs(min(P, Sh::KTOK)) - 1, sh_v = __ffs(min(P, Sh::VTOK)) - 1;
+        // this lane's box of a key slot and of a value slot: its first token in the
+        // tile, its place across the heads and in the slot
+        const int lb_k = __ffs(Sh::KTOK) - 1 - sh_k, lb_v = __ffs(Sh::VTOK) - 1 - sh_v;      // log2 of the boxes down
+        const int32_t ch_k = lane >> lb_k, ch_v = lane >> lb_v;
+        const int32_t dn_k = (lane & ((1 << lb_k) - 1)) << sh_k, dn_v = (lane & ((1 << lb_v) - 1)) << sh_v;
+        const int32_t off_k = rank * Sh::KTOK + dn_k, off_v = dn_v;
+        const int32_t x_k = ch_k * CK, x_v = rank * (D / 2) + ch_v * CV;
+        const uint32_t at_k = (ch_k * Sh::KTOK + dn_k) * 128, at_v = (ch_v * Sh::VTOK + dn_v) * (Q8 ? CV : 128);
+        const int32_t nowhere = p.kv.num_pages << p.kv.page_shift;      // a row past the cache: reads zeros
+        const uint32_t full0 = of_first(&c.full[0]);
         RingPos<Sh> pos;
         uint32_t rslot = 0, rphase = 0, used = 0, last = 0;   // raw slots; those loaded at least once, their latest phases
         uint32_t nb = 0;                                      // boundary tiles so far
         bool ok = true;
-        // this lane's box of a slot: place in the tensor and in the slot
-        int32_t x = 0, y = 0;
-        uint32_t at = 0;
-        bool mine = false;
-        const int32_t *bt = nullptr;
-        auto plan = [&](int32_t e) {
-            bool v;
-            int32_t tile;
-            slot_at<Sh::LEAD>(e, w.n, &v, &tile);
-            const int sh = v ? sh_v : sh_k;
-            const int32_t toks = v ? Sh::VTOK : Sh::KTOK;
-            const int lb = __ffs(toks) - 1 - sh;              // log2 of the boxes down
-            const int32_t ch = lane >> lb, i = lane & ((1 << lb) - 1);
-            mine = ch < (v ? VCH : KCH);
-            const int32_t tok = (w.j0 + tile) * CH_TILE + (v ? 0 : rank * Sh::KTOK) + (i << sh);
-            x = w.g * D + (v ? rank * (D / 2) + ch * CV : ch * CK);
-            const int32_t row_bytes = v && Q8 ? CV : 128;
-            at = static_cast<uint32_t>((ch * toks + (i << sh)) * row_bytes);
-            // boxes without a visible token read zeros (a row past the cache)
-            y = p.kv.num_pages << p.kv.page_shift;
-            if (mine && tok <= w.hi_tok && tok + (1 << sh) > w.lo_tok) {
-                const int32_t page = __ldg(bt + (tok >> p.kv.page_shift));
-                if (page >= 0 && page < p.kv.num_pages) y = (page << p.kv.page_shift) + (tok & (P - 1));
-                else record_error(p.kv.status, ST_BAD_PAGE);
-            }
-        };
         while (next_segment()) {
             if (!ok) continue;
-            bt = p.kv.block_table + static_cast<int64_t>(w.b) * p.kv.max_pages;
-            const int32_t n = w.n;
-            plan(0);
-            for (int32_t e = 0; e < 2 * n; ++e) {
-                bool v;
-                int32_t tile;
-                slot_at<Sh::LEAD>(e, n, &v, &tile);
-                const int32_t xx = x, yy = y;
-                const uint32_t aa = at;
-                const bool mm = mine;
-                if (e + 1 < 2 * n) plan(e + 1);               // page lookups run under this slot's wait
-                const uint32_t slot = Q8 ? rslot : pos.slot(v), phase = Q8 ? rphase : pos.phase(v);
+            const int32_t *bt = p.kv.block_table + static_cast<int64_t>(w.b) * p.kv.max_pages;
+            const int32_t n = w.n, tok0 = w.j0 * CH_TILE;
+            // the pages of the next key and value slots, looked up a slot ahead
+            int32_t page_k = -1, page_v = -1;
+            auto page_of = [&](auto is_v, int32_t tile) -> int32_t {
+                constexpr bool V = decltype(is_v)::value;
+                const int32_t tok = tok0 + tile * CH_TILE + (V ? off_v : off_k);
+                const bool mine = V ? ch_v < VCH : ch_k < KCH;
+                // boxes without a visible token read zeros
+                const bool seen = tok <= w.hi_tok && tok + (1 << (V ? sh_v : sh_k)) > w.lo_tok;
+                return mine && seen ? __ldg(bt + (tok >> p.kv.page_shift)) : INT32_MAX;
+            };
+            // This loop has to keep up with the products (a few hundred clocks per
+            // slot with 128-wide heads), on a warp that shares its issue slots and
+            // instruction cache with the softmax: few instructions matter most.
+            auto load = [&](auto is_v, int32_t tile) {
+                constexpr bool V = decltype(is_v)::value;
+                const uint32_t slot = Q8 ? rslot : pos.slot(V), phase = Q8 ? rphase : pos.phase(V);
+                const int32_t page = V ? page_v : page_k;
+                int32_t y = nowhere;
+                if (static_cast<uint32_t>(page) < static_cast<uint32_t>(p.kv.num_pages))
+                    y = (page << p.kv.page_shift) + ((V ? off_v : off_k) + tile * CH_TILE + tok0 & (P - 1));
+                else if (page != INT32_MAX)
+                    record_error(p.kv.status, ST_BAD_PAGE);
+                if (tile + 1 < n) (V ? page_v : page_k) = page_of(is_v, tile + 1);
                 if (!warp_wait(&empty[slot], phase ^ 1u, abort, lim)) {
                     ok = false;
-                    break;
+                    return;
                 }
                 uint32_t bar;
                 if constexpr (Q8) {
                     bar = smem_u32(&c.raw_full[slot]);
                     if (lane == 0) mbar_arrive_expect_tx(&c.raw_full[slot], BYTES);
-                } else if (v && w.cut(tile, CH_TILE)) {
+                } else if (V && w.cut(tile, CH_TILE)) {
                     // the helpers clear rows of this one before the products see it
                     bar = smem_u32(&c.bnd[nb & 7u]);
                     if (lane == 0) mbar_arrive_expect_tx(&c.bnd[nb & 7u], BYTES);
                     ++nb;
                 } else {
-                    bar = of_first(&c.full[slot]);
+                    bar = full0 + slot * 8u;
                     if (lane == 0) cluster_arrive_expect_tx(bar, BYTES);
                 }
                 __syncwarp();
-                if (mm) tma_load_2d_pair(dst0 + slot * BYTES + aa, v ? &tv : &tk, bar, xx, yy);
+                if (V ? ch_v < VCH : ch_k < KCH)
+                    tma_load_2d_pair(dst0 + slot * BYTES + (V ? at_v : at_k), V ? &tv : &tk, bar, w.g * D + (V ? x_v : x_k), y);
                 if (Q8) {
                     used |= 1u << rslot;
                     last = (last & ~(1u << rslot)) | (rphase << rslot);
@@ -488,8 +487,17 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                         rphase ^= 1u;
                     }
                 } else {
-                    pos.next(v);
+                    pos.next(V);
                 }
+            };
+            page_k = page_of(std::false_type{}, 0);
+            page_v = page_of(std::true_type{}, 0);
+            // the order of slot_at
+            const int32_t lead = min(Sh::LEAD, n);
+            for (int32_t j = 0; ok && j < lead; ++j) load(std::false_type{}, j);
+            for (int32_t j = 0; ok && j < n; ++j) {
+                load(std::true_type{}, j);
+                if (ok && j + lead < n) load(std::false_type{}, j + lead);
             }
         }
         // after an abort copies may be in flight: let them land (their barriers
