@@ -124,7 +124,7 @@ struct RingPos {
 struct Ctrl {
     SegRing segs;
     uint64_t full[MAX_SLOTS], empty[MAX_SLOTS], raw_full[RAWS], raw_empty[RAWS], bnd[8];
-    uint64_t s_full[2], s_free[2], p_full[2], o_done[2], m_out[2][4], q_full[2], q_free[2], drain;
+    uint64_t s_full[2], s_free[2], p_full[2][2], o_done[2], m_out[2][4], q_full[2], q_free[2], drain;
     alignas(8) float mrow[2][CH_HALF];       // [tile parity][row]: maximum in use at the group's last tile; sums at a segment's end
     alignas(8) uint16_t scale[2][CH_TILE];   // [slot parity][token]: FP16 scale (E4M3)
     Share share;
@@ -370,7 +370,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
         for (int i = 0; i < 8; ++i) mbar_init(&c.bnd[i], 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&c.s_full[i], 1);
-            mbar_init(&c.p_full[i], CH_SOFT);                // four warps of each CTA
+            for (int k = 0; k < 2; ++k) mbar_init(&c.p_full[i][k], CH_SOFT);    // four warps of each CTA
             mbar_init(&c.s_free[i], CH_SOFT);
             mbar_init(&c.o_done[i], 1);
             for (int k = 0; k < 4; ++k) mbar_init(&c.m_out[i][k], 1);
@@ -556,21 +556,29 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
         auto values = [&](uint32_t i, bool first) {
             const uint32_t slot = ringpos.slot(true);
             ok = ok && warp_wait(&c.full[slot], ringpos.phase(true), abort, lim);
-            ok = ok && warp_wait(&c.p_full[i & 1u], (i >> 1) & 1u, abort, lim);
+            ok = ok && warp_wait(&c.p_full[i & 1u][0], (i >> 1) & 1u, abort, lim);
             if (!ok) return;
             ringpos.next(true);
-            tc_fence_after();
             const uint64_t vd = vd0 | (uniform(ring_a + slot * SLOT) >> 4);
             const uint32_t pa = tm + Sh::TM_P + uniform(i & 1u) * Sh::P_STRIDE;
             const uint32_t add = uniform(first ? 0u : 1u);
-            if (elect_one()) {
+            // the first half's products start while the softmax is at the second
 #pragma unroll
-                for (int kk = 0; kk < CH_TILE / 16; ++kk)
-                    umma2_f16_ta(tm + TM_O, pa + kk * 8u, vd + ((kk * 2048u) >> 4), idesc_o, kk > 0 ? 1u : add);
-                umma2_commit(&c.o_done[i & 1u]);
-                umma2_commit(&c.empty[slot]);
+            for (int half = 0; half < 2; ++half) {
+                if (half == 1) ok = warp_wait(&c.p_full[i & 1u][1], (i >> 1) & 1u, abort, lim);
+                if (!ok) return;
+                tc_fence_after();
+                if (elect_one()) {
+#pragma unroll
+                    for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
+                        umma2_f16_ta(tm + TM_O, pa + kk * 8u, vd + ((kk * 2048u) >> 4), idesc_o, kk > 0 ? 1u : add);
+                    if (half == 1) {
+                        umma2_commit(&c.o_done[i & 1u]);
+                        umma2_commit(&c.empty[slot]);
+                    }
+                }
+                __syncwarp();
             }
-            __syncwarp();
         };
         while (next_segment()) {
             if (!ok || !(do_s || do_o)) continue;
@@ -739,8 +747,14 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
         const uint32_t ts = tmem + TM_S + grp * 128u + lane_base;
         const uint32_t tp = tmem + Sh::TM_P + grp * Sh::P_STRIDE + lane_base;
         const float cs = p.scale * 1.4426950408889634f;        // scores in powers of two
-        const uint32_t p_full0 = of_first(&c.p_full[grp]), s_free0 = of_first(&c.s_free[grp]);
+        const uint32_t p_full0 = of_first(&c.p_full[grp][0]), s_free0 = of_first(&c.s_free[grp]);
         uint32_t it = 0;                                       // tiles before the segment
+        // Waits until the second product of tile i is done.  A parity wait is right
+        // while the barrier is in that phase or just past it.  Past the one
+        // before: the product of tile i - 1 has been seen to end, and products end
+        // in order.  Not past the one after: the product of tile i + 2 needs this
+        // warp's own P of tile i + 1 or i + 2, which it has still to give.
+        auto o_done = [&](uint32_t i) { return warp_wait(&c.o_done[i & 1u], (i >> 1) & 1u, abort, lim); };
         bool ok = true;                                        // false: keep to the barriers, do nothing
         while (next_segment()) {
             const int32_t n = w.n;
@@ -796,7 +810,30 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&c.m_out[grp][lq]);
                 // P's columns are free when the tile before last is done with them
-                if (Sh::OWN_P && ok && i > 1) ok = warp_wait(&c.o_done[grp], ((i - 2) >> 1) & 1u, abort, lim);
+                if (ok && i > 1) ok = o_done(i - 2);
+                tc_fence_after();
+                if (ok && live && j > 0 && __any_sync(0xffffffffu, grow)) {
+                    // only here the product before must have ended
+                    ok = o_done(i - 1);
+                    tc_fence_after();
+                    const float alpha = grow ? exp2_approx((mp - mi) * cs) : 1.0f;
+                    uint32_t u[32];
+#pragma unroll 1
+                    for (int k = 0; k < D / 32; ++k) {
+                        tmem_ld_32x32b_x32(tmem + TM_O + lane_base + k * 32u, u);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * alpha);
+                        tmem_st_x32(tmem + TM_O + lane_base + k * 32u, u);
+                    }
+                }
+                // P, in two halves; the products of the first start at once
+                auto give = [&](int half) {
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (ok && lane == 0) cluster_arrive(p_full0 + half * 8u);
+                };
                 if (ok && live) {
                     const float mc = mi == -INFINITY ? 0.0f : mi * cs;
                     if (m != mi) l *= exp2_approx(m * cs - mc);                // 0 at the first
@@ -815,31 +852,16 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                             o[e] = *reinterpret_cast<const uint32_t *>(&h);
                         }
                         tmem_st_x16(tp + k * 16u, o);
+                        if (k == 1) give(0);
                     }
                     l += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
                 }
-                if (ok && i > 0) ok = warp_wait(&c.o_done[grp ^ 1], ((i - 1) >> 1) & 1u, abort, lim);
-                if (ok && live && j > 0 && __any_sync(0xffffffffu, grow)) {
-                    tc_fence_after();
-                    const float alpha = grow ? exp2_approx((mp - mi) * cs) : 1.0f;
-                    uint32_t u[32];
-#pragma unroll 1
-                    for (int k = 0; k < D / 32; ++k) {
-                        tmem_ld_32x32b_x32(tmem + TM_O + lane_base + k * 32u, u);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * alpha);
-                        tmem_st_x32(tmem + TM_O + lane_base + k * 32u, u);
-                    }
-                }
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (ok && lane == 0) cluster_arrive(p_full0);
+                if (!live) give(0);
+                give(1);
             }
             it += n;
             // the segment's sums: its rows' output, or its part of it
-            if (ok) ok = warp_wait(&c.o_done[(it - 1) & 1u], ((it - 1) >> 1) & 1u, abort, lim);
+            if (ok) ok = (it < 2 || o_done(it - 2)) && o_done(it - 1);
             named_barrier(BAR_PAIR + lq, 64);
             // both groups' sums at the last tile's maximum, exchanged in place of the maxima
             const float mlast = c.mrow[(it - 1) & 1u][row];
