@@ -198,6 +198,19 @@ __device__ __forceinline__ void umma2_commit(uint64_t *bar)
         : "memory");
 }
 
+// 32 bytes, in one store where they are aligned.
+__device__ __forceinline__ void store32(void *dst, const uint32_t *v, bool whole)
+{
+    if (whole) {
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
+                     "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4 *>(dst)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<uint4 *>(dst)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+    }
+}
+
 // One thread of the (converged) warp.
 __device__ __forceinline__ bool elect_one()
 {
@@ -878,6 +891,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                 const int32_t h = vr - tok * p.group, ur = rank * CH_HALF + row;
                 __half *out = static_cast<__half *>(p.out) +
                               ((static_cast<int64_t>(w.s0) + tok) * p.hq + w.g * p.group + h) * D + grp * OC;
+                const bool out_32 = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;      // (16 bytes are promised)
                 float *part = nullptr;
                 if (!whole) {
                     part = reinterpret_cast<float *>(p.ws + ws_o<CH_ROWS, CHUNK_MAX_PAIRS>()) + (static_cast<int64_t>(w.place) * p.ws_rows + ur) * D + grp * OC;
@@ -894,20 +908,15 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                     if (!in) continue;
                     if (whole) {
 #pragma unroll
-                        for (int i = 0; i < 32; i += 8) {
-                            uint32_t x[4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const __half2 hh = __floats2half2_rn(__uint_as_float(u[i + 2 * e]) * inv,
-                                                                     __uint_as_float(u[i + 2 * e + 1]) * inv);
-                                x[e] = *reinterpret_cast<const uint32_t *>(&hh);
-                            }
-                            *reinterpret_cast<uint4 *>(out + 32 * k + i) = make_uint4(x[0], x[1], x[2], x[3]);
+                        for (int i = 0; i < 32; i += 2) {
+                            const __half2 hh = __floats2half2_rn(__uint_as_float(u[i]) * inv, __uint_as_float(u[i + 1]) * inv);
+                            u[i >> 1] = *reinterpret_cast<const uint32_t *>(&hh);
                         }
+                        store32(out + 32 * k, u, out_32);
+                        store32(out + 32 * k + 16, u + 8, out_32);
                     } else {
 #pragma unroll
-                        for (int i = 0; i < 32; i += 4)
-                            *reinterpret_cast<uint4 *>(part + 32 * k + i) = make_uint4(u[i], u[i + 1], u[i + 2], u[i + 3]);
+                        for (int i = 0; i < 32; i += 8) store32(part + 32 * k + i, u + i, true);
                     }
                 }
                 tc_fence_before();
