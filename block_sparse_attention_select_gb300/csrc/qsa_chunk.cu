@@ -18,37 +18,49 @@
 // (token * group + head) of one request and KV head.
 //
 // Work: the units' tiles, in the order (request, rows, KV head), form one line
-// that the CTA pairs share out evenly (each unit a little longer than its tiles
-// for what it costs besides them: without that, pairs with many short units
-// ended last, 1,019 us against 8xx us on four prompts of 4,096 tokens), so one row over a long cache,
-// a batch of unequal requests and a long prompt all fill the card.  A unit that
+// that the CTA pairs share out evenly (each unit UNIT_COST tiles longer than it
+// is, for what it costs besides them: counted as 2, 3, 4 and 5 tiles, four prompts
+// of 4,096 tokens take 500, 453, 427 and 437 us), so one row over a long cache, a
+// batch of unequal requests and a long prompt all fill the card.  A unit that
 // lies across pairs leaves unnormalised FP32 partial sums with their maxima in
 // the workspace (at most two per pair), which a second kernel joins.  Every
 // pair finds its share itself from seq_start and pos_start: no plan kernel and
 // no host knowledge of the lengths.
 //
 // A CTA's warps: 0-7 softmax, 8 loads K and V by TMA, one box per page piece,
-// through the block table, 9 issues the MMAs (in the first CTA of the pair),
+// through the block table, 9 issues the MMAs (in the first CTA of the pair; with
+// D = 128 warp 11 issues the second products, so that neither product waits for
+// what the other needs), 10 walks through the share and hands out its segments,
 // 12-15 load the queries, clear the value rows that nothing attends and, from
-// the E4M3 cache, turn the loaded codes into FP16 tiles; 10 and 11 only give
-// their registers away.  K and V share a ring of slots in the order of use.
+// the E4M3 cache, turn the loaded codes into FP16 tiles.  K and V share a ring of
+// slots in the order of use; with D = 128 each has its own.
 //
 // Softmax warps 0-3 take the even tiles and 4-7 the odd ones (warp w: TMEM lane
 // quarter w % 4, a row per thread), so that one group's exponentials run beside
 // the other's waits; S has a buffer for each.  A thread takes its 128 scores
 // into registers, its row's running maximum passes on from tile to tile, from
 // one group to the other, before the exponentials start, and each group keeps
-// its own sum.  P goes to TMEM as FP16 and is the A operand of the second
-// product from there.  With D = 128, P has columns of its own, so the score
+// its own sum.  P goes to TMEM as FP16, in two halves, and is the A operand of the
+// second product from there.  With D = 128, P has columns of its own, so the score
 // product of the tile after next starts as soon as the scores are in registers:
 //   S(0) S(1) | S(2) O(0) | S(3) O(1) | ...
 // With D = 256, TMEM is full (2 x 128 for S, 256 for O): P overwrites its
 // scores and the order is S(0) S(1) | O(0) S(2) | O(1) S(3) | ...
 //
+// What bounds it: with D = 256 and a long context the tensor cores (the
+// 1,616-row chunk over 29,000 tokens, 12 query heads to a KV head: 575 us, 1,950 TF/s, at the rate of
+// the library's large bf16 products).  With D = 128 a tile's products take half
+// as long and its exponentials the same, so the softmax warps' latency does (four
+// prompts of 4,096 tokens, 32 heads: 428 us, 1,280 TF/s; tensor pipe 48%, issue
+// slots 36%).  From the E4M3 cache the turning of codes into FP16 tiles (three
+// chunks of 517 over 12,345 tokens: 161 us, 1,210 TF/s).  A short call is the
+// ends of its units: two chunks of 1,023 tokens with a window of 1,000 take 41 us
+// where their products need 9.
+//
 // The accumulator is rescaled only when a row's maximum has grown by more than
-// 2^8 since the one in use: P is then at most 256, far inside FP16, and the sum
-// uses the same stale maximum, so the result is the same.  Rounding P to FP16
-// (2^-11 of each weight) is of the size of the output's own rounding.
+// 2^8 since the one in use: the sum uses the same stale maximum, so the result
+// is the same.  Rounding P to FP16 (2^-11 of each weight, with the smallest ones
+// kept by a factor, see RESCALE) is of the size of the output's own rounding.
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -74,7 +86,6 @@ constexpr int CH_THREADS = 32 * CH_WARPS;
 constexpr int RAWS = 4;                      // slots of loaded codes (E4M3)
 constexpr int MAX_SLOTS = 10;                // slots of the ring at most
 constexpr uint32_t RING = 229376;            // bytes for Q and the ring
-constexpr float RESCALE = 8.0f;              // log2 of the growth that rescales
 constexpr uint32_t TM_S = 0, TM_O = 256;     // TMEM columns: two S buffers of 128, O
 constexpr int BAR_PAIR = 1, BAR_HELP = 5;    // named barriers: four softmax warp pairs, the helpers
 
@@ -456,7 +467,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                 const int32_t tok = tok0 + tile * CH_TILE + (V ? off_v : off_k);
                 const bool mine = V ? ch_v < VCH : ch_k < KCH;
                 // boxes without a visible token read zeros
-                const bool seen = tok <= w.hi_tok && tok + (1 << (V ? sh_v : sh_k)) > w.lo_tok;
+                const bool seen = tok <= w.hi_tok && tok + ((1 << (V ? sh_v : sh_k)) - 1) >= w.lo_tok;
                 return mine && seen ? __ldg(bt + (tok >> p.kv.page_shift)) : INT32_MAX;
             };
             // This loop has to keep up with the products (a few hundred clocks per
@@ -518,9 +529,9 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
         if (!ok && lane == 0) {
             if (Q8)
                 for (int i = 0; i < RAWS; ++i)
-                    if (used & (1u << i)) mbar_wait_bounded(&c.raw_full[i], (last >> i) & 1u, lim);
+                    if (used & (1u << i)) mbar_wait_bounded(&c.raw_full[i], (last >> i) & 1u, drain_limit(lim));
             const long long t0 = clock64();
-            while (clock64() - t0 < 4000000) {}
+            while (clock64() - t0 < static_cast<long long>(2 * DRAIN_NS)) {}
         }
         __syncwarp();
     } else if (warp == CH_SCHED) {
@@ -622,7 +633,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
         if (!ok) {                                            // products still running
             if (elect_one()) {
                 umma2_commit(&c.drain);
-                mbar_wait_bounded(&c.drain, 0, lim);
+                mbar_wait_bounded(&c.drain, 0, drain_limit(lim));
             }
             __syncwarp();
         }
@@ -852,7 +863,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                     if (m != mi) l *= exp2_approx(m * cs - mc);                // 0 at the first
                     m = mi;
                     float2 sum[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
-                    const float2 c2 = make_float2(cs, cs), mc2 = make_float2(-mc, -mc);
+                    const float2 c2 = make_float2(cs, cs), mc2 = make_float2(P_UP - mc, P_UP - mc);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         uint32_t o[16];

@@ -44,6 +44,7 @@ struct Split {
 // unit begun before its share, 1 for one that goes on after it) the rows'
 // (maximum in powers of two, sum), then their unnormalised outputs.
 constexpr size_t WS_ML = 4096;
+static_assert(sizeof(Split) * CHUNK_MAX_CTAS <= WS_ML && sizeof(Split) * CHUNK_MAX_PAIRS <= WS_ML, "workspace");
 template <int ROWS, int WORKERS>
 constexpr size_t ws_o() { return WS_ML + size_t{2} * WORKERS * ROWS * 8; }
 
@@ -122,8 +123,7 @@ struct Share {
 template <typename G>
 struct FindScratch {
     int32_t prefix[G::THREADS];
-    int32_t units[G::WARPS];
-    int64_t costs[G::WARPS];
+    int64_t units[G::WARPS], costs[G::WARPS];
 };
 
 // Finds worker `me`'s share of the line (of `n_workers`), by the whole CTA.  Each
@@ -137,13 +137,18 @@ __device__ __forceinline__ void find_work(const ChunkParams &p, Share &c, FindSc
     int32_t *prefix = s.prefix;
     const int32_t run = (p.kv.n_reqs + G::THREADS - 1) / G::THREADS;
     const int32_t r0 = min(t * run, p.kv.n_reqs), r1 = min(r0 + run, p.kv.n_reqs);
-    int32_t mine = 0, units;
+    int64_t mine = 0, all;
     for (int32_t b = r0; b < r1; ++b) {
         bool bad;
         mine += units_of<G>(p, seq_of(p.kv, b, &bad));
         if (bad && blockIdx.x == 0) record_error(p.kv.status, ST_BAD_ROW);
     }
-    prefix[t] = block_scan<G>(mine, s.units, warp, lane, &units);
+    const int64_t before = block_scan<G>(mine, s.units, warp, lane, &all);
+    prefix[t] = static_cast<int32_t>(before);
+    // more units than the rows allow: requests that share rows, or none in order
+    const bool wrong = all > INT32_MAX;
+    if (wrong && blockIdx.x == 0 && t == 0) record_error(p.kv.status, ST_BAD_ROW);
+    const int32_t units = wrong ? 0 : static_cast<int32_t>(all);
     __syncthreads();
     const int32_t u0 = static_cast<int32_t>(static_cast<int64_t>(units) * t / G::THREADS);
     const int32_t u1 = static_cast<int32_t>(static_cast<int64_t>(units) * (t + 1) / G::THREADS);
@@ -198,8 +203,8 @@ __device__ __forceinline__ void find_work(const ChunkParams &p, Share &c, FindSc
             if (w0 < at + static_cast<int64_t>(len) * p.kv.hkv) {
                 c.b = b0;
                 c.m = m0;
-                c.g = static_cast<int32_t>(w0 - at) / len;
-                c.off = static_cast<int32_t>(w0 - at) % len;
+                c.g = static_cast<int32_t>((w0 - at) / len);
+                c.off = static_cast<int32_t>((w0 - at) % len);
                 break;
             }
             at += static_cast<int64_t>(len) * p.kv.hkv;
@@ -272,6 +277,11 @@ struct Walk {
 // through a ring; `me` writes its split unit, if any, for the join kernel.
 constexpr int SEGS = 4;                      // segments it may be ahead
 constexpr uint64_t SEG_WAIT_NS = 10000000000ull;
+// After a time-out, what is in flight is waited for at least this long, however
+// short the limit that ran out: copies and products land within microseconds.
+constexpr uint64_t DRAIN_NS = 10000000ull;
+__device__ __forceinline__ uint64_t drain_limit(uint64_t lim) { return lim > DRAIN_NS ? lim : DRAIN_NS; }
+
 struct SegRing {
     Seg seg[SEGS];
     uint64_t full[SEGS], empty[SEGS];
@@ -330,6 +340,14 @@ __device__ __forceinline__ uint32_t sw128(uint32_t row, uint32_t c)
 {
     return (row >> 3) * 1024u + (row & 7u) * 128u + ((c ^ (row & 7u)) << 4);
 }
+
+// Weights are kept as 2^P_UP exp(s - m), with m the maximum in use.  That one is
+// at most RESCALE powers of two below the row's own, so a weight is at most 2^15,
+// inside FP16; and one that FP16 rounds in its subnormal range is off by at most
+// 2^-32 of the largest weight, so that the many small weights of a long context
+// (2^20 tokens: 2^-12 of the largest) are not lost.  (Without the factor, 2^-25:
+// 2^18 equal weights below that vanished from the output, though not from the sum.)
+constexpr float RESCALE = 8.0f, P_UP = 7.0f;
 
 __device__ __forceinline__ float exp2_approx(float x)
 {

@@ -43,7 +43,6 @@ constexpr int CR_WARPS = 12;
 constexpr int CR_THREADS = 32 * CR_WARPS;
 constexpr int CR_MAX_STAGES = 8;
 constexpr int BAR_COMP = 1;
-constexpr float CR_RESCALE = 8.0f;           // log2 of the growth of a maximum that rescales
 
 struct RowsGeometry {
     static constexpr int ROWS = CR_ROWS, TILE = CR_TILE, UNIT_COST = 4, MIN_SHARE = 3, THREADS = CR_THREADS, WARPS = CR_WARPS,
@@ -203,7 +202,7 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
             // copies still in flight (only after an abort: otherwise they were waited for)
             if (lane == 0)
                 for (int i = 0; i < NS; ++i)
-                    if (used & (1u << i)) mbar_wait_bounded(&c.full[i], (last >> i) & 1u, lim);
+                    if (used & (1u << i)) mbar_wait_bounded(&c.full[i], (last >> i) & 1u, drain_limit(lim));
             __syncwarp();
         } else if (Q8) {
             // ---------------------------------------------------------- scales
@@ -377,7 +376,7 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
                         mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
                         mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
                     }
-                    const bool grow0 = mx[0] > m[0] + CR_RESCALE, grow1 = mx[1] > m[1] + CR_RESCALE;
+                    const bool grow0 = mx[0] > m[0] + RESCALE, grow1 = mx[1] > m[1] + RESCALE;
                     if (__any_sync(0xffffffffu, grow0 || grow1)) {
                         const float a0 = grow0 ? exp2_approx(m[0] - mx[0]) : 1.0f, a1 = grow1 ? exp2_approx(m[1] - mx[1]) : 1.0f;
                         if (grow0) m[0] = mx[0];
@@ -399,7 +398,7 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
                     for (int n = 0; n < 2; ++n)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            const float mm = m[e] == -INFINITY ? 0.0f : m[e];
+                            const float mm = m[e] == -INFINITY ? 0.0f : m[e] - P_UP;
                             const float x = exp2_approx(s[n][2 * e] - mm), y = exp2_approx(s[n][2 * e + 1] - mm);
                             l[e] += x + y;
                             const __half2 hh = __floats2half2_rn(x, y);
