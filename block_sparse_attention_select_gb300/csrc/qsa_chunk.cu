@@ -290,6 +290,23 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&v)[
         : "memory");
 }
 
+// 32 columns, and their maximum in each lane.
+__device__ __forceinline__ float tmem_ld_max_x32(uint32_t taddr, uint32_t (&v)[32])
+{
+    float m;
+    asm volatile(
+        "tcgen05.ld.red.sync.aligned.32x32b.x32.max.f32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, %32, [%33];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
+          "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
+          "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31]), "=f"(m)
+        : "r"(taddr)
+        : "memory");
+    return m;
+}
+
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // two FP32 lanes at once
@@ -799,30 +816,24 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                 float mx = -INFINITY;
                 if (ok && live) {
                     tc_fence_after();
+                    float a[4];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) tmem_ld_32x32b_x32(ts + k * 32u, s[k]);
+                    for (int k = 0; k < 4; ++k) a[k] = tmem_ld_max_x32(ts + k * 32u, s[k]);
                     tmem_ld_wait();
+                    mx = fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3]));
                 }
                 if constexpr (Sh::OWN_P) {
                     tc_fence_before();
                     __syncwarp();
                     if (ok && lane == 0) cluster_arrive(s_free0);
                 }
-                if (ok && live) {
-                    if (masked) {
+                if (ok && live && masked) {
+                    float a[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                        for (int e = 0; e < CH_TILE; ++e)
-                            if (e > hi || e < lo) s[e >> 5][e & 31] = 0xff800000u;       // -inf
+                    for (int e = 0; e < CH_TILE; ++e) {
+                        if (e > hi || e < lo) s[e >> 5][e & 31] = 0xff800000u;           // -inf
+                        a[e & 3] = fmaxf(a[e & 3], __uint_as_float(s[e >> 5][e & 31]));
                     }
-                    float a[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) a[e] = fmaxf(__uint_as_float(s[0][e]), __uint_as_float(s[0][e + 4]));
-#pragma unroll
-                    for (int e = 8; e < CH_TILE; e += 8)
-#pragma unroll
-                        for (int f = 0; f < 4; ++f)
-                            a[f] = fmaxf(fmaxf(a[f], __uint_as_float(s[e >> 5][(e & 31) + f])),
-                                         __uint_as_float(s[e >> 5][(e & 31) + f + 4]));
                     mx = fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3]));
                 }
                 // the maximum in use at the tile before, and the one for this tile
