@@ -882,17 +882,19 @@ qsa_status check_cache(const qsa_kv_cache *c)
     return QSA_OK;
 }
 
-// A cache as [tokens][hkv * head_dim], boxes of `bytes` x `box` tokens, in the
-// 128-byte swizzled layout or as they are.
-qsa_status make_tmap_kv(CUtensorMap *tm, const qsa_kv_cache *c, const void *base, int32_t bytes, int32_t box, bool swizzle)
+// A cache as [pieces of a token][tokens][bytes of a piece], in the 128-byte swizzled
+// layout or as it is.
+qsa_status make_tmap_kv(CUtensorMap *tm, const qsa_kv_cache *c, const void *base, const ChunkBox &box, bool swizzle)
 {
     const bool q8 = c->dtype == QSA_KV_E4M3;
-    const cuuint64_t width = static_cast<cuuint64_t>(c->hkv) * c->head_dim;
-    cuuint64_t dims[2] = {width, static_cast<cuuint64_t>(c->num_pages) * c->page_tokens};
-    cuuint64_t strides[1] = {width * (q8 ? 1 : 2)};
-    cuuint32_t boxes[2] = {static_cast<cuuint32_t>(q8 ? bytes : bytes / 2), static_cast<cuuint32_t>(box)};
-    cuuint32_t estr[2] = {1, 1};
-    const CUresult r = g_encode(tm, q8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+    const int32_t es = q8 ? 1 : 2;
+    const cuuint64_t width = static_cast<cuuint64_t>(c->hkv) * c->head_dim * es;
+    const cuuint32_t row = static_cast<cuuint32_t>(box.row);
+    cuuint64_t dims[3] = {row / es, static_cast<cuuint64_t>(c->num_pages) * c->page_tokens, width / row};
+    cuuint64_t strides[2] = {width, row};
+    cuuint32_t boxes[3] = {row / es, static_cast<cuuint32_t>(box.box), static_cast<cuuint32_t>(box.chunks)};
+    cuuint32_t estr[3] = {1, 1, 1};
+    const CUresult r = g_encode(tm, q8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
                                 const_cast<void *>(base), dims, strides, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                                 swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
                                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -1033,17 +1035,16 @@ qsa_status qsa_chunk_attention(const void *q, int64_t q_stride, int32_t rows, in
     CUtensorMap tk, tv;
     if (few_rows(rows, p.group, n_reqs)) {
         p.ws_rows = chunk_rows_part_rows(rows, p.group);
-        const int32_t box = chunk_rows_box(cache->page_tokens);
-        if ((st = make_tmap_kv(&tk, cache, cache->k, 128, box, true)) != QSA_OK) return st;
-        if ((st = make_tmap_kv(&tv, cache, cache->v, 128, box, true)) != QSA_OK) return st;
+        const ChunkBox box = {128, chunk_rows_box(cache->page_tokens), 1};
+        if ((st = make_tmap_kv(&tk, cache, cache->k, box, true)) != QSA_OK) return st;
+        if ((st = make_tmap_kv(&tv, cache, cache->v, box, true)) != QSA_OK) return st;
         st = launch_rc(launch_chunk_rows(p, &tk, &tv, d->sms, g_overlap, stream));
     } else {
         p.ws_rows = chunk_part_rows(rows, p.group);
-        int32_t box_k, box_v;
-        chunk_boxes(cache->head_dim, cache->page_tokens, &box_k, &box_v);
-        const int32_t v_bytes = p.kv.e4m3 ? cache->head_dim / 2 : 128;
-        if ((st = make_tmap_kv(&tk, cache, cache->k, 128, box_k, !p.kv.e4m3)) != QSA_OK) return st;
-        if ((st = make_tmap_kv(&tv, cache, cache->v, v_bytes, box_v, !p.kv.e4m3)) != QSA_OK) return st;
+        ChunkBox box_k, box_v;
+        chunk_boxes(cache->head_dim, cache->page_tokens, p.kv.e4m3, &box_k, &box_v);
+        if ((st = make_tmap_kv(&tk, cache, cache->k, box_k, !p.kv.e4m3)) != QSA_OK) return st;
+        if ((st = make_tmap_kv(&tv, cache, cache->v, box_v, !p.kv.e4m3)) != QSA_OK) return st;
         st = launch_rc(launch_chunk(p, &tk, &tv, d->sms, g_overlap, stream));
     }
     if (st == QSA_OK) ++g_launches;                      // the join kernel

@@ -252,18 +252,25 @@ __device__ __forceinline__ void cluster_arrive_expect_tx(uint32_t bar, uint32_t 
                  : "memory");
 }
 
+// The same on a barrier of this CTA.
+__device__ __forceinline__ void mbar_expect_tx_at(uint32_t bar, uint32_t bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
 __device__ __forceinline__ void cluster_sync()
 {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// 2-D tiled load into this CTA, completing on a barrier of either CTA of the pair.
-__device__ __forceinline__ void tma_load_2d_pair(void *dst_smem, const void *tmap, uint32_t bar, int32_t x, int32_t y)
+// 3-D tiled load (from x = 0) into this CTA, completing on a barrier of either CTA
+// of the pair.
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const void *tmap, uint32_t bar, int32_t y, int32_t z)
 {
     asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst_smem)),
-        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(x), "r"(y)
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(0), "r"(y), "r"(z)
         : "memory");
 }
 
@@ -451,22 +458,23 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == CH_LOAD) {
         // ---------------------------------------------------------- K, V loads
-        uint8_t *dst0 = Q8 ? raw : ring;
+        // This loop has to keep up with the products (a few hundred clocks per slot
+        // with 128-wide heads), on a warp that shares its issue slots and instruction
+        // cache with the softmax, so few instructions matter most: one copy per slot
+        // where a page holds its tokens, page lookups for many tiles at once, one
+        // thread that issues.  (With a box per 128-byte chunk, a lane each, and
+        // lookups tile by tile the loop took 1,600 clocks per tile and the products
+        // waited for it: 810 us on 512 new tokens of four requests over 32,768.)
+        const uint32_t dst0 = Q8 ? smem_u32(raw) : ring_a;
         constexpr uint32_t BYTES = Q8 ? RAW : SLOT;
         // elements of a box row: 128 bytes, or half a 128-wide head's 64 codes
         constexpr int CK = Q8 ? 128 : 64, CV = Q8 ? D / 2 : 64;
-        constexpr int KCH = D / CK, VCH = D / 2 / CV;         // boxes across
+        constexpr int KCH = D / CK, VCH = D / 2 / CV;         // such rows of a token
         uint64_t *empty = Q8 ? c.raw_empty : c.empty;
         const int32_t P = p.kv.page_tokens;
-        const int sh_k = __ffs(min(P, Sh::KTOK)) - 1, sh_v = __ffs(min(P, Sh::VTOK)) - 1;
-        // this lane's box of a key slot and of a value slot: its first token in the
-        // tile, its place across the heads and in the slot
-        const int lb_k = __ffs(Sh::KTOK) - 1 - sh_k, lb_v = __ffs(Sh::VTOK) - 1 - sh_v;      // log2 of the boxes down
-        const int32_t ch_k = lane >> lb_k, ch_v = lane >> lb_v;
-        const int32_t dn_k = (lane & ((1 << lb_k) - 1)) << sh_k, dn_v = (lane & ((1 << lb_v) - 1)) << sh_v;
-        const int32_t off_k = rank * Sh::KTOK + dn_k, off_v = dn_v;
-        const int32_t x_k = ch_k * CK, x_v = rank * (D / 2) + ch_v * CV;
-        const uint32_t at_k = (ch_k * Sh::KTOK + dn_k) * 128, at_v = (ch_v * Sh::VTOK + dn_v) * (Q8 ? CV : 128);
+        const int sh = __ffs(min(P, CH_TILE)) - 1;            // log2 of a piece: tokens of a tile in one page
+        const int ld = 7 - sh;                                // log2 of the pieces of a tile
+        const int32_t batch = 32 >> ld;                       // tiles whose pieces the lanes look up at a time
         const int32_t nowhere = p.kv.num_pages << p.kv.page_shift;      // a row past the cache: reads zeros
         const uint32_t full0 = of_first(&c.full[0]);
         RingPos<Sh> pos;
@@ -476,50 +484,71 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
         while (next_segment()) {
             if (!ok) continue;
             const int32_t *bt = p.kv.block_table + static_cast<int64_t>(w.b) * p.kv.max_pages;
-            const int32_t n = w.n, tok0 = w.j0 * CH_TILE;
-            // the pages of the next key and value slots, looked up a slot ahead
-            int32_t page_k = -1, page_v = -1;
-            auto page_of = [&](auto is_v, int32_t tile) -> int32_t {
-                constexpr bool V = decltype(is_v)::value;
-                const int32_t tok = tok0 + tile * CH_TILE + (V ? off_v : off_k);
-                const bool mine = V ? ch_v < VCH : ch_k < KCH;
-                // boxes without a visible token read zeros
-                const bool seen = tok <= w.hi_tok && tok + ((1 << (V ? sh_v : sh_k)) - 1) >= w.lo_tok;
-                return mine && seen ? __ldg(bt + (tok >> p.kv.page_shift)) : INT32_MAX;
+            const int32_t n = w.n;
+            const int32_t lane_tok = w.j0 * CH_TILE + (lane << sh);     // the lane's piece of the first tiles
+            // this lane's page of tiles j .. j + batch - 1; none without a token that
+            // is attended
+            auto page_of = [&](int32_t j) -> int32_t {
+                const int32_t tok = lane_tok + j * CH_TILE;
+                const bool seen = j + (lane >> ld) < n && tok <= w.hi_tok && tok + ((1 << sh) - 1) >= w.lo_tok;
+                return seen ? __ldg(bt + (tok >> p.kv.page_shift)) : INT32_MAX;
             };
-            // This loop has to keep up with the products (a few hundred clocks per
-            // slot with 128-wide heads), on a warp that shares its issue slots and
-            // instruction cache with the softmax: few instructions matter most.
+            auto row_of = [&](int32_t page, int32_t j) -> int32_t {
+                if (static_cast<uint32_t>(page) < static_cast<uint32_t>(p.kv.num_pages))
+                    return (page << p.kv.page_shift) + (lane_tok + j * CH_TILE & (P - 1));
+                if (page != INT32_MAX) record_error(p.kv.status, ST_BAD_PAGE);
+                return nowhere;
+            };
+            int32_t page_k = page_of(0), page_v = page_k, row_k = 0, row_v = 0;  // pages of the next batch, rows of this one
             auto load = [&](auto is_v, int32_t tile) {
                 constexpr bool V = decltype(is_v)::value;
+                constexpr int TOKS = V ? Sh::VTOK : Sh::KTOK, CH = V ? VCH : KCH;
+                constexpr uint32_t ROW = V ? (Q8 ? CV : 128) : 128;      // bytes of a box row
                 const uint32_t slot = Q8 ? rslot : pos.slot(V), phase = Q8 ? rphase : pos.phase(V);
-                const int32_t page = V ? page_v : page_k;
-                int32_t y = nowhere;
-                if (static_cast<uint32_t>(page) < static_cast<uint32_t>(p.kv.num_pages))
-                    y = (page << p.kv.page_shift) + ((V ? off_v : off_k) + tile * CH_TILE + tok0 & (P - 1));
-                else if (page != INT32_MAX)
-                    record_error(p.kv.status, ST_BAD_PAGE);
-                if (tile + 1 < n) (V ? page_v : page_k) = page_of(is_v, tile + 1);
+                const int32_t in = tile & (batch - 1);
+                if (in == 0) {
+                    (V ? row_v : row_k) = row_of(V ? page_v : page_k, tile);
+                    (V ? page_v : page_k) = page_of(tile + batch);
+                }
+                const int32_t row = V ? row_v : row_k;
                 if (!warp_wait(&empty[slot], phase ^ 1u, abort, lim)) {
                     ok = false;
                     return;
                 }
                 uint32_t bar;
-                if constexpr (Q8) {
+                const bool local = Q8 || (V && w.cut(tile, CH_TILE));
+                if (Q8) {
                     bar = smem_u32(&c.raw_full[slot]);
-                    if (lane == 0) mbar_arrive_expect_tx(&c.raw_full[slot], BYTES);
-                } else if (V && w.cut(tile, CH_TILE)) {
+                } else if (local) {
                     // the helpers clear rows of this one before the products see it
                     bar = smem_u32(&c.bnd[nb & 7u]);
-                    if (lane == 0) mbar_arrive_expect_tx(&c.bnd[nb & 7u], BYTES);
                     ++nb;
                 } else {
                     bar = full0 + slot * 8u;
-                    if (lane == 0) cluster_arrive_expect_tx(bar, BYTES);
+                }
+                const uint32_t dst = dst0 + slot * BYTES;
+                const int32_t z = V ? (w.g * D + rank * (D / 2)) / CV : w.g * (D / CK);
+                // a key slot holds the rank's half of the tile: of one piece, one piece, or half of them
+                if ((TOKS >> sh) <= 1) {
+                    const int32_t y = __shfl_sync(0xffffffffu, row, V ? in : sh == 7 ? in : 2 * in + rank);
+                    if (elect_one()) {
+                        if (local) mbar_expect_tx_at(bar, BYTES);
+                        else cluster_arrive_expect_tx(bar, BYTES);
+                        tma_load_3d_pair(dst, V ? &tv : &tk, bar,
+                                         static_cast<int32_t>(static_cast<uint32_t>(y) + (!V && sh == 7 ? rank * 64u : 0u)), z);
+                    }
+                } else {
+                    // a lane for each piece and chunk
+                    const int32_t lp = (V ? 7 : 6) - sh, ch = lane >> lp, i = lane & ((1 << lp) - 1);
+                    const int32_t y = __shfl_sync(0xffffffffu, row, (in << ld) + (V ? 0 : rank << (ld - 1)) + i);
+                    if (lane == 0) {
+                        if (local) mbar_expect_tx_at(bar, BYTES);
+                        else cluster_arrive_expect_tx(bar, BYTES);
+                    }
+                    __syncwarp();
+                    if (ch < CH) tma_load_3d_pair(dst + (ch * TOKS + (i << sh)) * ROW, V ? &tv : &tk, bar, y, z + ch);
                 }
                 __syncwarp();
-                if (V ? ch_v < VCH : ch_k < KCH)
-                    tma_load_2d_pair(dst0 + slot * BYTES + (V ? at_v : at_k), V ? &tv : &tk, bar, w.g * D + (V ? x_v : x_k), y);
                 if (Q8) {
                     used |= 1u << rslot;
                     last = (last & ~(1u << rslot)) | (rphase << rslot);
@@ -531,13 +560,10 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                     pos.next(V);
                 }
             };
-            page_k = page_of(std::false_type{}, 0);
-            page_v = page_of(std::true_type{}, 0);
             // the order of slot_at
             const int32_t lead = min(Sh::LEAD, n);
-            for (int32_t j = 0; ok && j < lead; ++j) load(std::false_type{}, j);
-            for (int32_t j = 0; ok && j < n; ++j) {
-                load(std::true_type{}, j);
+            for (int32_t j = -lead; ok && j < n; ++j) {
+                if (j >= 0) load(std::true_type{}, j);
                 if (ok && j + lead < n) load(std::false_type{}, j + lead);
             }
         }
@@ -805,20 +831,28 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
             const int32_t tok = by_group(p, vr), pos = w.p0 + tok;
             const int32_t first = p.window > 0 ? max(0, pos - p.window + 1) : 0;
             const bool live = lq * 32 < mine;                  // some row of this warp is in use
+            // the warp's first row sees the least at the end, the last one at the start
+            const int32_t w_hi = __shfl_sync(0xffffffffu, pos, 0), w_lo = __shfl_sync(0xffffffffu, first, 31);
             float m = -INFINITY, l = 0.0f;
             for (int32_t j = (grp - it) & 1; ok && j < n; j += 2) {
                 const uint32_t i = it + j;                     // tile i & 1 == grp
                 ok = warp_wait(&c.s_full[grp], (i >> 1) & 1u, abort, lim);
                 const int32_t base = (w.j0 + j) * CH_TILE;
-                const int32_t hi = pos - base, lo = first - base;              // visible: lo <= column <= hi
-                const bool masked = __any_sync(0xffffffffu, hi < CH_TILE - 1 || lo > 0);
+                const bool load = ok && live;
                 uint32_t s[4][32];
-                float mx = -INFINITY;
-                if (ok && live) {
+                float a[4];
+                if (load) {
                     tc_fence_after();
-                    float a[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) a[k] = tmem_ld_max_x32(ts + k * 32u, s[k]);
+                }
+                // while the scores come: the maximum in use at the tile before, and
+                // P's columns, free when the tile before last is done with them
+                if (ok && i > 0) ok = warp_wait(&c.m_out[grp ^ 1][lq], ((i - 1) >> 1) & 1u, abort, lim);
+                const float mp = j > 0 ? c.mrow[grp ^ 1][row] : -INFINITY;
+                if (ok && i > 1) ok = o_done(i - 2);
+                float mx = -INFINITY;
+                if (load) {
                     tmem_ld_wait();
                     mx = fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3]));
                 }
@@ -827,8 +861,10 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                     __syncwarp();
                     if (ok && lane == 0) cluster_arrive(s_free0);
                 }
-                if (ok && live && masked) {
-                    float a[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                if (load && (base + CH_TILE - 1 > w_hi || base < w_lo)) {
+                    const int32_t hi = pos - base, lo = first - base;          // visible: lo <= column <= hi
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) a[k] = -INFINITY;
 #pragma unroll
                     for (int e = 0; e < CH_TILE; ++e) {
                         if (e > hi || e < lo) s[e >> 5][e & 31] = 0xff800000u;           // -inf
@@ -836,16 +872,11 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                     }
                     mx = fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3]));
                 }
-                // the maximum in use at the tile before, and the one for this tile
-                if (ok && i > 0) ok = warp_wait(&c.m_out[grp ^ 1][lq], ((i - 1) >> 1) & 1u, abort, lim);
-                const float mp = j > 0 ? c.mrow[grp ^ 1][row] : -INFINITY;
                 const bool grow = (mx - mp) * cs > RESCALE;
                 const float mi = grow ? mx : mp;
-                c.mrow[grp][row] = mi;
+                c.mrow[grp][row] = mi;                         // the maximum in use at this tile
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&c.m_out[grp][lq]);
-                // P's columns are free when the tile before last is done with them
-                if (ok && i > 1) ok = o_done(i - 2);
                 tc_fence_after();
                 if (ok && live && j > 0 && __any_sync(0xffffffffu, grow)) {
                     // only here the product before must have ended
@@ -886,8 +917,9 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                             const __half2 h = __floats2half2_rn(z.x, z.y);
                             o[e] = *reinterpret_cast<const uint32_t *>(&h);
                         }
+                        // (by now the first half's stores are done: no wait for them)
+                        if (k == 2) give(0);
                         tmem_st_x16(tp + k * 16u, o);
-                        if (k == 1) give(0);
                     }
                     l += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
                 }
@@ -1000,12 +1032,16 @@ size_t chunk_workspace_bytes(int32_t rows, int32_t group, int32_t head_dim)
     return ws_o<CH_ROWS, CHUNK_MAX_PAIRS>() + size_t{2} * CHUNK_MAX_PAIRS * chunk_part_rows(rows, group) * head_dim * 4;
 }
 
-// tokens per box of the K and V tensor maps
-void chunk_boxes(int32_t head_dim, int32_t page_tokens, int32_t *box_k, int32_t *box_v)
+// Tensor maps of K and V: `row` bytes of a token and `chunks` such rows, of `box`
+// tokens, per copy.
+void chunk_boxes(int32_t head_dim, int32_t page_tokens, bool e4m3, ChunkBox *k, ChunkBox *v)
 {
-    (void)head_dim;
-    *box_k = std::min(page_tokens, CH_TILE / 2);
-    *box_v = std::min(page_tokens, CH_TILE);
+    k->row = 128;
+    k->box = std::min(page_tokens, CH_TILE / 2);
+    k->chunks = k->box == CH_TILE / 2 ? head_dim * (e4m3 ? 1 : 2) / k->row : 1;
+    v->row = e4m3 ? head_dim / 2 : 128;
+    v->box = std::min(page_tokens, CH_TILE);
+    v->chunks = v->box == CH_TILE ? head_dim / 2 * (e4m3 ? 1 : 2) / v->row : 1;
 }
 
 int launch_chunk(const ChunkParams &p, const void *tk, const void *tv, int sms, bool overlap, void *stream)

@@ -183,8 +183,8 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
                         const int32_t ya = __shfl_sync(0xffffffffu, row[0], first & 31);
                         const int32_t yb = __shfl_sync(0xffffffffu, row[1], first & 31);
                         if (i < boxes)
-                            tma_load_2d(dst + (v ? HALF : 0u) + ch * (CR_TILE * 128) + first * 128, v ? &tv : &tk, &c.full[slot],
-                                        w.g * D + ch * (128 / Sh::ES), first < 32 ? ya : yb);
+                            tma_load_3d(dst + (v ? HALF : 0u) + ch * (CR_TILE * 128) + first * 128, v ? &tv : &tk, &c.full[slot],
+                                        0, first < 32 ? ya : yb, w.g * Sh::CHUNKS + ch);
                     }
                     used |= 1u << slot;
                     last = (last & ~(1u << slot)) | (phase << slot);

@@ -249,16 +249,18 @@ int launch_attend(const AttendParams &p, void *stream);
 int launch_kv_store(const KvParams &p, const void *k, int64_t k_stride, const void *v, int64_t v_stride, int sms,
                     void *stream);
 int launch_kv_load(const KvParams &p, void *k, int64_t k_stride, void *v, int64_t v_stride, int sms, void *stream);
-// tk, tv: 2-D tensor maps of the caches [num_pages * page_tokens][hkv * head_dim]
-// with boxes of 128 bytes (FP16: 128-byte swizzle; the codes of half a 128-wide
-// head: 64 bytes) x chunk_boxes() tokens
+// tk, tv: tensor maps of the caches as [pieces of a token][tokens][bytes], with the
+// piece and the box of chunk_boxes(); FP16: 128-byte swizzle.
+struct ChunkBox {
+    int32_t row, box, chunks;            // bytes of a piece; tokens and pieces per copy
+};
 constexpr int32_t CHUNK_MAX_PAIRS = 80;
 int launch_chunk(const ChunkParams &p, const void *tk, const void *tv, int sms, bool overlap, void *stream);
 int32_t chunk_part_rows(int32_t rows, int32_t group);
 size_t chunk_workspace_bytes(int32_t rows, int32_t group, int32_t head_dim);
-void chunk_boxes(int32_t head_dim, int32_t page_tokens, int32_t *box_k, int32_t *box_v);
-// The kernel for few rows (units of 16 pairs); tk, tv: boxes of 128 bytes x
-// chunk_rows_box() tokens, 128-byte swizzle for both cache types.
+void chunk_boxes(int32_t head_dim, int32_t page_tokens, bool e4m3, ChunkBox *k, ChunkBox *v);
+// The kernel for few rows (units of 16 pairs); tk, tv: the same with pieces of 128
+// bytes, one per copy, chunk_rows_box() tokens, swizzled for both cache types.
 constexpr int32_t CHUNK_MAX_CTAS = 160;
 int launch_chunk_rows(const ChunkParams &p, const void *tk, const void *tv, int sms, bool overlap, void *stream);
 int32_t chunk_rows_part_rows(int32_t rows, int32_t group);
