@@ -109,6 +109,7 @@ struct Shape {
     static constexpr int NK = OWN_P ? NS / 2 : NS, NV = OWN_P ? NS - NK : 1;   // slots 0 .. NK - 1, then the values'
     static constexpr uint32_t TM_P = OWN_P ? 384 : TM_S, P_STRIDE = OWN_P ? 64 : 128;
     static constexpr int LEAD = OWN_P ? 3 : 2;                         // key tiles loaded before the first value tile
+    static constexpr bool HELP_OUT = !Q8;                              // the helpers write a unit's output
 };
 
 // A role's place in the ring of slots (one ring, or one for keys and one for
@@ -136,8 +137,12 @@ struct Ctrl {
     SegRing segs;
     uint64_t full[MAX_SLOTS], empty[MAX_SLOTS], raw_full[RAWS], raw_empty[RAWS], bnd[8];
     uint64_t s_full[2], s_free[2], p_full[2][2], o_done[2], m_out[2][4], q_full[2], q_free[2], drain;
+    uint64_t o_last, o_free, f_full[2], f_free[2];
     alignas(8) float mrow[2][CH_HALF];       // [tile parity][row]: maximum in use at the group's last tile; sums at a segment's end
-    alignas(8) uint16_t scale[2][CH_TILE];   // [slot parity][token]: FP16 scale (E4M3)
+    union {
+        uint16_t scale[2][CH_TILE];          // [slot parity][token]: FP16 scale (E4M3)
+        float factor[2][CH_HALF];            // [segment parity][row]: what the output is multiplied by (FP16 cache)
+    };
     Share share;
     uint32_t tmem;
     int32_t abort;
@@ -314,6 +319,17 @@ __device__ __forceinline__ float tmem_ld_max_x32(uint32_t taddr, uint32_t (&v)[3
     return m;
 }
 
+__device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&v)[16])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(taddr)
+        : "memory");
+}
+
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // two FP32 lanes at once
@@ -432,6 +448,12 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
             mbar_init(&c.segs.empty[i], CH_ROLES);
         }
         mbar_init(&c.drain, 1);
+        mbar_init(&c.o_last, 1);
+        mbar_init(&c.o_free, 2 * CH_HELPERS);                 // in the first CTA, for both
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&c.f_full[i], 4);
+            mbar_init(&c.f_free[i], CH_HELPERS);
+        }
         c.abort = 0;
         fence_barrier_init();
     }
@@ -620,8 +642,10 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
             __syncwarp();
         };
         // O (+)= P(i) . V(i)
-        auto values = [&](uint32_t i, bool first) {
+        auto values = [&](uint32_t i, bool first, bool last) {
             const uint32_t slot = ringpos.slot(true);
+            // the unit before has been read
+            if (Sh::HELP_OUT && first && seg > 0) ok = ok && warp_wait(&c.o_free, (seg - 1) & 1u, abort, lim);
             ok = ok && warp_wait(&c.full[slot], ringpos.phase(true), abort, lim);
             ok = ok && warp_wait(&c.p_full[i & 1u][0], (i >> 1) & 1u, abort, lim);
             if (!ok) return;
@@ -642,6 +666,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                     if (half == 1) {
                         umma2_commit(&c.o_done[i & 1u]);
                         umma2_commit(&c.empty[slot]);
+                        if (Sh::HELP_OUT && last) umma2_commit(&c.o_last);
                     }
                 }
                 __syncwarp();
@@ -659,14 +684,14 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                         if (i > 1) ok = warp_wait(&c.s_free[i & 1u], ((i - 2) >> 1) & 1u, abort, lim);
                         scores(i, j == n - 1);
                     } else {
-                        values(i, j == 0);
+                        values(i, j == 0, j == n - 1);
                     }
                 }
             } else {
                 scores(it, n == 1);
                 if (n > 1) scores(it + 1, n == 2);
                 for (int32_t j = 0; ok && j < n; ++j) {
-                    values(it + j, j == 0);
+                    values(it + j, j == 0, j == n - 1);
                     if (j + 2 < n) scores(it + j + 2, j + 3 == n);
                 }
             }
@@ -688,6 +713,61 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
         RingPos<Sh> pos;
         uint32_t seg = 0, rslot = 0, rphase = 0, ring0 = 0, nb = 0;         // ring0: the segment's first slot (OWN_P: value slot)
         bool ok = true;                                       // false: keep to the barriers, do nothing
+        // A unit's output (or its part of it), while the softmax is at the next unit
+        // (by the softmax warps themselves, a unit's end took them 2,400 clocks of
+        // code that had left the instruction cache).  Warp w: TMEM lane quarter w % 4.
+        Seg before;
+        before.n = 0;
+        auto write_out = [&]() {
+            if (Sh::HELP_OUT && before.n > 0 && ok) {
+                const uint32_t u = seg - 1;                    // its number
+                const int lq = warp & 3, ur = rank * CH_HALF + ht;
+                ok = warp_wait(&c.f_full[u & 1u], (u >> 1) & 1u, abort, lim) && warp_wait(&c.o_last, u & 1u, abort, lim);
+                if (!ok) return;
+                tc_fence_after();
+                const float f = c.factor[u & 1u][ht];
+                if (rank * CH_HALF + lq * 32 < before.rows) {
+                    const bool in = ur < before.rows, whole = before.place < 0;
+                    const bool out_32 = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;      // (16 bytes are promised)
+                    const int32_t v = before.v0 + ur, tok = by_group(p, v), h = v - tok * p.group;
+                    uint8_t *dst = whole ? static_cast<uint8_t *>(p.out) +
+                                               ((static_cast<int64_t>(before.s0) + tok) * p.hq + before.g * p.group + h) * D * 2
+                                         : p.ws + ws_o<CH_ROWS, CHUNK_MAX_PAIRS>() +
+                                               (static_cast<int64_t>(before.place) * p.ws_rows + ur) * D * 4;
+                    const uint32_t to = tmem + TM_O + (static_cast<uint32_t>(lq * 32) << 16);
+#pragma unroll 1
+                    for (int k = 0; k < D / 16; ++k) {
+                        uint32_t x[16];
+                        tmem_ld_x16(to + k * 16u, x);
+                        tmem_ld_wait();
+                        if (k == D / 16 - 1) {                 // O is read
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) {
+                                cluster_arrive(of_first(&c.o_free));
+                                mbar_arrive(&c.f_free[u & 1u]);
+                            }
+                        }
+                        if (!in) continue;
+                        if (whole) {
+#pragma unroll
+                            for (int i = 0; i < 16; i += 2) {
+                                const __half2 hh = __floats2half2_rn(__uint_as_float(x[i]) * f, __uint_as_float(x[i + 1]) * f);
+                                x[i >> 1] = *reinterpret_cast<const uint32_t *>(&hh);
+                            }
+                            store32(dst + 32 * k, x, out_32);
+                        } else {
+                            store32(dst + 64 * k, x, true);
+                            store32(dst + 64 * k + 32, x + 8, true);
+                        }
+                    }
+                } else if (lane == 0) {
+                    cluster_arrive(of_first(&c.o_free));
+                    mbar_arrive(&c.f_free[u & 1u]);
+                }
+                __syncwarp();
+            }
+        };
         while (next_segment()) {
             const int32_t n = w.n;
             const uint32_t qb = Sh::QBUFS == 2 ? seg & 1u : 0u, quse = Sh::QBUFS == 2 ? seg >> 1 : seg;   // buffer, its uses before
@@ -716,6 +796,8 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                 __syncwarp();
                 if (lane == 0) cluster_arrive(of_first(&c.q_full[qb]));
             }
+            write_out();
+            before = w;
             ++seg;
             if constexpr (!Q8) {
                 // Rows of V that nothing attends may hold anything (the ends of
@@ -805,6 +887,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                 }
             }
         }
+        write_out();
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         // ------------------------------------------------------------- softmax
@@ -815,7 +898,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
         const uint32_t tp = tmem + Sh::TM_P + grp * Sh::P_STRIDE + lane_base;
         const float cs = p.scale * 1.4426950408889634f;        // scores in powers of two
         const uint32_t p_full0 = of_first(&c.p_full[grp][0]), s_free0 = of_first(&c.s_free[grp]);
-        uint32_t it = 0;                                       // tiles before the segment
+        uint32_t it = 0, seg = 0;                              // tiles before the segment, segments
         // Waits until the second product of tile i is done.  A parity wait is right
         // while the barrier is in that phase or just past it.  Past the one
         // before: the product of tile i - 1 has been seen to end, and products end
@@ -928,7 +1011,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
             }
             it += n;
             // the segment's sums: its rows' output, or its part of it
-            if (ok) ok = (it < 2 || o_done(it - 2)) && o_done(it - 1);
+            if (!Sh::HELP_OUT && ok) ok = (it < 2 || o_done(it - 2)) && o_done(it - 1);
             named_barrier(BAR_PAIR + lq, 64);
             // both groups' sums at the last tile's maximum, exchanged in place of the maxima
             const float mlast = c.mrow[(it - 1) & 1u][row];
@@ -937,22 +1020,29 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
             c.mrow[grp][row] = l;
             named_barrier(BAR_PAIR + lq, 64);
             l += c.mrow[grp ^ 1][row];
-            if (ok && live) {
+            if (grp == 0 && row < mine && w.place >= 0)
+                *reinterpret_cast<float2 *>(p.ws + WS_ML + (static_cast<int64_t>(w.place) * CH_ROWS + rank * CH_HALF + row) * 8) =
+                    make_float2(mlast == -INFINITY ? -INFINITY : mlast * cs, l);
+            const float inv = w.place >= 0 ? 1.0f : l > 0.0f ? 1.0f / l : 0.0f;
+            if constexpr (Sh::HELP_OUT) {
+                // handed to the helpers
+                if (grp == 0 && ok) {
+                    if (seg > 1) ok = warp_wait(&c.f_free[seg & 1u], ((seg >> 1) - 1) & 1u, abort, lim);
+                    c.factor[seg & 1u][row] = inv;
+                    __syncwarp();
+                    if (ok && lane == 0) mbar_arrive(&c.f_full[seg & 1u]);
+                }
+                ++seg;
+            } else if (ok && live) {
                 tc_fence_after();
                 const uint32_t to = tmem + TM_O + lane_base + grp * OC;
                 const bool in = row < mine, whole = w.place < 0;
-                const float inv = l > 0.0f ? 1.0f / l : 0.0f;
                 const int32_t h = vr - tok * p.group, ur = rank * CH_HALF + row;
                 __half *out = static_cast<__half *>(p.out) +
                               ((static_cast<int64_t>(w.s0) + tok) * p.hq + w.g * p.group + h) * D + grp * OC;
                 const bool out_32 = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;      // (16 bytes are promised)
-                float *part = nullptr;
-                if (!whole) {
-                    part = reinterpret_cast<float *>(p.ws + ws_o<CH_ROWS, CHUNK_MAX_PAIRS>()) + (static_cast<int64_t>(w.place) * p.ws_rows + ur) * D + grp * OC;
-                    if (in && grp == 0)
-                        *reinterpret_cast<float2 *>(p.ws + WS_ML + (static_cast<int64_t>(w.place) * CH_ROWS + ur) * 8) =
-                            make_float2(mlast == -INFINITY ? -INFINITY : mlast * cs, l);
-                }
+                float *part = reinterpret_cast<float *>(p.ws + ws_o<CH_ROWS, CHUNK_MAX_PAIRS>()) +
+                              (static_cast<int64_t>(w.place) * p.ws_rows + ur) * D + grp * OC;
                 // rolled: a unit's end is code that has left the instruction cache
 #pragma unroll 1
                 for (int k = 0; k < OC / 32; ++k) {
