@@ -140,7 +140,7 @@ struct Ctrl {
     uint64_t o_last, o_free, f_full[2], f_free[2];
     alignas(8) float mrow[2][CH_HALF];       // [tile parity][row]: maximum in use at the group's last tile; sums at a segment's end
     union {
-        uint16_t scale[2][CH_TILE];          // [slot parity][token]: FP16 scale (E4M3)
+        uint32_t scale[2][CH_TILE];          // [slot parity][token]: FP16 scale, twice (E4M3)
         float factor[2][CH_HALF];            // [segment parity][row]: what the output is multiplied by (FP16 cache)
     };
     Share share;
@@ -150,17 +150,9 @@ struct Ctrl {
 
 // ------------------------------------------------------------------- pieces --
 
-// Slot e of a segment of n tiles, in the order of use: LEAD key tiles, then
-// value and key tiles in turn, then the value tiles left,
-// e.g. K(0) K(1) V(0) K(2) V(1) ... K(n-1) V(n-2) V(n-1).
-template <int LEAD>
-__device__ __forceinline__ void slot_at(int32_t e, int32_t n, bool *is_v, int32_t *tile)
-{
-    const int32_t lead = min(LEAD, n), r = e - lead, turns = 2 * (n - lead);
-    *is_v = r >= 0 && (r >= turns || (r & 1) == 0);
-    *tile = r < 0 ? e : r >= turns ? r - (n - lead) : (r >> 1) + ((r & 1) ? lead : 0);
-}
-
+// Slots of a segment of n tiles, in the order of use: LEAD key tiles, then value
+// and key tiles in turn, then the value tiles left,
+// e.g. K(0) K(1) V(0) K(2) V(1) ... K(n-1) V(n-2) V(n-1); here that of a value tile.
 template <int LEAD>
 __device__ __forceinline__ int32_t slot_of_v(int32_t tile, int32_t n)
 {
@@ -359,7 +351,7 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b)
 // token's 128 (64) dims; a thread keeps its place in the row and steps over rows,
 // so that all its addresses are one base and constants.
 template <int D, bool V>
-__device__ __forceinline__ void codes_to_half(const uint8_t *src, uint8_t *dst, const uint16_t *scale, int ht, int a, int z)
+__device__ __forceinline__ void codes_to_half(const uint8_t *src, uint8_t *dst, const uint32_t *scale, int ht, int a, int z)
 {
     constexpr int SH = V && D == 128 ? 2 : 3;                 // log2 of a row's 16-code pieces
     constexpr int TOKS = V ? CH_TILE : 64, STEP = 128 >> SH;  // tokens of the slot, rows per pass
@@ -381,7 +373,7 @@ __device__ __forceinline__ void codes_to_half(const uint8_t *src, uint8_t *dst, 
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int blk = (STEP * (i0 + i)) / TOKS, tk = (STEP * (i0 + i)) % TOKS;     // 128 dims, token - r0
-            const uint32_t sc = scale[r0 + tk] * 0x10001u;
+            const uint32_t sc = scale[r0 + tk];
             const uint32_t cw[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
             uint32_t o[8];
 #pragma unroll
@@ -582,7 +574,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                     pos.next(V);
                 }
             };
-            // the order of slot_at
+            // the order of slots
             const int32_t lead = min(Sh::LEAD, n);
             for (int32_t j = -lead; ok && j < n; ++j) {
                 if (j >= 0) load(std::true_type{}, j);
@@ -711,7 +703,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
         // --------------------- queries, cut value tiles, E4M3 codes to FP16 tiles
         const int ht = t - CH_HELP * 32;                      // 0 .. 127
         RingPos<Sh> pos;
-        uint32_t seg = 0, rslot = 0, rphase = 0, ring0 = 0, nb = 0;         // ring0: the segment's first slot (OWN_P: value slot)
+        uint32_t seg = 0, rslot = 0, rphase = 0, par = 0, ring0 = 0, nb = 0;     // ring0: the segment's first slot (OWN_P: value slot)
         bool ok = true;                                       // false: keep to the barriers, do nothing
         // A unit's output (or its part of it), while the softmax is at the next unit
         // (by the softmax warps themselves, a unit's end took them 2,400 clocks of
@@ -828,49 +820,45 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
             } else {
                 const int32_t *bt = p.kv.block_table + static_cast<int64_t>(w.b) * p.kv.max_pages;
                 // Scale bytes of the slot's tokens, one per thread, looked up ahead:
-                // the page two slots, the byte one.
-                struct Look {
-                    bool v;
-                    int32_t tile, tok, page;                   // page: -1 none
+                // the page two tiles, the byte one.  Keys and values have their own,
+                // so that nothing depends on the order of the slots (with one chain
+                // over both, finding tile and kind of the slot two ahead cost 600
+                // clocks a slot, next to 950 for the codes).
+                const int32_t tok_v = w.j0 * CH_TILE + ht, tok_k = tok_v + rank * Sh::KTOK;
+                auto page_of = [&](auto is_v, int32_t tile) -> int32_t {
+                    constexpr bool V = decltype(is_v)::value;
+                    const int32_t tok = (V ? tok_v : tok_k) + tile * CH_TILE;
+                    const bool seen = (V || ht < Sh::KTOK) && tile < n && tok >= w.lo_tok && tok <= w.hi_tok;
+                    return seen ? __ldg(bt + (tok >> p.kv.page_shift)) : -1;
                 };
-                auto look = [&](int32_t e) {
-                    Look k{false, 0, 0, -1};
-                    if (e < 2 * n) {
-                        slot_at<Sh::LEAD>(e, n, &k.v, &k.tile);
-                        k.tok = (w.j0 + k.tile) * CH_TILE + (k.v ? 0 : rank * Sh::KTOK) + ht;
-                        if (ht < (k.v ? Sh::VTOK : Sh::KTOK) && k.tok >= w.lo_tok && k.tok <= w.hi_tok)
-                            k.page = __ldg(bt + (k.tok >> p.kv.page_shift));
-                    }
-                    return k;
+                auto byte_of = [&](auto is_v, int32_t tile, int32_t page) -> uint32_t {
+                    constexpr bool V = decltype(is_v)::value;
+                    if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(p.kv.num_pages)) return 127u;
+                    const int32_t tok = (V ? tok_v : tok_k) + tile * CH_TILE;
+                    const int32_t at = (page << p.kv.page_shift) + (tok & (p.kv.page_tokens - 1));
+                    return __ldg((V ? p.kv.v_scale : p.kv.k_scale) + (static_cast<int64_t>(at) * p.kv.hkv + w.g));
                 };
-                auto byte_of = [&](const Look &k) -> uint32_t {
-                    if (k.page < 0 || k.page >= p.kv.num_pages) return 127u;
-                    return __ldg((k.v ? p.kv.v_scale : p.kv.k_scale) +
-                                 ((static_cast<int64_t>(k.page) << p.kv.page_shift) + (k.tok & (p.kv.page_tokens - 1))) * p.kv.hkv + w.g);
-                };
-                Look now = look(0), next = look(1);
-                uint32_t byte = byte_of(now);
-                uint32_t par = 0;
-                for (int32_t e = 0; e < 2 * n; ++e) {
-                    const bool v = now.v;
-                    const int32_t tok0 = (w.j0 + now.tile) * CH_TILE;  // V: rows outside lo_tok .. hi_tok are cleared
-                    const int32_t a = w.lo_tok - tok0, z = w.hi_tok + 1 - tok0;
-                    // 2^(byte - 127) as FP16 (2^-15 is subnormal)
+                uint32_t byte_k = byte_of(std::false_type{}, 0, page_of(std::false_type{}, 0));
+                uint32_t byte_v = byte_of(std::true_type{}, 0, page_of(std::true_type{}, 0));
+                int32_t page_k = page_of(std::false_type{}, 1), page_v = page_of(std::true_type{}, 1);
+                auto turn = [&](auto is_v, int32_t tile) {
+                    constexpr bool V = decltype(is_v)::value;
+                    uint32_t &byte = V ? byte_v : byte_k;
+                    int32_t &page = V ? page_v : page_k;
+                    // 2^(byte - 127) as FP16 (2^-15 is subnormal), twice
                     const int x = max(112, min(135, static_cast<int>(byte))) - 127;
-                    c.scale[par][ht] = static_cast<uint16_t>(x >= -14 ? (x + 15) << 10 : 0x200);
-                    byte = byte_of(next);                              // in flight under the conversion
-                    now = next;
-                    next = look(e + 2);
-                    const uint32_t slot = pos.slot(v);
+                    c.scale[par][ht] = (x >= -14 ? (x + 15) << 10 : 0x200) * 0x10001u;
+                    byte = byte_of(is_v, tile + 1, page);      // in flight until the next tile
+                    page = page_of(is_v, tile + 2);
+                    const uint32_t slot = pos.slot(V);
                     if (ok)
                         ok = __all_sync(0xffffffffu, mbar_wait(&c.raw_full[rslot], rphase, abort, lim) &&
-                                                         mbar_wait(&c.empty[slot], pos.phase(v) ^ 1u, abort, lim));
+                                                         mbar_wait(&c.empty[slot], pos.phase(V) ^ 1u, abort, lim));
                     named_barrier(BAR_HELP, 32 * CH_HELPERS);          // the scales are in
                     if (ok) {
-                        const uint8_t *src = raw + rslot * RAW;
-                        uint8_t *dst = ring + slot * SLOT;
-                        if (v) codes_to_half<D, true>(src, dst, c.scale[par], ht, a, z);
-                        else codes_to_half<D, false>(src, dst, c.scale[par], ht, 0, Sh::KTOK);
+                        // V: rows outside lo_tok .. hi_tok are cleared
+                        const int32_t tok0 = (w.j0 + tile) * CH_TILE, a = w.lo_tok - tok0, z = w.hi_tok + 1 - tok0;
+                        codes_to_half<D, V>(raw + rslot * RAW, ring + slot * SLOT, c.scale[par], ht, V ? a : 0, V ? z : Sh::KTOK);
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0) {
@@ -879,11 +867,16 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                         }
                     }
                     par ^= 1u;
-                    pos.next(v);
+                    pos.next(V);
                     if (++rslot == RAWS) {
                         rslot = 0;
                         rphase ^= 1u;
                     }
+                };
+                const int32_t lead = min(Sh::LEAD, n);                 // the order of slots
+                for (int32_t j = -lead; j < n; ++j) {
+                    if (j >= 0) turn(std::true_type{}, j);
+                    if (j + lead < n) turn(std::false_type{}, j + lead);
                 }
             }
         }
