@@ -703,7 +703,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
         // --------------------- queries, cut value tiles, E4M3 codes to FP16 tiles
         const int ht = t - CH_HELP * 32;                      // 0 .. 127
         RingPos<Sh> pos;
-        uint32_t seg = 0, rslot = 0, rphase = 0, par = 0, ring0 = 0, nb = 0;     // ring0: the segment's first slot (OWN_P: value slot)
+        uint32_t seg = 0, rslot = 0, rphase = 0, par = 0, ring0 = 0, ring_b = 0, nb = 0;  // ring0: the next segment's first slot (OWN_P: value slot), ring_b: this one's
         bool ok = true;                                       // false: keep to the barriers, do nothing
         // A unit's output (or its part of it), while the softmax is at the next unit
         // (by the softmax warps themselves, a unit's end took them 2,400 clocks of
@@ -760,9 +760,8 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                 __syncwarp();
             }
         };
-        while (next_segment()) {
-            const int32_t n = w.n;
-            const uint32_t qb = Sh::QBUFS == 2 ? seg & 1u : 0u, quse = Sh::QBUFS == 2 ? seg >> 1 : seg;   // buffer, its uses before
+        auto load_q = [&](uint32_t number) {
+            const uint32_t qb = Sh::QBUFS == 2 ? number & 1u : 0u, quse = Sh::QBUFS == 2 ? number >> 1 : number;   // buffer, its uses before
             if (ok && quse > 0) ok = warp_wait(&c.q_free[qb], (quse - 1) & 1u, abort, lim);
             if (ok) {
                 // the warp's 32 rows: a lane finds one row's queries, then
@@ -788,36 +787,34 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                 __syncwarp();
                 if (lane == 0) cluster_arrive(of_first(&c.q_full[qb]));
             }
-            write_out();
-            before = w;
-            ++seg;
-            if constexpr (!Q8) {
-                // Rows of V that nothing attends may hold anything (the ends of
-                // loaded pages): zero weights must meet zeros.
+        };
+        // Rows of V that nothing attends may hold anything (the ends of loaded pages):
+        // zero weights must meet zeros.  r0: the segment's first slot.
+        auto clear = [&](const Seg &x, uint32_t r0, int32_t tile) {
+            if (!x.cut(tile, CH_TILE)) return;
+            if (ok) ok = warp_wait(&c.bnd[nb & 7u], (nb >> 3) & 1u, abort, lim);
+            ++nb;
+            const uint32_t vs = Sh::OWN_P ? Sh::NK + (r0 + tile) % Sh::NV : (r0 + slot_of_v<Sh::LEAD>(tile, x.n)) % NS;
+            if (ok) {
+                uint8_t *v = ring + vs * SLOT;
+                const int32_t a = x.lo_tok - (x.j0 + tile) * CH_TILE, z = x.hi_tok + 1 - (x.j0 + tile) * CH_TILE;
+                if (ht < a || ht >= z) {
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const int32_t tile = k == 0 ? 0 : n - 1;
-                    if ((k == 1 && n == 1) || !w.cut(tile, CH_TILE)) continue;
-                    if (ok) ok = warp_wait(&c.bnd[nb & 7u], (nb >> 3) & 1u, abort, lim);
-                    ++nb;
-                    const uint32_t vs = Sh::OWN_P ? Sh::NK + (ring0 + tile) % Sh::NV : (ring0 + slot_of_v<Sh::LEAD>(tile, n)) % NS;
-                    if (ok) {
-                        uint8_t *v = ring + vs * SLOT;
-                        const int32_t a = w.lo_tok - (w.j0 + tile) * CH_TILE, z = w.hi_tok + 1 - (w.j0 + tile) * CH_TILE;
-                        if (ht < a || ht >= z) {
+                    for (int ch = 0; ch < D / 128; ++ch)
 #pragma unroll
-                            for (int ch = 0; ch < D / 128; ++ch)
-#pragma unroll
-                                for (int i = 0; i < 8; ++i)
-                                    *reinterpret_cast<uint4 *>(v + (ch * CH_TILE + ht) * 128 + i * 16) = make_uint4(0u, 0u, 0u, 0u);
-                        }
-                        fence_proxy_async_smem();
-                    }
-                    named_barrier(BAR_HELP, 32 * CH_HELPERS);
-                    if (ok && ht == 0) cluster_arrive(of_first(&c.full[vs]));
+                        for (int i = 0; i < 8; ++i)
+                            *reinterpret_cast<uint4 *>(v + (ch * CH_TILE + ht) * 128 + i * 16) = make_uint4(0u, 0u, 0u, 0u);
                 }
-                ring0 = Sh::OWN_P ? (ring0 + n) % Sh::NV : (ring0 + 2 * n) % NS;
-            } else {
+                fence_proxy_async_smem();
+            }
+            named_barrier(BAR_HELP, 32 * CH_HELPERS);
+            if (ok && ht == 0) cluster_arrive(of_first(&c.full[vs]));
+        };
+        if constexpr (Q8) {
+            while (next_segment()) {
+                const int32_t n = w.n;
+                load_q(seg);
+                ++seg;
                 const int32_t *bt = p.kv.block_table + static_cast<int64_t>(w.b) * p.kv.max_pages;
                 // Scale bytes of the slot's tokens, one per thread, looked up ahead:
                 // the page two tiles, the byte one.  Keys and values have their own,
@@ -879,8 +876,23 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                     if (j + lead < n) turn(std::false_type{}, j + lead);
                 }
             }
+        } else {
+            while (true) {
+                const bool more = next_segment();
+                if (more) load_q(seg);
+                // with two buffers the next queries are loaded before the last value
+                // tile of a segment, which comes late
+                if (Sh::QBUFS == 2 && before.n > 1) clear(before, ring_b, before.n - 1);
+                write_out();
+                if (!more) break;
+                before = w;
+                ++seg;
+                ring_b = ring0;
+                ring0 = Sh::OWN_P ? (ring0 + w.n) % Sh::NV : (ring0 + 2 * w.n) % NS;
+                clear(w, ring_b, 0);
+                if (Sh::QBUFS == 1 && w.n > 1) clear(w, ring_b, w.n - 1);
+            }
         }
-        write_out();
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         // ------------------------------------------------------------- softmax
@@ -907,7 +919,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
             const int32_t tok = by_group(p, vr), pos = w.p0 + tok;
             const int32_t first = p.window > 0 ? max(0, pos - p.window + 1) : 0;
             const bool live = lq * 32 < mine;                  // some row of this warp is in use
-            // the warp's first row sees the least at the end, the last one at the start
+            // tokens that all rows of the warp see
             const int32_t w_hi = __shfl_sync(0xffffffffu, pos, 0), w_lo = __shfl_sync(0xffffffffu, first, 31);
             float m = -INFINITY, l = 0.0f;
             for (int32_t j = (grp - it) & 1; ok && j < n; j += 2) {

@@ -114,10 +114,23 @@ __device__ __forceinline__ T block_scan(T x, T *warp_total, int warp, int lane, 
 
 // A worker's share of the line.
 struct Share {
-    int64_t w0, w1, total;                   // w0 .. w1, the line's length
-    int32_t workers;                         // those that have work
+    int64_t w0, w1;
+    int64_t each;                            // the line's length, each * workers + rest,
+    int32_t workers, rest;                   // over the workers that have work, the first ones
     int32_t b, m, g, off;                    // the unit that w0 lies in, and w0's place in it
+
+    // length * worker / workers, rounded down
+    __device__ __forceinline__ int64_t start(int32_t worker) const
+    {
+        return each * worker + static_cast<uint32_t>(rest * worker) / static_cast<uint32_t>(workers);
+    }
 };
+
+// a / b for 0 <= a, 0 < b: the 64-bit division is a call of some hundred instructions.
+__device__ __forceinline__ int64_t divide(int64_t a, int32_t b)
+{
+    return a >> 32 ? a / b : static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b));
+}
 
 // Shared memory that find_work needs.
 template <typename G>
@@ -181,15 +194,20 @@ __device__ __forceinline__ void find_work(const ChunkParams &p, Share &c, FindSc
         cost *= p.kv.hkv;
     }
     int64_t at = block_scan<G>(cost, s.costs, warp, lane, &total);
-    // MIN_SHARE each at least: a smaller share costs more in the join than it
-    // saves here; and the workers with work are the first ones
-    const int32_t workers = static_cast<int32_t>(min((total + G::MIN_SHARE - 1) / G::MIN_SHARE, static_cast<int64_t>(n_workers)));
-    const int64_t w0 = me < workers ? total * me / workers : 0, w1 = me < workers ? total * (me + 1) / workers : 0;
+    // MIN_SHARE each at least: a smaller share costs more in the join than it saves here
+    const int32_t workers = total >= static_cast<int64_t>(n_workers) * G::MIN_SHARE
+                                ? n_workers : (static_cast<int32_t>(total) + G::MIN_SHARE - 1) / G::MIN_SHARE;
+    Share x;
+    x.workers = max(workers, 1);
+    x.each = divide(total, x.workers);
+    x.rest = static_cast<int32_t>(total - x.each * x.workers);
+    const int64_t w0 = me < workers ? x.start(me) : 0, w1 = me < workers ? x.start(me + 1) : 0;
     if (t == 0) {
         c.w0 = w0;
         c.w1 = w1;
-        c.total = total;
-        c.workers = workers;
+        c.each = x.each;
+        c.workers = x.workers;
+        c.rest = x.rest;
     }
     if (w0 < w1 && at <= w0 && w0 < at + cost) {
         for (;; ++m0) {
@@ -203,8 +221,8 @@ __device__ __forceinline__ void find_work(const ChunkParams &p, Share &c, FindSc
             if (w0 < at + static_cast<int64_t>(len) * p.kv.hkv) {
                 c.b = b0;
                 c.m = m0;
-                c.g = static_cast<int32_t>((w0 - at) / len);
-                c.off = static_cast<int32_t>((w0 - at) % len);
+                c.g = static_cast<int32_t>(divide(w0 - at, len));
+                c.off = static_cast<int32_t>(w0 - at - static_cast<int64_t>(c.g) * len);
                 break;
             }
             at += static_cast<int64_t>(len) * p.kv.hkv;
@@ -300,7 +318,7 @@ __device__ __forceinline__ void schedule(const ChunkParams &p, const Share &c, S
         if (x.n > 0 && head && rest > 0) {
             // the unit's other tiles lie in the next workers' shares
             split.parts = 1;
-            while (c.total * (me + split.parts) / c.workers < c.w1 + rest) ++split.parts;
+            while (c.start(me + split.parts) < c.w1 + rest) ++split.parts;
             split.rows = x.rows;
             split.s0 = x.s0;
             split.v0 = x.v0;
