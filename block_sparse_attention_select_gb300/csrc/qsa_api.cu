@@ -918,8 +918,12 @@ qsa_status check_batch(int32_t rows, int32_t n_reqs, const int32_t *seq_start, c
 }
 
 // Which attention kernel: units of 16 (token, query head) pairs read straight
-// from the cache's bytes while requests have no more than that on average, the
-// tensor-core pairs of SMs above.
+// from the cache's bytes while requests have no more than that on average, pairs
+// of SMs with units of 256 above.  On 64 single tokens over up to 32,768, 12 query
+// heads to a KV head, the first takes 299 us from the FP16 cache and 170 us from
+// the E4M3 cache, the second 298 and 466 us; with four times the pairs the first
+// reads the cache four times.  (An average, for the lengths are on the device: a
+// long prompt among many empty requests is slow, not wrong.)
 bool few_rows(int32_t rows, int32_t group, int32_t n_reqs)
 {
     return static_cast<int64_t>(rows) * group <= int64_t{16} * n_reqs;

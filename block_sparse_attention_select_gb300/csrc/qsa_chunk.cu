@@ -20,8 +20,8 @@
 // Work: the units' tiles, in the order (request, rows, KV head), form one line
 // that the CTA pairs share out evenly (each unit UNIT_COST tiles longer than it
 // is, for what it costs besides them: counted as 2, 3, 4 and 5 tiles, four prompts
-// of 4,096 tokens take 500, 453, 427 and 437 us), so one row over a long cache, a
-// batch of unequal requests and a long prompt all fill the card.  A unit that
+// of 4,096 tokens took 495, 483, 419 and 460 us on one warm card), so one row over
+// a long cache, a batch of unequal requests and a long prompt all fill the card.  A unit that
 // lies across pairs leaves unnormalised FP32 partial sums with their maxima in
 // the workspace (at most two per pair), which a second kernel joins.  Every
 // pair finds its share itself from seq_start and pos_start: no plan kernel and
@@ -31,9 +31,10 @@
 // through the block table, 9 issues the MMAs (in the first CTA of the pair; with
 // D = 128 warp 11 issues the second products, so that neither product waits for
 // what the other needs), 10 walks through the share and hands out its segments,
-// 12-15 load the queries, clear the value rows that nothing attends and, from
-// the E4M3 cache, turn the loaded codes into FP16 tiles.  K and V share a ring of
-// slots in the order of use; with D = 128 each has its own.
+// 12-15 load the queries, clear the value rows that nothing attends and write the
+// outputs or, from the E4M3 cache, turn the loaded codes into FP16 tiles (the
+// softmax warps then write the outputs).  K and V share a ring of slots in the
+// order of use; with D = 128 each has its own.
 //
 // Softmax warps 0-3 take the even tiles and 4-7 the odd ones (warp w: TMEM lane
 // quarter w % 4, a row per thread), so that one group's exponentials run beside
@@ -48,14 +49,15 @@
 // scores and the order is S(0) S(1) | O(0) S(2) | O(1) S(3) | ...
 //
 // What bounds it: with D = 256 and a long context the tensor cores (the
-// 1,616-row chunk over 29,000 tokens, 12 query heads to a KV head: 575 us, 1,950 TF/s, at the rate of
-// the library's large bf16 products).  With D = 128 a tile's products take half
-// as long and its exponentials the same, so the softmax warps' latency does (four
-// prompts of 4,096 tokens, 32 heads: 428 us, 1,280 TF/s; tensor pipe 48%, issue
-// slots 36%).  From the E4M3 cache the turning of codes into FP16 tiles (three
-// chunks of 517 over 12,345 tokens: 161 us, 1,210 TF/s).  A short call is the
-// ends of its units: two chunks of 1,023 tokens with a window of 1,000 take 41 us
-// where their products need 9.
+// 1,616-row chunk over 29,000 tokens, 12 query heads to a KV head: 575 us, 1,950
+// TF/s, tensor pipe 94% busy).  With D = 128 a tile's products take half as long
+// and its exponentials the same, so the latency of two softmax warps per scheduler
+// shows (four prompts of 4,096 tokens, 32 heads: 381 us, 1,440 TF/s; tensor pipe
+// 67%, issue slots 48%).  From the E4M3 cache the turning of codes into FP16 tiles
+// (three chunks of 517 over 12,345 tokens: 153 us, 1,270 TF/s, tensor pipe 59%).
+// A short call is the search for its work, its first loads and its last output:
+// two chunks of 1,023 tokens with a window of 1,000 take 42 us where their products
+// need 9.
 //
 // The accumulator is rescaled only when a row's maximum has grown by more than
 // 2^8 since the one in use: the sum uses the same stale maximum, so the result

@@ -23,6 +23,11 @@
 //   V: thread (r, q) reads piece r of chunk i of tokens 2 q, 2 q + 1, 2 q + 8 and
 //      2 q + 9; byte permutes pair up two tokens' values of a dim.
 // With the 128-byte swizzle both patterns touch all banks evenly.
+//
+// Bound by the loads: 64 requests' tokens over up to 32,768 tokens take 299 us from
+// the FP16 cache (6.48 TB/s) and 170 us from the E4M3 cache (6.2 TB/s; its scales
+// are single bytes 2 x hkv apart).  One token over 4,096 takes 14 us: the launch,
+// the search for its work, one memory latency each for table, keys and join.
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
