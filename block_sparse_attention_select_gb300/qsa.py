@@ -495,7 +495,7 @@ def chunk_attention(q, seq_start, pos_start, cache: KVCache, window: int = 0, sc
         raise ValueError("ws must be contiguous, on the cache's device")
     scale = cache.head_dim ** -0.5 if scale is None else float(scale)
     _call(cache, stream, load().qsa_chunk_attention, q.data_ptr(), qs, rows, hq, n, seq_start.data_ptr(),
-          pos_start.data_ptr(), cache.ref, int(window), scale, out.data_ptr(), ws.data_ptr(),
+          pos_start.data_ptr(), cache.ref, min(max(int(window), -1), 2 ** 31 - 1), scale, out.data_ptr(), ws.data_ptr(),
           ws.numel() * ws.element_size(), made=made)
     return out
 

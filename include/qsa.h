@@ -245,7 +245,8 @@ qsa_status qsa_block_select(const void *q, int32_t rows, int32_t H, const void *
  *
  * head_dim 128 or 256, page_tokens a power of two in [8, 256], 1 <= hkv <= 1024
  * (QSA_ERR_UNSUPPORTED otherwise); k and v 16-byte aligned; num_pages *
- * page_tokens and max_pages * page_tokens below 2^31.  n_reqs <= num_reqs.
+ * page_tokens and max_pages * page_tokens below 2^31 - 1.  n_reqs <= num_reqs and
+ * 65,535 (QSA_ERR_UNSUPPORTED above).
  * Device-side problems are reported by qsa_get_device_status(): a request whose
  * seq_start or pos_start is out of range (decreasing, past `rows`, negative,
  * past the block table) is skipped, a token whose page id is outside the cache

@@ -211,3 +211,14 @@ def test_requests_out_of_order_are_flagged(quantised):
     off = np.abs(out.cpu().numpy()[:10].astype(np.float64) - want[:10])
     assert np.all(off <= tolerance(want[:10], mag[:10], b.lens, 6.0))
     assert torch.all(out[10:] == 7.0)
+
+
+def test_a_window_past_32_bits_is_no_window():
+    b = Batch(59, [(70, 300), (1, 40)], hkv=1, group=2, head_dim=128, page=16, quantised=False)
+    caches = b.stored()
+    first = attend(b, caches)
+    for window in (2 ** 31 - 1, 2 ** 32, 2 ** 40 + 5):
+        assert torch.equal(attend(b, caches, window=window), first)
+    with pytest.raises(qsa.QSAError):
+        attend(b, caches, window=-2 ** 32)
+    ok()
