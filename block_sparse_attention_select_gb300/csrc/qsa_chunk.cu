@@ -367,15 +367,20 @@ __device__ __forceinline__ void codes_to_half(const uint8_t *src, uint8_t *dst, 
     uint8_t *out = dst + (pc >> 2) * (TOKS * 128) + r0 * 128;
     const uint32_t p0 = 2 * (pc & 3), o0 = (p0 ^ (r0 & 7)) << 4, o1 = ((p0 + 1) ^ (r0 & 7)) << 4;
     const bool cut = a > 0 || z < TOKS;
-#pragma unroll
+    // four pieces at a time, rolled: half the code at D = 256 (unrolled, its time
+    // moved by 8% with whatever else changed in the kernel's code)
+    static_assert(4 * STEP == TOKS || 4 * STEP == TOKS / 2, "a pass is the tile's tokens or half of them");
+    constexpr bool WHOLE = 4 * STEP == TOKS;                  // then the next pass has the next 128 dims
+    const uint32_t *sc_at = scale + r0;
+    int tok = r0;
+#pragma unroll 1
     for (int i0 = 0; i0 < N; i0 += 4) {
         uint4 x[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const uint4 *>(in + (i0 + i) * (16 * 128));
+        for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const uint4 *>(in + i * (16 * 128));
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int blk = (STEP * (i0 + i)) / TOKS, tk = (STEP * (i0 + i)) % TOKS;     // 128 dims, token - r0
-            const uint32_t sc = scale[r0 + tk];
+            const uint32_t sc = sc_at[STEP * i];
             const uint32_t cw[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
             uint32_t o[8];
 #pragma unroll
@@ -386,13 +391,18 @@ __device__ __forceinline__ void codes_to_half(const uint8_t *src, uint8_t *dst, 
                     : "r"(cw[k]));
 #pragma unroll
             for (int k = 0; k < 8; ++k) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(o[k]) : "r"(sc));
-            if (cut && (r0 + tk < a || r0 + tk >= z)) {
+            if (cut && (tok + STEP * i < a || tok + STEP * i >= z)) {
 #pragma unroll
                 for (int k = 0; k < 8; ++k) o[k] = 0u;
             }
-            uint8_t *at = out + (2 * blk * TOKS + tk) * 128;
-            *reinterpret_cast<uint4 *>(at + o0) = make_uint4(o[0], o[1], o[2], o[3]);
-            *reinterpret_cast<uint4 *>(at + o1) = make_uint4(o[4], o[5], o[6], o[7]);
+            *reinterpret_cast<uint4 *>(out + STEP * i * 128 + o0) = make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4 *>(out + STEP * i * 128 + o1) = make_uint4(o[4], o[5], o[6], o[7]);
+        }
+        in += 4 * 16 * 128;
+        out += WHOLE ? 2 * TOKS * 128 : 4 * STEP * 128;
+        if (!WHOLE) {
+            sc_at += 4 * STEP;
+            tok += 4 * STEP;
         }
     }
 }
@@ -784,10 +794,14 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                                  "l"((src ? src : reinterpret_cast<uint64_t>(p.q)) + (src ? pc * 16 : 0)), "r"(src ? 16 : 0)
                                  : "memory");
                 }
+            }
+        };
+        auto q_loaded = [&](uint32_t number) {
+            if (ok) {
                 asm volatile("cp.async.wait_all;" ::: "memory");
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) cluster_arrive(of_first(&c.q_full[qb]));
+                if (lane == 0) cluster_arrive(of_first(&c.q_full[Sh::QBUFS == 2 ? number & 1u : 0u]));
             }
         };
         // Rows of V that nothing attends may hold anything (the ends of loaded pages):
@@ -816,7 +830,6 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
             while (next_segment()) {
                 const int32_t n = w.n;
                 load_q(seg);
-                ++seg;
                 const int32_t *bt = p.kv.block_table + static_cast<int64_t>(w.b) * p.kv.max_pages;
                 // Scale bytes of the slot's tokens, one per thread, looked up ahead:
                 // the page two tiles, the byte one.  Keys and values have their own,
@@ -876,12 +889,17 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                 for (int32_t j = -lead; j < n; ++j) {
                     if (j >= 0) turn(std::true_type{}, j);
                     if (j + lead < n) turn(std::false_type{}, j + lead);
+                    if (j == -lead) q_loaded(seg);         // landed under the first codes
                 }
+                ++seg;
             }
         } else {
             while (true) {
                 const bool more = next_segment();
-                if (more) load_q(seg);
+                if (more) {
+                    load_q(seg);
+                    q_loaded(seg);
+                }
                 // with two buffers the next queries are loaded before the last value
                 // tile of a segment, which comes late
                 if (Sh::QBUFS == 2 && before.n > 1) clear(before, ring_b, before.n - 1);
@@ -956,9 +974,18 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
 #pragma unroll
                     for (int k = 0; k < 4; ++k) a[k] = -INFINITY;
 #pragma unroll
-                    for (int e = 0; e < CH_TILE; ++e) {
-                        if (e > hi || e < lo) s[e >> 5][e & 31] = 0xff800000u;           // -inf
-                        a[e & 3] = fmaxf(a[e & 3], __uint_as_float(s[e >> 5][e & 31]));
+                    for (int k = 0; k < 4; ++k) {
+                        // bits of the visible columns (a shift past 31 gives zero)
+                        uint32_t below, from;
+                        asm("shl.b32 %0, 2, %1;" : "=r"(below) : "r"(min(max(hi - 32 * k, -1), 31) & 31));
+                        below = hi < 32 * k ? 0u : below - 1u;
+                        asm("shl.b32 %0, 0xffffffff, %1;" : "=r"(from) : "r"(max(lo - 32 * k, 0)));
+                        const uint32_t bits = below & from;
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            if (!(bits & (1u << e))) s[k][e] = 0xff800000u;              // -inf
+                            a[e & 3] = fmaxf(a[e & 3], __uint_as_float(s[k][e]));
+                        }
                     }
                     mx = fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3]));
                 }
