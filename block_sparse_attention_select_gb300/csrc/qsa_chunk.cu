@@ -49,14 +49,14 @@
 // scores and the order is S(0) S(1) | O(0) S(2) | O(1) S(3) | ...
 //
 // What bounds it: with D = 256 and a long context the tensor cores (the
-// 1,616-row chunk over 29,000 tokens, 12 query heads to a KV head: 575 us, 1,950
+// 1,616-row chunk over 29,000 tokens, 12 query heads to a KV head: 568 us, 1,970
 // TF/s, tensor pipe 94% busy).  With D = 128 a tile's products take half as long
 // and its exponentials the same, so the latency of two softmax warps per scheduler
-// shows (four prompts of 4,096 tokens, 32 heads: 381 us, 1,440 TF/s; tensor pipe
+// shows (four prompts of 4,096 tokens, 32 heads: 379 us, 1,450 TF/s; tensor pipe
 // 67%, issue slots 48%).  From the E4M3 cache the turning of codes into FP16 tiles
-// (three chunks of 517 over 12,345 tokens: 153 us, 1,270 TF/s, tensor pipe 59%).
+// (three chunks of 517 over 12,345 tokens: 151 us, 1,290 TF/s, tensor pipe 59%).
 // A short call is the search for its work, its first loads and its last output:
-// two chunks of 1,023 tokens with a window of 1,000 take 42 us where their products
+// two chunks of 1,023 tokens with a window of 1,000 take 40 us where their products
 // need 9.
 //
 // The accumulator is rescaled only when a row's maximum has grown by more than
