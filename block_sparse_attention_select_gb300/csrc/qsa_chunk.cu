@@ -490,7 +490,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
         // where a page holds its tokens, page lookups for many tiles at once, one
         // thread that issues.  (With a box per 128-byte chunk, a lane each, and
         // lookups tile by tile the loop took 1,600 clocks per tile and the products
-        // waited for it: 810 us on 512 new tokens of four requests over 32,768.)
+        // waited for it: 796 us on 512 new tokens of four requests over 32,768, 755 so.)
         const uint32_t dst0 = Q8 ? smem_u32(raw) : ring_a;
         constexpr uint32_t BYTES = Q8 ? RAW : SLOT;
         // elements of a box row: 128 bytes, or half a 128-wide head's 64 codes
