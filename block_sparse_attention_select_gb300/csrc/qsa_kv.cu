@@ -48,7 +48,8 @@ __device__ __forceinline__ int32_t find_line(const KvParams &p, int32_t row)
     }
     bool bad;
     const Seq s = seq_of(p, lo, &bad);
-    if (row < s.s0 || row - s.s0 >= s.n) return -1;
+    // (n > 0 first: a skipped request's start may be any number, and the difference wrap)
+    if (s.n <= 0 || row < s.s0 || row - s.s0 >= s.n) return -1;
     const int32_t pos = s.p0 + (row - s.s0);
     const int32_t page = __ldg(p.block_table + static_cast<int64_t>(lo) * p.max_pages + (pos >> p.page_shift));
     if (page >= 0 && page < p.num_pages) return (page << p.page_shift) + (pos & (p.page_tokens - 1));
