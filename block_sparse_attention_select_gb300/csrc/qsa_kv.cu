@@ -35,8 +35,22 @@ constexpr int KV_THREADS = 256;
 constexpr int KV_BATCH = 8;        // vectors in flight per thread
 constexpr int KV_MAX_ROWS = 16;    // rows per warp
 
-// Cache line (page * page_tokens + slot) of `row`, a row per lane: -1 no
-// request or skipped, -2 a page outside the cache.
+// Whether a request has the row.  (n > 0 first: a skipped request's start may be any
+// number, and the difference wrap.)
+__device__ __forceinline__ bool has_row(const Seq &s, int32_t row) { return s.n > 0 && row >= s.s0 && row - s.s0 < s.n; }
+
+// Cache line (page * page_tokens + slot) of a row of request b: -2 a page outside
+// the cache.
+__device__ __forceinline__ int32_t line_of(const KvParams &p, int32_t b, const Seq &s, int32_t row)
+{
+    const int32_t pos = s.p0 + (row - s.s0);
+    const int32_t page = __ldg(p.block_table + static_cast<int64_t>(b) * p.max_pages + (pos >> p.page_shift));
+    if (page >= 0 && page < p.num_pages) return (page << p.page_shift) + (pos & (p.page_tokens - 1));
+    record_error(p.status, ST_BAD_PAGE);
+    return -2;
+}
+
+// Cache line of `row`, a row per lane: -1 no request or skipped.
 __device__ __forceinline__ int32_t find_line(const KvParams &p, int32_t row)
 {
     // the last request that starts at or before the row
@@ -48,13 +62,21 @@ __device__ __forceinline__ int32_t find_line(const KvParams &p, int32_t row)
     }
     bool bad;
     const Seq s = seq_of(p, lo, &bad);
-    // (n > 0 first: a skipped request's start may be any number, and the difference wrap)
-    if (s.n <= 0 || row < s.s0 || row - s.s0 >= s.n) return -1;
-    const int32_t pos = s.p0 + (row - s.s0);
-    const int32_t page = __ldg(p.block_table + static_cast<int64_t>(lo) * p.max_pages + (pos >> p.page_shift));
-    if (page >= 0 && page < p.num_pages) return (page << p.page_shift) + (pos & (p.page_tokens - 1));
-    record_error(p.status, ST_BAD_PAGE);
-    return -2;
+    return has_row(s, row) ? line_of(p, lo, s, row) : -1;
+}
+
+// The same where the starts fall somewhere, by all lanes of a warp, request by
+// request: slow, but no well-formed request loses its rows to another's mistake.
+__device__ __forceinline__ int32_t find_line_unsorted(const KvParams &p, int32_t row, bool wanted)
+{
+    int32_t line = -1;
+#pragma unroll 1
+    for (int32_t b = 0; b < p.n_reqs; ++b) {
+        bool bad;
+        const Seq s = seq_of(p, b, &bad);
+        if (wanted && line == -1 && has_row(s, row)) line = line_of(p, b, s, row);
+    }
+    return line;
 }
 
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d)
@@ -94,9 +116,23 @@ kv_kernel(const KvParams p, uint8_t *kr, uint8_t *vr, int64_t k_stride, int64_t 
     wait_prior_grid();
     if (blockIdx.x == 0) flag_bad_requests(p);
     const int64_t first = (static_cast<int64_t>(blockIdx.x) * (KV_THREADS / 32) + warp) * rows_per_warp;
-    if (first >= p.rows) return;
-    const int32_t row0 = static_cast<int32_t>(first), n_rows = min(rows_per_warp, p.rows - row0);
-    const int32_t mine = lane < n_rows ? find_line(p, row0 + lane) : -1;
+    const int32_t row0 = static_cast<int32_t>(min(first, static_cast<int64_t>(p.rows)));
+    const int32_t n_rows = min(rows_per_warp, p.rows - row0);
+    int32_t mine = lane < n_rows ? find_line(p, row0 + lane) : -1;
+    // No request: a row behind the last one or a request that is skipped, where the
+    // starts are in order; otherwise the search may have passed the row's request by.
+    bool lost = lane < n_rows && mine == -1;
+    if (__syncthreads_or(lost)) {
+        bool falls = false;
+#pragma unroll 4
+        for (int32_t b = threadIdx.x; b < p.n_reqs; b += KV_THREADS)
+            falls = falls || __ldg(p.seq_start + b + 1) < __ldg(p.seq_start + b);
+        if (__syncthreads_or(falls) && __any_sync(0xffffffffu, lost)) {
+            const int32_t line = find_line_unsorted(p, row0 + lane, lost);
+            if (lost) mine = line;
+        }
+    }
+    if (n_rows <= 0) return;
 
     const int sub = lane / LPV, l = lane % LPV;
     const int32_t per_row = 2 * p.hkv;              // vectors of a row: K heads, then V heads

@@ -249,9 +249,10 @@ qsa_status qsa_block_select(const void *q, int32_t rows, int32_t H, const void *
  * 65,535 (QSA_ERR_UNSUPPORTED above).
  * Device-side problems are reported by qsa_get_device_status(): a request whose
  * seq_start or pos_start is out of range (decreasing, past `rows`, negative,
- * past the block table) is skipped, a token whose page id is outside the cache
- * is not written, reads back as zeros, and counts as a zero key and value in the
- * attention. */
+ * past the block table) is skipped and the others are served by each of the
+ * calls (where falling starts make two of them claim a row, that row's result is
+ * undefined), a token whose page id is outside the cache is not written, reads
+ * back as zeros, and counts as a zero key and value in the attention. */
 #define QSA_KV_FP16 0
 #define QSA_KV_E4M3 1
 typedef struct {

@@ -16,10 +16,13 @@ LENS = [(10, 90), (4, 44), (6, 50), (3, 61)]
 FIRST = [80, 40, 44, 58]
 # seq_start, pos_start, the requests that are served (no two claim a row)
 CASES = {
+    "falls_to_empty_ones": ([0, 10, 3, 3, 3], FIRST, [0]),
+    "leaves_the_rows": ([0, 5, 1000, 5, 9], FIRST, [0, 3]),
     "falls_in_front": ([7, 3, 9, 12, 14], FIRST, [1, 2, 3]),
     "starts_below_zero": ([-3, 4, 8, 8, 10], FIRST, [1, 3]),
     "ends_past_the_rows": ([0, 6, 10, 14, 27], FIRST, [0, 1, 2]),
     "starts_at_the_smallest_number": ([-2 ** 31, 4, 8, 8, 10], FIRST, [1, 3]),
+    "falls_to_the_smallest_number": ([0, 10, -2 ** 31, 14, 20], FIRST, [0, 3]),
     "falls_at_the_end": ([0, 10, 14, 20, 2], FIRST, [0, 1, 2]),
     "rises_far_and_returns": ([12, 1 << 30, 12, 12, 15], FIRST, [3]),
     "negative_position": ([0, 10, 14, 20, 23], [80, -1, 44, 58], [0, 2, 3]),
@@ -63,3 +66,13 @@ def test_well_formed_requests_are_served_and_nothing_else(starts, first, good, q
         assert np.all(off <= tolerance(ref[rows], mag[rows], LENS, 6.0))
     for got in (gk, gv, out):
         assert np.all(got.cpu().numpy()[~taken] == 7.0)
+
+
+def test_padding_behind_many_requests():
+    """Rows behind the last of 700 requests, in CTAs of their own and in shared ones."""
+    lens = [(1 + i % 3, 2 + i % 5 + i % 3) for i in range(700)]
+    b = Batch(62, lens, hkv=1, group=1, head_dim=128, page=8, quantised=False, pad_rows=900)
+    cache = device_cache(b)
+    _, k, v, ss, ps = on_gpu(b)
+    qsa.kv_store(k, v, ss, ps, cache)
+    check(cache, b.stored())
