@@ -1008,7 +1008,8 @@ qsa_status qsa_chunk_attention(const void *q, int64_t q_stride, int32_t rows, in
 {
     g_launches = 0;
     bool any;
-    if (hq < 1 || window < 0 || !(scale > 0.0f) || !std::isfinite(scale)) return QSA_ERR_INVALID_ARG;
+    // (the kernels multiply by scale * log2 e)
+    if (hq < 1 || window < 0 || !(scale > 0.0f) || !std::isfinite(scale * 1.4426950408889634f)) return QSA_ERR_INVALID_ARG;
     qsa_status st = check_batch(rows, n_reqs, seq_start, pos_start, cache, &any);
     if (st != QSA_OK) return st;
     if (hq % cache->hkv != 0 || hq / cache->hkv > 128) return QSA_ERR_UNSUPPORTED;

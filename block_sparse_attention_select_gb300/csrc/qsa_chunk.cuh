@@ -42,7 +42,7 @@ struct Split {
 
 // Workspace: a Split per worker, then per place (two for each worker: 0 for a
 // unit begun before its share, 1 for one that goes on after it) the rows'
-// (maximum in powers of two, sum), then their unnormalised outputs.
+// (maximum score before the scale, sum), then their unnormalised outputs.
 constexpr size_t WS_ML = 4096;
 static_assert(sizeof(Split) * CHUNK_MAX_CTAS <= WS_ML && sizeof(Split) * CHUNK_MAX_PAIRS <= WS_ML, "workspace");
 template <int ROWS, int WORKERS>
@@ -367,6 +367,12 @@ __device__ __forceinline__ uint32_t sw128(uint32_t row, uint32_t c)
 // 2^18 equal weights below that vanished from the output, though not from the sum.)
 constexpr float RESCALE = 8.0f, P_UP = 7.0f;
 
+// A weight's exponent is (s - m) * scale * log2 e.  The scores stay in the units
+// that the products give, where differences near the maximum are exact: turned into
+// powers of two first, each is rounded to 2^-24 of its size, at 2^23 half a power
+// of two.
+constexpr float LOG2_E = 1.4426950408889634f;
+
 __device__ __forceinline__ float exp2_approx(float x)
 {
     float y;
@@ -407,6 +413,7 @@ chunk_join_kernel(const ChunkParams p)
     const Split sp = reinterpret_cast<const Split *>(p.ws)[blockIdx.x];
     const int32_t n = sp.parts;
     if (n == 0) return;
+    const float cs = G::RAW_MAX ? p.scale * LOG2_E : 1.0f;
     const float2 *ml = reinterpret_cast<const float2 *>(p.ws + WS_ML);
     const float *po = reinterpret_cast<const float *>(p.ws + ws_o<G::ROWS, G::WORKERS>());
     auto place = [&](int32_t i) { return 2 * (static_cast<int64_t>(blockIdx.x) + i) + (i == 0 ? 1 : 0); };
@@ -424,7 +431,7 @@ chunk_join_kernel(const ChunkParams p)
             float wt = 0.0f;
             if (i0 + lane < n) {
                 const float2 x = ml[place(i0 + lane) * G::ROWS + row];
-                wt = x.x == -INFINITY ? 0.0f : exp2_approx(x.x - mx);      // a part in which the row saw nothing
+                wt = x.x == -INFINITY ? 0.0f : exp2_approx((x.x - mx) * cs);   // a part in which the row saw nothing
                 sum = fmaf(x.y, wt, sum);
             }
             const int32_t k = min(32, n - i0);

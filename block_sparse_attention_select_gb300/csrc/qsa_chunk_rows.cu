@@ -50,6 +50,7 @@ constexpr int CR_MAX_STAGES = 8;
 constexpr int BAR_COMP = 1;
 
 struct RowsGeometry {
+    static constexpr bool RAW_MAX = true;    // the parts' maxima: scores before the scale
     static constexpr int ROWS = CR_ROWS, TILE = CR_TILE, UNIT_COST = 4, MIN_SHARE = 3, THREADS = CR_THREADS, WARPS = CR_WARPS,
                          WORKERS = CHUNK_MAX_CTAS;
 };
@@ -283,7 +284,7 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
         constexpr int VI = Sh::CHUNKS;
         const int r = lane >> 2, q = lane & 3;
         const int grp = warp >> 2, sub = (warp & 3) * 16;          // stages of this parity, tokens sub .. + 15
-        const float cs = p.scale * 1.4426950408889634f;            // scores in powers of two
+        const float cs = p.scale * LOG2_E;
         uint32_t slot = 0, phase = 0, it = 0;
         bool ok = true;
         while (next_segment(c.segs, &segs, &w, lane)) {
@@ -356,22 +357,18 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
                             }
                         }
                     }
-                    // ---- softmax, in powers of two
+                    // ---- softmax
                     const bool edge = tok0 < w.lo_tok || tok0 + 15 > w.hi_tok;      // some token that no row attends
                     float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
                     for (int n = 0; n < 2; ++n) {
-                        float2 f = make_float2(cs, cs);
-                        if (Q8) {
-                            f = *reinterpret_cast<const float2 *>(&c.scale[sl][0][sub + 8 * n + 2 * q]);
-                            f.x *= cs;
-                            f.y *= cs;
-                        }
+                        float2 f = make_float2(1.0f, 1.0f);
+                        if (Q8) f = *reinterpret_cast<const float2 *>(&c.scale[sl][0][sub + 8 * n + 2 * q]);
                         const int32_t tk0 = tok0 + 8 * n + 2 * q;
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const int32_t tok = tk0 + (e & 1);
-                            s[n][e] *= (e & 1) ? f.y : f.x;
+                            if (Q8) s[n][e] *= (e & 1) ? f.y : f.x;
                             if (tok > pos[e >> 1] || tok < first[e >> 1]) s[n][e] = -INFINITY;
                             mx[e >> 1] = fmaxf(mx[e >> 1], s[n][e]);
                         }
@@ -381,9 +378,10 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
                         mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
                         mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
                     }
-                    const bool grow0 = mx[0] > m[0] + RESCALE, grow1 = mx[1] > m[1] + RESCALE;
+                    const bool grow0 = (mx[0] - m[0]) * cs > RESCALE, grow1 = (mx[1] - m[1]) * cs > RESCALE;
                     if (__any_sync(0xffffffffu, grow0 || grow1)) {
-                        const float a0 = grow0 ? exp2_approx(m[0] - mx[0]) : 1.0f, a1 = grow1 ? exp2_approx(m[1] - mx[1]) : 1.0f;
+                        const float a0 = grow0 ? exp2_approx((m[0] - mx[0]) * cs) : 1.0f;
+                        const float a1 = grow1 ? exp2_approx((m[1] - mx[1]) * cs) : 1.0f;
                         if (grow0) m[0] = mx[0];
                         if (grow1) m[1] = mx[1];
                         l[0] *= a0;
@@ -403,8 +401,9 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
                     for (int n = 0; n < 2; ++n)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            const float mm = m[e] == -INFINITY ? 0.0f : m[e] - P_UP;
-                            const float x = exp2_approx(s[n][2 * e] - mm), y = exp2_approx(s[n][2 * e + 1] - mm);
+                            const float mm = m[e] == -INFINITY ? 0.0f : m[e];
+                            const float x = exp2_approx(fmaf(s[n][2 * e] - mm, cs, P_UP));
+                            const float y = exp2_approx(fmaf(s[n][2 * e + 1] - mm, cs, P_UP));
                             l[e] += x + y;
                             const __half2 hh = __floats2half2_rn(x, y);
                             pw[2 * n + e] = *reinterpret_cast<const uint32_t *>(&hh);
@@ -465,7 +464,7 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
                 mt[e] = c.m[0][r + 8 * e];
 #pragma unroll
                 for (int k = 1; k < CR_COMP; ++k) mt[e] = fmaxf(mt[e], c.m[k][r + 8 * e]);
-                f[e] = m[e] == -INFINITY ? 0.0f : exp2_approx(m[e] - mt[e]);
+                f[e] = m[e] == -INFINITY ? 0.0f : exp2_approx((m[e] - mt[e]) * cs);
                 if (q == 0) c.l[warp][r + 8 * e] = l[e] * f[e];
             }
             // Eight steps; in each every warp lays down PD / 8 dims of each chunk, and

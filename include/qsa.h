@@ -283,6 +283,9 @@ qsa_status qsa_kv_load(void *k, int64_t k_stride, void *v, int64_t v_stride, int
  * p of request b attends tokens max(0, p - window + 1) .. p (window 0: 0 .. p),
  * query head h reads KV head h / (hq / hkv),
  *   out[r, h, :] = sum_t softmax_t(scale * q[r, h, :] . k_t) * v_t
+ * scale: positive, and scale * log2(e) a finite FP32 number (QSA_ERR_INVALID_ARG
+ * otherwise).  |scale * q . k| has to stay below 1.8e8 (the weights are relative to
+ * the largest, and rows with larger scores may lose all of them).
  * q: FP16, row r at q + r * q_stride elements (a multiple of 8, at least hq *
  * head_dim), out: FP16 [rows, hq, head_dim]; both 16-byte aligned.  hq / hkv <=
  * 128.  Pages that no row attends are not read (their table entries may hold
