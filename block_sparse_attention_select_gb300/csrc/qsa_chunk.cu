@@ -756,10 +756,8 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                         if (!in) continue;
                         if (whole) {
 #pragma unroll
-                            for (int i = 0; i < 16; i += 2) {
-                                const __half2 hh = __floats2half2_rn(__uint_as_float(x[i]) * f, __uint_as_float(x[i + 1]) * f);
-                                x[i >> 1] = *reinterpret_cast<const uint32_t *>(&hh);
-                            }
+                            for (int i = 0; i < 16; i += 2)
+                                x[i >> 1] = to_half2(__uint_as_float(x[i]) * f, __uint_as_float(x[i + 1]) * f);
                             store32(dst + 32 * k, x, out_32);
                         } else {
                             store32(dst + 64 * k, x, true);
@@ -1097,10 +1095,8 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                     if (!in) continue;
                     if (whole) {
 #pragma unroll
-                        for (int i = 0; i < 32; i += 2) {
-                            const __half2 hh = __floats2half2_rn(__uint_as_float(u[i]) * inv, __uint_as_float(u[i + 1]) * inv);
-                            u[i >> 1] = *reinterpret_cast<const uint32_t *>(&hh);
-                        }
+                        for (int i = 0; i < 32; i += 2)
+                            u[i >> 1] = to_half2(__uint_as_float(u[i]) * inv, __uint_as_float(u[i + 1]) * inv);
                         store32(out + 32 * k, u, out_32);
                         store32(out + 32 * k + 16, u + 8, out_32);
                     } else {

@@ -380,6 +380,16 @@ __device__ __forceinline__ float exp2_approx(float x)
     return y;
 }
 
+// Two outputs as FP16, `a` in the lower half.  An output is a mean of finite values,
+// but its weights are rounded and their sum is not, which can carry a mean of values
+// near 65,504 past the border to infinity: it stops at 65,504.
+__device__ __forceinline__ uint32_t to_half2(float a, float b)
+{
+    uint32_t h;
+    asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(b), "f"(a));
+    return h;
+}
+
 __device__ __forceinline__ void named_barrier(int id, int threads)
 {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
@@ -476,12 +486,8 @@ chunk_join_kernel(const ChunkParams p)
                       ((static_cast<int64_t>(sp.s0) + tok) * p.hq + sp.g * p.group + h) * D;
 #pragma unroll
         for (int e = 0; e < N / 4; ++e) {
-            const __half2 a = __floats2half2_rn(acc[e].x * inv, acc[e].y * inv);
-            const __half2 b = __floats2half2_rn(acc[e].z * inv, acc[e].w * inv);
-            uint2 u;
-            u.x = *reinterpret_cast<const uint32_t *>(&a);
-            u.y = *reinterpret_cast<const uint32_t *>(&b);
-            reinterpret_cast<uint2 *>(out)[32 * e + lane] = u;
+            reinterpret_cast<uint2 *>(out)[32 * e + lane] =
+                make_uint2(to_half2(acc[e].x * inv, acc[e].y * inv), to_half2(acc[e].z * inv, acc[e].w * inv));
         }
     }
 }

@@ -513,10 +513,7 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
                     for (int d = 0; d < PD; d += 8) {
                         uint32_t u[4];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const __half2 hh = __floats2half2_rn(x[k][d + 2 * j] * inv, x[k][d + 2 * j + 1] * inv);
-                            u[j] = *reinterpret_cast<const uint32_t *>(&hh);
-                        }
+                        for (int j = 0; j < 4; ++j) u[j] = to_half2(x[k][d + 2 * j] * inv, x[k][d + 2 * j + 1] * inv);
                         *reinterpret_cast<uint4 *>(out + d) = make_uint4(u[0], u[1], u[2], u[3]);
                     }
                 } else {

@@ -287,7 +287,8 @@ qsa_status qsa_kv_load(void *k, int64_t k_stride, void *v, int64_t v_stride, int
  * otherwise).  |scale * q . k| has to stay below 1.8e8 (the weights are relative to
  * the largest, and rows with larger scores may lose all of them).
  * q: FP16, row r at q + r * q_stride elements (a multiple of 8, at least hq *
- * head_dim), out: FP16 [rows, hq, head_dim]; both 16-byte aligned.  hq / hkv <=
+ * head_dim), out: FP16 [rows, hq, head_dim], values past 65,504 by rounding stored
+ * as that; both 16-byte aligned.  hq / hkv <=
  * 128.  Pages that no row attends are not read (their table entries may hold
  * anything), and cache slots that no row of the request attends may hold
  * anything, NaN included; keys and values that some row attends must be

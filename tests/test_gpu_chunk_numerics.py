@@ -89,3 +89,23 @@ def test_maximum_that_grows_far_from_zero(D, quantised, rows):
     tol = 2.0 ** -11 * want.abs() + (2.0 ** -11 + 2.0 ** -18 + n * 2.0 ** -24) * mag + 2.0 ** -25
     off = (out - want).abs()
     assert torch.all(off <= tol), float((off / tol).max())
+
+
+@ROWS
+@DIM
+def test_values_of_the_largest_size_stay_finite(D, rows):
+    """All values 65,504 or its negative: so is every output.  Fifteen of sixteen
+    weights are 2^-1 (1 + 0.51 * 2^-10), which FP16 rounds up by 2^-11, past what
+    65,504 leaves to the border of infinity."""
+    n = 2000
+    k = torch.zeros(n, 1, D, dtype=torch.float16, device="cuda")
+    k[:, :, 0] = -1.0
+    k[::16, :, 0] = 0.0
+    v = torch.full((n, 1, D), 65504.0, dtype=torch.float16, device="cuda")
+    v[:, :, ::2] = -65504.0
+    cache = filled(k, v, False)
+    q = torch.zeros(rows, 4, D, dtype=torch.float16, device="cuda")
+    q[:, :, 0] = 1.0
+    scale = -float(np.log(0.5 * (1 + 0.51 * 2.0 ** -10)))
+    out = attend(q, cache, n, scale)
+    assert torch.equal(out, v[:1, :].double().expand(rows, 4, D))
