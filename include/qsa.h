@@ -241,7 +241,9 @@ qsa_status qsa_block_select(const void *q, int32_t rows, int32_t H, const void *
  * is off by at most 1/16 of itself or 2^(e - 10), whichever is larger.
  * Infinities are stored as the largest value, a NaN as NaN (it does not count
  * for the scale).  Scale bytes outside [112, 135] are read as the nearer of the
- * two.
+ * two.  In a cache filled by something else, codes above 240 in magnitude at a scale
+ * byte of 135 or more stand for numbers past FP16: they read back as infinity, and
+ * no row may attend them.
  *
  * head_dim 128 or 256, page_tokens a power of two in [8, 256], 1 <= hkv <= 1024
  * (QSA_ERR_UNSUPPORTED otherwise); k and v 16-byte aligned; num_pages *
@@ -292,7 +294,7 @@ qsa_status qsa_kv_load(void *k, int64_t k_stride, void *v, int64_t v_stride, int
  * 128.  Pages that no row attends are not read (their table entries may hold
  * anything), and cache slots that no row of the request attends may hold
  * anything, NaN included; keys and values that some row attends must be
- * finite.  ws: qsa_chunk_attention_workspace_bytes(...) bytes, 256-byte
+ * finite FP16 numbers.  ws: qsa_chunk_attention_workspace_bytes(...) bytes, 256-byte
  * aligned; calls that may overlap need workspaces of their own (two captured
  * graphs replayed on different streams, too). */
 size_t qsa_chunk_attention_workspace_bytes(int32_t rows, int32_t hq, int32_t hkv, int32_t head_dim);
