@@ -139,7 +139,7 @@ struct RingPos {
 struct Ctrl {
     SegRing segs;
     uint64_t full[MAX_SLOTS], empty[MAX_SLOTS], raw_full[RAWS], raw_empty[RAWS], bnd[8];
-    uint64_t s_full[2], s_free[2], p_full[2][2], o_done[2], m_out[2][4], q_full[2], q_free[2], drain;
+    uint64_t s_full[2], s_free[2], p_full[2][2], o_done[2], m_out[2][4], q_full[2], q_free[2], drain[2];
     uint64_t o_last, o_free, f_full[2], f_free[2];
     alignas(8) float mrow[2][CH_HALF];       // [tile parity][row]: maximum in use at the group's last tile; sums at a segment's end
     union {
@@ -239,6 +239,14 @@ __device__ __forceinline__ uint32_t of_first(const void *p)
     uint32_t a;
     asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_u32(p)));
     return a;
+}
+
+// Writes a word of the other CTA's shared memory.
+__device__ __forceinline__ void tell_other(const void *p, uint32_t other, uint32_t value)
+{
+    uint32_t a;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(other));
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(a), "r"(value) : "memory");
 }
 
 __device__ __forceinline__ void cluster_arrive(uint32_t bar)
@@ -452,7 +460,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
             mbar_init(&c.segs.full[i], 1);
             mbar_init(&c.segs.empty[i], CH_ROLES);
         }
-        mbar_init(&c.drain, 1);
+        for (int i = 0; i < 2; ++i) mbar_init(&c.drain[i], 1);
         mbar_init(&c.o_last, 1);
         mbar_init(&c.o_free, 2 * CH_HELPERS);                 // in the first CTA, for both
         for (int i = 0; i < 2; ++i) {
@@ -594,15 +602,10 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                 if (ok && j + lead < n) load(std::false_type{}, j + lead);
             }
         }
-        // after an abort copies may be in flight: let them land (their barriers
-        // may be the other CTA's, so give them the time instead)
-        if (!ok && lane == 0) {
-            if (Q8)
-                for (int i = 0; i < RAWS; ++i)
-                    if (used & (1u << i)) mbar_wait_bounded(&c.raw_full[i], (last >> i) & 1u, drain_limit(lim));
-            const long long t0 = clock64();
-            while (clock64() - t0 < static_cast<long long>(2 * DRAIN_NS)) {}
-        }
+        // codes still in flight, whoever gave up (otherwise the helpers waited for them)
+        if (Q8 && lane == 0)
+            for (int i = 0; i < RAWS; ++i)
+                if (used & (1u << i)) mbar_wait_bounded(&c.raw_full[i], (last >> i) & 1u, drain_limit(lim));
         __syncwarp();
     } else if (warp == CH_SCHED) {
         // ----------------------------------------------------------- segments
@@ -703,13 +706,6 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
             it += n;
             ++seg;
         }
-        if (!ok) {                                            // products still running
-            if (elect_one()) {
-                umma2_commit(&c.drain);
-                mbar_wait_bounded(&c.drain, 0, drain_limit(lim));
-            }
-            __syncwarp();
-        }
     }
     } else if (warp >= CH_HELP) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
@@ -796,8 +792,8 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
             }
         };
         auto q_loaded = [&](uint32_t number) {
+            asm volatile("cp.async.wait_all;" ::: "memory");
             if (ok) {
-                asm volatile("cp.async.wait_all;" ::: "memory");
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) cluster_arrive(of_first(&c.q_full[Sh::QBUFS == 2 ? number & 1u : 0u]));
@@ -1113,7 +1109,28 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
 
     tc_fence_before();
     __syncthreads();
+    if (t == 0 && *abort) tell_other(&c.abort, rank ^ 1, 1u);
+    __syncwarp();
     cluster_sync();                                          // nothing of the pair reaches into the other any more
+    if (*abort) {
+        // After a time-out in either CTA, work of roles that had no reason to wait may
+        // be in flight: products, and copies that complete on the other CTA's barriers.
+        // Every role of both has joined, so nothing new is issued.  Each issuing warp
+        // waits for its own products; the copies get the time (they land within
+        // microseconds).
+        const int issuer = warp == CH_MMA ? 0 : Sh::OWN_P && warp == CH_MMA2 ? 1 : -1;
+        if (rank == 0 && issuer >= 0 && elect_one()) {
+            umma2_commit(&c.drain[issuer]);
+            mbar_wait_bounded(&c.drain[issuer], 0, drain_limit(lim));
+        }
+        if (t == CH_LOAD * 32) {
+            const long long t0 = clock64();
+            while (clock64() - t0 < static_cast<long long>(2 * DRAIN_NS)) {}
+        }
+        __syncwarp();
+        __syncthreads();
+        cluster_sync();
+    }
     tc_fence_after();
     if (t == 0 && c.abort) record_error(p.kv.status, ST_TIMEOUT);
     if (warp == CH_MMA)
