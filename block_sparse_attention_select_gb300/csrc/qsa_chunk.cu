@@ -714,6 +714,14 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
         RingPos<Sh> pos;
         uint32_t seg = 0, rslot = 0, rphase = 0, par = 0, ring0 = 0, ring_b = 0, nb = 0;  // ring0: the next segment's first slot (OWN_P: value slot), ring_b: this one's
         bool ok = true;                                       // false: keep to the barriers, do nothing
+        // The limit bounds one step, a tile; waits of these warps for the end of a
+        // segment span all of its tiles (and a few steps' worth around them).
+        auto span = [&](const Seg &x) -> uint64_t {
+            if (!Sh::HELP_OUT) return lim;                     // these are never a segment ahead
+            const uint64_t step = lim < (1ull << 36) ? lim : 1ull << 36;
+            const uint64_t all = step * static_cast<uint32_t>(x.n + 8);
+            return all > lim ? all : lim;
+        };
         // A unit's output (or its part of it), while the softmax is at the next unit
         // (by the softmax warps themselves, a unit's end took them 2,400 clocks of
         // code that had left the instruction cache).  Warp w: TMEM lane quarter w % 4.
@@ -723,7 +731,8 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
             if (Sh::HELP_OUT && before.n > 0 && ok) {
                 const uint32_t u = seg - 1;                    // its number
                 const int lq = warp & 3, ur = rank * CH_HALF + ht;
-                ok = warp_wait(&c.f_full[u & 1u], (u >> 1) & 1u, abort, lim) && warp_wait(&c.o_last, u & 1u, abort, lim);
+                ok = warp_wait(&c.f_full[u & 1u], (u >> 1) & 1u, abort, span(before)) &&
+                     warp_wait(&c.o_last, u & 1u, abort, span(before));
                 if (!ok) return;
                 tc_fence_after();
                 const float f = c.factor[u & 1u][ht];
@@ -769,7 +778,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
         };
         auto load_q = [&](uint32_t number) {
             const uint32_t qb = Sh::QBUFS == 2 ? number & 1u : 0u, quse = Sh::QBUFS == 2 ? number >> 1 : number;   // buffer, its uses before
-            if (ok && quse > 0) ok = warp_wait(&c.q_free[qb], (quse - 1) & 1u, abort, lim);
+            if (ok && quse > 0) ok = warp_wait(&c.q_free[qb], (quse - 1) & 1u, abort, span(before));
             if (ok) {
                 // the warp's 32 rows: a lane finds one row's queries, then
                 // all lanes copy the rows, 512 bytes at a time
@@ -803,7 +812,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
         // zero weights must meet zeros.  r0: the segment's first slot.
         auto clear = [&](const Seg &x, uint32_t r0, int32_t tile) {
             if (!x.cut(tile, CH_TILE)) return;
-            if (ok) ok = warp_wait(&c.bnd[nb & 7u], (nb >> 3) & 1u, abort, lim);
+            if (ok) ok = warp_wait(&c.bnd[nb & 7u], (nb >> 3) & 1u, abort, span(x));
             ++nb;
             const uint32_t vs = Sh::OWN_P ? Sh::NK + (r0 + tile) % Sh::NV : (r0 + slot_of_v<Sh::LEAD>(tile, x.n)) % NS;
             if (ok) {

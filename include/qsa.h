@@ -308,7 +308,8 @@ const char *qsa_status_string(qsa_status status);
 /* Tuning / test switches, process-wide (not thread-safe against concurrent
  * calls).  QSA_CFG_PATH: 0 = automatic, 1 = materialise logits then select,
  * 2 = sampled-threshold filter path.  QSA_CFG_WAIT_LIMIT_NS: time after which
- * a pipeline wait gives up and records QSA_ERR_TIMEOUT (default 2 s).
+ * a pipeline wait gives up and records QSA_ERR_TIMEOUT (default 2 s; in
+ * qsa_chunk_attention a wait for a run of key tiles takes that much per tile).
  * Returns QSA_ERR_INVALID_ARG for an unknown key or value. */
 #define QSA_CFG_PATH 1
 #define QSA_CFG_WAIT_LIMIT_NS 2

@@ -49,3 +49,11 @@ def test_a_wait_that_runs_out_is_reported_and_harms_nothing_after(call):
         again, status = call(2_000_000_000)
         assert status == qsa.QSA_OK
         assert torch.equal(again, first)
+
+
+def test_a_limit_of_a_step_does_not_end_a_long_unit(call):
+    first, status = call(2_000_000_000)
+    assert status == qsa.QSA_OK
+    again, status = call(1_000_000)                          # a millisecond, for steps of two microseconds
+    assert status == qsa.QSA_OK
+    assert torch.equal(again, first)
