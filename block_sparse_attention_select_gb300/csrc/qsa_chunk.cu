@@ -706,6 +706,14 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
             it += n;
             ++seg;
         }
+        // the warp's own products, whoever gave up (otherwise they were waited for)
+        if (do_s || do_o) {
+            if (elect_one()) {
+                umma2_commit(&c.drain[do_s ? 0 : 1]);
+                mbar_wait_bounded(&c.drain[do_s ? 0 : 1], 0, drain_limit(lim));
+            }
+            __syncwarp();
+        }
     }
     } else if (warp >= CH_HELP) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
@@ -1122,16 +1130,10 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
     __syncwarp();
     cluster_sync();                                          // nothing of the pair reaches into the other any more
     if (*abort) {
-        // After a time-out in either CTA, work of roles that had no reason to wait may
-        // be in flight: products, and copies that complete on the other CTA's barriers.
-        // Every role of both has joined, so nothing new is issued.  Each issuing warp
-        // waits for its own products; the copies get the time (they land within
-        // microseconds).
-        const int issuer = warp == CH_MMA ? 0 : Sh::OWN_P && warp == CH_MMA2 ? 1 : -1;
-        if (rank == 0 && issuer >= 0 && elect_one()) {
-            umma2_commit(&c.drain[issuer]);
-            mbar_wait_bounded(&c.drain[issuer], 0, drain_limit(lim));
-        }
+        // After a time-out in either CTA, copies may be in flight that complete on the
+        // other one's barriers, whatever became of the loader itself.  Every role of
+        // both has joined, so nothing new is issued: they get the time (they land
+        // within microseconds).
         if (t == CH_LOAD * 32) {
             const long long t0 = clock64();
             while (clock64() - t0 < static_cast<long long>(2 * DRAIN_NS)) {}
