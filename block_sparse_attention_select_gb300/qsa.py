@@ -332,7 +332,8 @@ def block_select(q, k_cache, block_table, row_req, row_token, k: int, out_idx=No
 class KVCache:
     """Paged K/V cache: k, v FP16 or float8_e4m3fn [num_pages, page_tokens, hkv,
     head_dim] (quantised: with uint8 scale bytes k_scale, v_scale [num_pages,
-    page_tokens, hkv]), block_table int32 [B, max_pages]."""
+    page_tokens, hkv]), block_table int32 [B, max_pages].  The tensors' contents
+    may change, the tensors themselves not: the calls take their addresses from here."""
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, block_table: torch.Tensor, k_scale=None, v_scale=None):
         if k.dtype not in (torch.float16, torch.float8_e4m3fn):
@@ -358,6 +359,11 @@ class KVCache:
                           npg, pt, self.hkv, self.head_dim, block_table.data_ptr(), int(block_table.shape[0]),
                           int(block_table.shape[1]))
         self.ref = ctypes.byref(self.c)
+
+    def __setattr__(self, name, value):
+        if "ref" in self.__dict__:
+            raise AttributeError(f"a KVCache is fixed once made: make another one with the new {name}")
+        super().__setattr__(name, value)
 
     @classmethod
     def empty(cls, num_pages: int, page_tokens: int, hkv: int, head_dim: int, block_table: torch.Tensor,

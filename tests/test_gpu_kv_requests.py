@@ -76,3 +76,15 @@ def test_padding_behind_many_requests():
     _, k, v, ss, ps = on_gpu(b)
     qsa.kv_store(k, v, ss, ps, cache)
     check(cache, b.stored())
+
+
+def test_a_cache_keeps_its_tensors():
+    """Another tensor put in a cache's attribute would not reach the kernels."""
+    table = torch.zeros(2, 4, dtype=torch.int32, device="cuda")
+    for quantised in (False, True):
+        cache = qsa.KVCache.empty(3, 16, 2, 128, table, quantised=quantised)
+        for name in ("k", "v", "block_table", "k_scale", "v_scale"):
+            before = getattr(cache, name)
+            with pytest.raises(AttributeError):
+                setattr(cache, name, torch.zeros(5, device="cuda"))
+            assert getattr(cache, name) is before
