@@ -5,6 +5,7 @@ import pytest
 import torch
 
 from block_sparse_attention_select_gb300 import qsa
+from test_gpu_chunk_attention import reference64
 
 pytestmark = pytest.mark.gpu
 
@@ -109,3 +110,41 @@ def test_values_of_the_largest_size_stay_finite(D, rows):
     scale = -float(np.log(0.5 * (1 + 0.51 * 2.0 ** -10)))
     out = attend(q, cache, n, scale)
     assert torch.equal(out, v[:1, :].double().expand(rows, 4, D))
+
+
+@pytest.mark.parametrize("lens", [[(1, 120000)], [(70, 120000)], [(600, 9000), (1, 5000), (40, 41)], [(1, 30011), (3, 20000), (2, 7)]])
+@QUANT
+@DIM
+def test_long_contexts_lose_no_small_weights(D, quantised, lens):
+    """Unit-variance inputs.  An output is off by its rounding (2^-11), the weights'
+    (2^-11 of sum w |v|, and 2^-32 of the largest weight where FP16 is subnormal, times
+    the largest |v|), and the FP32 scores' (head_dim * 2^-24 * scale * sum |q k| <
+    2^-12 of each weight, twice with the normalisation)."""
+    g = torch.Generator(device="cuda").manual_seed(73)
+    hkv, group, page = 2, 5, 64
+    need = [-(-c // page) for _, c in lens]
+    table = torch.full((len(lens), max(need)), -1, dtype=torch.int32)
+    perm, at = torch.randperm(sum(need), generator=torch.Generator().manual_seed(74)).to(torch.int32), 0
+    for b, m in enumerate(need):
+        table[b, :m] = perm[at:at + m]
+        at += m
+    cache = qsa.KVCache.empty(sum(need), page, hkv, D, table.cuda(), quantised=quantised)
+    T, C = sum(n for n, _ in lens), sum(c for _, c in lens)
+    kv = torch.randn(C, 2 * hkv, D, generator=g, device="cuda", dtype=torch.float16)
+    starts = i32(np.concatenate([[0], np.cumsum([c for _, c in lens])]).tolist())
+    zero = torch.zeros(len(lens), dtype=torch.int32, device="cuda")
+    qsa.kv_store(kv[:, :hkv], kv[:, hkv:], starts, zero, cache)
+    k, v = qsa.kv_load(starts, zero, C, cache)
+    q = torch.randn(T, hkv * group, D, generator=g, device="cuda", dtype=torch.float16)
+    out = qsa.chunk_attention(q, i32(np.concatenate([[0], np.cumsum([n for n, _ in lens])]).tolist()),
+                              i32([c - n for n, c in lens]), cache).double()
+    st = qsa.get_device_status()
+    assert st == qsa.QSA_OK, qsa.status_string(st)
+    want, mag = reference64(q, k, v, lens)
+    row = 0
+    for n, c in lens:
+        r = slice(row, row + n)
+        tol = 2.0 ** -11 * want[r].abs() + 2.0 ** -10 * mag[r] + c * 2.0 ** -32 * 6.0 + 2.0 ** -25
+        off = (out[r] - want[r]).abs()
+        assert torch.all(off <= tol), (n, c, float((off / tol).max()))
+        row += n
