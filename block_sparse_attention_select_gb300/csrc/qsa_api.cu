@@ -434,7 +434,8 @@ qsa_status qsa_set_config(int32_t key, int64_t value)
     }
     if (key == QSA_CFG_WAIT_LIMIT_NS) {
         if (value <= 0) return QSA_ERR_INVALID_ARG;
-        g_wait_ns = static_cast<uint64_t>(value);
+        // (the kernels count two clocks per ns, in 64 bits)
+        g_wait_ns = static_cast<uint64_t>(std::min<int64_t>(value, int64_t{1} << 61));
         return QSA_OK;
     }
     return QSA_ERR_INVALID_ARG;

@@ -57,3 +57,12 @@ def test_a_limit_of_a_step_does_not_end_a_long_unit(call):
     again, status = call(1_000_000)                          # a millisecond, for steps of two microseconds
     assert status == qsa.QSA_OK
     assert torch.equal(again, first)
+
+
+@pytest.mark.parametrize("limit_ns", [2 ** 62, 2 ** 63 - 1])
+def test_the_largest_limit_is_no_limit(call, limit_ns):
+    first, status = call(2_000_000_000)
+    assert status == qsa.QSA_OK
+    again, status = call(limit_ns)
+    assert status == qsa.QSA_OK
+    assert torch.equal(again, first)
