@@ -1129,6 +1129,10 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
     if (t == 0 && *abort) tell_other(&c.abort, rank ^ 1, 1u);
     __syncwarp();
     cluster_sync();                                          // nothing of the pair reaches into the other any more
+    // the last commits have arrived in the first CTA; here, too
+    if (rank == 1 && t == 0)
+        for (int i = 0; i < (Sh::OWN_P ? 2 : 1); ++i) mbar_wait_bounded(&c.drain[i], 0, DRAIN_NS);
+    __syncwarp();
     if (*abort) {
         // After a time-out in either CTA, copies may be in flight that complete on the
         // other one's barriers, whatever became of the loader itself.  Every role of
