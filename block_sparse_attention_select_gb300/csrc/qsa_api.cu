@@ -920,11 +920,21 @@ qsa_status check_batch(int32_t rows, int32_t n_reqs, const int32_t *seq_start, c
 
 // Which attention kernel: units of 16 (token, query head) pairs read straight
 // from the cache's bytes while requests have no more than that on average, pairs
-// of SMs with units of 256 above.  On 64 single tokens over up to 32,768, 12 query
-// heads to a KV head, the first takes 299 us from the FP16 cache and 170 us from
-// the E4M3 cache, the second 298 and 466 us; with four times the pairs the first
-// reads the cache four times.  (An average, for the lengths are on the device: a
-// long prompt among many empty requests is slow, not wrong.)
+// of SMs with units of 256 above.  The first reads the cache once for every 16
+// pairs, the second turns E4M3 codes into FP16 for units that are mostly empty.
+// 64 requests over 16,384 tokens each, 2 KV heads of 256, us of the first and second:
+//   pairs per request     16           32            64            128
+//   FP16 cache         328,  325     633,  328   1,243,   331   2,465,   342
+//   E4M3 cache         177,  349     336,  353     652,   366   1,287,   377
+// and over 8 KV heads of 128
+//   FP16 cache         644,  660   1,271,  712   2,517,   686   4,973,   720
+//   E4M3 cache         495, 1,002    974, 1,008  1,925, 1,032   3,823, 1,076
+// It is an average, for the lengths are on the device, and one kernel serves the
+// whole batch.  60 single tokens over 16,384 and a chunk of 512 (24 heads over 2
+// x 256) take 392 us from the FP16 cache, 304 and 145 in two calls, and 482 us from
+// the E4M3 cache, 166 and 157 in two.  The other way round, 63 single tokens over
+// 4,096 and a prompt of 961 with one query head to a KV head take 171 and 163 us in
+// the first kernel, 177 and 267 in the second.
 bool few_rows(int32_t rows, int32_t group, int32_t n_reqs)
 {
     return static_cast<int64_t>(rows) * group <= int64_t{16} * n_reqs;

@@ -20,7 +20,8 @@
 // Work: the units' tiles, in the order (request, rows, KV head), form one line
 // that the CTA pairs share out evenly (each unit UNIT_COST tiles longer than it
 // is, for what it costs besides them: counted as 2, 3, 4 and 5 tiles, four prompts
-// of 4,096 tokens took 495, 483, 419 and 460 us on one warm card), so one row over
+// of 4,096 tokens took 495, 483, 419 and 460 us on one warm card; taken over for
+// 256-wide heads and E4M3, where it was not measured), so one row over
 // a long cache, a batch of unequal requests and a long prompt all fill the card.  A unit that
 // lies across pairs leaves unnormalised FP32 partial sums with their maxima in
 // the workspace (at most two per pair), which a second kernel joins.  Every
@@ -48,16 +49,21 @@
 // With D = 256, TMEM is full (2 x 128 for S, 256 for O): P overwrites its
 // scores and the order is S(0) S(1) | O(0) S(2) | O(1) S(3) | ...
 //
-// What bounds it: with D = 256 and a long context the tensor cores (the
-// 1,616-row chunk over 29,000 tokens, 12 query heads to a KV head: 568 us, 1,970
-// TF/s, tensor pipe 94% busy).  With D = 128 a tile's products take half as long
-// and its exponentials the same, so the latency of two softmax warps per scheduler
-// shows (four prompts of 4,096 tokens, 32 heads: 379 us, 1,450 TF/s; tensor pipe
-// 67%, issue slots 48%).  From the E4M3 cache the turning of codes into FP16 tiles
-// (three chunks of 517 over 12,345 tokens: 151 us, 1,290 TF/s, tensor pipe 59%).
-// A short call is the search for its work, its first loads and its last output:
-// two chunks of 1,023 tokens with a window of 1,000 take 40 us where their products
-// need 9.
+// What bounds it (times of single calls on a cool card, in parentheses in a stream
+// of calls, where the power cap takes some of the clock): with D = 256 and a long
+// context the tensor cores (the 1,616-row chunk over 29,000 tokens, 12 query heads
+// to a KV head: 567 us (661), 1,970 TF/s, tensor pipe 94% busy).  With D = 128 a
+// tile's products take half as long and its exponentials the same, so the latency
+// of two softmax warps per scheduler shows (four prompts of 4,096 tokens, 32 heads:
+// 377 us (424), 1,460 TF/s; tensor pipe 69%, issue slots 48%).  From the E4M3 cache
+// the turning of codes into FP16 tiles, anew for each unit of 256 pairs (three
+// chunks of up to 517 over up to 12,345 tokens: 151 us (156), 1,290 TF/s, tensor pipe
+// 59%).  Two chunks of up to 1,023 tokens with a window of 1,000 take 40 us (43) where
+// their products need 9: the search for the work, the first loads and the last
+// output are a third of it, the rest has not been taken apart.
+//
+// From the E4M3 cache times move by up to 8% with the place of the kernel's code:
+// two groups of warps in long unrolled loops share the instruction caches.
 //
 // The accumulator is rescaled only when a row's maximum has grown by more than
 // 2^8 since the one in use: the sum uses the same stale maximum, so the result

@@ -13,8 +13,8 @@
 //
 // Why not the tcgen05 kernel: from the E4M3 cache its tiles have to be written
 // back to shared memory as FP16 before the products can read them, three times
-// the loaded bytes through a port that the MMA operands need too (466 us on the
-// 64-request step).  Here a thread turns the codes that it loads into operand
+// the loaded bytes through a port that the MMA operands need too (64 requests' tokens
+// over 16,384: 349 us, 177 here).  Here a thread turns the codes that it loads into operand
 // registers.  The order of the dimensions inside a product is free, as long as
 // both operands agree, so each thread takes 16 contiguous bytes of a token:
 //   K: thread (r, q) = (lane / 4, lane % 4) reads piece 2 q + (i & 1) of 128-byte
@@ -24,8 +24,8 @@
 //      2 q + 9; byte permutes pair up two tokens' values of a dim.
 // With the 128-byte swizzle both patterns touch all banks evenly.
 //
-// Bound by the loads: 64 requests' tokens over up to 32,768 tokens take 299 us from
-// the FP16 cache (6.48 TB/s) and 170 us from the E4M3 cache (6.2 TB/s; its scales
+// Bound by the loads: 64 requests' tokens over up to 32,768 tokens take 290 to 299 us
+// from the FP16 cache (6.5 to 6.7 TB/s) and 171 us from the E4M3 cache (6.2 TB/s; its scales
 // are single bytes 2 x hkv apart).  One token over 4,096 takes 14 us: the launch,
 // the search for its work, one memory latency each for table, keys and join.
 #include <cuda.h>

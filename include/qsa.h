@@ -289,14 +289,17 @@ qsa_status qsa_kv_load(void *k, int64_t k_stride, void *v, int64_t v_stride, int
  * otherwise).  |scale * q . k| has to stay below 1.8e8 (the weights are relative to
  * the largest, and rows with larger scores may lose all of them).
  * q: FP16, row r at q + r * q_stride elements (a multiple of 8, at least hq *
- * head_dim), out: FP16 [rows, hq, head_dim], values past 65,504 by rounding stored
- * as that; both 16-byte aligned.  hq / hkv <=
- * 128.  Pages that no row attends are not read (their table entries may hold
- * anything), and cache slots that no row of the request attends may hold
- * anything, NaN included; keys and values that some row attends must be
- * finite FP16 numbers.  ws: qsa_chunk_attention_workspace_bytes(...) bytes, 256-byte
- * aligned; calls that may overlap need workspaces of their own (two captured
- * graphs replayed on different streams, too). */
+ * head_dim), out: FP16 [rows, hq, head_dim], values past 65,504 by rounding
+ * stored as that; both 16-byte aligned.  hq / hkv <= 128.  Pages that no row
+ * attends are not read (their table entries may hold anything), and cache
+ * slots that no row of the request attends may hold anything, NaN included;
+ * keys and values that some row attends must be finite FP16 numbers.  One of
+ * two kernels serves the whole batch, by its average of rows * (hq / hkv) /
+ * n_reqs (up to 16: the one for few rows), so from the E4M3 cache many single
+ * tokens and a long chunk take less time in two calls.  ws:
+ * qsa_chunk_attention_workspace_bytes(...) bytes, 256-byte aligned; calls
+ * that may overlap need workspaces of their own (two captured graphs replayed
+ * on different streams, too). */
 size_t qsa_chunk_attention_workspace_bytes(int32_t rows, int32_t hq, int32_t hkv, int32_t head_dim);
 qsa_status qsa_chunk_attention(const void *q, int64_t q_stride, int32_t rows, int32_t hq, int32_t n_reqs,
                                const int32_t *seq_start, const int32_t *pos_start, const qsa_kv_cache *cache,
