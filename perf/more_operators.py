@@ -315,7 +315,7 @@ def _tables(st):
     table.copy_(torch.where(put, page, table))
     row, b = _rows(seq_start, rows)
     inside = row < seq_start[-1]
-    b = torch.where(inside, b, 0)
+    b = torch.where(inside, b, torch.searchsorted(seq_start[1:], seq_start[-1:] - 1, right=True))   # the last row's
     tok = torch.where(inside, ctx[b] + row - seq_start[b], 0).to(torch.int32)
     slot = torch.where(inside, table[b, (tok // P).long()] * P + tok % P, -1)
     return {"block_table": table, "seq_start": seq_start, "pos_start": ctx.clone(), "total_len": ctx + n,
@@ -451,7 +451,7 @@ def _exact_tables(case, st):
         out["seq_start"].append(rows)
         out["total_len"].append(p + a)
     out["row_visible"] = [(t + 1) // 4 for t in out["row_token"]]
-    for name, nothing in (("row_req", 0), ("row_token", 0), ("row_visible", 0), ("slot", -1)):
+    for name, nothing in (("row_req", out["row_req"][-1] if rows else 0), ("row_token", 0), ("row_visible", 0), ("slot", -1)):
         out[name] += [nothing] * (case["rows"] - rows)
     out["block_table"], out["state"] = table, [rows, left, served]
     return {name: _int32(x) for name, x in out.items()}
