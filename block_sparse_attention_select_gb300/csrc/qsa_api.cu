@@ -971,6 +971,25 @@ KvParams kv_params(const qsa_kv_cache *c, int32_t rows, int32_t n_reqs, const in
     return p;
 }
 
+ChunkParams chunk_params(const void *q, int64_t q_stride, int32_t hq, const KvParams &kv, float scale, void *out, void *ws)
+{
+    ChunkParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.kv = kv;
+    p.q = q;
+    p.q_stride = q_stride;
+    p.out = out;
+    p.hq = hq;
+    p.group = hq / kv.hkv;
+    p.group_shift = 31;
+    while ((1 << (p.group_shift - 31)) < p.group) ++p.group_shift;
+    p.group_mul = static_cast<uint32_t>(((uint64_t{1} << p.group_shift) + p.group - 1) / p.group);
+    p.scale = scale;
+    p.ws = static_cast<uint8_t *>(ws);
+    p.wait_limit_ns = g_wait_ns;
+    return p;
+}
+
 }  // namespace
 
 extern "C" {
@@ -1033,21 +1052,8 @@ qsa_status qsa_chunk_attention(const void *q, int64_t q_stride, int32_t rows, in
     if (!aligned(ws, 256)) return QSA_ERR_INVALID_ARG;
     DeviceInfo *d = nullptr;
     if ((st = device_info(&d)) != QSA_OK) return st;
-    ChunkParams p;
-    std::memset(&p, 0, sizeof(p));
-    p.kv = kv_params(cache, rows, n_reqs, seq_start, pos_start, d);
-    p.q = q;
-    p.q_stride = q_stride;
-    p.out = out;
-    p.hq = hq;
-    p.group = hq / cache->hkv;
-    p.group_shift = 31;
-    while ((1 << (p.group_shift - 31)) < p.group) ++p.group_shift;
-    p.group_mul = static_cast<uint32_t>(((uint64_t{1} << p.group_shift) + p.group - 1) / p.group);
+    ChunkParams p = chunk_params(q, q_stride, hq, kv_params(cache, rows, n_reqs, seq_start, pos_start, d), scale, out, ws);
     p.window = window;
-    p.scale = scale;
-    p.ws = static_cast<uint8_t *>(ws);
-    p.wait_limit_ns = g_wait_ns;
     CUtensorMap tk, tv;
     if (few_rows(rows, p.group, n_reqs)) {
         p.ws_rows = chunk_rows_part_rows(rows, p.group);
@@ -1065,6 +1071,191 @@ qsa_status qsa_chunk_attention(const void *q, int64_t q_stride, int32_t rows, in
     }
     if (st == QSA_OK) ++g_launches;                      // the join kernel
     return st;
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// Around the block scorer: a batch's tables, rotary positions, attention over
+// the selected blocks
+
+extern "C" {
+
+qsa_status qsa_batch_tables(const int32_t *new_len, const int32_t *ctx_len, int32_t n_reqs, int32_t rows,
+                            int32_t page_tokens, int32_t *block_table, int32_t max_pages, const int32_t *free_pages,
+                            int32_t free_capacity, const int32_t *free_count, const qsa_batch *batch, void *stream)
+{
+    g_launches = 0;
+    if (n_reqs < 0 || rows < 0 || max_pages < 1 || free_capacity < 0 || !batch) return QSA_ERR_INVALID_ARG;
+    if (page_tokens < 8 || page_tokens > 256 || (page_tokens & (page_tokens - 1)) != 0) return QSA_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(max_pages) * page_tokens >= INT32_MAX || n_reqs > 65535) return QSA_ERR_UNSUPPORTED;
+    if (n_reqs > 0 && (!new_len || !ctx_len || !block_table || !batch->pos_start)) return QSA_ERR_INVALID_ARG;
+    if (!batch->seq_start || !batch->state || !free_count || (free_capacity > 0 && !free_pages)) return QSA_ERR_INVALID_ARG;
+    for (const void *p : {static_cast<const void *>(new_len), static_cast<const void *>(ctx_len),
+                          static_cast<const void *>(block_table), static_cast<const void *>(free_pages),
+                          static_cast<const void *>(free_count), static_cast<const void *>(batch->seq_start),
+                          static_cast<const void *>(batch->pos_start), static_cast<const void *>(batch->total_len),
+                          static_cast<const void *>(batch->row_req), static_cast<const void *>(batch->row_token),
+                          static_cast<const void *>(batch->row_visible), static_cast<const void *>(batch->slot),
+                          static_cast<const void *>(batch->state)})
+        if (!aligned(p, 4)) return QSA_ERR_INVALID_ARG;
+    DeviceInfo *d = nullptr;
+    const qsa_status st = device_info(&d);
+    if (st != QSA_OK) return st;
+    TablesParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.new_len = new_len;
+    p.ctx_len = ctx_len;
+    p.free_pages = free_pages;
+    p.free_count = free_count;
+    p.block_table = block_table;
+    p.seq_start = batch->seq_start;
+    p.pos_start = batch->pos_start;
+    p.total_len = batch->total_len;
+    p.row_req = batch->row_req;
+    p.row_token = batch->row_token;
+    p.row_visible = batch->row_visible;
+    p.slot = batch->slot;
+    p.state = batch->state;
+    p.n_reqs = n_reqs;
+    p.rows = rows;
+    p.page_tokens = page_tokens;
+    p.page_shift = log2_exact(page_tokens);
+    p.max_pages = max_pages;
+    p.free_capacity = free_capacity;
+    p.status = d->status;
+    return launch_rc(launch_tables(p, stream));
+}
+
+qsa_status qsa_rotary_table(float *table, int32_t n_pos, int32_t rope_dim, double theta,
+                            const qsa_rope_scaling *scaling, void *stream)
+{
+    g_launches = 0;
+    auto positive = [](double x) { return x > 0.0 && std::isfinite(x); };
+    if (n_pos < 0 || !positive(theta)) return QSA_ERR_INVALID_ARG;
+    if (rope_dim < 16 || rope_dim > 256 || rope_dim % 16 != 0) return QSA_ERR_UNSUPPORTED;
+    RotaryAngles a;
+    a.amplitude = 1.0;
+    double base = theta;
+    if (scaling) {
+        const qsa_rope_scaling &s = *scaling;
+        if (s.kind != QSA_ROPE_LINEAR && s.kind != QSA_ROPE_BASE && s.kind != QSA_ROPE_PARTS) return QSA_ERR_INVALID_ARG;
+        if (!positive(s.factor) || !positive(s.amplitude)) return QSA_ERR_INVALID_ARG;
+        if (s.kind == QSA_ROPE_PARTS && (!positive(s.original) || !(s.slow >= 0.0) || !(s.fast > s.slow) || !std::isfinite(s.fast)))
+            return QSA_ERR_INVALID_ARG;
+        a.amplitude = s.amplitude;
+        if (s.kind == QSA_ROPE_BASE) base = theta * std::pow(s.factor, static_cast<double>(rope_dim) / (rope_dim - 2));
+        if (!positive(base)) return QSA_ERR_INVALID_ARG;
+    }
+    for (int32_t j = 0; j < rope_dim / 2; ++j) {
+        double f = std::pow(base, -2.0 * j / rope_dim);
+        if (scaling && scaling->kind == QSA_ROPE_LINEAR) f /= scaling->factor;
+        if (scaling && scaling->kind == QSA_ROPE_PARTS) {
+            const double turns = scaling->original * f / (2.0 * 3.14159265358979323846);
+            const double g = std::min(1.0, std::max(0.0, (turns - scaling->slow) / (scaling->fast - scaling->slow)));
+            f *= g + (1.0 - g) / scaling->factor;
+        }
+        a.f[j] = f;
+    }
+    if (n_pos == 0) return QSA_OK;
+    if (!table || !aligned(table, 16)) return QSA_ERR_INVALID_ARG;
+    DeviceInfo *d = nullptr;
+    const qsa_status st = device_info(&d);
+    if (st != QSA_OK) return st;
+    return launch_rc(launch_rotary_table(table, n_pos, rope_dim, a, d->sms, stream));
+}
+
+qsa_status qsa_rotary(const void *q, int64_t q_stride, int32_t q_heads, void *out_q, int64_t out_q_stride,
+                      const void *k, int64_t k_stride, int32_t k_heads, void *out_k, int64_t out_k_stride,
+                      int32_t rows, int32_t head_dim, int32_t first, int32_t rope_dim, int32_t layout, int32_t n_reqs,
+                      const int32_t *seq_start, const int32_t *pos_start, const float *table, int32_t n_pos,
+                      void *stream)
+{
+    g_launches = 0;
+    if (rows < 0 || n_reqs < 0 || n_pos < 1 || q_heads < 1 || k_heads < 0 || first < 0) return QSA_ERR_INVALID_ARG;
+    if (layout != QSA_ROPE_HALVES && layout != QSA_ROPE_NEIGHBOURS) return QSA_ERR_INVALID_ARG;
+    if (head_dim < 16 || head_dim > 512 || head_dim % 16 != 0 || rope_dim < 16 || rope_dim > 256 || rope_dim % 16 != 0)
+        return QSA_ERR_UNSUPPORTED;
+    if (first % 8 != 0 || static_cast<int64_t>(first) + rope_dim > head_dim || n_reqs > 65535 ||
+        static_cast<int64_t>(q_heads) + k_heads > 4096)
+        return QSA_ERR_UNSUPPORTED;
+    if (rows == 0 || n_reqs == 0) return QSA_OK;
+    if (!seq_start || !pos_start || !aligned(seq_start, 4) || !aligned(pos_start, 4)) return QSA_ERR_INVALID_ARG;
+    if (!table || !aligned(table, 16)) return QSA_ERR_INVALID_ARG;
+    const int64_t q_width = static_cast<int64_t>(q_heads) * head_dim, k_width = static_cast<int64_t>(k_heads) * head_dim;
+    if (!row_array_ok(q, q_stride, q_width) || !row_array_ok(out_q, out_q_stride, q_width)) return QSA_ERR_INVALID_ARG;
+    if (k_heads > 0 && (!row_array_ok(k, k_stride, k_width) || !row_array_ok(out_k, out_k_stride, k_width)))
+        return QSA_ERR_INVALID_ARG;
+    // in place with other strides: rows would overwrite each other's inputs
+    if ((q == out_q && q_stride != out_q_stride) || (k_heads > 0 && k == out_k && k_stride != out_k_stride))
+        return QSA_ERR_INVALID_ARG;
+    DeviceInfo *d = nullptr;
+    const qsa_status st = device_info(&d);
+    if (st != QSA_OK) return st;
+    RotaryParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.seq.seq_start = seq_start;
+    p.seq.pos_start = pos_start;
+    p.seq.rows = rows;
+    p.seq.n_reqs = n_reqs;
+    p.seq.max_pages = n_pos;
+    p.seq.status = d->status;
+    p.q = static_cast<const uint16_t *>(q);
+    p.k = static_cast<const uint16_t *>(k);
+    p.out_q = static_cast<uint16_t *>(out_q);
+    p.out_k = static_cast<uint16_t *>(out_k);
+    p.q_stride = q_stride;
+    p.k_stride = k_stride;
+    p.out_q_stride = out_q_stride;
+    p.out_k_stride = out_k_stride;
+    p.table = table;
+    p.q_heads = q_heads;
+    p.k_heads = k_heads;
+    p.head_dim = head_dim;
+    p.first = first;
+    p.rope_dim = rope_dim;
+    const bool in_place = q == out_q && (k_heads == 0 || k == out_k);
+    p.items = (in_place ? rope_dim : head_dim) / 16;
+    return launch_rc(launch_rotary(p, layout == QSA_ROPE_NEIGHBOURS, d->sms, stream));
+}
+
+size_t qsa_block_attention_workspace_bytes(int32_t rows, int32_t hq, int32_t hkv, int32_t head_dim, int32_t k,
+                                           int32_t recent, int32_t row_capacity)
+{
+    return 256;
+}
+
+qsa_status qsa_block_attention(const void *q, int64_t q_stride, int32_t rows, int32_t hq, int32_t n_reqs,
+                               const int32_t *seq_start, const int32_t *pos_start, const qsa_kv_cache *cache,
+                               const int32_t *sel, int32_t k, int32_t recent, float scale, void *out, void *ws,
+                               size_t ws_bytes, void *stream)
+{
+    g_launches = 0;
+    bool any;
+    if (hq < 1 || k < 0 || recent < 0 || !(scale > 0.0f) || !std::isfinite(scale * 1.4426950408889634f))
+        return QSA_ERR_INVALID_ARG;
+    qsa_status st = check_batch(rows, n_reqs, seq_start, pos_start, cache, &any);
+    if (st != QSA_OK) return st;
+    if (hq % cache->hkv != 0 || hq / cache->hkv > 128 || k > QSA_MAX_K || recent > QSA_MAX_K) return QSA_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(cache->max_pages) * cache->page_tokens > BLOCKS_MAX_TOKENS) return QSA_ERR_UNSUPPORTED;
+    if (!any) return QSA_OK;
+    const int64_t width = static_cast<int64_t>(hq) * cache->head_dim;
+    if (static_cast<int64_t>(rows) * hq >= INT32_MAX) return QSA_ERR_UNSUPPORTED;
+    if (!row_array_ok(q, q_stride, width) || !out || !aligned(out, 16)) return QSA_ERR_INVALID_ARG;
+    if (k > 0 && (!sel || !aligned(sel, 4))) return QSA_ERR_INVALID_ARG;
+    if (!ws || ws_bytes < qsa_block_attention_workspace_bytes(rows, hq, cache->hkv, cache->head_dim, k, recent,
+                                                              cache->max_pages * cache->page_tokens))
+        return QSA_ERR_WORKSPACE;
+    if (!aligned(ws, 256)) return QSA_ERR_INVALID_ARG;
+    DeviceInfo *d = nullptr;
+    if ((st = device_info(&d)) != QSA_OK) return st;
+    BlocksParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.c = chunk_params(q, q_stride, hq, kv_params(cache, rows, n_reqs, seq_start, pos_start, d), scale, out, ws);
+    p.sel = sel;
+    p.k = k;
+    p.recent = recent;
+    return launch_rc(launch_blocks(p, d->sms, g_overlap, stream));
 }
 
 }  // extern "C"

@@ -202,6 +202,38 @@ struct ChunkParams {
     uint64_t wait_limit_ns;
 };
 
+// Attention over selected blocks: see qsa_blocks.cu.  c.window is 0.
+struct BlocksParams {
+    ChunkParams c;
+    const int32_t *sel;         // [rows, hkv, k] blocks of 128 tokens, -1: none
+    int32_t k, recent;
+};
+
+// Rotary positions: see qsa_rotary.cu.
+struct RotaryParams {
+    KvParams seq;               // seq_start, pos_start, rows, n_reqs; max_pages: positions of the table
+    const uint16_t *q, *k;      // FP16, rows at strides in elements
+    uint16_t *out_q, *out_k;
+    int64_t q_stride, k_stride, out_q_stride, out_k_stride;
+    const float *table;         // [positions, rope_dim]
+    int32_t q_heads, k_heads, head_dim, first, rope_dim;
+    int32_t items;              // 16-dim pieces of a head to go through
+    int32_t slices, cta_rows;   // set by the launcher: threads that share a token's heads, rows of a CTA
+};
+struct RotaryAngles {
+    double f[128];              // angle per position of each pair
+    double amplitude;
+};
+
+// Tables of a batch from its requests' lengths: see qsa_tables.cu.
+struct TablesParams {
+    const int32_t *new_len, *ctx_len, *free_pages, *free_count;
+    int32_t *block_table;       // [n_reqs, max_pages]
+    int32_t *seq_start, *pos_start, *total_len, *row_req, *row_token, *row_visible, *slot, *state;
+    int32_t n_reqs, rows, page_tokens, page_shift, max_pages, free_capacity;
+    uint32_t *status;
+};
+
 // Launchers (one translation unit each); return cudaError_t as int.  With
 // `overlap` the launch carries programmatic stream serialization: the kernel
 // may be scheduled while the previous kernel of the stream is still running
@@ -266,5 +298,12 @@ int launch_chunk_rows(const ChunkParams &p, const void *tk, const void *tv, int 
 int32_t chunk_rows_part_rows(int32_t rows, int32_t group);
 size_t chunk_rows_workspace_bytes(int32_t rows, int32_t group, int32_t head_dim);
 int32_t chunk_rows_box(int32_t page_tokens);
+
+constexpr int32_t BLOCK_TOKENS = 128;        // tokens of a selected block
+constexpr int64_t BLOCKS_MAX_TOKENS = int64_t{1} << 25;   // tokens of a request at most
+int launch_blocks(const BlocksParams &p, int sms, bool overlap, void *stream);
+int launch_rotary_table(float *table, int32_t n_pos, int32_t rope_dim, const RotaryAngles &angles, int sms, void *stream);
+int launch_rotary(const RotaryParams &p, bool neighbours, int sms, void *stream);
+int launch_tables(const TablesParams &p, void *stream);
 
 }  // namespace qsa

@@ -41,10 +41,6 @@ constexpr int KV_THREADS = 256;
 constexpr int KV_BATCH = 8;        // vectors in flight per thread
 constexpr int KV_MAX_ROWS = 16;    // rows per warp
 
-// Whether a request has the row.  (n > 0 first: a skipped request's start may be any
-// number, and the difference wrap.)
-__device__ __forceinline__ bool has_row(const Seq &s, int32_t row) { return s.n > 0 && row >= s.s0 && row - s.s0 < s.n; }
-
 // Cache line (page * page_tokens + slot) of a row of request b: -2 a page outside
 // the cache.
 __device__ __forceinline__ int32_t line_of(const KvParams &p, int32_t b, const Seq &s, int32_t row)

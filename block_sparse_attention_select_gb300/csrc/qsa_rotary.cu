@@ -1,0 +1,174 @@
+// Rotary positions: the table of cosines and sines, and the rotation of queries
+// and keys.
+//
+// Bound by memory: every value is read and written once.  A thread takes 16 dims
+// of a head as two 16-byte vectors (both halves of eight pairs) and goes through
+// the heads of its token with them, so that it reads its eight cosines and sines
+// once for all heads; ROT_BATCH heads' loads are in flight together.
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "qsa_device.cuh"
+#include "qsa_internal.h"
+#include "qsa_seq.cuh"
+
+namespace qsa {
+namespace {
+
+constexpr int ROT_THREADS = 256;
+constexpr int ROT_ROWS = 32;                 // rows of a CTA at most
+constexpr int ROT_BATCH = 4;
+
+// Eight pairs: a and b of each as FP16 halves of four words; neighbours: a0 b0 a1 b1 ...
+template <bool NEIGHBOURS>
+__device__ __forceinline__ void rotate8(uint4 &x, uint4 &y, const float (&cs)[8], const float (&sn)[8])
+{
+    uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+    if (NEIGHBOURS) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+            const __half2 h = __floats2half2_rn(v.x * cs[i] - v.y * sn[i], v.y * cs[i] + v.x * sn[i]);
+            w[i] = *reinterpret_cast<const uint32_t *>(&h);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+            const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&w[4 + i]));
+            const __half2 h = __floats2half2_rn(a.x * cs[2 * i] - b.x * sn[2 * i], a.y * cs[2 * i + 1] - b.y * sn[2 * i + 1]);
+            const __half2 l = __floats2half2_rn(b.x * cs[2 * i] + a.x * sn[2 * i], b.y * cs[2 * i + 1] + a.y * sn[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t *>(&h);
+            w[4 + i] = *reinterpret_cast<const uint32_t *>(&l);
+        }
+    }
+    x = make_uint4(w[0], w[1], w[2], w[3]);
+    y = make_uint4(w[4], w[5], w[6], w[7]);
+}
+
+template <bool NEIGHBOURS>
+__global__ void __launch_bounds__(ROT_THREADS)
+rotary_kernel(const RotaryParams p)
+{
+    __shared__ int32_t pos_s[ROT_ROWS];
+    const int t = threadIdx.x;
+    wait_prior_grid();
+    if (blockIdx.x == 0) flag_bad_requests(p.seq);
+    const int32_t row0 = blockIdx.x * p.cta_rows, n_rows = min(p.cta_rows, p.seq.rows - row0);
+    Seq s;
+    const int32_t b = requests_of_rows(p.seq, row0, n_rows, &s);
+    if (t < n_rows) pos_s[t] = b < 0 ? -1 : s.p0 + (row0 + t - s.s0);
+    __syncthreads();
+
+    const int32_t turned = p.rope_dim / 16;                  // items of a head that rotate, then those that are copied
+    const int32_t items = p.items, per_row = items * p.slices, total = n_rows * per_row;
+    const int32_t heads = p.q_heads + p.k_heads;
+    for (int32_t i = t; i < total; i += ROT_THREADS) {
+        const int32_t r = i / per_row, in = i - r * per_row, slice = in / items, item = in - slice * items;
+        const int32_t at = pos_s[r];
+        if (at < 0) continue;
+        const bool turn = item < turned;
+        // the item's two vectors, as dims of a head
+        int32_t d0, d1;
+        float cs[8], sn[8];
+        if (turn) {
+            d0 = p.first + (NEIGHBOURS ? 16 : 8) * item;
+            d1 = d0 + (NEIGHBOURS ? 8 : p.rope_dim / 2);
+            const float4 *tab = reinterpret_cast<const float4 *>(p.table + static_cast<int64_t>(at) * p.rope_dim + 8 * item);
+            const float4 *tbs = reinterpret_cast<const float4 *>(p.table + static_cast<int64_t>(at) * p.rope_dim + p.rope_dim / 2 + 8 * item);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const float4 c = __ldg(tab + k), s = __ldg(tbs + k);
+                cs[4 * k] = c.x, cs[4 * k + 1] = c.y, cs[4 * k + 2] = c.z, cs[4 * k + 3] = c.w;
+                sn[4 * k] = s.x, sn[4 * k + 1] = s.y, sn[4 * k + 2] = s.z, sn[4 * k + 3] = s.w;
+            }
+        } else {
+            // vectors outside the rotated part, in order
+            const int32_t v = 2 * (item - turned), skip = p.rope_dim / 8, before = p.first / 8;
+            d0 = 8 * (v < before ? v : v + skip);
+            d1 = 8 * (v + 1 < before ? v + 1 : v + 1 + skip);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) cs[k] = 1.0f, sn[k] = 0.0f;
+        }
+        const int64_t row = row0 + r;
+        auto in_of = [&](int32_t h) {
+            return h < p.q_heads ? p.q + (row * p.q_stride + static_cast<int64_t>(h) * p.head_dim)
+                                 : p.k + (row * p.k_stride + static_cast<int64_t>(h - p.q_heads) * p.head_dim);
+        };
+        auto out_of = [&](int32_t h) {
+            return h < p.q_heads ? p.out_q + (row * p.out_q_stride + static_cast<int64_t>(h) * p.head_dim)
+                                 : p.out_k + (row * p.out_k_stride + static_cast<int64_t>(h - p.q_heads) * p.head_dim);
+        };
+        for (int32_t h0 = slice; h0 < heads; h0 += p.slices * ROT_BATCH) {
+            uint4 x[ROT_BATCH], y[ROT_BATCH];
+#pragma unroll
+            for (int k = 0; k < ROT_BATCH; ++k) {
+                const int32_t h = h0 + k * p.slices;
+                if (h >= heads) break;
+                x[k] = *reinterpret_cast<const uint4 *>(in_of(h) + d0);
+                y[k] = *reinterpret_cast<const uint4 *>(in_of(h) + d1);
+            }
+#pragma unroll
+            for (int k = 0; k < ROT_BATCH; ++k) {
+                const int32_t h = h0 + k * p.slices;
+                if (h >= heads) break;
+                if (!turn && in_of(h) == out_of(h)) continue;     // in place
+                if (turn) rotate8<NEIGHBOURS>(x[k], y[k], cs, sn);
+                *reinterpret_cast<uint4 *>(out_of(h) + d0) = x[k];
+                *reinterpret_cast<uint4 *>(out_of(h) + d1) = y[k];
+            }
+        }
+    }
+    allow_next_grid();
+}
+
+__global__ void __launch_bounds__(256)
+rotary_table_kernel(float *table, int32_t n_pos, int32_t half, const RotaryAngles a)
+{
+    const int64_t n = static_cast<int64_t>(n_pos) * half;
+    wait_prior_grid();
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n;
+         i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+        const int64_t pos = i / half;
+        const int32_t j = static_cast<int32_t>(i - pos * half);
+        double s, c;
+        sincos(static_cast<double>(pos) * a.f[j], &s, &c);
+        float *row = table + pos * (2 * half);
+        row[j] = static_cast<float>(a.amplitude * c);
+        row[half + j] = static_cast<float>(a.amplitude * s);
+    }
+}
+
+}  // namespace
+
+int launch_rotary_table(float *table, int32_t n_pos, int32_t rope_dim, const RotaryAngles &angles, int sms, void *stream)
+{
+    int32_t half = rope_dim / 2;
+    const int64_t blocks = (static_cast<int64_t>(n_pos) * half + 255) / 256;
+    const int grid = static_cast<int>(std::min<int64_t>(blocks, 8 * sms));
+    void *args[] = {&table, &n_pos, &half, const_cast<RotaryAngles *>(&angles)};
+    return launch_kernel(reinterpret_cast<const void *>(&rotary_table_kernel), dim3(grid), dim3(256), 0,
+                         static_cast<cudaStream_t>(stream), false, args);
+}
+
+int launch_rotary(const RotaryParams &in, bool neighbours, int sms, void *stream)
+{
+    RotaryParams p = in;
+    const int32_t heads = p.q_heads + p.k_heads;
+    // head slices: few heads to a thread while threads are few
+    const int64_t want = static_cast<int64_t>(sms) * 2048;
+    p.slices = 1;
+    while (p.slices * 2 <= heads && static_cast<int64_t>(p.seq.rows) * p.items * p.slices < want) p.slices *= 2;
+    const int64_t per_row = static_cast<int64_t>(p.items) * p.slices;
+    p.cta_rows = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(ROT_ROWS, ROT_THREADS / per_row)));
+    const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(p.seq.rows) + p.cta_rows - 1) / p.cta_rows);
+    void *args[] = {&p};
+    return launch_kernel(neighbours ? reinterpret_cast<const void *>(&rotary_kernel<true>)
+                                    : reinterpret_cast<const void *>(&rotary_kernel<false>),
+                         dim3(grid), dim3(ROT_THREADS), 0, static_cast<cudaStream_t>(stream), false, args);
+}
+
+}  // namespace qsa

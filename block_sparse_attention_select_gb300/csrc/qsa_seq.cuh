@@ -29,6 +29,57 @@ __device__ __forceinline__ Seq seq_of(const KvParams &p, int32_t b, bool *bad)
     return s;
 }
 
+// Whether a request has the row.  (n > 0 first: a skipped request's start may be any
+// number, and the difference wrap.)
+__device__ __forceinline__ bool has_row(const Seq &s, int32_t row) { return s.n > 0 && row >= s.s0 && row - s.s0 < s.n; }
+
+// The request of a row, or -1; its tokens in *s.
+__device__ __forceinline__ int32_t request_of(const KvParams &p, int32_t row, Seq *s)
+{
+    // the last request that starts at or before the row
+    int32_t lo = 0, hi = p.n_reqs;
+    while (hi - lo > 1) {
+        const int32_t mid = (lo + hi) >> 1;
+        if (__ldg(p.seq_start + mid) <= row) lo = mid;
+        else hi = mid;
+    }
+    bool bad;
+    *s = seq_of(p, lo, &bad);
+    return has_row(*s, row) ? lo : -1;
+}
+
+// The same where the starts fall somewhere: the first request that has the row.
+__device__ __forceinline__ int32_t request_of_unsorted(const KvParams &p, int32_t row, Seq *s)
+{
+#pragma unroll 1
+    for (int32_t b = 0; b < p.n_reqs; ++b) {
+        bool bad;
+        *s = seq_of(p, b, &bad);
+        if (has_row(*s, row)) return b;
+    }
+    return -1;
+}
+
+// Requests of rows row0 .. row0 + n - 1, a row per thread of the CTA (n <= its
+// threads), -1 for rows of no request; every thread of the CTA calls it.
+__device__ __forceinline__ int32_t requests_of_rows(const KvParams &p, int32_t row0, int32_t n, Seq *s)
+{
+    const int t = threadIdx.x;
+    int32_t b = -1;
+    if (t < n) b = request_of(p, row0 + t, s);
+    const bool lost = t < n && b < 0;
+    // no request: a row behind the last one or of a request that is skipped, or the
+    // search passed it by where the starts are out of order
+    if (__syncthreads_or(lost)) {
+        bool falls = false;
+#pragma unroll 4
+        for (int32_t i = t; i < p.n_reqs; i += blockDim.x)
+            falls = falls || __ldg(p.seq_start + i + 1) < __ldg(p.seq_start + i);
+        if (__syncthreads_or(falls) && lost) b = request_of_unsorted(p, row0 + t, s);
+    }
+    return b;
+}
+
 // Every request of the batch checked by one CTA (a search by row skips the rows of
 // a bad request, so nothing else would notice some of them).
 __device__ __forceinline__ void flag_bad_requests(const KvParams &p)

@@ -34,6 +34,9 @@ QSA_ERR_STATIC_LIMIT = 9
 QSA_KV_FP16 = 0
 QSA_KV_E4M3 = 1
 
+QSA_ROPE_HALVES, QSA_ROPE_NEIGHBOURS = 0, 1
+QSA_ROPE_LINEAR, QSA_ROPE_BASE, QSA_ROPE_PARTS = 1, 2, 3
+
 QSA_CFG_PATH = 1
 QSA_CFG_WAIT_LIMIT_NS = 2
 QSA_CFG_KERNEL_TIMING = 3
@@ -71,6 +74,16 @@ class KVCacheC(ctypes.Structure):
                 ("v_scale", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("num_pages", ctypes.c_int32),
                 ("page_tokens", ctypes.c_int32), ("hkv", ctypes.c_int32), ("head_dim", ctypes.c_int32),
                 ("block_table", ctypes.c_void_p), ("num_reqs", ctypes.c_int32), ("max_pages", ctypes.c_int32)]
+
+
+class BatchC(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("seq_start", "pos_start", "total_len", "row_req", "row_token",
+                                               "row_visible", "slot", "state")]
+
+
+class RopeScalingC(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32)] + [(n, ctypes.c_double) for n in ("factor", "original", "fast", "slow",
+                                                                           "amplitude")]
 
 
 _lib = None
@@ -129,6 +142,17 @@ def load(path: str = LIB_PATH):
     lib.qsa_chunk_attention_workspace_bytes.argtypes = [i32, i32, i32, i32]
     lib.qsa_chunk_attention.restype = ctypes.c_int
     lib.qsa_chunk_attention.argtypes = [vp, i64, i32, i32, i32, vp, vp, cp, i32, ctypes.c_float, vp, vp, sz, vp]
+    lib.qsa_batch_tables.restype = ctypes.c_int
+    lib.qsa_batch_tables.argtypes = [vp, vp, i32, i32, i32, vp, i32, vp, i32, vp, ctypes.POINTER(BatchC), vp]
+    lib.qsa_rotary_table.restype = ctypes.c_int
+    lib.qsa_rotary_table.argtypes = [vp, i32, i32, ctypes.c_double, ctypes.POINTER(RopeScalingC), vp]
+    lib.qsa_rotary.restype = ctypes.c_int
+    lib.qsa_rotary.argtypes = [vp, i64, i32, vp, i64, vp, i64, i32, vp, i64, i32, i32, i32, i32, i32, i32, vp, vp, vp,
+                               i32, vp]
+    lib.qsa_block_attention_workspace_bytes.restype = sz
+    lib.qsa_block_attention_workspace_bytes.argtypes = [i32] * 7
+    lib.qsa_block_attention.restype = ctypes.c_int
+    lib.qsa_block_attention.argtypes = [vp, i64, i32, i32, i32, vp, vp, cp, vp, i32, i32, ctypes.c_float, vp, vp, sz, vp]
     _lib = lib
     return lib
 
@@ -502,6 +526,197 @@ def chunk_attention(q, seq_start, pos_start, cache: KVCache, window: int = 0, sc
     scale = cache.head_dim ** -0.5 if scale is None else float(scale)
     _call(cache, stream, load().qsa_chunk_attention, q.data_ptr(), qs, rows, hq, n, seq_start.data_ptr(),
           pos_start.data_ptr(), cache.ref, min(max(int(window), -1), 2 ** 31 - 1), scale, out.data_ptr(), ws.data_ptr(),
+          ws.numel() * ws.element_size(), made=made)
+    return out
+
+
+class _Device:
+    """Where a call without a cache runs."""
+
+    def __init__(self, device):
+        self.device, self.index = device, device.index
+
+
+class Batch:
+    """Arrays that describe a batch, as batch_tables fills them: seq_start int32
+    [n + 1], pos_start, total_len [n], row_req, row_token, row_visible, slot
+    [rows], state [3] (rows in use, free pages left, first request that did not
+    fit).  The tensors' contents may change, the tensors themselves not."""
+
+    _NAMES = ("seq_start", "pos_start", "total_len", "row_req", "row_token", "row_visible", "slot", "state")
+
+    def __init__(self, seq_start, pos_start, total_len, row_req, row_token, row_visible, slot, state):
+        tensors = (seq_start, pos_start, total_len, row_req, row_token, row_visible, slot, state)
+        n, rows = pos_start.numel(), row_req.numel()
+        for t, name, size in zip(tensors, self._NAMES, (n + 1, n, n, rows, rows, rows, rows, 3)):
+            _need(t, torch.int32, name)
+            if t.shape != (size,):
+                raise ValueError(f"{name} must be [{size}], got {list(t.shape)}")
+            if t.device != seq_start.device:
+                raise ValueError("the tensors of a batch must be on one device")
+        for t, name in zip(tensors, self._NAMES):
+            setattr(self, name, t)
+        self.n, self.rows, self.device, self.index = n, rows, seq_start.device, seq_start.device.index
+        self.c = BatchC(*(t.data_ptr() for t in tensors))
+        self.ref = ctypes.byref(self.c)
+
+    def __setattr__(self, name, value):
+        if "ref" in self.__dict__:
+            raise AttributeError(f"a Batch is fixed once made: make another one with the new {name}")
+        super().__setattr__(name, value)
+
+    @classmethod
+    def empty(cls, n_reqs: int, rows: int, device=None):
+        """Uninitialised arrays for n_reqs requests and up to `rows` rows."""
+        def make(k):
+            return torch.empty(int(k), dtype=torch.int32, device=device or "cuda")
+        return cls(make(n_reqs + 1), make(n_reqs), make(n_reqs), *(make(rows) for _ in range(4)), make(3))
+
+
+def batch_tables(new_len, ctx_len, free_pages, free_count, block_table, page_tokens: int, batch: Batch, stream=None):
+    """Describe a batch from its requests' lengths and give it the pages that its
+    new tokens need: new_len, ctx_len int32 [n]; free_pages int32 [F] with
+    free_count int32 [1] of them in use, taken from the end; block_table int32 [n
+    or more, max_pages], filled in place.  Requests are served in order until one does
+    not fit in batch.rows or the free pages (batch.state).  total_len may be ctx_len
+    and free_count batch.state[1:2], so that the next call goes on from this one."""
+    n, dev = batch.n, batch.device
+    for t, name in ((new_len, "new_len"), (ctx_len, "ctx_len"), (free_pages, "free_pages"),
+                    (free_count, "free_count"), (block_table, "block_table")):
+        if t.dtype is not torch.int32 or t.device != dev or not t.is_contiguous():
+            _need(t, torch.int32, name)
+            raise ValueError(f"{name} must be on the batch's device")
+    if new_len.shape != (n,) or ctx_len.shape != (n,) or free_pages.dim() != 1 or free_count.shape != (1,):
+        raise ValueError("new_len and ctx_len must be [n], free_pages [F], free_count [1]")
+    if block_table.dim() != 2 or block_table.shape[0] < n:
+        raise ValueError("block_table must be [n or more, max_pages]")
+    _call(batch, stream, load().qsa_batch_tables, new_len.data_ptr(), ctx_len.data_ptr(), n, batch.rows,
+          int(page_tokens), block_table.data_ptr(), block_table.shape[1], free_pages.data_ptr(), free_pages.shape[0],
+          free_count.data_ptr(), batch.ref)
+    return batch
+
+
+class RopeScaling:
+    """How a rotary table is scaled for long contexts: kind "linear" (angles over
+    factor), "base" (a larger theta) or "parts" (slow pairs over factor, fast ones
+    as they are: the ramp goes from `slow` to `fast` turns over the `original`
+    positions); amplitude multiplies cosines and sines."""
+
+    KINDS = {"linear": QSA_ROPE_LINEAR, "base": QSA_ROPE_BASE, "parts": QSA_ROPE_PARTS}
+
+    def __init__(self, kind: str, factor: float, original: float = 0.0, fast: float = 32.0, slow: float = 1.0,
+                 amplitude: float = 1.0):
+        if kind not in self.KINDS:
+            raise ValueError(f"kind must be one of {sorted(self.KINDS)}, got {kind!r}")
+        self.c = RopeScalingC(self.KINDS[kind], float(factor), float(original), float(fast), float(slow), float(amplitude))
+
+
+def rotary_table(n_pos: int, rope_dim: int, theta: float = 10000.0, scaling: RopeScaling = None, device=None, stream=None):
+    """Cosines and sines of positions 0 .. n_pos - 1: FP32 [n_pos, rope_dim]."""
+    device = torch.empty(0, device=device or "cuda").device
+    with torch.cuda.device(device):
+        t = torch.empty((int(n_pos), int(rope_dim)), dtype=torch.float32, device=device)
+        _call(_Device(device), stream, load().qsa_rotary_table, t.data_ptr(), int(n_pos), int(rope_dim), float(theta),
+              None if scaling is None else ctypes.byref(scaling.c), made=[t])
+    return t
+
+
+def _head_rows(t, like, name: str):
+    """Checks an FP16 row array [rows, heads, head_dim] and returns (address, row
+    stride, heads): rows may be slices of wider ones, a row itself is contiguous."""
+    shape, stride = t.shape, t.stride()
+    if t.dtype is not torch.float16:
+        raise TypeError(f"{name} must be {torch.float16}, got {t.dtype}")
+    if t.device != like.device or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor on q's device")
+    if len(shape) != 3 or shape[0] != like.shape[0] or shape[2] != like.shape[2]:
+        raise ValueError(f"{name} must be [rows, heads, head_dim] with q's rows and head_dim, got {list(shape)}")
+    if stride[2] != 1 or (shape[1] > 1 and stride[1] != shape[2]):
+        raise ValueError(f"each row of {name} must be contiguous")
+    return t.data_ptr(), stride[0] if shape[0] > 1 else shape[1] * shape[2], shape[1]
+
+
+def rotary(q, k, seq_start, pos_start, table, first: int = 0, interleaved: bool = False, out_q=None, out_k=None,
+           stream=None):
+    """Rotate dims first .. first + table.shape[1] - 1 of the heads of q [T, hq, D]
+    and k [T, hk, D] (FP16, rows may be strided; k may be None) by their tokens'
+    positions and copy the others.  Pairs are (j, j + half), or neighbours
+    (interleaved).  out_q may be q and out_k k, in place; rows past the last
+    request are left as they are.  Returns (out_q, out_k)."""
+    if q.dim() != 3 or table.dim() != 2 or table.dtype is not torch.float32 or not table.is_contiguous():
+        raise ValueError("q must be [rows, heads, head_dim], table contiguous float32 [positions, rope_dim]")
+    if not q.is_cuda or table.device != q.device:
+        raise ValueError("q and table must be on one CUDA device")
+    where = _Device(q.device)
+    n = _requests(seq_start, pos_start, where)
+    made = []
+    if out_q is None:
+        out_q = torch.empty(q.shape, dtype=torch.float16, device=q.device)
+        made.append(out_q)
+    if k is None and out_k is not None:
+        raise ValueError("out_k goes with k")
+    if k is not None and out_k is None:
+        out_k = torch.empty(k.shape, dtype=torch.float16, device=q.device)
+        made.append(out_k)
+    qp, qs, hq = _head_rows(q, q, "q")
+    oqp, oqs, ohq = _head_rows(out_q, q, "out_q")
+    kp, ks, hk, okp, oks, ohk = 0, 0, 0, 0, 0, 0
+    if k is not None:
+        kp, ks, hk = _head_rows(k, q, "k")
+        okp, oks, ohk = _head_rows(out_k, q, "out_k")
+    if ohq != hq or ohk != hk:
+        raise ValueError("out_q and out_k must have q's and k's shapes")
+    _call(where, stream, load().qsa_rotary, qp, qs, hq, oqp, oqs, kp, ks, hk, okp, oks, q.shape[0], q.shape[2],
+          int(first), table.shape[1], QSA_ROPE_NEIGHBOURS if interleaved else QSA_ROPE_HALVES, n,
+          seq_start.data_ptr(), pos_start.data_ptr(), table.data_ptr(), table.shape[0], made=made)
+    return out_q, out_k
+
+
+def block_attention_workspace_bytes(rows: int, hq: int, hkv: int, head_dim: int, k: int, recent: int,
+                                    row_capacity: int) -> int:
+    return int(load().qsa_block_attention_workspace_bytes(int(rows), int(hq), int(hkv), int(head_dim), int(k),
+                                                          int(recent), int(row_capacity)))
+
+
+def alloc_block_attention_workspace(cache: KVCache, rows: int, hq: int, k: int, recent: int = 0) -> torch.Tensor:
+    n = block_attention_workspace_bytes(rows, hq, cache.hkv, cache.head_dim, k, recent, cache.c.max_pages * cache.c.page_tokens)
+    return torch.empty(n, dtype=torch.uint8, device=cache.device)
+
+
+def block_attention(q, sel, seq_start, pos_start, cache: KVCache, recent: int = 0, scale=None, out=None, ws=None,
+                    stream=None):
+    """Attention of new tokens over the blocks of 128 tokens selected for them
+    (block_select): the row at position p attends, for the query heads of KV head
+    g, tokens up to p of the blocks sel[row, g, :] (int32 [T, hkv, k], -1 for none)
+    and of its `recent` last blocks.  q FP16 [T, hq, head_dim] (rows may be
+    strided); returns FP16 [T, hq, head_dim], zeros for a row that attends
+    nothing, rows past the last request left as they are."""
+    n = _requests(seq_start, pos_start, cache)
+    hq = q.shape[1] if q.dim() == 3 else 0
+    qs = _row_stride(q, cache, hq, "q")
+    rows = q.shape[0]
+    if sel.dtype is not torch.int32 or sel.device != cache.device or not sel.is_contiguous():
+        _need(sel, torch.int32, "sel")
+        raise ValueError("sel must be on the cache's device")
+    if sel.dim() != 3 or sel.shape[0] != rows or sel.shape[1] != cache.hkv:
+        raise ValueError(f"sel must be [{rows}, {cache.hkv}, k], got {list(sel.shape)}")
+    k = sel.shape[2]
+    made = []
+    if out is None:
+        out = torch.empty((rows, hq, cache.head_dim), dtype=torch.float16, device=cache.device)
+        made.append(out)
+    elif out.shape != q.shape or out.device != cache.device:
+        raise ValueError("out must have q's shape and device")
+    else:
+        _need(out, torch.float16, "out")
+    if ws is None:
+        ws = alloc_block_attention_workspace(cache, rows, hq, k, recent)
+        made.append(ws)
+    elif ws.device != cache.device or not ws.is_contiguous():
+        raise ValueError("ws must be contiguous, on the cache's device")
+    scale = cache.head_dim ** -0.5 if scale is None else float(scale)
+    _call(cache, stream, load().qsa_block_attention, q.data_ptr(), qs, rows, hq, n, seq_start.data_ptr(),
+          pos_start.data_ptr(), cache.ref, sel.data_ptr(), k, int(recent), scale, out.data_ptr(), ws.data_ptr(),
           ws.numel() * ws.element_size(), made=made)
     return out
 

@@ -305,6 +305,110 @@ qsa_status qsa_chunk_attention(const void *q, int64_t q_stride, int32_t rows, in
                                const int32_t *seq_start, const int32_t *pos_start, const qsa_kv_cache *cache,
                                int32_t window, float scale, void *out, void *ws, size_t ws_bytes, void *stream);
 
+/* ---- A batch from its requests' lengths -----------------------------------
+ * The arrays that the calls of this library take for a batch, and the pages that
+ * its new tokens need, made on the device, so that a captured step goes on from
+ * its own results.  Request b has ctx_len[b] tokens in the cache, in pages
+ * block_table[b, 0 .. ceil(ctx_len[b] / page_tokens) - 1], and brings new_len[b]
+ * more.  Requests are served in order until one does not fit: its rows past
+ * `rows`, or its pages past those left in the list; neither it nor any behind it
+ * gets rows or pages then (state tells; this is no error).  A served request's
+ * pages come off the end of the list, free_pages[free_count - 1] first, and go
+ * into its row of the block table in order; the list itself is not written.
+ *   seq_start [n_reqs + 1], pos_start [n_reqs]: as the calls take them;
+ *   total_len [n_reqs]: ctx_len, and new_len of a served request (NULL: not wanted;
+ *     may be ctx_len itself);
+ *   row_req, row_token, row_visible, slot [rows] (each NULL if not wanted): a row's
+ *     request, its token's position t, (t + 1) / 4 (its visible compressed
+ *     positions), its place page * page_tokens + t % page_tokens in the cache;
+ *     rows behind the last request: the last row's request (0
+     if there is none), so that padding names a request with tokens, 0, 0 and -1;
+ *   state [3]: rows in use, free pages left, number of the first request that did
+ *     not fit (n_reqs: none).  free_count may be state + 1.
+ * No other two arrays may overlap.  A request with a negative length, or more
+ * tokens than its row of the block table holds, gets nothing, holds up nobody, and
+ * is reported by qsa_get_device_status(), as is a free_count outside 0 ..
+ * free_capacity (taken as the nearer of the two), and a page of the table that is
+ * negative or whose places pass 2^31 - 1 (slot -1).  page_tokens a power of two in
+ * [8, 256], max_pages * page_tokens below 2^31 - 1, n_reqs <= 65,535
+ * (QSA_ERR_UNSUPPORTED otherwise). */
+typedef struct {
+    int32_t *seq_start, *pos_start, *total_len;
+    int32_t *row_req, *row_token, *row_visible, *slot;
+    int32_t *state;
+} qsa_batch;
+qsa_status qsa_batch_tables(const int32_t *new_len, const int32_t *ctx_len, int32_t n_reqs, int32_t rows,
+                            int32_t page_tokens, int32_t *block_table, int32_t max_pages, const int32_t *free_pages,
+                            int32_t free_capacity, const int32_t *free_count, const qsa_batch *batch, void *stream);
+
+/* ---- Rotary positions of queries and keys ---------------------------------
+ * What goes into the cache and the scorers is rotated first.  With f_j the angle
+ * per position of pair j (j < rope_dim / 2), the pair (a, b) of a token at position
+ * p becomes (a cos - b sin, b cos + a sin) of p * f_j, both times the amplitude.
+ *
+ * qsa_rotary_table: table[p * rope_dim + j] = amplitude * cos(p f_j), table[p *
+ * rope_dim + rope_dim / 2 + j] the same of the sine, for p < n_pos, in FP64 and
+ * stored as FP32.  f_j = theta^(-2j / rope_dim), and with `scaling` (NULL: none)
+ *   QSA_ROPE_LINEAR  f_j / factor;
+ *   QSA_ROPE_BASE    theta * factor^(rope_dim / (rope_dim - 2)) in place of theta;
+ *   QSA_ROPE_PARTS   f_j * (g + (1 - g) / factor): pairs that turn `fast` times or
+ *                    more over the `original` positions keep their speed, those
+ *                    that turn `slow` times or less are slowed down, g = (original
+ *                    f_j / 2 pi - slow) / (fast - slow) within [0, 1] in between.
+ * rope_dim a multiple of 16 in [16, 256]; theta, factor, original and amplitude
+ * positive and finite, 0 <= slow < fast, finite.  table: 16-byte aligned, n_pos * rope_dim floats. */
+#define QSA_ROPE_LINEAR 1
+#define QSA_ROPE_BASE 2
+#define QSA_ROPE_PARTS 3
+typedef struct {
+    int32_t kind;
+    double factor, original, fast, slow, amplitude;   /* original, fast, slow: QSA_ROPE_PARTS */
+} qsa_rope_scaling;
+qsa_status qsa_rotary_table(float *table, int32_t n_pos, int32_t rope_dim, double theta,
+                            const qsa_rope_scaling *scaling, void *stream);
+
+/* qsa_rotary: rotates dims first .. first + rope_dim - 1 of every head of q and k
+ * and copies the others.  layout QSA_ROPE_HALVES pairs (j, j + rope_dim / 2) of
+ * them, QSA_ROPE_NEIGHBOURS (2 j, 2 j + 1).  A batch is described as for
+ * qsa_index_key_produce; rows of no request are neither read nor written.  q, k,
+ * out_q, out_k: FP16, row r at q + r * q_stride elements, heads * head_dim
+ * contiguous values, 16-byte aligned, strides multiples of 8.  out_q may be q (with
+ * the same stride: in place), out_k may be k; beyond that outputs and inputs must
+ * not overlap.  k_heads may be 0 (k, out_k NULL).  Results are rounded once, past
+ * FP16's range to infinity.  head_dim a multiple of 16 in [16, 512], first a
+ * multiple of 8 with first + rope_dim <= head_dim, 1 <= q_heads, q_heads + k_heads
+ * <= 4096 (QSA_ERR_UNSUPPORTED otherwise).  A request that is out of range, or
+ * whose positions reach past the table, is skipped and reported by
+ * qsa_get_device_status(). */
+#define QSA_ROPE_HALVES 0
+#define QSA_ROPE_NEIGHBOURS 1
+qsa_status qsa_rotary(const void *q, int64_t q_stride, int32_t q_heads, void *out_q, int64_t out_q_stride,
+                      const void *k, int64_t k_stride, int32_t k_heads, void *out_k, int64_t out_k_stride,
+                      int32_t rows, int32_t head_dim, int32_t first, int32_t rope_dim, int32_t layout, int32_t n_reqs,
+                      const int32_t *seq_start, const int32_t *pos_start, const float *table, int32_t n_pos,
+                      void *stream);
+
+/* ---- Attention over selected blocks ---------------------------------------
+ * What qsa_block_select chooses blocks for: the row at position p of request b
+ * attends, for the query heads of KV head g, the tokens t <= p whose block t / 128
+ * is one of sel[r, g, 0 .. k) or of the row's last `recent` blocks (p / 128 -
+ * recent < t / 128), whichever pages hold them:
+ *   out[r, h, :] = sum_t softmax_t(scale * q[r, h, :] . k_t) * v_t
+ * sel: int32 [rows, hkv, k], -1 for none, in any order; a block that is named twice
+ * counts once.  A row that attends nothing gets zeros.  A block below -1 or past
+ * p / 128 is ignored and reported by qsa_get_device_status().  q, out, scale, the
+ * batch, the cache and the workspace are as for qsa_chunk_attention, cache slots
+ * that no row attends may hold anything.  0 <= k <= QSA_MAX_K, 0 <= recent <=
+ * QSA_MAX_K, hq / hkv <= 128, max_pages * page_tokens <= 2^25
+ * (QSA_ERR_UNSUPPORTED otherwise).  ws: qsa_block_attention_workspace_bytes(...)
+ * bytes, with row_capacity = max_pages * page_tokens of the cache. */
+size_t qsa_block_attention_workspace_bytes(int32_t rows, int32_t hq, int32_t hkv, int32_t head_dim, int32_t k,
+                                           int32_t recent, int32_t row_capacity);
+qsa_status qsa_block_attention(const void *q, int64_t q_stride, int32_t rows, int32_t hq, int32_t n_reqs,
+                               const int32_t *seq_start, const int32_t *pos_start, const qsa_kv_cache *cache,
+                               const int32_t *sel, int32_t k, int32_t recent, float scale, void *out, void *ws,
+                               size_t ws_bytes, void *stream);
+
 /* Static, NUL-terminated description of a status code. */
 const char *qsa_status_string(qsa_status status);
 
