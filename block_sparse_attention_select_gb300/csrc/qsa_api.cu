@@ -902,7 +902,17 @@ qsa_status make_tmap_kv(CUtensorMap *tm, const qsa_kv_cache *c, const void *base
     return r == CUDA_SUCCESS ? QSA_OK : QSA_ERR_INVALID_ARG;
 }
 
-// Checks shared by the three calls; `any` is false when there is nothing to do.
+// The maps of the attention kernels: few, the one for few rows.
+qsa_status make_tmaps(CUtensorMap *tk, CUtensorMap *tv, const qsa_kv_cache *c, bool few)
+{
+    const bool q8 = c->dtype == QSA_KV_E4M3;
+    ChunkBox box_k = {128, chunk_rows_box(c->page_tokens), 1}, box_v = box_k;
+    if (!few) chunk_boxes(c->head_dim, c->page_tokens, q8, &box_k, &box_v);
+    const qsa_status st = make_tmap_kv(tk, c, c->k, box_k, few || !q8);
+    return st != QSA_OK ? st : make_tmap_kv(tv, c, c->v, box_v, few || !q8);
+}
+
+// Checks shared by the calls; `any` is false when there is nothing to do.
 qsa_status check_batch(int32_t rows, int32_t n_reqs, const int32_t *seq_start, const int32_t *pos_start,
                        const qsa_kv_cache *cache, bool *any)
 {
@@ -1055,20 +1065,11 @@ qsa_status qsa_chunk_attention(const void *q, int64_t q_stride, int32_t rows, in
     ChunkParams p = chunk_params(q, q_stride, hq, kv_params(cache, rows, n_reqs, seq_start, pos_start, d), scale, out, ws);
     p.window = window;
     CUtensorMap tk, tv;
-    if (few_rows(rows, p.group, n_reqs)) {
-        p.ws_rows = chunk_rows_part_rows(rows, p.group);
-        const ChunkBox box = {128, chunk_rows_box(cache->page_tokens), 1};
-        if ((st = make_tmap_kv(&tk, cache, cache->k, box, true)) != QSA_OK) return st;
-        if ((st = make_tmap_kv(&tv, cache, cache->v, box, true)) != QSA_OK) return st;
-        st = launch_rc(launch_chunk_rows(p, &tk, &tv, d->sms, g_overlap, stream));
-    } else {
-        p.ws_rows = chunk_part_rows(rows, p.group);
-        ChunkBox box_k, box_v;
-        chunk_boxes(cache->head_dim, cache->page_tokens, p.kv.e4m3, &box_k, &box_v);
-        if ((st = make_tmap_kv(&tk, cache, cache->k, box_k, !p.kv.e4m3)) != QSA_OK) return st;
-        if ((st = make_tmap_kv(&tv, cache, cache->v, box_v, !p.kv.e4m3)) != QSA_OK) return st;
-        st = launch_rc(launch_chunk(p, &tk, &tv, d->sms, g_overlap, stream));
-    }
+    const bool few = few_rows(rows, p.group, n_reqs);
+    if ((st = make_tmaps(&tk, &tv, cache, few)) != QSA_OK) return st;
+    p.ws_rows = few ? chunk_rows_part_rows(rows, p.group) : chunk_part_rows(rows, p.group);
+    st = launch_rc(few ? launch_chunk_rows(p, &tk, &tv, d->sms, g_overlap, stream)
+                       : launch_chunk(p, &tk, &tv, d->sms, g_overlap, stream));
     if (st == QSA_OK) ++g_launches;                      // the join kernel
     return st;
 }
@@ -1222,7 +1223,9 @@ qsa_status qsa_rotary(const void *q, int64_t q_stride, int32_t q_heads, void *ou
 size_t qsa_block_attention_workspace_bytes(int32_t rows, int32_t hq, int32_t hkv, int32_t head_dim, int32_t k,
                                            int32_t recent, int32_t row_capacity)
 {
-    return 256;
+    if (rows <= 0 || hq <= 0 || hkv <= 0 || head_dim <= 0 || k < 0 || recent < 0 || row_capacity <= 0) return 256;
+    return blocks_workspace_bytes(rows, std::max(1, std::min(128, hq / hkv)), hkv, head_dim, std::min(k, QSA_MAX_K),
+                                  std::min(recent, QSA_MAX_K), row_capacity);
 }
 
 qsa_status qsa_block_attention(const void *q, int64_t q_stride, int32_t rows, int32_t hq, int32_t n_reqs,
@@ -1255,7 +1258,13 @@ qsa_status qsa_block_attention(const void *q, int64_t q_stride, int32_t rows, in
     p.sel = sel;
     p.k = k;
     p.recent = recent;
-    return launch_rc(launch_blocks(p, d->sms, g_overlap, stream));
+    // (units of whole tokens, so no more than 16 query heads to a KV head)
+    const bool few = p.c.group <= 16 && few_rows(rows, p.c.group, n_reqs);
+    CUtensorMap tk, tv;
+    if ((st = make_tmaps(&tk, &tv, cache, few)) != QSA_OK) return st;
+    st = launch_rc(launch_blocks(p, few, &tk, &tv, d->sms, g_overlap, stream));
+    if (st == QSA_OK) g_launches += 2;                   // the attention's and the join kernel
+    return st;
 }
 
 }  // extern "C"

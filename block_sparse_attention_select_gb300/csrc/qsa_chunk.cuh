@@ -1,5 +1,7 @@
-// Dense attention over the paged cache: what its two kernels share, the line of
-// work and its segments, and the kernel that joins partial results.
+// Attention over the paged cache: what its two kernels share, the line of work
+// and its segments, and the kernel that joins partial results.  The kernels serve
+// dense attention (units attend a run of tokens) and attention over selected
+// blocks (G::BLOCKS: units attend a list of blocks, made by qsa_blocks.cu).
 #pragma once
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -15,6 +17,18 @@ namespace {
 // (tokens of a tile), UNIT_COST (tiles' worth of time that a unit costs besides
 // its tiles), THREADS and WARPS of a CTA, WORKERS (at most; a worker is a CTA or
 // a pair of them).
+
+// Lists of blocks.  A unit is whole tokens, p.unit_tokens of them, with all their
+// query heads.  Its list holds the blocks that some row attends, in ascending
+// order: the block's number, and how many of its tokens some row attends (all but
+// in the last three entries at most, for a unit's tokens lie in three blocks at
+// most).  A unit that attends nothing has one entry, NO_BLOCK.  A row of bits per
+// token says which entries it attends.  Where two requests claim a row, lists may
+// be mixed up or hold anything: the kernels rely on no order, and blocks that the
+// block table has no place for are not read.
+constexpr int32_t NO_BLOCK = -1;
+__device__ __forceinline__ int32_t entry_block(int32_t e) { return e & 0xffffff; }
+__device__ __forceinline__ int32_t entry_seen(int32_t e) { return e < 0 ? 0 : (e >> 24) + 1; }
 
 // A run of tiles of one unit, a worker's next piece of work.
 struct alignas(16) Seg {
@@ -66,6 +80,7 @@ __device__ __forceinline__ int32_t by_group(const ChunkParams &p, int32_t v)
 template <typename G>
 __device__ __forceinline__ int32_t units_of(const ChunkParams &p, const Seq &s)
 {
+    if constexpr (G::BLOCKS) return (s.n + p.unit_tokens - 1) / p.unit_tokens;
     return (s.n * p.group + G::ROWS - 1) / G::ROWS;
 }
 
@@ -73,6 +88,14 @@ template <typename G>
 __device__ __forceinline__ Unit unit_of(const ChunkParams &p, const Seq &s, int32_t m)
 {
     Unit u;
+    if constexpr (G::BLOCKS) {
+        const int32_t t0 = m * p.unit_tokens, n = min(s.n - t0, p.unit_tokens);
+        u.v0 = t0 * p.group;
+        u.rows = n * p.group;
+        u.hi_tok = s.p0 + t0 + n - 1;
+        u.lo_tok = u.lo = u.hi = 0;
+        return u;
+    }
     u.v0 = m * G::ROWS;
     const int32_t end = min(s.n * p.group, u.v0 + G::ROWS);
     u.rows = end - u.v0;
@@ -82,6 +105,27 @@ __device__ __forceinline__ Unit unit_of(const ChunkParams &p, const Seq &s, int3
     u.lo = u.lo_tok / G::TILE;
     u.hi = u.hi_tok / G::TILE + 1;
     return u;
+}
+
+// Tiles of unit m (u) for KV head g.
+template <typename G>
+__device__ __forceinline__ int32_t tiles_of(const ChunkParams &p, const Seq &s, const Unit &u, int32_t m, int32_t g)
+{
+    if constexpr (G::BLOCKS)
+        // (within bounds even where two requests claim the row and neither left a count)
+        return max(1, min(p.max_entries, __ldg(p.counts + (static_cast<int64_t>(g) * p.kv.rows + s.s0 + m * p.unit_tokens)))) *
+               (BLOCK_TOKENS / G::TILE);
+    return u.hi - u.lo;
+}
+
+// The unit's list, and the row of bits of the request's token number tok.
+__device__ __forceinline__ const int32_t *list_of(const ChunkParams &p, const Seg &w)
+{
+    return p.lists + (static_cast<int64_t>(w.g) * p.kv.rows + w.s0 + by_group(p, w.v0)) * p.list_stride;
+}
+__device__ __forceinline__ const uint32_t *bits_of(const ChunkParams &p, const Seg &w, int32_t tok)
+{
+    return p.bits + (static_cast<int64_t>(w.g) * p.kv.rows + w.s0 + tok) * p.words;
 }
 
 template <typename T>
@@ -189,9 +233,13 @@ __device__ __forceinline__ void find_work(const ChunkParams &p, Share &c, FindSc
                 m = 0;
             }
             const Unit un = unit_of<G>(p, sb, m);
-            cost += G::UNIT_COST + un.hi - un.lo;
+            if constexpr (G::BLOCKS) {
+                for (int32_t g = 0; g < p.kv.hkv; ++g) cost += G::UNIT_COST + tiles_of<G>(p, sb, un, m, g);
+            } else {
+                cost += G::UNIT_COST + un.hi - un.lo;
+            }
         }
-        cost *= p.kv.hkv;
+        if (!G::BLOCKS) cost *= p.kv.hkv;
     }
     int64_t at = block_scan<G>(cost, s.costs, warp, lane, &total);
     // MIN_SHARE each at least: a smaller share costs more in the join than it saves here
@@ -217,6 +265,20 @@ __device__ __forceinline__ void find_work(const ChunkParams &p, Share &c, FindSc
                 m0 = 0;
             }
             const Unit un = unit_of<G>(p, s0, m0);
+            if constexpr (G::BLOCKS) {
+                int32_t g = 0;
+                for (; g < p.kv.hkv; ++g) {
+                    const int32_t len = G::UNIT_COST + tiles_of<G>(p, s0, un, m0, g);
+                    if (w0 < at + len) break;
+                    at += len;
+                }
+                if (g == p.kv.hkv) continue;
+                c.b = b0;
+                c.m = m0;
+                c.g = g;
+                c.off = static_cast<int32_t>(w0 - at);
+                break;
+            }
             const int32_t len = G::UNIT_COST + un.hi - un.lo;
             if (w0 < at + static_cast<int64_t>(len) * p.kv.hkv) {
                 c.b = b0;
@@ -264,7 +326,8 @@ struct Walk {
             m = 0;
             load(p);
         }
-        const Unit u = unit_of<G>(p, s, m);
+        Unit u = unit_of<G>(p, s, m);
+        if constexpr (G::BLOCKS) u.hi = tiles_of<G>(p, s, u, m, g);
         // a unit's place in the line: G::UNIT_COST, then its tiles
         const int32_t len = G::UNIT_COST + u.hi - u.lo;
         const int32_t end = static_cast<int32_t>(min(static_cast<int64_t>(len), off + left));

@@ -200,6 +200,11 @@ struct ChunkParams {
     uint8_t *ws;
     int32_t ws_rows;            // rows of a partial output in the workspace
     uint64_t wait_limit_ns;
+    // attention over selected blocks: see qsa_chunk.cuh
+    const int32_t *counts;      // [hkv][rows], at a unit's first row: entries of its list
+    const int32_t *lists;       // [hkv][rows][list_stride], a unit's from its first row on
+    const uint32_t *bits;       // [hkv][rows][words]
+    int32_t list_stride, words, unit_tokens, max_entries;
 };
 
 // Attention over selected blocks: see qsa_blocks.cu.  c.window is 0.
@@ -301,7 +306,9 @@ int32_t chunk_rows_box(int32_t page_tokens);
 
 constexpr int32_t BLOCK_TOKENS = 128;        // tokens of a selected block
 constexpr int64_t BLOCKS_MAX_TOKENS = int64_t{1} << 25;   // tokens of a request at most
-int launch_blocks(const BlocksParams &p, int sms, bool overlap, void *stream);
+int launch_blocks(const BlocksParams &p, bool few_rows, const void *tk, const void *tv, int sms, bool overlap, void *stream);
+size_t blocks_workspace_bytes(int32_t rows, int32_t group, int32_t hkv, int32_t head_dim, int32_t k, int32_t recent,
+                              int32_t row_capacity);
 int launch_rotary_table(float *table, int32_t n_pos, int32_t rope_dim, const RotaryAngles &angles, int sms, void *stream);
 int launch_rotary(const RotaryParams &p, bool neighbours, int sms, void *stream);
 int launch_tables(const TablesParams &p, void *stream);
