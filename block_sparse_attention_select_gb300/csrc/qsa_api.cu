@@ -1262,8 +1262,9 @@ qsa_status qsa_block_attention(const void *q, int64_t q_stride, int32_t rows, in
     const bool few = p.c.group <= 16 && few_rows(rows, p.c.group, n_reqs);
     CUtensorMap tk, tv;
     if ((st = make_tmaps(&tk, &tv, cache, few)) != QSA_OK) return st;
-    st = launch_rc(launch_blocks(p, few, &tk, &tv, d->sms, g_overlap, stream));
-    if (st == QSA_OK) g_launches += 2;                   // the attention's and the join kernel
+    int launches = 0;
+    st = launch_rc(launch_blocks(p, few, &tk, &tv, d->sms, g_overlap, stream, &launches));
+    if (st == QSA_OK) g_launches = launches;
     return st;
 }
 

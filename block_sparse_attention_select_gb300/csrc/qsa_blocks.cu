@@ -169,11 +169,27 @@ size_t blocks_workspace_bytes(int32_t rows, int32_t group, int32_t hkv, int32_t 
     return ListSizes(rows, group, hkv, head_dim, k, recent, row_capacity, pair_tokens(group)).bytes;
 }
 
-int launch_blocks(const BlocksParams &in, bool few_rows, const void *tk, const void *tv, int sms, bool overlap, void *stream)
+int launch_blocks(const BlocksParams &in, bool few_rows, const void *tk, const void *tv, int sms, bool overlap, void *stream,
+                  int *launches)
 {
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     ChunkParams c = in.c;
     const KvParams &kv = c.kv;
+    // Few rows whose units would be single tokens: no lists, no join.
+    if (few_rows && in.k + in.recent <= DIRECT_BLOCKS && (c.group > CR_ROWS / 2 || kv.rows <= kv.n_reqs)) {
+        const int32_t units = kv.rows * kv.hkv;
+        c.sel = in.sel;
+        c.sel_k = in.k;
+        c.recent = in.recent;
+        c.split = 1;
+        while (c.split < DIRECT_SPLIT && units * c.split * 2 <= sms) c.split *= 2;
+        const int grid = c.split > 1 ? units * c.split : std::min(units, sms);
+        *launches = 1;
+        if (kv.head_dim == 128)
+            return kv.e4m3 ? launch_direct<128, true>(c, tk, tv, grid, st) : launch_direct<128, false>(c, tk, tv, grid, st);
+        return kv.e4m3 ? launch_direct<256, true>(c, tk, tv, grid, st) : launch_direct<256, false>(c, tk, tv, grid, st);
+    }
+    *launches = 3;
     c.unit_tokens = few_rows ? CR_ROWS / c.group : pair_tokens(c.group);
     const int32_t capacity = kv.max_pages * kv.page_tokens;
     const ListSizes place(kv.rows, c.group, kv.hkv, kv.head_dim, in.k, in.recent, capacity, pair_tokens(c.group));

@@ -151,11 +151,14 @@ struct Ctrl {
     SegRing segs;
     uint64_t full[MAX_SLOTS], empty[MAX_SLOTS], raw_full[RAWS], raw_empty[RAWS], bnd[8];
     uint64_t s_full[2], s_free[2], p_full[2][2], o_done[2], m_out[2][4], q_full[2], q_free[2], drain[2];
-    uint64_t o_last, o_free, f_full[2], f_free[2];
-    alignas(8) float mrow[2][CH_HALF];       // [tile parity][row]: maximum in use at the group's last tile; sums at a segment's end
+    uint64_t o_last, o_free, f_full, f_free, l_out[4];
+    alignas(8) float mrow[2][CH_HALF];       // [tile parity][row]: maximum in use at the group's last tile; E4M3: sums at a segment's end
     union {
         uint32_t scale[2][CH_TILE];          // [slot parity][token]: FP16 scale, twice (E4M3)
-        float factor[2][CH_HALF];            // [segment parity][row]: what the output is multiplied by (FP16 cache)
+        struct {                             // (FP16 cache)
+            float factor[CH_HALF];           // [row]: what the unit's output is multiplied by
+            float lrow[CH_HALF];             // [row]: the sum of the group that does not have the segment's last tile
+        };
     };
     Share share;
     uint32_t tmem;
@@ -275,11 +278,6 @@ __device__ __forceinline__ void cluster_arrive_expect_tx(uint32_t bar, uint32_t 
 __device__ __forceinline__ void mbar_expect_tx_at(uint32_t bar, uint32_t bytes)
 {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
-}
-
-__device__ __forceinline__ void cluster_sync()
-{
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // 3-D tiled load (from x = 0) into this CTA, completing on a barrier of either CTA
@@ -474,10 +472,9 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
         for (int i = 0; i < 2; ++i) mbar_init(&c.drain[i], 1);
         mbar_init(&c.o_last, 1);
         mbar_init(&c.o_free, 2 * CH_HELPERS);                 // in the first CTA, for both
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&c.f_full[i], 4);
-            mbar_init(&c.f_free[i], CH_HELPERS);
-        }
+        mbar_init(&c.f_full, 4);
+        mbar_init(&c.f_free, CH_HELPERS);
+        for (int i = 0; i < 4; ++i) mbar_init(&c.l_out[i], 1);
         c.abort = 0;
         fence_barrier_init();
     }
@@ -767,11 +764,14 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
             if (Sh::HELP_OUT && before.n > 0 && ok) {
                 const uint32_t u = seg - 1;                    // its number
                 const int lq = warp & 3, ur = rank * CH_HALF + ht;
-                ok = warp_wait(&c.f_full[u & 1u], (u >> 1) & 1u, abort, span(before)) &&
-                     warp_wait(&c.o_last, u & 1u, abort, span(before));
+                ok = warp_wait(&c.f_full, u & 1u, abort, span(before));
+                if (!ok) return;
+                const float f = c.factor[ht];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&c.f_free);
+                ok = warp_wait(&c.o_last, u & 1u, abort, span(before));
                 if (!ok) return;
                 tc_fence_after();
-                const float f = c.factor[u & 1u][ht];
                 if (rank * CH_HALF + lq * 32 < before.rows) {
                     const bool in = ur < before.rows, whole = before.place < 0;
                     const bool out_32 = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;      // (16 bytes are promised)
@@ -789,10 +789,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                         if (k == D / 16 - 1) {                 // O is read
                             tc_fence_before();
                             __syncwarp();
-                            if (lane == 0) {
-                                cluster_arrive(of_first(&c.o_free));
-                                mbar_arrive(&c.f_free[u & 1u]);
-                            }
+                            if (lane == 0) cluster_arrive(of_first(&c.o_free));
                         }
                         if (!in) continue;
                         if (whole) {
@@ -807,7 +804,6 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                     }
                 } else if (lane == 0) {
                     cluster_arrive(of_first(&c.o_free));
-                    mbar_arrive(&c.f_free[u & 1u]);
                 }
                 __syncwarp();
             }
@@ -1013,6 +1009,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
         // warp's own P of tile i + 1 or i + 2, which it has still to give.
         auto o_done = [&](uint32_t i) { return warp_wait(&c.o_done[i & 1u], (i >> 1) & 1u, abort, lim); };
         bool ok = true;                                        // false: keep to the barriers, do nothing
+        bool zeros = false;                                    // the group's P holds zeros
         while (next_segment()) {
             const int32_t n = w.n;
             // rows past the unit's last behave like it (their queries are zeros)
@@ -1025,14 +1022,23 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
             const int32_t w_hi = __shfl_sync(0xffffffffu, pos, 0), w_lo = __shfl_sync(0xffffffffu, first, 31);
             const int32_t *list = G::BLOCKS ? list_of(p, w) + w.j0 : nullptr;
             const uint32_t *bits = G::BLOCKS ? bits_of(p, w, tok) : nullptr;
+            // a list's entry and bits of the next tile, a tile ahead
+            const int32_t jf = (grp - it) & 1, jl = min(jf, n - 1);
+            int32_t ent_next = G::BLOCKS ? __ldg(list + jl) : 0;
+            uint32_t word_next = G::BLOCKS ? __ldg(bits + ((w.j0 + jl) >> 5)) : 0u;
             float cm = 0.0f, l = 0.0f;                         // the sum, and the constant of its exponents
-            for (int32_t j = (grp - it) & 1; ok && j < n; j += 2) {
+            for (int32_t j = jf; ok && j < n; j += 2) {
                 const uint32_t i = it + j;                     // tile i & 1 == grp
-                const int32_t base = (G::BLOCKS ? entry_block(__ldg(list + j)) : w.j0 + j) * CH_TILE;
-                // whether the row attends the tile, and some row of the warp does
-                const bool att = !G::BLOCKS || ((__ldg(bits + ((w.j0 + j) >> 5)) >> ((w.j0 + j) & 31)) & 1u);
-                const bool some = !G::BLOCKS || __any_sync(0xffffffffu, att);
                 ok = warp_wait(&c.s_full[grp], (i >> 1) & 1u, abort, lim);
+                const int32_t base = (G::BLOCKS ? entry_block(ent_next) : w.j0 + j) * CH_TILE;
+                // whether the row attends the tile, and some row of the warp does
+                const bool att = !G::BLOCKS || ((word_next >> ((w.j0 + j) & 31)) & 1u);
+                const bool some = !G::BLOCKS || __any_sync(0xffffffffu, att);
+                if constexpr (G::BLOCKS) {
+                    const int32_t ahead = min(j + 2, n - 1);
+                    ent_next = __ldg(list + ahead);
+                    word_next = __ldg(bits + ((w.j0 + ahead) >> 5));
+                }
                 const bool load = ok && live && some;
                 uint32_t s[4][32];
                 float a[4];
@@ -1106,14 +1112,19 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                     if (ok && lane == 0) cluster_arrive(p_full0 + half * 8u);
                 };
                 if (ok && live && !some) {
-                    uint32_t o[16];
+                    // P beside S may hold zeros already
+                    if (!Sh::OWN_P || !zeros) {
+                        uint32_t o[16];
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) o[e] = 0u;
+                        for (int e = 0; e < 16; ++e) o[e] = 0u;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) tmem_st_x16(tp + k * 16u, o);
+                        for (int k = 0; k < 4; ++k) tmem_st_x16(tp + k * 16u, o);
+                    }
+                    zeros = true;
                     give(0);
                 }
                 if (ok && live && some) {
+                    zeros = false;
                     const float cn = level(mi);
                     if (cn != cm) l *= exp2_approx(fminf(cn - cm, 0.0f));      // (0 at the first)
                     cm = cn;
@@ -1142,8 +1153,36 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                 give(1);
             }
             it += n;
+            if constexpr (Sh::HELP_OUT) {
+                // The segment's sums.  The group that has the last tile adds up both and
+                // hands the helpers what the output is multiplied by; the other goes on
+                // at once.  (That one waits for the last tile's maximum, which its next
+                // tile would wait for, so the sum before has been read.  With all eight
+                // warps meeting at named barriers a unit's end took 3,400 clocks.)
+                const bool ends = ((it - 1) & 1u) == static_cast<uint32_t>(grp);
+                if (!ends && ok) ok = warp_wait(&c.m_out[grp ^ 1][lq], ((it - 1) >> 1) & 1u, abort, lim);
+                const float mlast = c.mrow[(it - 1) & 1u][row], clast = level(mlast);
+                l = l > 0.0f ? l * exp2_approx(fminf(clast - cm, 0.0f)) : 0.0f;
+                if (!ends) {
+                    c.lrow[row] = l;
+                    __syncwarp();
+                    if (ok && lane == 0) mbar_arrive(&c.l_out[lq]);
+                } else {
+                    if (ok) ok = warp_wait(&c.l_out[lq], seg & 1u, abort, lim);
+                    l += c.lrow[row];
+                    if (row < mine && w.place >= 0)
+                        *reinterpret_cast<float2 *>(p.ws + WS_ML + (static_cast<int64_t>(w.place) * CH_ROWS + rank * CH_HALF + row) * 8) =
+                            make_float2(mlast == -INFINITY ? -INFINITY : -clast, l);
+                    if (ok && seg > 0) ok = warp_wait(&c.f_free, (seg - 1) & 1u, abort, lim);
+                    if (ok) c.factor[row] = w.place >= 0 ? 1.0f : l > 0.0f ? 1.0f / l : 0.0f;
+                    __syncwarp();
+                    if (ok && lane == 0) mbar_arrive(&c.f_full);
+                }
+                ++seg;
+                continue;
+            }
             // the segment's sums: its rows' output, or its part of it
-            if (!Sh::HELP_OUT && ok) ok = (it < 2 || o_done(it - 2)) && o_done(it - 1);
+            if (ok) ok = (it < 2 || o_done(it - 2)) && o_done(it - 1);
             named_barrier(BAR_PAIR + lq, 64);
             // both groups' sums at the last tile's maximum, exchanged in place of the maxima
             const float mlast = c.mrow[(it - 1) & 1u][row];
@@ -1157,16 +1196,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                 *reinterpret_cast<float2 *>(p.ws + WS_ML + (static_cast<int64_t>(w.place) * CH_ROWS + rank * CH_HALF + row) * 8) =
                     make_float2(mlast == -INFINITY ? -INFINITY : -clast, l);
             const float inv = w.place >= 0 ? 1.0f : l > 0.0f ? 1.0f / l : 0.0f;
-            if constexpr (Sh::HELP_OUT) {
-                // handed to the helpers
-                if (grp == 0 && ok) {
-                    if (seg > 1) ok = warp_wait(&c.f_free[seg & 1u], ((seg >> 1) - 1) & 1u, abort, lim);
-                    c.factor[seg & 1u][row] = inv;
-                    __syncwarp();
-                    if (ok && lane == 0) mbar_arrive(&c.f_full[seg & 1u]);
-                }
-                ++seg;
-            } else if (ok && live) {
+            if (ok && live) {
                 tc_fence_after();
                 const uint32_t to = tmem + TM_O + lane_base + grp * OC;
                 const bool in = row < mine, whole = w.place < 0;

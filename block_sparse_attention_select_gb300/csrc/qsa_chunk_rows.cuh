@@ -54,12 +54,20 @@ constexpr int BAR_COMP = 1;
 struct RowsGeometry {
     static constexpr bool BLOCKS = false;
     static constexpr bool RAW_MAX = true;    // the parts' maxima: scores before the scale
+    static constexpr bool DIRECT = false;
     static constexpr int ROWS = CR_ROWS, TILE = CR_TILE, UNIT_COST = 4, MIN_SHARE = 3, THREADS = CR_THREADS, WARPS = CR_WARPS,
                          WORKERS = CHUNK_MAX_CTAS;
 };
 struct BlockRowsGeometry : RowsGeometry {
     static constexpr bool BLOCKS = true;
 };
+// Blocks taken straight from the selections: a unit is one token of a row array's
+// row and a KV head, on a cluster of p.split CTAs that share its tiles.
+struct DirectRowsGeometry : BlockRowsGeometry {
+    static constexpr bool DIRECT = true;
+};
+constexpr int DIRECT_BLOCKS = 32;            // blocks of a unit at most, a lane each
+constexpr int DIRECT_SPLIT = 8;              // CTAs of a cluster at most
 
 // A unit's list of blocks, 32 entries in the lanes and the next 32 on their way;
 // a tile (two to a block) is asked for no more than 32 blocks ahead of advance().
@@ -74,6 +82,13 @@ struct ListWindow {
         base = w.j0 >> 1;
         cur = base + lane < n ? __ldg(list + base + lane) : NO_BLOCK;
         next = base + 32 + lane < n ? __ldg(list + base + 32 + lane) : NO_BLOCK;
+    }
+    __device__ __forceinline__ void start(int32_t entry)       // a lane's, of the whole list
+    {
+        n = 0;
+        base = 0;
+        cur = entry;
+        next = NO_BLOCK;
     }
     __device__ __forceinline__ void advance(int32_t tile, int lane)
     {
@@ -100,11 +115,15 @@ template <int D, bool Q8>
 struct RowShape {
     static constexpr int ES = Q8 ? 1 : 2;
     static constexpr uint32_t HALF = CR_TILE * D * ES, STAGE = 2 * HALF;   // K, then V
-    static constexpr uint32_t SUM = CR_ROWS * D * 4;                       // an eighth of the eight warps' outputs
+    static constexpr uint32_t SUM1 = CR_ROWS * D * 4;                      // an eighth of the eight warps' outputs
     // an even number of stages: a stage then belongs to one group of warps, which
     // waits for each of its phases (a parity wait must not skip one)
     static constexpr uint32_t QF = CR_ROWS * D * 2;                        // queries as A operands
-    static constexpr int FIT = (227 * 1024 - 8192 - SUM - QF) / STAGE, NS = (FIT < CR_MAX_STAGES ? FIT : CR_MAX_STAGES) & ~1;
+    static constexpr int FIT = (227 * 1024 - 8192 - SUM1 - QF) / STAGE, NS = (FIT < CR_MAX_STAGES ? FIT : CR_MAX_STAGES) & ~1;
+    // the warps' outputs are added up in 8 / SUMS steps, as few as there is room for
+    static constexpr uint32_t ROOM = (227 * 1024 - 8192 - QF - NS * STAGE) / SUM1;
+    static constexpr int SUMS = ROOM >= 8 ? 8 : ROOM >= 4 ? 4 : ROOM >= 2 ? 2 : 1;
+    static constexpr uint32_t SUM = SUMS * SUM1;
     static constexpr int CHUNKS = D * ES / 128;                            // 128-byte chunks of a vector
     static constexpr int PD = 16 / ES;                                     // dims of a 16-byte piece
 };
@@ -116,6 +135,8 @@ struct RowCtrl {
     float scale[CR_MAX_STAGES][2][CR_TILE];  // K and V scales of a stage's tokens (E4M3)
     float m[CR_COMP][CR_ROWS], l[CR_COMP][CR_ROWS];
     int32_t entry[CR_MAX_STAGES];            // list entry of a stage's tile
+    int32_t blocks[SEGS][DIRECT_BLOCKS];     // list of a segment of the ring (DIRECT)
+    float2 part[CR_ROWS];                    // the CTA's maxima and sums, for its cluster (DIRECT)
     int32_t abort;
 };
 
@@ -145,6 +166,83 @@ __device__ __forceinline__ uint32_t half2_mul(uint32_t a, uint32_t b)
 __device__ __forceinline__ uint32_t word(const uint4 &v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
 __device__ __forceinline__ uint4 lds128(const uint8_t *a) { return *reinterpret_cast<const uint4 *>(a); }
+
+// The scheduler warp of a DIRECT kernel: units in the order (row, KV head), one
+// after the other to the clusters in turn.  A lane holds one of the row's blocks.
+__device__ __forceinline__ void schedule_direct(const ChunkParams &p, RowCtrl &c, int lane)
+{
+    const int32_t split = p.split, rank = blockIdx.x % split, clusters = gridDim.x / split;
+    const int32_t units = p.kv.rows * p.kv.hkv;
+    int falls = -1;                          // whether starts fall somewhere (-1: not known)
+    uint32_t i = 0;
+    // place: the entry's place in the list
+    auto give = [&](const Seg &x, int32_t place, int32_t entry) {
+        const uint32_t k = i % SEGS;
+        if (i >= SEGS) mbar_wait_bounded(&c.segs.empty[k], (i / SEGS - 1) & 1u, SEG_WAIT_NS);
+        __syncwarp();
+        c.blocks[k][lane] = NO_BLOCK;
+        __syncwarp();
+        if (place >= 0) c.blocks[k][place] = entry;
+        if (lane == 0) c.segs.seg[k] = x;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&c.segs.full[k]);
+        ++i;
+    };
+    Seg x;
+    for (int32_t u = blockIdx.x / split; u < units; u += clusters) {
+        const int32_t row = u / p.kv.hkv;
+        Seq s;
+        const int32_t b = request_of_by_warp(p.kv, row, lane, &falls, &s);
+        if (b < 0) continue;
+        x.g = u - row * p.kv.hkv;
+        const int32_t tok = row - s.s0, pos = s.p0 + tok, own = pos / BLOCK_TOKENS;
+        int32_t block = NO_BLOCK;
+        if (lane < p.sel_k) {
+            block = __ldg(p.sel + static_cast<int64_t>(u) * p.sel_k + lane);
+            if (block < -1 || block > own) {
+                record_error(p.kv.status, ST_BAD_ROW);
+                block = NO_BLOCK;
+            }
+        } else if (lane < p.sel_k + p.recent) {
+            block = max(NO_BLOCK, own - (lane - p.sel_k));
+        }
+        // each block once, without gaps
+        const uint32_t same = __match_any_sync(0xffffffffu, block);
+        const bool kept = block >= 0 && __ffs(same) - 1 == lane;
+        const uint32_t all = __ballot_sync(0xffffffffu, kept);
+        const int32_t count = max(1, __popc(all));
+        // the CTA's share of the tiles: may be none
+        const int32_t tiles = count * (BLOCK_TOKENS / CR_TILE);
+        x.j0 = tiles * rank / split;
+        x.n = tiles * (rank + 1) / split - x.j0;
+        x.b = b;
+        x.s0 = s.s0;
+        x.p0 = s.p0;
+        x.v0 = tok * p.group;
+        x.rows = p.group;
+        x.lo_tok = 0;
+        x.hi_tok = pos;
+        x.place = -1;
+        give(x, kept ? __popc(all & ((1u << lane) - 1u)) : -1, block | min(pos - block * BLOCK_TOKENS, BLOCK_TOKENS - 1) << 24);
+    }
+    x.n = x.rows = 0;
+    give(x, -1, NO_BLOCK);
+}
+
+// next_segment of a DIRECT kernel, whose segments may be empty: the last one has no
+// rows.  *entry: the lane's list entry.
+__device__ __forceinline__ bool next_direct(RowCtrl &c, uint32_t *i, Seg *w, int32_t *entry, int lane)
+{
+    const uint32_t k = *i % SEGS;
+    bool got = mbar_wait_bounded(&c.segs.full[k], (*i / SEGS) & 1u, SEG_WAIT_NS);
+    got = __all_sync(0xffffffffu, got);
+    *w = c.segs.seg[k];
+    *entry = c.blocks[k][lane];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&c.segs.empty[k]);
+    ++*i;
+    return got && w->rows > 0;
+}
 
 template <int D, bool Q8, typename G>
 __global__ void __launch_bounds__(CR_THREADS, 1)
@@ -177,15 +275,30 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
     wait_prior_grid();
     // (the sums' place is free until a segment's end)
     static_assert(sizeof(FindScratch<G>) <= Sh::SUM, "scratch");
-    find_work<G>(p, c.share, *reinterpret_cast<FindScratch<G> *>(sum), blockIdx.x, gridDim.x, warp, lane);
+    if constexpr (G::DIRECT) {
+        if (blockIdx.x == 0) flag_bad_requests(p.kv);
+        __syncthreads();
+    } else {
+        find_work<G>(p, c.share, *reinterpret_cast<FindScratch<G> *>(sum), blockIdx.x, gridDim.x, warp, lane);
+    }
     uint32_t segs = 0;
     Seg w;
+    int32_t entry = NO_BLOCK;                                  // (DIRECT) the lane's entry of w's list
+    auto next = [&](Seg *x) -> bool {
+        if constexpr (G::DIRECT) return next_direct(c, &segs, x, &entry, lane);
+        else return next_segment(c.segs, &segs, x, lane);
+    };
+    auto start = [&](ListWindow &win) {
+        if constexpr (G::DIRECT) win.start(entry);
+        else win.start(p, w, lane);
+    };
 
     // registers after the split: 8 x 32 x 216 + 4 x 32 x 72 = 384 x 168
     if (warp >= CR_COMP) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (warp == CR_SCHED) {
-            schedule<G>(p, c.share, c.segs, blockIdx.x, true, lane);
+            if constexpr (G::DIRECT) schedule_direct(p, c, lane);
+            else schedule<G>(p, c.share, c.segs, blockIdx.x, true, lane);
         } else if (warp == CR_LOAD) {
             // ------------------------------------------------------ K, V loads
             const int32_t P = p.kv.page_tokens;
@@ -193,14 +306,14 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
             const int32_t down = CR_TILE >> sh, boxes = 2 * Sh::CHUNKS * down;
             uint32_t slot = 0, phase = 0, used = 0, last = 0;
             bool ok = true;
-            while (next_segment(c.segs, &segs, &w, lane)) {
+            while (next(&w)) {
                 if (!ok) continue;
                 const int32_t *bt = p.kv.block_table + static_cast<int64_t>(w.b) * p.kv.max_pages;
                 // a lane looks up the cache rows of tokens lane and lane + 32, two
                 // stages ahead
                 const int32_t nowhere = p.kv.num_pages << p.kv.page_shift;       // past the cache: reads zeros
                 ListWindow win;
-                if (G::BLOCKS) win.start(p, w, lane);
+                if (G::BLOCKS) start(win);
                 auto row_of = [&](int32_t j, int k) -> int32_t {
                     if constexpr (G::BLOCKS) {
                         const int32_t ent = win.entry(w.j0 + j), off = lane + 32 * k;
@@ -235,11 +348,12 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
                     const int32_t ent = G::BLOCKS ? win.entry(w.j0 + j) : 0;
                     if (lane == 0) {
                         if (G::BLOCKS) c.entry[slot] = ent;
-                        mbar_arrive_expect_tx(&c.full[slot], STAGE);
+                        if (!G::BLOCKS || tile_seen(ent, w.j0 + j) > 0) mbar_arrive_expect_tx(&c.full[slot], STAGE);
+                        else mbar_arrive(&c.full[slot]);           // nothing to load
                     }
                     __syncwarp();
                     uint8_t *dst = smem + slot * STAGE;
-                    for (int32_t i0 = 0; i0 < boxes; i0 += 32) {
+                    for (int32_t i0 = 0; i0 < boxes && (!G::BLOCKS || tile_seen(ent, w.j0 + j) > 0); i0 += 32) {
                         const int32_t i = i0 + lane;
                         const int32_t d = i & (down - 1), ch = (i / down) % Sh::CHUNKS;
                         const bool v = i >= boxes / 2;
@@ -278,11 +392,11 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
             const int which = warp - CR_SCALE;
             uint32_t slot = 0, phase = 0;
             bool ok = true;
-            while (next_segment(c.segs, &segs, &w, lane)) {
+            while (next(&w)) {
                 if (!ok) continue;
                 const int32_t *bt = p.kv.block_table + static_cast<int64_t>(w.b) * p.kv.max_pages;
                 ListWindow win;
-                if (G::BLOCKS) win.start(p, w, lane);
+                if (G::BLOCKS) start(win);
                 auto page_of = [&](int32_t j, int k) -> int32_t {
                     if constexpr (G::BLOCKS) {
                         const int32_t ent = win.entry(w.j0 + j), off = lane + 32 * k;
@@ -355,33 +469,50 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
         const float cs = p.scale * LOG2_E;
         uint32_t slot = 0, phase = 0, it = 0;
         bool ok = true;
-        while (next_segment(c.segs, &segs, &w, lane)) {
-            const uint32_t *bits[2];                               // which entries the rows' tokens attend
-            int32_t pos[2], first[2];
-            const uint8_t *qrow[2];                                // rows r and r + 8 of the unit
+        // The queries as A operands, in shared memory (in registers they spilled:
+        // 294 us on the 64-request E4M3 step).  Product k of piece i takes dims
+        // 8 PD (i / 2) + PD (2 q + i % 2) + 4 k .. + 3.  They are loaded while the
+        // segment before is added up.
+        uint2 xq[(KS + CR_COMP - 1) / CR_COMP][2];
+        auto load_q = [&](const Seg &x) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int row = r + 8 * e;
-                const int32_t v = w.v0 + min(row, w.rows - 1), tok = by_group(p, v), h = v - tok * p.group;
-                pos[e] = w.p0 + tok;
-                bits[e] = G::BLOCKS ? bits_of(p, w, tok) : nullptr;
-                first[e] = p.window > 0 ? max(0, pos[e] - p.window + 1) : 0;
-                qrow[e] = row >= w.rows ? nullptr : static_cast<const uint8_t *>(p.q) +
-                          ((static_cast<int64_t>(w.s0) + tok) * p.q_stride + (w.g * p.group + h) * D) * 2;
-            }
-            // The queries as A operands, in shared memory (in registers they
-            // spilled: 294 us on the 64-request E4M3 step).  Product k of
-            // piece i takes dims 8 PD (i / 2) + PD (2 q + i % 2) + 4 k .. + 3.
-            for (int k = warp; k < KS; k += CR_COMP) {
-                const int i = k / (PD / 4), j = k % (PD / 4);
-                const int dim = 8 * PD * (i >> 1) + PD * (2 * q + (i & 1)) + 4 * j;
-                uint2 x[2];
+                const int32_t v = x.v0 + min(row, x.rows - 1), tok = by_group(p, v), h = v - tok * p.group;
+                const uint8_t *src = static_cast<const uint8_t *>(p.q) +
+                                     ((static_cast<int64_t>(x.s0) + tok) * p.q_stride + (x.g * p.group + h) * D) * 2;
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    x[e] = qrow[e] ? __ldg(reinterpret_cast<const uint2 *>(qrow[e] + dim * 2)) : make_uint2(0u, 0u);
-                qf[k * 32 + lane] = make_uint4(x[0].x, x[1].x, x[0].y, x[1].y);
+                for (int a = 0; a < (KS + CR_COMP - 1) / CR_COMP; ++a) {
+                    const int k = warp + a * CR_COMP, i = k / (PD / 4), j = k % (PD / 4);
+                    const int dim = 8 * PD * (i >> 1) + PD * (2 * q + (i & 1)) + 4 * j;
+                    xq[a][e] = k < KS && row < x.rows ? __ldg(reinterpret_cast<const uint2 *>(src + dim * 2)) : make_uint2(0u, 0u);
+                }
             }
-            named_barrier(BAR_COMP, 32 * CR_COMP);
+        };
+        auto give_q = [&]() {
+#pragma unroll
+            for (int a = 0; a < (KS + CR_COMP - 1) / CR_COMP; ++a)
+                if (warp + a * CR_COMP < KS)
+                    qf[(warp + a * CR_COMP) * 32 + lane] = make_uint4(xq[a][0].x, xq[a][1].x, xq[a][0].y, xq[a][1].y);
+        };
+        bool more = next(&w);
+        if (more) {
+            load_q(w);
+            give_q();
+        }
+        named_barrier(BAR_COMP, 32 * CR_COMP);
+        while (more) {
+            const uint32_t *bits[2];                               // which entries the rows' tokens attend
+            int32_t pos[2], first[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int32_t tok = by_group(p, w.v0 + min(r + 8 * e, w.rows - 1));
+                pos[e] = w.p0 + tok;
+                bits[e] = G::BLOCKS && !G::DIRECT ? bits_of(p, w, tok) : nullptr;
+                first[e] = p.window > 0 ? max(0, pos[e] - p.window + 1) : 0;
+            }
+            int32_t word_at = -1;
+            uint32_t words[2] = {~0u, ~0u};
             float o[VI][PD][4];
 #pragma unroll
             for (int i = 0; i < VI; ++i)
@@ -399,15 +530,17 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
                 }
                 if ((it & 1u) != static_cast<uint32_t>(grp)) continue;
                 const int32_t at = (w.j0 + j) >> 1;                // (list entry)
-                uint32_t att[2] = {1u, 1u};
-                if constexpr (G::BLOCKS)
+                if (G::BLOCKS && !G::DIRECT && at >> 5 != word_at) {
+                    word_at = at >> 5;
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) att[e] = (__ldg(bits[e] + (at >> 5)) >> (at & 31)) & 1u;
+                    for (int e = 0; e < 2; ++e) words[e] = __ldg(bits[e] + word_at);
+                }
                 ok = warp_wait(&c.full[sl], ph, abort, lim);
                 const int32_t ent = G::BLOCKS ? c.entry[sl] : 0;
                 // tokens that some row attends, of a list's tile
                 const int32_t seen = G::BLOCKS ? tile_seen(ent, w.j0 + j) : 0;
                 const int32_t tok0 = (G::BLOCKS ? entry_block(ent) * BLOCK_TOKENS + (w.j0 + j & 1) * CR_TILE : (w.j0 + j) * CR_TILE) + sub;
+                const bool att[2] = {((words[0] >> (at & 31)) & 1u) != 0, ((words[1] >> (at & 31)) & 1u) != 0};
                 if (ok && (G::BLOCKS ? sub < seen : tok0 <= w.hi_tok && tok0 + 15 >= w.lo_tok)) {
                     const uint8_t *ka = smem + sl * STAGE, *va = ka + HALF;
                     // ---- scores of tokens sub + 8 n + 2 q + {0, 1}
@@ -530,6 +663,10 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
                 __syncwarp();
                 if (ok && lane == 0) mbar_arrive(&c.empty[sl]);
             }
+            // ---- the next queries
+            Seg w_next;
+            const bool more_next = next(&w_next);
+            if (more_next) load_q(w_next);
             // ---- the eight warps' sums, at the largest maximum
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -547,13 +684,13 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
                 f[e] = m[e] == -INFINITY ? 0.0f : exp2_approx((m[e] - mt[e]) * cs);
                 if (q == 0) c.l[warp][r + 8 * e] = l[e] * f[e];
             }
-            // Eight steps; in each every warp lays down PD / 8 dims of each chunk, and
+            // 8 / SUMS steps; in each every warp lays down DS dims of each chunk, and
             // thread t adds up the eight warps' values of place t: chunk i, row
             // r' + 8 (e / 2), dims 8 PD i + PD (2 q' + e % 2) .., where t = (i, lane', e).
-            constexpr int DS = PD / 8, OWN = (VI * 128 + 255) / 256;    // dims per step, places per thread
+            constexpr int DS = PD * Sh::SUMS / 8, OWN = (VI * 128 + 255) / 256;    // dims per step, places per thread
             float x[OWN][PD];
 #pragma unroll
-            for (int st = 0; st < 8; ++st) {
+            for (int st = 0; st < 8 / Sh::SUMS; ++st) {
 #pragma unroll
                 for (int i = 0; i < VI; ++i)
 #pragma unroll
@@ -576,6 +713,28 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
                     }
                 named_barrier(BAR_COMP, 32 * CR_COMP);
             }
+            if (G::DIRECT && p.split > 1) {
+                // the CTA's sums and maxima, for its cluster
+                float *mine = reinterpret_cast<float *>(sum);
+#pragma unroll
+                for (int k = 0; k < OWN; ++k) {
+                    const int at = t + 256 * k, i = at >> 7, ln = (at >> 2) & 31, e = at & 3;
+                    const int row = (ln >> 2) + 8 * (e >> 1), dim = 8 * PD * i + PD * (2 * (ln & 3) + (e & 1));
+                    if (at >= VI * 128) continue;
+#pragma unroll
+                    for (int d = 0; d < PD; d += 4)
+                        *reinterpret_cast<float4 *>(mine + row * D + dim + d) = make_float4(x[k][d], x[k][d + 1], x[k][d + 2], x[k][d + 3]);
+                    if (dim == 0) {
+                        float lt = 0.0f, ma = c.m[0][row];
+#pragma unroll
+                        for (int j = 0; j < CR_COMP; ++j) {
+                            lt += c.l[j][row];
+                            ma = fmaxf(ma, c.m[j][row]);
+                        }
+                        c.part[row] = make_float2(ma, lt);
+                    }
+                }
+            } else
 #pragma unroll
             for (int k = 0; k < OWN; ++k) {
                 const int at = t + 256 * k, i = at >> 7, ln = (at >> 2) & 31, e = at & 3;
@@ -611,12 +770,73 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
                     }
                 }
             }
-            named_barrier(BAR_COMP, 32 * CR_COMP);                 // read before the next segment's sums
+            if (more_next) give_q();
+            w = w_next;
+            more = more_next;
+            named_barrier(BAR_COMP, 32 * CR_COMP);                 // sums read before the next segment's, queries in
         }
     }
     __syncthreads();
+    if constexpr (G::DIRECT) {
+        if (p.split > 1) {
+            // The cluster had one unit at most.  Each CTA adds up an equal run of dims
+            // of all rows and writes it (by the warps that have the registers for it).
+            cluster_sync();
+            w = c.segs.seg[0];
+            if (warp >= CR_COMP) w.rows = 0;
+            const float cs = p.scale * LOG2_E;
+            const float *mine = reinterpret_cast<const float *>(sum);
+            const int32_t per = D / p.split / 4, rank = blockIdx.x % p.split;               // float4s of a row
+            for (int32_t at = t; at < w.rows * per && !c.abort; at += 32 * CR_COMP) {
+                const int32_t row = at / per, dim = (rank * per + at - row * per) * 4;
+                float2 ml[DIRECT_SPLIT];
+                float4 y[DIRECT_SPLIT];
+#pragma unroll
+                for (int k = 0; k < DIRECT_SPLIT; ++k) {
+                    if (k >= p.split) break;
+                    ml[k] = ld_cluster_f2(&c.part[row], k);
+                    y[k] = ld_cluster_f4(mine + row * D + dim, k);
+                }
+                float ma = -INFINITY, lt = 0.0f;
+#pragma unroll
+                for (int k = 0; k < DIRECT_SPLIT; ++k)
+                    if (k < p.split) ma = fmaxf(ma, ml[k].x);
+                float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                for (int k = 0; k < DIRECT_SPLIT; ++k) {
+                    if (k >= p.split) break;
+                    const float wt = ml[k].x == -INFINITY ? 0.0f : exp2_approx((ml[k].x - ma) * cs);
+                    lt = fmaf(ml[k].y, wt, lt);
+                    v.x = fmaf(y[k].x, wt, v.x);
+                    v.y = fmaf(y[k].y, wt, v.y);
+                    v.z = fmaf(y[k].z, wt, v.z);
+                    v.w = fmaf(y[k].w, wt, v.w);
+                }
+                const float inv = lt > 0.0f ? 1.0f / lt : 0.0f;
+                const int32_t vr = w.v0 + row, tok = by_group(p, vr), h = vr - tok * p.group;
+                __half *out = static_cast<__half *>(p.out) +
+                              ((static_cast<int64_t>(w.s0) + tok) * p.hq + w.g * p.group + h) * D + dim;
+                *reinterpret_cast<uint2 *>(out) = make_uint2(to_half2(v.x * inv, v.y * inv), to_half2(v.z * inv, v.w * inv));
+            }
+            __syncwarp();
+            cluster_sync();                                      // read by the whole cluster
+        }
+    }
     if (t == 0 && c.abort) record_error(p.kv.status, ST_TIMEOUT);
     allow_next_grid();
+}
+
+// Lets the kernel have `smem` bytes, once per device.
+inline int allow_smem(const void *kernel, size_t smem, std::mutex &mu, bool (&done)[64])
+{
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 0 || dev >= 64) return static_cast<int>(cudaErrorInvalidDevice);
+    std::lock_guard<std::mutex> lk(mu);
+    if (done[dev]) return 0;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    done[dev] = e == cudaSuccess;
+    return static_cast<int>(e);
 }
 
 // after_lists: as in launch_pairs.
@@ -628,26 +848,32 @@ int launch_rows(const ChunkParams &p, const void *tk, const void *tv, int grid, 
     static_assert(SMEM <= 232448, "shared memory budget");
     static std::mutex mu;
     static bool done[64] = {};
-    int dev = 0;
-    cudaGetDevice(&dev);
-    if (dev < 0 || dev >= 64) return static_cast<int>(cudaErrorInvalidDevice);
-    {
-        std::lock_guard<std::mutex> lk(mu);
-        if (!done[dev]) {
-            const cudaError_t e = cudaFuncSetAttribute(chunk_rows_kernel<D, Q8, G>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                       static_cast<int>(SMEM));
-            if (e != cudaSuccess) return static_cast<int>(e);
-            done[dev] = true;
-        }
-    }
+    int rc = allow_smem(reinterpret_cast<const void *>(&chunk_rows_kernel<D, Q8, G>), SMEM, mu, done);
+    if (rc != 0) return rc;
     void *args[] = {const_cast<void *>(tk), const_cast<void *>(tv), const_cast<ChunkParams *>(&p)};
-    const int rc = launch_kernel(reinterpret_cast<const void *>(&chunk_rows_kernel<D, Q8, G>), dim3(grid), dim3(CR_THREADS), SMEM,
+    rc = launch_kernel(reinterpret_cast<const void *>(&chunk_rows_kernel<D, Q8, G>), dim3(grid), dim3(CR_THREADS), SMEM,
                                  stream, after_lists && overlap, args);
     if (rc != 0) return rc;
     void *join[] = {const_cast<ChunkParams *>(&p)};
     const unsigned y = static_cast<unsigned>(p.ws_rows);
     return launch_kernel(reinterpret_cast<const void *>(&chunk_join_kernel<G, D>), dim3(grid, y), dim3(256), 0, stream,
                          overlap, join);
+}
+
+// The DIRECT kernel: no lists before it, nothing to join after it.
+template <int D, bool Q8>
+int launch_direct(const ChunkParams &p, const void *tk, const void *tv, int grid, cudaStream_t stream)
+{
+    using Sh = RowShape<D, Q8>;
+    constexpr size_t SMEM = Sh::NS * Sh::STAGE + Sh::SUM + Sh::QF + sizeof(RowCtrl);
+    static_assert(SMEM <= 232448, "shared memory budget");
+    const void *kernel = reinterpret_cast<const void *>(&chunk_rows_kernel<D, Q8, DirectRowsGeometry>);
+    static std::mutex mu;
+    static bool done[64] = {};
+    const int rc = allow_smem(kernel, SMEM, mu, done);
+    if (rc != 0) return rc;
+    void *args[] = {const_cast<void *>(tk), const_cast<void *>(tv), const_cast<ChunkParams *>(&p)};
+    return launch_kernel(kernel, dim3(grid), dim3(CR_THREADS), SMEM, stream, false, args, p.split);
 }
 
 template <typename G>

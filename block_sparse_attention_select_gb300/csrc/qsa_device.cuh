@@ -33,20 +33,29 @@ __device__ __forceinline__ void wait_prior_grid() { asm volatile("griddepcontrol
 __device__ __forceinline__ void allow_next_grid() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // Host side: launch `kernel` with its argument pointers, with or without the
-// programmatic-serialization attribute.
+// programmatic-serialization attribute, in clusters along x.
 inline int launch_kernel(const void *kernel, dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
-                         bool overlap, void **args)
+                         bool overlap, void **args, unsigned cluster = 1)
 {
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchAttribute attr[2];
+    unsigned n = 0;
+    if (overlap) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (cluster > 1) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = cluster;
+        attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
+        ++n;
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = block;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cfg.attrs = attr;
-    cfg.numAttrs = overlap ? 1u : 0u;
+    cfg.numAttrs = n;
     const cudaError_t e = cudaLaunchKernelExC(&cfg, kernel, args);
     return static_cast<int>(e != cudaSuccess ? e : cudaGetLastError());
 }

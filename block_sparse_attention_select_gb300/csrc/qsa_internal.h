@@ -205,6 +205,8 @@ struct ChunkParams {
     const int32_t *lists;       // [hkv][rows][list_stride], a unit's from its first row on
     const uint32_t *bits;       // [hkv][rows][words]
     int32_t list_stride, words, unit_tokens, max_entries;
+    const int32_t *sel;         // or the selections themselves, [rows][hkv][sel_k]: see qsa_chunk_rows.cuh
+    int32_t sel_k, recent, split;
 };
 
 // Attention over selected blocks: see qsa_blocks.cu.  c.window is 0.
@@ -306,7 +308,8 @@ int32_t chunk_rows_box(int32_t page_tokens);
 
 constexpr int32_t BLOCK_TOKENS = 128;        // tokens of a selected block
 constexpr int64_t BLOCKS_MAX_TOKENS = int64_t{1} << 25;   // tokens of a request at most
-int launch_blocks(const BlocksParams &p, bool few_rows, const void *tk, const void *tv, int sms, bool overlap, void *stream);
+int launch_blocks(const BlocksParams &p, bool few_rows, const void *tk, const void *tv, int sms, bool overlap, void *stream,
+                  int *launches);
 size_t blocks_workspace_bytes(int32_t rows, int32_t group, int32_t hkv, int32_t head_dim, int32_t k, int32_t recent,
                               int32_t row_capacity);
 int launch_rotary_table(float *table, int32_t n_pos, int32_t rope_dim, const RotaryAngles &angles, int sms, void *stream);

@@ -60,6 +60,40 @@ __device__ __forceinline__ int32_t request_of_unsorted(const KvParams &p, int32_
     return -1;
 }
 
+// The same for one row by a whole warp, with the same result in every lane: each
+// step asks 32 places among the requests left.  *falls: whether starts fall
+// somewhere, found out where it matters (-1: not yet).
+__device__ __forceinline__ int32_t request_of_by_warp(const KvParams &p, int32_t row, int lane, int *falls, Seq *s)
+{
+    int32_t lo = 0, n = p.n_reqs;            // among requests lo .. lo + n - 1
+    while (n > 1) {
+        const int32_t step = (n + 31) / 32, at = lane * step;
+        const bool before = at < n && __ldg(p.seq_start + lo + at) <= row;
+        const uint32_t m = __ballot_sync(0xffffffffu, before);
+        const int32_t k = m ? 31 - __clz(m) : 0;
+        lo += k * step;
+        n = min(step, n - k * step);
+    }
+    bool bad;
+    *s = seq_of(p, lo, &bad);
+    if (has_row(*s, row)) return lo;
+    if (*falls < 0) {
+        bool f = false;
+        for (int32_t b = lane; b < p.n_reqs; b += 32) f = f || __ldg(p.seq_start + b + 1) < __ldg(p.seq_start + b);
+        *falls = __any_sync(0xffffffffu, f) ? 1 : 0;
+    }
+    if (*falls == 0) return -1;
+    for (int32_t b0 = 0; b0 < p.n_reqs; b0 += 32) {
+        *s = seq_of(p, min(b0 + lane, p.n_reqs - 1), &bad);
+        const uint32_t m = __ballot_sync(0xffffffffu, b0 + lane < p.n_reqs && has_row(*s, row));
+        if (m == 0) continue;
+        const int32_t b = b0 + __ffs(m) - 1;
+        *s = seq_of(p, b, &bad);
+        return b;
+    }
+    return -1;
+}
+
 // Requests of rows row0 .. row0 + n - 1, a row per thread of the CTA (n <= its
 // threads), -1 for rows of no request; every thread of the CTA calls it.
 __device__ __forceinline__ int32_t requests_of_rows(const KvParams &p, int32_t row0, int32_t n, Seq *s)

@@ -318,3 +318,54 @@ def test_refusals_in_python():
             call(**kw)
     assert call().shape == q.shape
     ok()
+
+
+# Selections taken straight, a cluster of CTAs to a row and KV head while those are
+# few (8, 4, 2 and 1), several rows to a CTA when they are many; 32 blocks at most.
+@pytest.mark.parametrize("quantised", [False, True])
+@pytest.mark.parametrize("D", [128, 256])
+@pytest.mark.parametrize("reqs,hkv,group,k,recent", [(1, 1, 1, 3, 0), (1, 2, 12, 16, 1), (3, 8, 4, 5, 0), (9, 5, 16, 31, 1),
+                                                     (40, 2, 3, 16, 2), (70, 3, 9, 32, 0), (2, 1, 7, 0, 32), (5, 2, 2, 33, 0)])
+def test_single_tokens(reqs, hkv, group, k, recent, D, quantised):
+    rng = np.random.default_rng(reqs)
+    lens = [(1, int(c)) for c in rng.integers(1, 2600 if reqs < 20 else 900, reqs)]
+    b = Batch(45, lens, hkv=hkv, group=group, head_dim=D, page=32, quantised=quantised)
+    caches = b.stored()
+    sel = select(b, k, 56)
+    hidden, table = hide(b, caches, sel, recent)
+    got = attend(b, hidden, sel, recent, table=table)
+    ok()
+    check(b, got, caches, sel, recent)
+
+
+@pytest.mark.parametrize("reqs", [3, 200])
+def test_single_tokens_of_a_changing_batch(reqs):
+    """Empty requests, padding, starts that fall and requests out of range among single tokens."""
+    rng = np.random.default_rng(7)
+    lens = [(int(rng.random() < 0.7), int(rng.integers(1, 700))) for _ in range(reqs)]
+    b = Batch(46, lens, hkv=2, group=3, head_dim=128, page=64, quantised=False, pad_rows=reqs - sum(n for n, _ in lens))
+    caches = b.stored()
+    sel = select(b, 4, 57)
+    got = attend(b, caches, sel, 1)
+    ok()
+    check(b, got, caches, sel, 1)
+    # the same rows in two runs, the later one first, and a request past the block table
+    n = int(b.seq_start[-1])
+    order = [i for i in range(reqs) if lens[i][0]]
+    order = order[len(order) // 2:] + order[:len(order) // 2]
+    starts = [int(b.seq_start[i]) for i in order]
+    ss = torch.tensor(starts + [starts[-1] + 1], dtype=torch.int32, device="cuda")
+    ps = torch.tensor(b.pos_start[order], device="cuda")
+    cache = device_cache(b, caches, np.concatenate([b.table[order], b.table[:1]]))
+    q, _, _, _, _ = on_gpu(b)
+    out = torch.full((b.T, b.hq, b.D), 7.0, dtype=torch.float16, device="cuda")
+    qsa.block_attention(q, torch.from_numpy(sel).cuda(), ss, ps, cache, recent=1, out=out)
+    k, v, ks, vs = caches
+    want, mag = O.attention(b.q, sel, b.seq_start, b.pos_start, b.table, k, v, ks, vs, 1)
+    got = out.cpu().numpy().astype(np.float64)
+    assert qsa.get_device_status() == (qsa.QSA_ERR_INVALID_ARG if len(order) > 1 else qsa.QSA_OK)
+    # where the starts fall, the request before has no rows (its end lies before its start)
+    lost = [s for s, e in zip(starts, starts[1:] + [starts[-1] + 1]) if e <= s]
+    rows = [r for r in range(n) if r not in lost]
+    assert np.all(np.abs(got[rows] - want[rows]) <= tolerance(want[rows], mag[rows], lens, 6.0))
+    assert np.all(got[lost] == 7.0) and np.all(got[n:] == 7.0)
