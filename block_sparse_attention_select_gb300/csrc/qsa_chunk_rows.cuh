@@ -111,6 +111,63 @@ __device__ __forceinline__ int32_t tile_seen(int32_t entry, int32_t tile)
     return entry_seen(entry) - (tile & 1) * CR_TILE;
 }
 
+// Where the tiles of a segment lie in the cache, piece by piece (a piece: the tokens
+// of a tile that are in one page).  The lanes look up the pieces of `batch` tiles at
+// a time, the pages one batch ahead.  (Looked up tile by tile, a lane per token, the
+// lookups took 1,500 clocks a stage, more than its bytes.  They have no branch around
+// a load: the compiler would wait for it where the branch ends.)
+template <typename G>
+struct PieceRows {
+    ListWindow win;
+    const int32_t *bt;
+    int32_t batch, off, tok, page, row;
+    int sh, ld;
+
+    // the lane's token of tiles j .. j + batch - 1, or -1: its piece is not attended
+    __device__ __forceinline__ int32_t token_of(const ChunkParams &p, const Seg &w, int32_t j, int lane) const
+    {
+        const int32_t at = j + (lane >> ld), tile = w.j0 + at;
+        if constexpr (G::BLOCKS) {
+            const int32_t e = win.entry(tile), t = entry_block(e) * BLOCK_TOKENS + (tile & 1) * CR_TILE + off;
+            return at < w.n && off < tile_seen(e, tile) && t >> p.kv.page_shift < p.kv.max_pages ? t : -1;
+        }
+        const int32_t t = tile * CR_TILE + off;
+        return at < w.n && t <= w.hi_tok && t + (1 << sh) > w.lo_tok ? t : -1;
+    }
+    __device__ __forceinline__ void look_up(const ChunkParams &p, const Seg &w, int32_t j, int lane)
+    {
+        tok = token_of(p, w, j, lane);
+        page = __ldg(bt + (max(tok, 0) >> p.kv.page_shift));
+    }
+    // (win has been started, for lists)
+    __device__ __forceinline__ void start(const ChunkParams &p, const Seg &w, int lane)
+    {
+        sh = __ffs(min(p.kv.page_tokens, CR_TILE)) - 1;
+        ld = 6 - sh;
+        batch = 32 >> ld;
+        off = (lane & ((1 << ld) - 1)) << sh;
+        bt = p.kv.block_table + static_cast<int64_t>(w.b) * p.kv.max_pages;
+        look_up(p, w, 0, lane);
+    }
+    // for each tile in turn, before piece() and entry(); bad pages are reported by one role
+    __device__ __forceinline__ void tile(const ChunkParams &p, const Seg &w, int32_t j, int lane, bool report)
+    {
+        if (G::BLOCKS) win.advance(w.j0 + j, lane);
+        if ((j & (batch - 1)) != 0) return;
+        const bool in = static_cast<uint32_t>(page) < static_cast<uint32_t>(p.kv.num_pages);
+        if (report && tok >= 0 && !in) record_error(p.kv.status, ST_BAD_PAGE);
+        // the row past the cache reads zeros
+        row = tok >= 0 && in ? (page << p.kv.page_shift) + (tok & (p.kv.page_tokens - 1)) : p.kv.num_pages << p.kv.page_shift;
+        look_up(p, w, j + batch, lane);
+    }
+    // the cache row of the tile's piece d (may differ by lane)
+    __device__ __forceinline__ int32_t piece(int32_t j, int32_t d) const
+    {
+        return __shfl_sync(0xffffffffu, row, ((j & (batch - 1)) << ld) + d);
+    }
+};
+static_assert(CR_TILE == 64, "pieces of a tile");
+
 template <int D, bool Q8>
 struct RowShape {
     static constexpr int ES = Q8 ? 1 : 2;
@@ -301,79 +358,44 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
             else schedule<G>(p, c.share, c.segs, blockIdx.x, true, lane);
         } else if (warp == CR_LOAD) {
             // ------------------------------------------------------ K, V loads
-            const int32_t P = p.kv.page_tokens;
-            const int sh = __ffs(min(P, CR_TILE)) - 1;             // log2 of a box's tokens
+            const int sh = __ffs(min(p.kv.page_tokens, CR_TILE)) - 1;       // log2 of a box's tokens
             const int32_t down = CR_TILE >> sh, boxes = 2 * Sh::CHUNKS * down;
             uint32_t slot = 0, phase = 0, used = 0, last = 0;
             bool ok = true;
             while (next(&w)) {
                 if (!ok) continue;
-                const int32_t *bt = p.kv.block_table + static_cast<int64_t>(w.b) * p.kv.max_pages;
-                // a lane looks up the cache rows of tokens lane and lane + 32, two
-                // stages ahead
-                const int32_t nowhere = p.kv.num_pages << p.kv.page_shift;       // past the cache: reads zeros
-                ListWindow win;
-                if (G::BLOCKS) start(win);
-                auto row_of = [&](int32_t j, int k) -> int32_t {
-                    if constexpr (G::BLOCKS) {
-                        const int32_t ent = win.entry(w.j0 + j), off = lane + 32 * k;
-                        const int32_t tok = entry_block(ent) * BLOCK_TOKENS + (w.j0 + j & 1) * CR_TILE + off;
-                        const int32_t at = tok >> p.kv.page_shift;
-                        if (j >= w.n || (off & ~((1 << sh) - 1)) >= tile_seen(ent, w.j0 + j) || at >= p.kv.max_pages) return nowhere;
-                        const int32_t page = __ldg(bt + at);
-                        if (page >= 0 && page < p.kv.num_pages) return (page << p.kv.page_shift) + (tok & (P - 1));
-                        record_error(p.kv.status, ST_BAD_PAGE);
-                        return nowhere;
-                    }
-                    const int32_t tok = (w.j0 + j) * CR_TILE + lane + 32 * k;
-                    // a box is loaded when any of its tokens is attended
-                    if (j >= w.n || (tok & ~((1 << sh) - 1)) > w.hi_tok || (tok | ((1 << sh) - 1)) < w.lo_tok) return nowhere;
-                    const int32_t page = __ldg(bt + (tok >> p.kv.page_shift));
-                    if (page >= 0 && page < p.kv.num_pages) return (page << p.kv.page_shift) + (tok & (P - 1));
-                    record_error(p.kv.status, ST_BAD_PAGE);
-                    return nowhere;
-                };
-                int32_t row[2], row1[2];
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    row[k] = row_of(0, k);
-                    row1[k] = row_of(1, k);
-                }
+                PieceRows<G> at;
+                if (G::BLOCKS) start(at.win);
+                at.start(p, w, lane);
                 for (int32_t j = 0; j < w.n; ++j) {
+                    at.tile(p, w, j, lane, true);
+                    const int32_t ent = G::BLOCKS ? at.win.entry(w.j0 + j) : 0;
+                    const bool some = !G::BLOCKS || tile_seen(ent, w.j0 + j) > 0;      // else nothing to load
                     if (!warp_wait(&c.empty[slot], phase ^ 1u, abort, lim)) {
                         ok = false;
                         break;
                     }
-                    if (G::BLOCKS) win.advance(w.j0 + j, lane);
-                    const int32_t ent = G::BLOCKS ? win.entry(w.j0 + j) : 0;
                     if (lane == 0) {
                         if (G::BLOCKS) c.entry[slot] = ent;
-                        if (!G::BLOCKS || tile_seen(ent, w.j0 + j) > 0) mbar_arrive_expect_tx(&c.full[slot], STAGE);
-                        else mbar_arrive(&c.full[slot]);           // nothing to load
+                        if (some) mbar_arrive_expect_tx(&c.full[slot], STAGE);
+                        else mbar_arrive(&c.full[slot]);
                     }
                     __syncwarp();
                     uint8_t *dst = smem + slot * STAGE;
-                    for (int32_t i0 = 0; i0 < boxes && (!G::BLOCKS || tile_seen(ent, w.j0 + j) > 0); i0 += 32) {
+                    for (int32_t i0 = 0; some && i0 < boxes; i0 += 32) {
                         const int32_t i = i0 + lane;
-                        const int32_t d = i & (down - 1), ch = (i / down) % Sh::CHUNKS;
+                        const int32_t d = i & (down - 1), ch = (i >> (6 - sh)) & (Sh::CHUNKS - 1);
                         const bool v = i >= boxes / 2;
-                        const int32_t first = d << sh;             // the box's first token, held by lane first % 32
-                        const int32_t ya = __shfl_sync(0xffffffffu, row[0], first & 31);
-                        const int32_t yb = __shfl_sync(0xffffffffu, row[1], first & 31);
+                        const int32_t y = at.piece(j, d);
                         if (i < boxes)
-                            tma_load_3d(dst + (v ? HALF : 0u) + ch * (CR_TILE * 128) + first * 128, v ? &tv : &tk, &c.full[slot],
-                                        0, first < 32 ? ya : yb, w.g * Sh::CHUNKS + ch);
+                            tma_load_3d(dst + (v ? HALF : 0u) + ch * (CR_TILE * 128) + (d << sh) * 128, v ? &tv : &tk, &c.full[slot], 0, y,
+                                        w.g * Sh::CHUNKS + ch);
                     }
                     used |= 1u << slot;
                     last = (last & ~(1u << slot)) | (phase << slot);
                     if (++slot == NS) {
                         slot = 0;
                         phase ^= 1u;
-                    }
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        row[k] = row1[k];
-                        row1[k] = row_of(j + 2, k);
                     }
                 }
             }
@@ -394,48 +416,27 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
             bool ok = true;
             while (next(&w)) {
                 if (!ok) continue;
-                const int32_t *bt = p.kv.block_table + static_cast<int64_t>(w.b) * p.kv.max_pages;
-                ListWindow win;
-                if (G::BLOCKS) start(win);
-                auto page_of = [&](int32_t j, int k) -> int32_t {
-                    if constexpr (G::BLOCKS) {
-                        const int32_t ent = win.entry(w.j0 + j), off = lane + 32 * k;
-                        const int32_t at = (entry_block(ent) * BLOCK_TOKENS + (w.j0 + j & 1) * CR_TILE + off) >> p.kv.page_shift;
-                        return j < w.n && off < tile_seen(ent, w.j0 + j) && at < p.kv.max_pages ? __ldg(bt + at) : -1;
-                    }
-                    const int32_t tok = (w.j0 + j) * CR_TILE + lane + 32 * k;
-                    return j < w.n && tok >= w.lo_tok && tok <= w.hi_tok ? __ldg(bt + (tok >> p.kv.page_shift)) : -1;
-                };
-                auto byte_of = [&](int32_t j, int k, int32_t page) -> uint32_t {
-                    const int32_t first = G::BLOCKS ? entry_block(win.entry(w.j0 + j)) * BLOCK_TOKENS + (w.j0 + j & 1) * CR_TILE
-                                                    : (w.j0 + j) * CR_TILE;
-                    if (page < 0 || page >= p.kv.num_pages) return 127u;
-                    const int32_t tok = first + lane + 32 * k;
-                    return __ldg(scale + ((static_cast<int64_t>(page) << p.kv.page_shift) + (tok & (p.kv.page_tokens - 1))) * p.kv.hkv + w.g);
-                };
-                int32_t page[4][2];
-                uint32_t byte[4][2];
-#pragma unroll
-                for (int u = 0; u < 4; ++u)
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) page[u][k] = page_of(u, k);
-#pragma unroll
-                for (int u = 0; u < 4; ++u)
+                PieceRows<G> at;
+                if (G::BLOCKS) start(at.win);
+                at.start(p, w, lane);
+                // the bytes of tokens lane and lane + 32 (what tokens get that no row
+                // attends does not matter)
+                auto bytes_of = [&](int32_t j, uint32_t (&x)[2]) {
+                    at.tile(p, w, j, lane, false);
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        byte[u][k] = byte_of(u, k, page[u][k]);
-                        page[u][k] = page_of(u + 4, k);
+                        const int32_t off = lane + 32 * k, y = at.piece(j, off >> at.sh);
+                        const int64_t line = y < p.kv.num_pages << p.kv.page_shift ? y + (off & ((1 << at.sh) - 1)) : 0;
+                        x[k] = __ldg(scale + line * p.kv.hkv + w.g);
                     }
+                };
+                uint32_t byte[4][2];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) bytes_of(u, byte[u]);
                 for (int32_t j = 0; ok && j < w.n; j += 4) {
-                    if (G::BLOCKS) win.advance(w.j0 + j, lane);
                     uint32_t next[4][2];
 #pragma unroll
-                    for (int u = 0; u < 4; ++u)
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            next[u][k] = byte_of(j + 4 + u, k, page[u][k]);
-                            page[u][k] = page_of(j + 8 + u, k);
-                        }
+                    for (int u = 0; u < 4; ++u) bytes_of(j + 4 + u, next[u]);
 #pragma unroll
                     for (int u = 0; u < 4; ++u) {
                         if (!ok || j + u >= w.n) break;
