@@ -3,8 +3,13 @@
 //
 // Bound by memory: every value is read and written once.  A thread takes 16 dims
 // of a head as two 16-byte vectors (both halves of eight pairs) and goes through
-// the heads of its token with them, so that it reads its eight cosines and sines
-// once for all heads; ROT_BATCH heads' loads are in flight together.
+// some heads of its token with them, so that it reads its eight cosines and sines
+// once for all of these; ROT_BATCH heads' loads are in flight together.  Four
+// prompts of 4,096 tokens, 40 heads of 128: 55 us with halves paired, 54 us with
+// neighbours (6.2 and 6.4 TB/s; neighbours as two 16-byte accesses 59 us; 4 or 20
+// heads to a thread 57 to 60 us).  The 1,616-row chunk, 26 heads of 256 of which 64
+// dims rotate: 9 us (a thread for every head or two: 11 us), 64 single tokens 4 us,
+// a launch and two memory latencies.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
@@ -20,7 +25,8 @@ namespace {
 
 constexpr int ROT_THREADS = 256;
 constexpr int ROT_ROWS = 32;                 // rows of a CTA at most
-constexpr int ROT_BATCH = 4;
+constexpr int ROT_BATCH = 4;                 // heads whose loads are in flight
+constexpr int ROT_HEADS = 10;                // heads that a thread goes through at most
 
 // Eight pairs: a and b of each as FP16 halves of four words; neighbours: a0 b0 a1 b1 ...
 template <bool NEIGHBOURS>
@@ -49,7 +55,32 @@ __device__ __forceinline__ void rotate8(uint4 &x, uint4 &y, const float (&cs)[8]
     y = make_uint4(w[4], w[5], w[6], w[7]);
 }
 
-template <bool NEIGHBOURS>
+// Two 16-byte vectors, side by side and 32-byte aligned when WIDE.
+template <bool WIDE>
+__device__ __forceinline__ void load_two(const uint16_t *a, const uint16_t *b, uint4 &x, uint4 &y)
+{
+    if (WIDE) {
+        asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w), "=r"(y.x), "=r"(y.y), "=r"(y.z), "=r"(y.w) : "l"(a) : "memory");
+    } else {
+        x = *reinterpret_cast<const uint4 *>(a);
+        y = *reinterpret_cast<const uint4 *>(b);
+    }
+}
+template <bool WIDE>
+__device__ __forceinline__ void store_two(uint16_t *a, uint16_t *b, const uint4 &x, const uint4 &y)
+{
+    if (WIDE) {
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(a), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w), "r"(y.x),
+                     "r"(y.y), "r"(y.z), "r"(y.w) : "memory");
+    } else {
+        *reinterpret_cast<uint4 *>(a) = x;
+        *reinterpret_cast<uint4 *>(b) = y;
+    }
+}
+
+// WIDE: neighbours, every head and its rotated part 32-byte aligned.
+template <bool NEIGHBOURS, bool WIDE>
 __global__ void __launch_bounds__(ROT_THREADS)
 rotary_kernel(const RotaryParams p)
 {
@@ -66,7 +97,7 @@ rotary_kernel(const RotaryParams p)
     const int32_t turned = p.rope_dim / 16;                  // items of a head that rotate, then those that are copied
     const int32_t items = p.items, per_row = items * p.slices, total = n_rows * per_row;
     const int32_t heads = p.q_heads + p.k_heads;
-    for (int32_t i = t; i < total; i += ROT_THREADS) {
+    for (int32_t i = t; i < total; i += blockDim.x) {
         const int32_t r = i / per_row, in = i - r * per_row, slice = in / items, item = in - slice * items;
         const int32_t at = pos_s[r];
         if (at < 0) continue;
@@ -108,8 +139,7 @@ rotary_kernel(const RotaryParams p)
             for (int k = 0; k < ROT_BATCH; ++k) {
                 const int32_t h = h0 + k * p.slices;
                 if (h >= heads) break;
-                x[k] = *reinterpret_cast<const uint4 *>(in_of(h) + d0);
-                y[k] = *reinterpret_cast<const uint4 *>(in_of(h) + d1);
+                load_two<WIDE>(in_of(h) + d0, in_of(h) + d1, x[k], y[k]);
             }
 #pragma unroll
             for (int k = 0; k < ROT_BATCH; ++k) {
@@ -117,8 +147,7 @@ rotary_kernel(const RotaryParams p)
                 if (h >= heads) break;
                 if (!turn && in_of(h) == out_of(h)) continue;     // in place
                 if (turn) rotate8<NEIGHBOURS>(x[k], y[k], cs, sn);
-                *reinterpret_cast<uint4 *>(out_of(h) + d0) = x[k];
-                *reinterpret_cast<uint4 *>(out_of(h) + d1) = y[k];
+                store_two<WIDE>(out_of(h) + d0, out_of(h) + d1, x[k], y[k]);
             }
         }
     }
@@ -158,17 +187,25 @@ int launch_rotary(const RotaryParams &in, bool neighbours, int sms, void *stream
 {
     RotaryParams p = in;
     const int32_t heads = p.q_heads + p.k_heads;
-    // head slices: few heads to a thread while threads are few
-    const int64_t want = static_cast<int64_t>(sms) * 2048;
-    p.slices = 1;
-    while (p.slices * 2 <= heads && static_cast<int64_t>(p.seq.rows) * p.items * p.slices < want) p.slices *= 2;
-    const int64_t per_row = static_cast<int64_t>(p.items) * p.slices;
-    p.cta_rows = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(ROT_ROWS, ROT_THREADS / per_row)));
+    // ROT_HEADS heads to a thread, fewer while threads are few
+    const int64_t want = static_cast<int64_t>(sms) * 1024;
+    const int64_t each = static_cast<int64_t>(p.seq.rows) * p.items * heads / want;
+    const int32_t mine = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(each, ROT_HEADS)));
+    const int32_t most = (heads + mine - 1) / mine;
+    p.slices = std::max(1, std::min(most, ROT_THREADS / p.items));
+    const int32_t per_row = p.items * p.slices;
+    p.cta_rows = std::max(1, std::min(ROT_ROWS, ROT_THREADS / per_row));
+    const unsigned threads = static_cast<unsigned>(std::max(p.cta_rows, std::min(ROT_THREADS, p.cta_rows * per_row)) + 31) / 32 * 32;
     const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(p.seq.rows) + p.cta_rows - 1) / p.cta_rows);
+    // neighbours in 32-byte pieces where all of them are aligned
+    const uint64_t places = reinterpret_cast<uintptr_t>(p.q) | reinterpret_cast<uintptr_t>(p.k) | reinterpret_cast<uintptr_t>(p.out_q) |
+                            reinterpret_cast<uintptr_t>(p.out_k) |
+                            2 * static_cast<uint64_t>(p.q_stride | p.k_stride | p.out_q_stride | p.out_k_stride | p.first);
+    const void *kernel = !neighbours ? reinterpret_cast<const void *>(&rotary_kernel<false, false>)
+                         : places % 32 == 0 ? reinterpret_cast<const void *>(&rotary_kernel<true, true>)
+                                            : reinterpret_cast<const void *>(&rotary_kernel<true, false>);
     void *args[] = {&p};
-    return launch_kernel(neighbours ? reinterpret_cast<const void *>(&rotary_kernel<true>)
-                                    : reinterpret_cast<const void *>(&rotary_kernel<false>),
-                         dim3(grid), dim3(ROT_THREADS), 0, static_cast<cudaStream_t>(stream), false, args);
+    return launch_kernel(kernel, dim3(grid), dim3(threads), 0, static_cast<cudaStream_t>(stream), false, args);
 }
 
 }  // namespace qsa
