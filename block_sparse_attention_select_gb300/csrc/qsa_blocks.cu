@@ -43,6 +43,7 @@ lists_kernel(const ListsParams p)
     const int32_t g = blockIdx.y;
     if (t == 0) n_units = 0;
     wait_prior_grid();
+    allow_next_grid();                                      // the attention's CTAs wait for the lists on the device
     if (blockIdx.x == 0 && g == 0) flag_bad_requests(p.kv);
     const int32_t row0 = blockIdx.x * p.window;
     Seq s;
@@ -136,7 +137,6 @@ lists_kernel(const ListsParams p)
             }
         __syncthreads();
     }
-    allow_next_grid();
 }
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
