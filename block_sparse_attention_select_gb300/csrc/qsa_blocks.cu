@@ -177,12 +177,12 @@ int launch_blocks(const BlocksParams &in, bool few_rows, const void *tk, const v
     const KvParams &kv = c.kv;
     // Few rows whose units would be single tokens: no lists, no join.
     if (few_rows && in.k + in.recent <= DIRECT_BLOCKS && (c.group > CR_ROWS / 2 || kv.rows <= kv.n_reqs)) {
-        const int32_t units = kv.rows * kv.hkv;
+        const int32_t units = kv.rows * kv.hkv;              // (below 2^31: rows * hq is)
         c.sel = in.sel;
         c.sel_k = in.k;
         c.recent = in.recent;
         c.split = 1;
-        while (c.split < DIRECT_SPLIT && units * c.split * 2 <= sms) c.split *= 2;
+        while (c.split < DIRECT_SPLIT && units <= sms / (2 * c.split)) c.split *= 2;
         const int grid = c.split > 1 ? units * c.split : std::min(units, sms);
         *launches = 1;
         if (kv.head_dim == 128)
