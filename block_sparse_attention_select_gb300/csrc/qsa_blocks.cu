@@ -181,13 +181,10 @@ int launch_blocks(const BlocksParams &in, bool few_rows, const void *tk, const v
         c.sel = in.sel;
         c.sel_k = in.k;
         c.recent = in.recent;
-        c.split = 1;
-        while (c.split < DIRECT_SPLIT && units <= sms / (2 * c.split)) c.split *= 2;
-        const int grid = c.split > 1 ? units * c.split : std::min(units, sms);
         *launches = 1;
         if (kv.head_dim == 128)
-            return kv.e4m3 ? launch_direct<128, true>(c, tk, tv, grid, st) : launch_direct<128, false>(c, tk, tv, grid, st);
-        return kv.e4m3 ? launch_direct<256, true>(c, tk, tv, grid, st) : launch_direct<256, false>(c, tk, tv, grid, st);
+            return kv.e4m3 ? launch_direct<128, true>(c, tk, tv, units, sms, st) : launch_direct<128, false>(c, tk, tv, units, sms, st);
+        return kv.e4m3 ? launch_direct<256, true>(c, tk, tv, units, sms, st) : launch_direct<256, false>(c, tk, tv, units, sms, st);
     }
     *launches = 3;
     c.unit_tokens = few_rows ? CR_ROWS / c.group : pair_tokens(c.group);

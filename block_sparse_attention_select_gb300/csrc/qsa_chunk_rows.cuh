@@ -248,6 +248,7 @@ __device__ __forceinline__ void schedule_direct(const ChunkParams &p, RowCtrl &c
     Seg x;
     for (int32_t u = blockIdx.x / split; u < units; u += clusters) {
         const int32_t row = u / p.kv.hkv;
+        const int32_t named = lane < p.sel_k ? __ldg(p.sel + static_cast<int64_t>(u) * p.sel_k + lane) : NO_BLOCK;
         Seq s;
         const int32_t b = request_of_by_warp(p.kv, row, lane, &falls, &s);
         if (b < 0) continue;
@@ -255,7 +256,7 @@ __device__ __forceinline__ void schedule_direct(const ChunkParams &p, RowCtrl &c
         const int32_t tok = row - s.s0, pos = s.p0 + tok, own = pos / BLOCK_TOKENS;
         int32_t block = NO_BLOCK;
         if (lane < p.sel_k) {
-            block = __ldg(p.sel + static_cast<int64_t>(u) * p.sel_k + lane);
+            block = named;
             if (block < -1 || block > own) {
                 record_error(p.kv.status, ST_BAD_ROW);
                 block = NO_BLOCK;
@@ -861,9 +862,32 @@ int launch_rows(const ChunkParams &p, const void *tk, const void *tv, int grid, 
                          overlap, join);
 }
 
-// The DIRECT kernel: no lists before it, nothing to join after it.
+// How many clusters of `size` CTAs the device runs at once (0: it cannot say).
+inline int clusters_at_once(const void *kernel, size_t smem, unsigned size)
+{
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = size;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(size);
+    cfg.blockDim = dim3(CR_THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    return n;
+}
+
+// The DIRECT kernel: no lists before it, nothing to join after it.  A unit takes as
+// many CTAs as leave all units running at once (8 requests of 2 KV heads: 12 us on
+// clusters of 4, 18 us on clusters of 8, of which not all 16 do).
 template <int D, bool Q8>
-int launch_direct(const ChunkParams &p, const void *tk, const void *tv, int grid, cudaStream_t stream)
+int launch_direct(const ChunkParams &in, const void *tk, const void *tv, int32_t units, int sms, cudaStream_t stream)
 {
     using Sh = RowShape<D, Q8>;
     constexpr size_t SMEM = Sh::NS * Sh::STAGE + Sh::SUM + Sh::QF + sizeof(RowCtrl);
@@ -871,9 +895,25 @@ int launch_direct(const ChunkParams &p, const void *tk, const void *tv, int grid
     const void *kernel = reinterpret_cast<const void *>(&chunk_rows_kernel<D, Q8, DirectRowsGeometry>);
     static std::mutex mu;
     static bool done[64] = {};
+    static int fit[64][4] = {};              // clusters of 2, 4 and 8 at once; -1: none
     const int rc = allow_smem(kernel, SMEM, mu, done);
     if (rc != 0) return rc;
-    void *args[] = {const_cast<void *>(tk), const_cast<void *>(tv), const_cast<ChunkParams *>(&p)};
+    ChunkParams p = in;
+    p.split = 1;
+    int dev = 0;
+    cudaGetDevice(&dev);
+    {
+        std::lock_guard<std::mutex> lk(mu);
+        for (int i = 3; i > 0 && p.split == 1; --i) {
+            int &n = fit[dev][i];
+            if (n == 0) n = std::max(clusters_at_once(kernel, SMEM, 1u << i), 0);
+            if (n == 0) n = -1;
+            if (units <= n) p.split = 1 << i;
+        }
+    }
+    static_assert(DIRECT_SPLIT == 8, "three sizes");
+    const int grid = p.split > 1 ? units * p.split : std::min(units, sms);
+    void *args[] = {const_cast<void *>(tk), const_cast<void *>(tv), &p};
     return launch_kernel(kernel, dim3(grid), dim3(CR_THREADS), SMEM, stream, false, args, p.split);
 }
 

@@ -13,13 +13,9 @@ struct Seq {
     int32_t s0, n, p0;
 };
 
-__device__ __forceinline__ Seq seq_of(const KvParams &p, int32_t b, bool *bad)
+__device__ __forceinline__ Seq seq_from(const KvParams &p, int32_t s0, int32_t s1, int32_t p0, bool *bad)
 {
-    Seq s;
-    s.s0 = __ldg(p.seq_start + b);
-    s.n = 0;
-    const int32_t s1 = __ldg(p.seq_start + b + 1);
-    s.p0 = __ldg(p.pos_start + b);
+    Seq s{s0, 0, p0};
     const int64_t n = static_cast<int64_t>(s1) - s.s0;
     const bool ok = s.s0 >= 0 && n >= 0 && s1 <= p.rows && s.p0 >= 0 &&
                     s.p0 + n <= (static_cast<int64_t>(p.max_pages) << p.page_shift);
@@ -27,6 +23,11 @@ __device__ __forceinline__ Seq seq_of(const KvParams &p, int32_t b, bool *bad)
     *bad = !ok && n != 0;
     if (ok) s.n = static_cast<int32_t>(n);
     return s;
+}
+
+__device__ __forceinline__ Seq seq_of(const KvParams &p, int32_t b, bool *bad)
+{
+    return seq_from(p, __ldg(p.seq_start + b), __ldg(p.seq_start + b + 1), __ldg(p.pos_start + b), bad);
 }
 
 // Whether a request has the row.  (n > 0 first: a skipped request's start may be any
@@ -60,11 +61,23 @@ __device__ __forceinline__ int32_t request_of_unsorted(const KvParams &p, int32_
     return -1;
 }
 
-// The same for one row by a whole warp, with the same result in every lane: each
-// step asks 32 places among the requests left.  *falls: whether starts fall
-// somewhere, found out where it matters (-1: not yet).
+// The same for one row by a whole warp, with the same result in every lane.  Up to
+// 32 requests are all looked at, after one memory latency; else each step asks 32
+// places among the requests left.  *falls: whether starts fall somewhere, found out
+// where it matters (-1: not yet).
 __device__ __forceinline__ int32_t request_of_by_warp(const KvParams &p, int32_t row, int lane, int *falls, Seq *s)
 {
+    if (p.n_reqs <= 32) {
+        bool bad;
+        const Seq x = seq_of(p, min(lane, p.n_reqs - 1), &bad);
+        const uint32_t m = __ballot_sync(0xffffffffu, has_row(x, row));
+        if (m == 0) return -1;
+        const int from = __ffs(m) - 1;
+        s->s0 = __shfl_sync(0xffffffffu, x.s0, from);
+        s->n = __shfl_sync(0xffffffffu, x.n, from);
+        s->p0 = __shfl_sync(0xffffffffu, x.p0, from);
+        return from;                         // (the first lane that has it: its own request)
+    }
     int32_t lo = 0, n = p.n_reqs;            // among requests lo .. lo + n - 1
     while (n > 1) {
         const int32_t step = (n + 31) / 32, at = lane * step;
