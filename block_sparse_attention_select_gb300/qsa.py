@@ -621,19 +621,20 @@ def rotary_table(n_pos: int, rope_dim: int, theta: float = 10000.0, scaling: Rop
     return t
 
 
-def _head_rows(t, like, name: str):
-    """Checks an FP16 row array [rows, heads, head_dim] and returns (address, row
-    stride, heads): rows may be slices of wider ones, a row itself is contiguous."""
+def _head_rows(t, rows: int, dim: int, device, name: str):
+    """Checks an FP16 row array [rows, heads, head_dim] and returns its row stride and
+    heads: rows may be slices of wider ones, a row itself is contiguous."""
     shape, stride = t.shape, t.stride()
     if t.dtype is not torch.float16:
         raise TypeError(f"{name} must be {torch.float16}, got {t.dtype}")
-    if t.device != like.device or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor on q's device")
-    if len(shape) != 3 or shape[0] != like.shape[0] or shape[2] != like.shape[2]:
-        raise ValueError(f"{name} must be [rows, heads, head_dim] with q's rows and head_dim, got {list(shape)}")
-    if stride[2] != 1 or (shape[1] > 1 and stride[1] != shape[2]):
+    if t.device != device:
+        raise ValueError(f"{name} must be on q's device")
+    if len(shape) != 3 or shape[0] != rows or shape[2] != dim:
+        raise ValueError(f"{name} must be [{rows}, heads, {dim}], got {list(shape)}")
+    heads = shape[1]
+    if stride[2] != 1 or (stride[1] != dim and heads > 1):
         raise ValueError(f"each row of {name} must be contiguous")
-    return t.data_ptr(), stride[0] if shape[0] > 1 else shape[1] * shape[2], shape[1]
+    return stride[0] if rows > 1 else heads * dim, heads
 
 
 def rotary(q, k, seq_start, pos_start, table, first: int = 0, interleaved: bool = False, out_q=None, out_k=None,
@@ -643,32 +644,37 @@ def rotary(q, k, seq_start, pos_start, table, first: int = 0, interleaved: bool 
     positions and copy the others.  Pairs are (j, j + half), or neighbours
     (interleaved).  out_q may be q and out_k k, in place; rows past the last
     request are left as they are.  Returns (out_q, out_k)."""
+    device = q.device
     if q.dim() != 3 or table.dim() != 2 or table.dtype is not torch.float32 or not table.is_contiguous():
         raise ValueError("q must be [rows, heads, head_dim], table contiguous float32 [positions, rope_dim]")
-    if not q.is_cuda or table.device != q.device:
+    if not q.is_cuda or table.device != device:
         raise ValueError("q and table must be on one CUDA device")
-    where = _Device(q.device)
+    where = _Device(device)
     n = _requests(seq_start, pos_start, where)
-    made = []
+    rows, hq, dim = q.shape
+    made = ()
     if out_q is None:
-        out_q = torch.empty(q.shape, dtype=torch.float16, device=q.device)
-        made.append(out_q)
-    if k is None and out_k is not None:
-        raise ValueError("out_k goes with k")
-    if k is not None and out_k is None:
-        out_k = torch.empty(k.shape, dtype=torch.float16, device=q.device)
-        made.append(out_k)
-    qp, qs, hq = _head_rows(q, q, "q")
-    oqp, oqs, ohq = _head_rows(out_q, q, "out_q")
-    kp, ks, hk, okp, oks, ohk = 0, 0, 0, 0, 0, 0
-    if k is not None:
-        kp, ks, hk = _head_rows(k, q, "k")
-        okp, oks, ohk = _head_rows(out_k, q, "out_k")
+        out_q = torch.empty(q.shape, dtype=torch.float16, device=device)
+        made += (out_q,)
+    qs, _ = _head_rows(q, rows, dim, device, "q")
+    oqs, ohq = (qs, hq) if out_q is q else _head_rows(out_q, rows, dim, device, "out_q")
+    if k is None:
+        if out_k is not None:
+            raise ValueError("out_k goes with k")
+        kp = ks = hk = okp = oks = ohk = 0
+    else:
+        if out_k is None:
+            out_k = torch.empty(k.shape, dtype=torch.float16, device=device)
+            made += (out_k,)
+        ks, hk = _head_rows(k, rows, dim, device, "k")
+        oks, ohk = (ks, hk) if out_k is k else _head_rows(out_k, rows, dim, device, "out_k")
+        kp, okp = k.data_ptr(), out_k.data_ptr()
     if ohq != hq or ohk != hk:
         raise ValueError("out_q and out_k must have q's and k's shapes")
-    _call(where, stream, load().qsa_rotary, qp, qs, hq, oqp, oqs, kp, ks, hk, okp, oks, q.shape[0], q.shape[2],
-          int(first), table.shape[1], QSA_ROPE_NEIGHBOURS if interleaved else QSA_ROPE_HALVES, n,
-          seq_start.data_ptr(), pos_start.data_ptr(), table.data_ptr(), table.shape[0], made=made)
+    positions, rope_dim = table.shape
+    _call(where, stream, load().qsa_rotary, q.data_ptr(), qs, hq, out_q.data_ptr(), oqs, kp, ks, hk, okp, oks, rows, dim,
+          first, rope_dim, QSA_ROPE_NEIGHBOURS if interleaved else QSA_ROPE_HALVES, n, seq_start.data_ptr(),
+          pos_start.data_ptr(), table.data_ptr(), positions, made=made)
     return out_q, out_k
 
 
