@@ -7,7 +7,12 @@
 // the lists instead of a run of tiles (qsa_chunk_pair.cuh, qsa_chunk_rows.cuh).
 // Neighbouring tokens select much the same blocks, so a unit reads a block once
 // for all of its tokens and the products stay dense; a row that does not attend a
-// tile gives it zero weights.
+// tile gives it zero weights.  (Reading each row's blocks for itself, the 1,616-row
+// chunk would bring 3.6 GB from the L2 cache.)
+//
+// Bound by latency: a chunk's lists take 7 us, those of four prompts of 8,192 tokens 24
+// (under the profiler, with cold caches), before attention of 140 and 1,120 us.  Single
+// tokens need no lists (qsa_chunk_rows.cuh).
 #include "qsa_chunk_pair.cuh"
 #include "qsa_chunk_rows.cuh"
 

@@ -66,6 +66,20 @@
 // From the E4M3 cache times move by up to 8% with the place of the kernel's code:
 // two groups of warps in long unrolled loops share the instruction caches.
 //
+// Over selected blocks (BlockPairGeometry) a unit is whole tokens, its tiles are the
+// blocks of its list (qsa_chunk.cuh), and a row that does not attend a tile takes
+// weights of zero; a warp none of whose rows does leaves its scores where they are.
+// So the products are those of the units' lists: the 1,616-row chunk over 184,320
+// tokens, 24 query heads over 2 KV heads of 128, 17 blocks to a row, has 21 tokens to
+// a unit and 77 blocks to a list, 22% of them of use to a row.  It takes 156 us, of
+// which the lists and the join of partial results are some 10; tensor pipe 64%, as in
+// dense attention with such heads.  Four prompts of 8,192 (32 tokens, 25 blocks to a
+// list, 58% of use): 1,150 to 1,190 us, 67%.  Three E4M3 chunks of up to 517 (256-wide
+// heads, 34 blocks): 88 us, 46%, the helpers' codes again.  UNIT_COST 1, 2, 6 and 8
+// for lists: the prompts take 1,281, 1,231, 1,190 and 1,190 us, the E4M3 chunks 91, 89,
+// 91 and 92.  (An entry and its bits are loaded a tile ahead: looked up at the tile they
+// cost the softmax 180 clocks of 3,000.)
+//
 // The accumulator is rescaled only when a row's maximum has grown by more than
 // 2^8 since the one in use: the sum uses the same stale maximum, so the result
 // is the same.  Rounding P to FP16 (2^-11 of each weight, with the smallest ones
@@ -105,7 +119,7 @@ struct PairGeometry {
     static constexpr int ROWS = CH_ROWS, TILE = CH_TILE, UNIT_COST = 4, MIN_SHARE = 4, THREADS = CH_THREADS, WARPS = CH_WARPS,
                          WORKERS = CHUNK_MAX_PAIRS;
 };
-struct BlockPairGeometry : PairGeometry {
+struct BlockPairGeometry : PairGeometry {       // tiles are the blocks of a list
     static constexpr bool BLOCKS = true;
 };
 
@@ -1158,7 +1172,9 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                 // hands the helpers what the output is multiplied by; the other goes on
                 // at once.  (That one waits for the last tile's maximum, which its next
                 // tile would wait for, so the sum before has been read.  With all eight
-                // warps meeting at named barriers a unit's end took 3,400 clocks.)
+                // warps meeting at named barriers a unit's end took them 3,400 clocks; the
+                // calls' times are the same, for the second products wait for the helpers'
+                // reading of the output as long.)
                 const bool ends = ((it - 1) & 1u) == static_cast<uint32_t>(grp);
                 if (!ends && ok) ok = warp_wait(&c.m_out[grp ^ 1][lq], ((it - 1) >> 1) & 1u, abort, lim);
                 const float mlast = c.mrow[(it - 1) & 1u][row], clast = level(mlast);

@@ -26,9 +26,19 @@
 // With the 128-byte swizzle both patterns touch all banks evenly.
 //
 // Bound by the loads: 64 requests' tokens over up to 32,768 tokens take 290 to 299 us
-// from the FP16 cache (6.5 to 6.7 TB/s) and 171 us from the E4M3 cache (6.2 TB/s; its scales
+// from the FP16 cache (6.5 to 6.7 TB/s) and 166 us from the E4M3 cache (6.4 TB/s; its scales
 // are single bytes 2 x hkv apart).  One token over 4,096 takes 14 us: the launch,
 // the search for its work, one memory latency each for table, keys and join.
+//
+// Over selected blocks the tiles are halves of the blocks of a unit's list, or (DIRECT)
+// of one token's selection of up to 32 blocks: then the scheduler warp reads the
+// selection itself, hands out whole (row, KV head) units without a search for work, and
+// while units are few a cluster of CTAs shares each, its sums joined through
+// distributed shared memory: no lists, no workspace, one launch.  16 of 1,440 blocks for
+// one token, 24 query heads over 2 KV heads of 128: 9.3 us (through lists and a join
+// 15.7).  64 tokens: 27 us (42), 5.0 TB/s with its first loads and last sums, 6.7
+// in between.  200 tokens from the E4M3 cache, 256-wide heads: 92 us (125 before the
+// lookups went piece by piece), 400 units in three rounds of 152.
 #pragma once
 #include <cuda.h>
 #include <cuda_fp16.h>
