@@ -71,8 +71,8 @@ struct RowsGeometry {
 struct BlockRowsGeometry : RowsGeometry {
     static constexpr bool BLOCKS = true;
 };
-// Blocks taken straight from the selections: a unit is one token of a row array's
-// row and a KV head, on a cluster of p.split CTAs that share its tiles.
+// Blocks taken straight from the selections: a unit is one row and KV head, on a
+// cluster of p.split CTAs that share its tiles.
 struct DirectRowsGeometry : BlockRowsGeometry {
     static constexpr bool DIRECT = true;
 };

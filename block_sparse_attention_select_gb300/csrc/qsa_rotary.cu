@@ -4,9 +4,10 @@
 // Bound by memory: every value is read and written once.  A thread takes 16 dims
 // of a head as two 16-byte vectors (both halves of eight pairs) and goes through
 // some heads of its token with them, so that it reads its eight cosines and sines
-// once for all of these; ROT_BATCH heads' loads are in flight together.  Four
-// prompts of 4,096 tokens, 40 heads of 128: 55 us with halves paired, 54 us with
-// neighbours (6.2 and 6.4 TB/s; neighbours as two 16-byte accesses 59 us; 4 or 20
+// once for all of these; ROT_BATCH heads' loads are in flight together, the first of
+// them while the rows' positions are looked up.  Four
+// prompts of 4,096 tokens, 40 heads of 128: 54 us with halves paired, 53 us with
+// neighbours (6.3 and 6.4 TB/s; neighbours as two 16-byte accesses 59 us; 4 or 20
 // heads to a thread 57 to 60 us).  The 1,616-row chunk, 26 heads of 256 of which 64
 // dims rotate: 9 us (a thread for every head or two: 11 us), 64 single tokens 4 us,
 // a launch and two memory latencies.
@@ -87,27 +88,62 @@ rotary_kernel(const RotaryParams p)
     __shared__ int32_t pos_s[ROT_ROWS];
     const int t = threadIdx.x;
     wait_prior_grid();
-    if (blockIdx.x == 0) flag_bad_requests(p.seq);
     const int32_t row0 = blockIdx.x * p.cta_rows, n_rows = min(p.cta_rows, p.seq.rows - row0);
+    const int32_t turned = p.rope_dim / 16;                  // items of a head that rotate, then those that are copied
+    const int32_t items = p.items, per_row = items * p.slices, total = n_rows * per_row;
+    const int32_t heads = p.q_heads + p.k_heads;
+    // a thread's work: a row, a piece of each head (as two vectors of dims), every slices-th head
+    int32_t r, slice, item, d0, d1;
+    int64_t row;
+    auto decode = [&](int32_t i) {
+        r = i / per_row;
+        const int32_t in = i - r * per_row;
+        slice = in / items;
+        item = in - slice * items;
+        row = row0 + r;
+        if (item < turned) {
+            d0 = p.first + (NEIGHBOURS ? 16 : 8) * item;
+            d1 = d0 + (NEIGHBOURS ? 8 : p.rope_dim / 2);
+        } else {
+            // vectors outside the rotated part, in order
+            const int32_t v = 2 * (item - turned), skip = p.rope_dim / 8, before = p.first / 8;
+            d0 = 8 * (v < before ? v : v + skip);
+            d1 = 8 * (v + 1 < before ? v + 1 : v + 1 + skip);
+        }
+    };
+    auto in_of = [&](int32_t h) {
+        return h < p.q_heads ? p.q + (row * p.q_stride + static_cast<int64_t>(h) * p.head_dim)
+                             : p.k + (row * p.k_stride + static_cast<int64_t>(h - p.q_heads) * p.head_dim);
+    };
+    auto out_of = [&](int32_t h) {
+        return h < p.q_heads ? p.out_q + (row * p.out_q_stride + static_cast<int64_t>(h) * p.head_dim)
+                             : p.out_k + (row * p.out_k_stride + static_cast<int64_t>(h - p.q_heads) * p.head_dim);
+    };
+    uint4 x[ROT_BATCH], y[ROT_BATCH];
+    auto load = [&](int32_t h0) {
+#pragma unroll
+        for (int k = 0; k < ROT_BATCH; ++k) {
+            const int32_t h = h0 + k * p.slices;
+            if (h >= heads) break;
+            load_two<WIDE>(in_of(h) + d0, in_of(h) + d1, x[k], y[k]);
+        }
+    };
+    // the first values are on their way while the rows' positions are looked up
+    if (t < total) {
+        decode(t);
+        load(slice);
+    }
+    if (blockIdx.x == 0) flag_bad_requests(p.seq);
     Seq s;
     const int32_t b = requests_of_rows(p.seq, row0, n_rows, &s);
     if (t < n_rows) pos_s[t] = b < 0 ? -1 : s.p0 + (row0 + t - s.s0);
     __syncthreads();
 
-    const int32_t turned = p.rope_dim / 16;                  // items of a head that rotate, then those that are copied
-    const int32_t items = p.items, per_row = items * p.slices, total = n_rows * per_row;
-    const int32_t heads = p.q_heads + p.k_heads;
-    for (int32_t i = t; i < total; i += blockDim.x) {
-        const int32_t r = i / per_row, in = i - r * per_row, slice = in / items, item = in - slice * items;
+    for (int32_t i = t; i < total;) {
         const int32_t at = pos_s[r];
-        if (at < 0) continue;
         const bool turn = item < turned;
-        // the item's two vectors, as dims of a head
-        int32_t d0, d1;
         float cs[8], sn[8];
-        if (turn) {
-            d0 = p.first + (NEIGHBOURS ? 16 : 8) * item;
-            d1 = d0 + (NEIGHBOURS ? 8 : p.rope_dim / 2);
+        if (at >= 0 && turn) {
             const float4 *tab = reinterpret_cast<const float4 *>(p.table + static_cast<int64_t>(at) * p.rope_dim + 8 * item);
             const float4 *tbs = reinterpret_cast<const float4 *>(p.table + static_cast<int64_t>(at) * p.rope_dim + p.rope_dim / 2 + 8 * item);
 #pragma unroll
@@ -117,30 +153,10 @@ rotary_kernel(const RotaryParams p)
                 sn[4 * k] = s.x, sn[4 * k + 1] = s.y, sn[4 * k + 2] = s.z, sn[4 * k + 3] = s.w;
             }
         } else {
-            // vectors outside the rotated part, in order
-            const int32_t v = 2 * (item - turned), skip = p.rope_dim / 8, before = p.first / 8;
-            d0 = 8 * (v < before ? v : v + skip);
-            d1 = 8 * (v + 1 < before ? v + 1 : v + 1 + skip);
 #pragma unroll
             for (int k = 0; k < 8; ++k) cs[k] = 1.0f, sn[k] = 0.0f;
         }
-        const int64_t row = row0 + r;
-        auto in_of = [&](int32_t h) {
-            return h < p.q_heads ? p.q + (row * p.q_stride + static_cast<int64_t>(h) * p.head_dim)
-                                 : p.k + (row * p.k_stride + static_cast<int64_t>(h - p.q_heads) * p.head_dim);
-        };
-        auto out_of = [&](int32_t h) {
-            return h < p.q_heads ? p.out_q + (row * p.out_q_stride + static_cast<int64_t>(h) * p.head_dim)
-                                 : p.out_k + (row * p.out_k_stride + static_cast<int64_t>(h - p.q_heads) * p.head_dim);
-        };
-        for (int32_t h0 = slice; h0 < heads; h0 += p.slices * ROT_BATCH) {
-            uint4 x[ROT_BATCH], y[ROT_BATCH];
-#pragma unroll
-            for (int k = 0; k < ROT_BATCH; ++k) {
-                const int32_t h = h0 + k * p.slices;
-                if (h >= heads) break;
-                load_two<WIDE>(in_of(h) + d0, in_of(h) + d1, x[k], y[k]);
-            }
+        for (int32_t h0 = slice; at >= 0 && h0 < heads;) {
 #pragma unroll
             for (int k = 0; k < ROT_BATCH; ++k) {
                 const int32_t h = h0 + k * p.slices;
@@ -149,6 +165,13 @@ rotary_kernel(const RotaryParams p)
                 if (turn) rotate8<NEIGHBOURS>(x[k], y[k], cs, sn);
                 store_two<WIDE>(out_of(h) + d0, out_of(h) + d1, x[k], y[k]);
             }
+            h0 += p.slices * ROT_BATCH;
+            if (h0 < heads) load(h0);
+        }
+        i += blockDim.x;
+        if (i < total) {
+            decode(i);
+            load(slice);
         }
     }
     allow_next_grid();

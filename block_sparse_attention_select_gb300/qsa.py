@@ -11,6 +11,7 @@ not pass them) and streams.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 
@@ -409,7 +410,7 @@ def _row_stride(t, cache: KVCache, heads: int, name: str) -> int:
     shape, stride = t.shape, t.stride()
     if t.dtype is not torch.float16:
         raise TypeError(f"{name} must be {torch.float16}, got {t.dtype}")
-    if t.device != cache.device:
+    if t.get_device() != cache.index:
         raise ValueError(f"{name} must be on the cache's device")
     if len(shape) != 3 or shape[1] != heads or shape[2] != cache.head_dim:
         raise ValueError(f"{name} must be [rows, {heads}, {cache.head_dim}], got {list(shape)}")
@@ -418,17 +419,19 @@ def _row_stride(t, cache: KVCache, heads: int, name: str) -> int:
     return stride[0] if shape[0] > 1 else heads * cache.head_dim
 
 
-def _requests(seq_start, pos_start, cache: KVCache) -> int:
-    """Checks the two arrays that describe a batch; the number of requests."""
-    dev, n = cache.device, pos_start.shape[0] if pos_start.dim() == 1 else -1
-    if not (seq_start.dtype is torch.int32 and pos_start.dtype is torch.int32 and seq_start.shape == (n + 1,)
-            and seq_start.device == dev and pos_start.device == dev and seq_start.is_contiguous()
-            and pos_start.is_contiguous()):
-        _need(seq_start, torch.int32, "seq_start"), _need(pos_start, torch.int32, "pos_start")
-        if seq_start.device != dev or pos_start.device != dev:
-            raise ValueError("seq_start and pos_start must be on the cache's device")
-        raise ValueError("seq_start must be int32 [n + 1] and pos_start int32 [n]")
-    return n
+def _requests(seq_start, pos_start, where) -> int:
+    """Checks the two arrays that describe a batch, on where's device; the number
+    of requests."""
+    index = where.index
+    if (seq_start.dtype is torch.int32 and pos_start.dtype is torch.int32 and seq_start.get_device() == index
+            and pos_start.get_device() == index and seq_start.is_contiguous() and pos_start.is_contiguous()):
+        shape = pos_start.shape
+        if len(shape) == 1 and seq_start.shape == (shape[0] + 1,):
+            return shape[0]
+    _need(seq_start, torch.int32, "seq_start"), _need(pos_start, torch.int32, "pos_start")
+    if seq_start.get_device() != index or pos_start.get_device() != index:
+        raise ValueError(f"seq_start and pos_start must be on {where.device}")
+    raise ValueError("seq_start must be int32 [n + 1] and pos_start int32 [n]")
 
 
 def _call(cache: KVCache, stream, fn, *args, made=()):
@@ -514,14 +517,14 @@ def chunk_attention(q, seq_start, pos_start, cache: KVCache, window: int = 0, sc
     if out is None:
         out = torch.empty((rows, hq, cache.head_dim), dtype=torch.float16, device=cache.device)
         made.append(out)
-    elif out.shape != q.shape or out.device != cache.device:
+    elif out.shape != q.shape or out.get_device() != cache.index:
         raise ValueError("out must have q's shape and device")
     else:
         _need(out, torch.float16, "out")
     if ws is None:
         ws = alloc_chunk_attention_workspace(cache, rows, hq)
         made.append(ws)
-    elif ws.device != cache.device or not ws.is_contiguous():
+    elif ws.get_device() != cache.index or not ws.is_contiguous():
         raise ValueError("ws must be contiguous, on the cache's device")
     scale = cache.head_dim ** -0.5 if scale is None else float(scale)
     _call(cache, stream, load().qsa_chunk_attention, q.data_ptr(), qs, rows, hq, n, seq_start.data_ptr(),
@@ -531,10 +534,15 @@ def chunk_attention(q, seq_start, pos_start, cache: KVCache, window: int = 0, sc
 
 
 class _Device:
-    """Where a call without a cache runs."""
+    """Where a call without a cache runs: the CUDA device with this index."""
 
-    def __init__(self, device):
-        self.device, self.index = device, device.index
+    def __init__(self, index: int):
+        self.index, self.device = index, torch.device("cuda", index)
+
+
+@functools.lru_cache(maxsize=None)
+def _device(index: int) -> _Device:
+    return _Device(index)
 
 
 class Batch:
@@ -580,10 +588,10 @@ def batch_tables(new_len, ctx_len, free_pages, free_count, block_table, page_tok
     or more, max_pages], filled in place.  Requests are served in order until one does
     not fit in batch.rows or the free pages (batch.state).  total_len may be ctx_len
     and free_count batch.state[1:2], so that the next call goes on from this one."""
-    n, dev = batch.n, batch.device
+    n, index = batch.n, batch.index
     for t, name in ((new_len, "new_len"), (ctx_len, "ctx_len"), (free_pages, "free_pages"),
                     (free_count, "free_count"), (block_table, "block_table")):
-        if t.dtype is not torch.int32 or t.device != dev or not t.is_contiguous():
+        if t.dtype is not torch.int32 or t.get_device() != index or not t.is_contiguous():
             _need(t, torch.int32, name)
             raise ValueError(f"{name} must be on the batch's device")
     if new_len.shape != (n,) or ctx_len.shape != (n,) or free_pages.dim() != 1 or free_count.shape != (1,):
@@ -616,25 +624,27 @@ def rotary_table(n_pos: int, rope_dim: int, theta: float = 10000.0, scaling: Rop
     device = torch.empty(0, device=device or "cuda").device
     with torch.cuda.device(device):
         t = torch.empty((int(n_pos), int(rope_dim)), dtype=torch.float32, device=device)
-        _call(_Device(device), stream, load().qsa_rotary_table, t.data_ptr(), int(n_pos), int(rope_dim), float(theta),
+        _call(_device(device.index), stream, load().qsa_rotary_table, t.data_ptr(), int(n_pos), int(rope_dim), float(theta),
               None if scaling is None else ctypes.byref(scaling.c), made=[t])
     return t
 
 
-def _head_rows(t, rows: int, dim: int, device, name: str):
-    """Checks an FP16 row array [rows, heads, head_dim] and returns its row stride and
-    heads: rows may be slices of wider ones, a row itself is contiguous."""
-    shape, stride = t.shape, t.stride()
+def _head_rows(t, rows: int, dim: int, index: int, name: str):
+    """Checks an FP16 row array [rows, heads, head_dim] on device `index` and returns
+    its heads and row stride: rows may be slices of wider ones, a row itself is
+    contiguous."""
     if t.dtype is not torch.float16:
         raise TypeError(f"{name} must be {torch.float16}, got {t.dtype}")
-    if t.device != device:
+    if t.get_device() != index:
         raise ValueError(f"{name} must be on q's device")
+    shape = t.shape
     if len(shape) != 3 or shape[0] != rows or shape[2] != dim:
         raise ValueError(f"{name} must be [{rows}, heads, {dim}], got {list(shape)}")
     heads = shape[1]
+    stride = t.stride()
     if stride[2] != 1 or (stride[1] != dim and heads > 1):
         raise ValueError(f"each row of {name} must be contiguous")
-    return stride[0] if rows > 1 else heads * dim, heads
+    return heads, stride[0] if rows > 1 else heads * dim
 
 
 def rotary(q, k, seq_start, pos_start, table, first: int = 0, interleaved: bool = False, out_q=None, out_k=None,
@@ -644,30 +654,30 @@ def rotary(q, k, seq_start, pos_start, table, first: int = 0, interleaved: bool 
     positions and copy the others.  Pairs are (j, j + half), or neighbours
     (interleaved).  out_q may be q and out_k k, in place; rows past the last
     request are left as they are.  Returns (out_q, out_k)."""
-    device = q.device
-    if q.dim() != 3 or table.dim() != 2 or table.dtype is not torch.float32 or not table.is_contiguous():
-        raise ValueError("q must be [rows, heads, head_dim], table contiguous float32 [positions, rope_dim]")
-    if not q.is_cuda or table.device != device:
-        raise ValueError("q and table must be on one CUDA device")
-    where = _Device(device)
+    index = q.get_device()
+    if index < 0 or q.dim() != 3:
+        raise ValueError("q must be a CUDA tensor [rows, heads, head_dim]")
+    if table.dtype is not torch.float32 or table.get_device() != index or table.dim() != 2 or not table.is_contiguous():
+        raise ValueError("table must be contiguous float32 [positions, rope_dim] on q's device")
+    where = _device(index)
     n = _requests(seq_start, pos_start, where)
     rows, hq, dim = q.shape
     made = ()
     if out_q is None:
-        out_q = torch.empty(q.shape, dtype=torch.float16, device=device)
+        out_q = torch.empty(q.shape, dtype=torch.float16, device=where.device)
         made += (out_q,)
-    qs, _ = _head_rows(q, rows, dim, device, "q")
-    oqs, ohq = (qs, hq) if out_q is q else _head_rows(out_q, rows, dim, device, "out_q")
+    _, qs = _head_rows(q, rows, dim, index, "q")
+    ohq, oqs = (hq, qs) if out_q is q else _head_rows(out_q, rows, dim, index, "out_q")
     if k is None:
         if out_k is not None:
             raise ValueError("out_k goes with k")
         kp = ks = hk = okp = oks = ohk = 0
     else:
         if out_k is None:
-            out_k = torch.empty(k.shape, dtype=torch.float16, device=device)
+            out_k = torch.empty(k.shape, dtype=torch.float16, device=where.device)
             made += (out_k,)
-        ks, hk = _head_rows(k, rows, dim, device, "k")
-        oks, ohk = (ks, hk) if out_k is k else _head_rows(out_k, rows, dim, device, "out_k")
+        hk, ks = _head_rows(k, rows, dim, index, "k")
+        ohk, oks = (hk, ks) if out_k is k else _head_rows(out_k, rows, dim, index, "out_k")
         kp, okp = k.data_ptr(), out_k.data_ptr()
     if ohq != hq or ohk != hk:
         raise ValueError("out_q and out_k must have q's and k's shapes")
@@ -701,7 +711,7 @@ def block_attention(q, sel, seq_start, pos_start, cache: KVCache, recent: int = 
     hq = q.shape[1] if q.dim() == 3 else 0
     qs = _row_stride(q, cache, hq, "q")
     rows = q.shape[0]
-    if sel.dtype is not torch.int32 or sel.device != cache.device or not sel.is_contiguous():
+    if sel.dtype is not torch.int32 or sel.get_device() != cache.index or not sel.is_contiguous():
         _need(sel, torch.int32, "sel")
         raise ValueError("sel must be on the cache's device")
     if sel.dim() != 3 or sel.shape[0] != rows or sel.shape[1] != cache.hkv:
@@ -711,14 +721,14 @@ def block_attention(q, sel, seq_start, pos_start, cache: KVCache, recent: int = 
     if out is None:
         out = torch.empty((rows, hq, cache.head_dim), dtype=torch.float16, device=cache.device)
         made.append(out)
-    elif out.shape != q.shape or out.device != cache.device:
+    elif out.shape != q.shape or out.get_device() != cache.index:
         raise ValueError("out must have q's shape and device")
     else:
         _need(out, torch.float16, "out")
     if ws is None:
         ws = alloc_block_attention_workspace(cache, rows, hq, k, recent)
         made.append(ws)
-    elif ws.device != cache.device or not ws.is_contiguous():
+    elif ws.get_device() != cache.index or not ws.is_contiguous():
         raise ValueError("ws must be contiguous, on the cache's device")
     scale = cache.head_dim ** -0.5 if scale is None else float(scale)
     _call(cache, stream, load().qsa_block_attention, q.data_ptr(), qs, rows, hq, n, seq_start.data_ptr(),

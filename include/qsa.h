@@ -370,7 +370,7 @@ qsa_status qsa_rotary_table(float *table, int32_t n_pos, int32_t rope_dim, doubl
 /* qsa_rotary: rotates dims first .. first + rope_dim - 1 of every head of q and k
  * and copies the others.  layout QSA_ROPE_HALVES pairs (j, j + rope_dim / 2) of
  * them, QSA_ROPE_NEIGHBOURS (2 j, 2 j + 1).  A batch is described as for
- * qsa_index_key_produce; rows of no request are neither read nor written.  q, k,
+ * qsa_index_key_produce; outputs of rows of no request are left as they are.  q, k,
  * out_q, out_k: FP16, row r at q + r * q_stride elements, heads * head_dim
  * contiguous values, 16-byte aligned, strides multiples of 8.  out_q may be q (with
  * the same stride: in place), out_k may be k; beyond that outputs and inputs must
