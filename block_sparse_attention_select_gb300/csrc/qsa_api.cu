@@ -950,6 +950,21 @@ bool few_rows(int32_t rows, int32_t group, int32_t n_reqs)
     return static_cast<int64_t>(rows) * group <= int64_t{16} * n_reqs;
 }
 
+// The same for attention over blocks, where each row (or 16 pairs) has a list of its
+// own in the first kernel and 256 pairs share one in the second: the first up to 24
+// pairs per request, from the E4M3 cache 32.  64 requests over 16,384 tokens each, 16
+// blocks to a row, 2 KV heads, us of the first and second:
+//   pairs per request (tokens x heads)   2 x 12    8 x 4     4 x 12    8 x 12
+//   FP16, 128-wide                       43, 53    73, 69    80, 61   136, 74
+//   FP16, 256-wide                       83, 83   153, 113  136, 99   215, 120
+//   E4M3, 128-wide                       45, 74    86, 101   80, 87   134, 104
+//   E4M3, 256-wide                       63, 87    99, 119  114, 104  196, 125
+// The first takes whole tokens, so no more than 16 query heads to a KV head.
+bool few_block_rows(int32_t rows, int32_t group, int32_t n_reqs, bool e4m3)
+{
+    return group <= 16 && static_cast<int64_t>(rows) * group <= int64_t{e4m3 ? 32 : 24} * n_reqs;
+}
+
 // A row array of `width` contiguous FP16 values per row.
 bool row_array_ok(const void *p, int64_t stride, int64_t width)
 {
@@ -1258,8 +1273,7 @@ qsa_status qsa_block_attention(const void *q, int64_t q_stride, int32_t rows, in
     p.sel = sel;
     p.k = k;
     p.recent = recent;
-    // (units of whole tokens, so no more than 16 query heads to a KV head)
-    const bool few = p.c.group <= 16 && few_rows(rows, p.c.group, n_reqs);
+    const bool few = few_block_rows(rows, p.c.group, n_reqs, p.c.kv.e4m3);
     CUtensorMap tk, tv;
     if ((st = make_tmaps(&tk, &tv, cache, few)) != QSA_OK) return st;
     int launches = 0;

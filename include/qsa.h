@@ -399,10 +399,10 @@ qsa_status qsa_rotary(const void *q, int64_t q_stride, int32_t q_heads, void *ou
  * p / 128 is ignored and reported by qsa_get_device_status().  q, out, scale, the
  * batch, the cache and the workspace are as for qsa_chunk_attention (where falling
  * starts make two requests claim a row, the results of both are undefined); cache
- * slots that no row attends may hold anything.  A batch of which requests have 16
- * (row, query head of a KV head) pairs or fewer on average, with up to 32 blocks a
- * row, takes the least time; many single tokens and a long chunk take less in two
- * calls.  0 <= k <= QSA_MAX_K, 0 <= recent <=
+ * slots that no row attends may hold anything.  One of two kernels serves the whole
+ * batch, by its average of rows * (hq / hkv) / n_reqs (up to 24, or 32 from the E4M3
+ * cache: the one for few rows, quickest with up to 32 blocks a row), so many single
+ * tokens and a long chunk take less time in two calls.  0 <= k <= QSA_MAX_K, 0 <= recent <=
  * QSA_MAX_K, hq / hkv <= 128, max_pages * page_tokens <= 2^25
  * (QSA_ERR_UNSUPPORTED otherwise).  ws: qsa_block_attention_workspace_bytes(...)
  * bytes, with row_capacity = max_pages * page_tokens of the cache. */
