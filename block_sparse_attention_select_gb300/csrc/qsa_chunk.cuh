@@ -185,19 +185,22 @@ struct FindScratch {
 
 // Finds worker `me`'s share of the line (of `n_workers`), by the whole CTA.  Each
 // thread counts the units of a run of requests, then adds up the lengths of an
-// equal run of units.
-template <typename G>
+// equal run of units.  `lengths` is called before the first length is needed (lists
+// of blocks: the kernel that makes them may still run until then; the requests are
+// the caller's).
+template <typename G, typename F>
 __device__ __forceinline__ void find_work(const ChunkParams &p, Share &c, FindScratch<G> &s, int32_t me,
-                                          int32_t n_workers, int warp, int lane)
+                                          int32_t n_workers, int warp, int lane, F &&lengths)
 {
     const int t = threadIdx.x;
     int32_t *prefix = s.prefix;
     const int32_t run = (p.kv.n_reqs + G::THREADS - 1) / G::THREADS;
     const int32_t r0 = min(t * run, p.kv.n_reqs), r1 = min(r0 + run, p.kv.n_reqs);
+    bool bad;
+    auto seq = [&](int32_t b) { return G::BLOCKS ? seq_of_early(p.kv, b, &bad) : seq_of(p.kv, b, &bad); };
     int64_t mine = 0, all;
     for (int32_t b = r0; b < r1; ++b) {
-        bool bad;
-        mine += units_of<G>(p, seq_of(p.kv, b, &bad));
+        mine += units_of<G>(p, seq(b));
         if (bad && blockIdx.x == 0) record_error(p.kv.status, ST_BAD_ROW);
     }
     const int64_t before = block_scan<G>(mine, s.units, warp, lane, &all);
@@ -219,17 +222,19 @@ __device__ __forceinline__ void find_work(const ChunkParams &p, Share &c, FindSc
             if (lo + step < G::THREADS && prefix[lo + step] <= u0) lo += step;
         b0 = lo * run;
         m0 = u0 - prefix[lo];
-        bool bad;
-        s0 = seq_of(p.kv, b0, &bad);
+        s0 = seq(b0);
         for (int32_t n = units_of<G>(p, s0); m0 >= n; n = units_of<G>(p, s0)) {
             m0 -= n;
-            s0 = seq_of(p.kv, ++b0, &bad);
+            s0 = seq(++b0);
         }
+    }
+    lengths();
+    if (u0 < u1) {
         int32_t b = b0, m = m0;
         Seq sb = s0;
         for (int32_t u = u0; u < u1; ++u, ++m) {
             while (m >= units_of<G>(p, sb)) {
-                sb = seq_of(p.kv, ++b, &bad);
+                sb = seq(++b);
                 m = 0;
             }
             const Unit un = unit_of<G>(p, sb, m);
@@ -260,8 +265,7 @@ __device__ __forceinline__ void find_work(const ChunkParams &p, Share &c, FindSc
     if (w0 < w1 && at <= w0 && w0 < at + cost) {
         for (;; ++m0) {
             while (m0 >= units_of<G>(p, s0)) {
-                bool bad;
-                s0 = seq_of(p.kv, ++b0, &bad);
+                s0 = seq(++b0);
                 m0 = 0;
             }
             const Unit un = unit_of<G>(p, s0, m0);
@@ -508,16 +512,64 @@ chunk_join_kernel(const ChunkParams p)
     __shared__ float part_sum[JOIN_WARPS][D];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     wait_prior_grid();
-    const Split sp = reinterpret_cast<const Split *>(p.ws)[blockIdx.x];
-    const int32_t n = sp.parts;
-    if (n == 0) return;
     const float cs = G::RAW_MAX ? p.scale * LOG2_E : 1.0f;
     const float2 *ml = reinterpret_cast<const float2 *>(p.ws + WS_ML);
     const float *po = reinterpret_cast<const float *>(p.ws + ws_o<G::ROWS, G::WORKERS>());
     auto place = [&](int32_t i) { return 2 * (static_cast<int64_t>(blockIdx.x) + i) + (i == 0 ? 1 : 0); };
+    auto write = [&](const Split &sp, int32_t row, const float4 (&acc)[N / 4], float inv) {
+        const int32_t v = sp.v0 + row, tok = by_group(p, v), h = v - tok * p.group;
+        __half *out = static_cast<__half *>(p.out) +
+                      ((static_cast<int64_t>(sp.s0) + tok) * p.hq + sp.g * p.group + h) * D;
+#pragma unroll
+        for (int e = 0; e < N / 4; ++e) {
+            reinterpret_cast<uint2 *>(out)[32 * e + lane] =
+                make_uint2(to_half2(acc[e].x * inv, acc[e].y * inv), to_half2(acc[e].z * inv, acc[e].w * inv));
+        }
+    };
+    // Most units of the pair kernel that are cut have two parts: the warp's first row of
+    // those is loaded beside the Split that says so (one memory latency, not three; the
+    // 1,616-row chunk over blocks 156 -> 150 us, with the CTAs set up earlier).
+    const int32_t row0 = blockIdx.y * JOIN_WARPS + warp;
+    const bool ahead = !G::RAW_MAX && row0 < p.ws_rows && blockIdx.x + 1 < G::WORKERS;
+    float2 ml2[2];
+    float4 x2[2][N / 4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        ml2[i] = ahead ? ml[place(i) * G::ROWS + row0] : make_float2(-INFINITY, 0.0f);
+#pragma unroll
+        for (int e = 0; e < N / 4; ++e)
+            x2[i][e] = ahead ? (reinterpret_cast<const float4 *>(po + (place(i) * p.ws_rows + row0) * D) + lane)[32 * e]
+                             : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    }
+    const Split sp = reinterpret_cast<const Split *>(p.ws)[blockIdx.x];
+    const int32_t n = sp.parts;
+    if (n == 0) return;
+    const bool two = n == 2 && ahead;
+    if (two && row0 < sp.rows) {
+        // (the sums and their order are those below)
+        const float mx = fmaxf(ml2[0].x, ml2[1].x);
+        float4 acc[N / 4];
+        float sum[2];
+#pragma unroll
+        for (int e = 0; e < N / 4; ++e) acc[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float f = ml2[i].x == -INFINITY ? 0.0f : exp2_approx((ml2[i].x - mx) * cs);
+            sum[i] = __fmul_rn(ml2[i].y, f);
+#pragma unroll
+            for (int e = 0; e < N / 4; ++e) {
+                acc[e].x = fmaf(x2[i][e].x, f, acc[e].x);
+                acc[e].y = fmaf(x2[i][e].y, f, acc[e].y);
+                acc[e].z = fmaf(x2[i][e].z, f, acc[e].z);
+                acc[e].w = fmaf(x2[i][e].w, f, acc[e].w);
+            }
+        }
+        const float s = __fadd_rn(sum[0], sum[1]);
+        write(sp, row0, acc, s > 0.0f ? 1.0f / s : 0.0f);
+    }
     const bool shared_row = n > JOIN_PARTS && sp.rows <= static_cast<int32_t>(gridDim.y);
     const int32_t step = shared_row ? gridDim.y : JOIN_WARPS * gridDim.y;
-    for (int32_t row = shared_row ? blockIdx.y : blockIdx.y * JOIN_WARPS + warp; row < sp.rows; row += step) {
+    for (int32_t row = shared_row ? blockIdx.y : two ? row0 + step : row0; row < sp.rows; row += step) {
         float mx = -INFINITY, sum = 0.0f;
         for (int32_t i = lane; i < n; i += 32) mx = fmaxf(mx, ml[place(i) * G::ROWS + row].x);
 #pragma unroll
@@ -568,15 +620,7 @@ chunk_join_kernel(const ChunkParams p)
             __syncthreads();
             if (warp != 0) continue;
         }
-        const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-        const int32_t v = sp.v0 + row, tok = by_group(p, v), h = v - tok * p.group;
-        __half *out = static_cast<__half *>(p.out) +
-                      ((static_cast<int64_t>(sp.s0) + tok) * p.hq + sp.g * p.group + h) * D;
-#pragma unroll
-        for (int e = 0; e < N / 4; ++e) {
-            reinterpret_cast<uint2 *>(out)[32 * e + lane] =
-                make_uint2(to_half2(acc[e].x * inv, acc[e].y * inv), to_half2(acc[e].z * inv, acc[e].w * inv));
-        }
+        write(sp, row, acc, sum > 0.0f ? 1.0f / sum : 0.0f);
     }
 }
 

@@ -71,11 +71,11 @@
 // weights of zero; a warp none of whose rows does leaves its scores where they are.
 // So the products are those of the units' lists: the 1,616-row chunk over 184,320
 // tokens, 24 query heads over 2 KV heads of 128, 17 blocks to a row, has 21 tokens to
-// a unit and 77 blocks to a list, 22% of them of use to a row.  It takes 156 us, of
-// which the lists and the join of partial results are some 10; tensor pipe 64%, as in
+// a unit and 77 blocks to a list, 22% of them of use to a row.  It takes 150 us, of
+// which the lists and the join of partial results are some 8; tensor pipe 64%, as in
 // dense attention with such heads.  Four prompts of 8,192 (32 tokens, 25 blocks to a
-// list, 58% of use): 1,150 to 1,190 us, 67%.  Three E4M3 chunks of up to 517 (256-wide
-// heads, 34 blocks): 88 us, 46%, the helpers' codes again.  UNIT_COST 1, 2, 6 and 8
+// list, 58% of use): 1,145 to 1,190 us, 67%.  Three E4M3 chunks of up to 517 (256-wide
+// heads, 34 blocks): 86 us, 46%, the helpers' codes again.  UNIT_COST 1, 2, 6 and 8
 // for lists: the prompts take 1,281, 1,231, 1,190 and 1,190 us, the E4M3 chunks 91, 89,
 // 91 and 92.  (An entry and its bits are loaded a tile ahead: looked up at the tile they
 // cost the softmax 180 clocks of 3,000.)
@@ -497,10 +497,13 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
-    wait_prior_grid();
+    if (!G::BLOCKS) wait_prior_grid();
+    allow_next_grid();                                       // the join's CTAs wait on the device
     // (the queries' place is free until the segments are known)
     static_assert(sizeof(FindScratch<G>) <= Sh::QB, "scratch");
-    find_work<G>(p, c.share, *reinterpret_cast<FindScratch<G> *>(q_s), blockIdx.x >> 1, gridDim.x >> 1, warp, lane);
+    find_work<G>(p, c.share, *reinterpret_cast<FindScratch<G> *>(q_s), blockIdx.x >> 1, gridDim.x >> 1, warp, lane, [&]() {
+        if (G::BLOCKS) wait_prior_grid();
+    });
     tc_fence_before();
     __syncthreads();
     cluster_sync();                                          // the pair's barriers and TMEM are ready
@@ -1273,7 +1276,6 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
     if (t == 0 && c.abort) record_error(p.kv.status, ST_TIMEOUT);
     if (warp == CH_MMA)
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
-    allow_next_grid();
 }
 
 constexpr size_t CH_SMEM = RING + sizeof(Ctrl);

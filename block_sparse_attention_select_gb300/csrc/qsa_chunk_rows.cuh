@@ -340,14 +340,16 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
         c.abort = 0;
         fence_barrier_init();
     }
-    wait_prior_grid();
+    if (!G::BLOCKS || G::DIRECT) wait_prior_grid();
     // (the sums' place is free until a segment's end)
     static_assert(sizeof(FindScratch<G>) <= Sh::SUM, "scratch");
     if constexpr (G::DIRECT) {
         if (blockIdx.x == 0) flag_bad_requests(p.kv);
         __syncthreads();
     } else {
-        find_work<G>(p, c.share, *reinterpret_cast<FindScratch<G> *>(sum), blockIdx.x, gridDim.x, warp, lane);
+        find_work<G>(p, c.share, *reinterpret_cast<FindScratch<G> *>(sum), blockIdx.x, gridDim.x, warp, lane, [&]() {
+            if (G::BLOCKS) wait_prior_grid();
+        });
     }
     uint32_t segs = 0;
     Seg w;

@@ -30,6 +30,13 @@ __device__ __forceinline__ Seq seq_of(const KvParams &p, int32_t b, bool *bad)
     return seq_from(p, __ldg(p.seq_start + b), __ldg(p.seq_start + b + 1), __ldg(p.pos_start + b), bad);
 }
 
+// The same past the L1 cache, for a kernel that looks before it has waited for the
+// kernel before it (which read them, too: they are older than both).
+__device__ __forceinline__ Seq seq_of_early(const KvParams &p, int32_t b, bool *bad)
+{
+    return seq_from(p, __ldcg(p.seq_start + b), __ldcg(p.seq_start + b + 1), __ldcg(p.pos_start + b), bad);
+}
+
 // Whether a request has the row.  (n > 0 first: a skipped request's start may be any
 // number, and the difference wrap.)
 __device__ __forceinline__ bool has_row(const Seq &s, int32_t row) { return s.n > 0 && row >= s.s0 && row - s.s0 < s.n; }
