@@ -59,7 +59,7 @@
 // 377 us (424), 1,460 TF/s; tensor pipe 69%, issue slots 48%).  From the E4M3 cache
 // the turning of codes into FP16 tiles, anew for each unit of 256 pairs (three
 // chunks of up to 517 over up to 12,345 tokens: 151 us (156), 1,290 TF/s, tensor pipe
-// 59%).  Two chunks of up to 1,023 tokens with a window of 1,000 take 40 us (43) where
+// 59%).  Two chunks of up to 1,023 tokens with a window of 1,000 take 38 us (43) where
 // their products need 9: the search for the work, the first loads and the last
 // output are a third of it, the rest has not been taken apart.
 //
@@ -498,7 +498,11 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
     if (!G::BLOCKS) wait_prior_grid();
-    allow_next_grid();                                       // the join's CTAs wait on the device
+    // The join's CTAs wait on the device: the windowed chunk 41 -> 38 us.  From the E4M3
+    // cache that hides nothing, and this instruction's place moves the turning of codes:
+    // with it, without it, dense 128-wide prompts 627 and 614 us, 256-wide chunks 154 and
+    // 152; lists, 256-wide chunks 87.5 and 86.2, 128-wide prompts 2,166 and 2,257.
+    if (!Q8 || (G::BLOCKS && D == 128)) allow_next_grid();
     // (the queries' place is free until the segments are known)
     static_assert(sizeof(FindScratch<G>) <= Sh::QB, "scratch");
     find_work<G>(p, c.share, *reinterpret_cast<FindScratch<G> *>(q_s), blockIdx.x >> 1, gridDim.x >> 1, warp, lane, [&]() {
