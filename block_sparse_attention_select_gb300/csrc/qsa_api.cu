@@ -1105,6 +1105,8 @@ qsa_status qsa_batch_tables(const int32_t *new_len, const int32_t *ctx_len, int3
     if (n_reqs < 0 || rows < 0 || max_pages < 1 || free_capacity < 0 || !batch) return QSA_ERR_INVALID_ARG;
     if (page_tokens < 8 || page_tokens > 256 || (page_tokens & (page_tokens - 1)) != 0) return QSA_ERR_UNSUPPORTED;
     if (static_cast<int64_t>(max_pages) * page_tokens >= INT32_MAX || n_reqs > 65535) return QSA_ERR_UNSUPPORTED;
+    // (the kernel's sums stop at 2^31 - 1, past both)
+    if (rows > TABLES_MAX || free_capacity > TABLES_MAX) return QSA_ERR_UNSUPPORTED;
     if (n_reqs > 0 && (!new_len || !ctx_len || !block_table || !batch->pos_start)) return QSA_ERR_INVALID_ARG;
     if (!batch->seq_start || !batch->state || !free_count || (free_capacity > 0 && !free_pages)) return QSA_ERR_INVALID_ARG;
     for (const void *p : {static_cast<const void *>(new_len), static_cast<const void *>(ctx_len),

@@ -232,6 +232,8 @@ struct RotaryAngles {
     double amplitude;
 };
 
+constexpr int32_t TABLES_MAX = 1 << 30;      // rows, and pages of the free list, at most
+
 // Tables of a batch from its requests' lengths: see qsa_tables.cu.
 struct TablesParams {
     const int32_t *new_len, *ctx_len, *free_pages, *free_count;

@@ -321,8 +321,8 @@ qsa_status qsa_chunk_attention(const void *q, int64_t q_stride, int32_t rows, in
  *   row_req, row_token, row_visible, slot [rows] (each NULL if not wanted): a row's
  *     request, its token's position t, (t + 1) / 4 (its visible compressed
  *     positions), its place page * page_tokens + t % page_tokens in the cache;
- *     rows behind the last request: the last row's request (0
-     if there is none), so that padding names a request with tokens, 0, 0 and -1;
+ *     rows behind the last request: the last row's request (0 if there is none), so
+ *     that padding names a request with tokens, 0, 0 and -1;
  *   state [3]: rows in use, free pages left, number of the first request that did
  *     not fit (n_reqs: none).  free_count may be state + 1.
  * No other two arrays may overlap.  A request with a negative length, or more
@@ -330,8 +330,8 @@ qsa_status qsa_chunk_attention(const void *q, int64_t q_stride, int32_t rows, in
  * is reported by qsa_get_device_status(), as is a free_count outside 0 ..
  * free_capacity (taken as the nearer of the two), and a page of the table that is
  * negative or whose places pass 2^31 - 1 (slot -1).  page_tokens a power of two in
- * [8, 256], max_pages * page_tokens below 2^31 - 1, n_reqs <= 65,535
- * (QSA_ERR_UNSUPPORTED otherwise). */
+ * [8, 256], max_pages * page_tokens below 2^31 - 1, n_reqs <= 65,535, rows and
+ * free_capacity <= 2^30 (QSA_ERR_UNSUPPORTED otherwise). */
 typedef struct {
     int32_t *seq_start, *pos_start, *total_len;
     int32_t *row_req, *row_token, *row_visible, *slot;

@@ -43,6 +43,14 @@ def test_tables(lib):
     assert _tables(lib, cap=0, free=None) == GO and _tables(lib, n=65535) == GO
 
 
+def test_tables_whose_sums_would_pass_31_bits(lib):
+    """Sums of rows and pages stop at 2^31 - 1, which has to lie past every limit, and
+    rows are stored in fours from a multiple of 4."""
+    for kw in (dict(rows=2 ** 31 - 1), dict(rows=2 ** 30 + 1), dict(cap=2 ** 31 - 1), dict(cap=2 ** 30 + 1)):
+        assert _tables(lib, **kw) == UNSUP, kw
+    assert _tables(lib, rows=2 ** 30) == GO and _tables(lib, cap=2 ** 30) == GO
+
+
 def _table(lib, kind=None, n=10, dim=64, theta=1e4, ptr=16, **kw):
     a = dict(factor=2.0, original=4096.0, fast=32.0, slow=1.0, amplitude=1.0)
     a.update(kw)
