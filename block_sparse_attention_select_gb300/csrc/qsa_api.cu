@@ -1173,6 +1173,7 @@ qsa_status qsa_rotary_table(float *table, int32_t n_pos, int32_t rope_dim, doubl
             const double g = std::min(1.0, std::max(0.0, (turns - scaling->slow) / (scaling->fast - scaling->slow)));
             f *= g + (1.0 - g) / scaling->factor;
         }
+        if (!std::isfinite(f * n_pos)) return QSA_ERR_INVALID_ARG;     // (sine and cosine would be NaN)
         a.f[j] = f;
     }
     if (n_pos == 0) return QSA_OK;

@@ -72,6 +72,13 @@ def test_rotary_table(lib):
     assert _table(lib, n=0) == qsa.QSA_OK and _table(lib, 1, original=0.0) == GO and _table(lib, dim=256) == GO
 
 
+def test_rotary_table_of_infinite_angles(lib):
+    for kw in (dict(theta=1e-320, dim=256, n=2 ** 20), dict(kind=1, factor=1e-308, n=100), dict(kind=3, factor=1e-308, n=10000),
+               dict(kind=2, theta=1e-300, factor=1e-20)):
+        assert _table(lib, **kw) == BAD, kw
+    assert _table(lib, theta=1e-3) == GO and _table(lib, 1, factor=1e-30) == GO
+
+
 def _rotary(lib, **kw):
     a = dict(q=16, qs=24 * 256, hq=24, oq=32, oqs=24 * 256, k=16, ks=512, hk=2, ok=32, oks=512, rows=4, D=256, first=0,
              dim=64, layout=0, n=2, ss=16, ps=16, tab=16, n_pos=100)
