@@ -107,7 +107,7 @@ constexpr int CH_ROLES = 15;                 // warps that read the segments: al
 constexpr int CH_HELPERS = 4;
 constexpr int CH_WARPS = CH_HELP + CH_HELPERS;
 constexpr int CH_THREADS = 32 * CH_WARPS;
-constexpr int RAWS = 4;                      // slots of loaded codes (E4M3)
+constexpr int MAX_RAWS = 4;                  // slots of loaded codes at most (E4M3)
 constexpr int MAX_SLOTS = 10;                // slots of the ring at most
 constexpr uint32_t RING = 229376;            // bytes for Q and the ring
 constexpr uint32_t TM_S = 0, TM_O = 256;     // TMEM columns: two S buffers of 128, O
@@ -115,12 +115,17 @@ constexpr int BAR_PAIR = 1, BAR_HELP = 5;    // named barriers: four softmax war
 
 struct PairGeometry {
     static constexpr bool BLOCKS = false;
+    static constexpr int RAWS = 4;           // slots of loaded codes (E4M3)
     static constexpr bool RAW_MAX = false;   // the parts' maxima: powers of two, or scores before the scale
     static constexpr int ROWS = CH_ROWS, TILE = CH_TILE, UNIT_COST = 4, MIN_SHARE = 4, THREADS = CH_THREADS, WARPS = CH_WARPS,
                          WORKERS = CHUNK_MAX_PAIRS;
 };
 struct BlockPairGeometry : PairGeometry {       // tiles are the blocks of a list
     static constexpr bool BLOCKS = true;
+    // As measured, the reason has not been found: 128-wide prompts with 4, 3 and 2 slots,
+    // lists (4 of 8,192) 2,168, 2,086 and 2,181 us, dense (4 of 4,096) 613, 619 and 657;
+    // 256-wide heads differ by 1%.
+    static constexpr int RAWS = 3;
 };
 
 template <int D, bool Q8>
@@ -130,7 +135,7 @@ struct Shape {
     // a CTA's half of a K tile: 64 tokens, or of a V tile: D / 2 dims of 128 tokens
     static constexpr uint32_t SLOT = 128 * D, RAW = SLOT / 2;
     static constexpr int KTOK = 64, VTOK = CH_TILE;
-    static constexpr int FIT = (RING - QBUFS * QB - (Q8 ? RAWS * RAW : 0)) / SLOT, NS = FIT < MAX_SLOTS ? FIT : MAX_SLOTS;
+    static constexpr int FIT = (RING - QBUFS * QB - (Q8 ? MAX_RAWS * RAW : 0)) / SLOT, NS = FIT < MAX_SLOTS ? FIT : MAX_SLOTS;
     static constexpr bool OWN_P = D == 128;                            // P beside S, not over it
     // With two issuing warps, keys and values have rings of their own, so that
     // each warp waits for every phase of its slots in turn.
@@ -163,7 +168,7 @@ struct RingPos {
 
 struct Ctrl {
     SegRing segs;
-    uint64_t full[MAX_SLOTS], empty[MAX_SLOTS], raw_full[RAWS], raw_empty[RAWS], bnd[8];
+    uint64_t full[MAX_SLOTS], empty[MAX_SLOTS], raw_full[MAX_RAWS], raw_empty[MAX_RAWS], bnd[8];
     uint64_t s_full[2], s_free[2], p_full[2][2], o_done[2], m_out[2][4], q_full[2], q_free[2], drain[2];
     uint64_t o_last, o_free, f_full, f_free, l_out[4];
     alignas(8) float mrow[2][CH_HALF];       // [tile parity][row]: maximum in use at the group's last tile; E4M3: sums at a segment's end
@@ -463,7 +468,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
             mbar_init(&c.full[i], Q8 ? 2 * CH_HELPERS : 2);
             mbar_init(&c.empty[i], 1);
         }
-        for (int i = 0; i < RAWS; ++i) {
+        for (int i = 0; i < G::RAWS; ++i) {
             mbar_init(&c.raw_full[i], 1);
             mbar_init(&c.raw_empty[i], CH_HELPERS);
         }
@@ -633,7 +638,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                 if (Q8) {
                     used |= 1u << rslot;
                     last = (last & ~(1u << rslot)) | (rphase << rslot);
-                    if (++rslot == RAWS) {
+                    if (++rslot == G::RAWS) {
                         rslot = 0;
                         rphase ^= 1u;
                     }
@@ -650,7 +655,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
         }
         // codes still in flight, whoever gave up (otherwise the helpers waited for them)
         if (Q8 && lane == 0)
-            for (int i = 0; i < RAWS; ++i)
+            for (int i = 0; i < G::RAWS; ++i)
                 if (used & (1u << i)) mbar_wait_bounded(&c.raw_full[i], (last >> i) & 1u, drain_limit(lim));
         __syncwarp();
     } else if (warp == CH_SCHED) {
@@ -956,7 +961,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUt
                     }
                     par ^= 1u;
                     pos.next(V);
-                    if (++rslot == RAWS) {
+                    if (++rslot == G::RAWS) {
                         rslot = 0;
                         rphase ^= 1u;
                     }

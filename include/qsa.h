@@ -400,7 +400,8 @@ qsa_status qsa_rotary(const void *q, int64_t q_stride, int32_t q_heads, void *ou
  * p / 128 is ignored and reported by qsa_get_device_status().  q, out, scale, the
  * batch, the cache and the workspace are as for qsa_chunk_attention (where falling
  * starts make two requests claim a row, the results of both are undefined); cache
- * slots that no row attends may hold anything.  One of two kernels serves the whole
+ * slots that no row attends may hold anything, keys and values that some row attends
+ * must be finite FP16 numbers.  One of two kernels serves the whole
  * batch, by its average of rows * (hq / hkv) / n_reqs (up to 24, or 32 from the E4M3
  * cache: the one for few rows, quickest with up to 32 blocks a row), so many single
  * tokens and a long chunk take less time in two calls.  0 <= k <= QSA_MAX_K, 0 <= recent <=
