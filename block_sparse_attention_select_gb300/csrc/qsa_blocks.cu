@@ -220,7 +220,7 @@ int launch_blocks(const BlocksParams &in, bool few_rows, const void *tk, const v
     c.ws_rows = few_rows ? chunk_rows_part_rows(kv.rows, c.group) : chunk_part_rows(kv.rows, c.group);
 
     const size_t smem = size_t{8} * l.map_words;
-    if (smem > 48 * 1024) {
+    if (smem > 40 * 1024) {                      // (with the 2 KB of its own, past what a kernel has without asking)
         const cudaError_t e = cudaFuncSetAttribute(lists_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                    static_cast<int>(BLOCKS_MAX_TOKENS / BLOCK_TOKENS / 32 * 8));
         if (e != cudaSuccess) return static_cast<int>(e);
