@@ -804,8 +804,8 @@ qsa_status qsa_block_select(const void *q, int32_t rows, int32_t H, const void *
                          HEAD_DIM * 2, static_cast<uint64_t>(H) * HEAD_DIM * 2, 1, TILE_M)) != QSA_OK)
         return st;
     const int32_t RVi = static_cast<int32_t>(RV);
-    if ((st = launch_rc(launch_block_rows(row_req, row_token, rows, H, num_reqs, i32(L.vreq), i32(L.vtok),
-                                          i32(L.vblk), d->status, stream))) != QSA_OK)
+    if ((st = launch_rc(launch_block_rows(row_req, row_token, rows, H, num_reqs, block_table, max_blocks,
+                                          num_pages, i32(L.vreq), i32(L.vtok), i32(L.vblk), d->status, stream))) != QSA_OK)
         return st;
     if ((st = launch_rc(timed(K_PLAN, stream, [&] {
              // groups of BR_ROWS virtual rows of one head, tiles of two 128-token blocks

@@ -211,7 +211,9 @@ attend_kernel(const AttendParams p)
             int32_t line_mine = -1;                        // page-token row of the cache, -1 = none
             if (pos_c >= 0) {
                 if (page_c >= 0 && page_c < p.num_pages) line_mine = page_c * p.page_tokens + (pos_c & (p.page_tokens - 1));
-                else record_error(p.status, ST_BAD_PAGE);
+                else if (tok_r > 0) record_error(p.status, ST_BAD_PAGE);
+                // (a row at token 0: padding, of a batch with nothing in use or of a
+                // request that has given its first page back)
             }
 #pragma unroll
             for (int j = 0; j < AT_TPW; ++j) {

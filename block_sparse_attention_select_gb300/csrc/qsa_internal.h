@@ -279,10 +279,11 @@ uint32_t score_smem_bytes();
 int launch_pad(float *logits, int64_t ld, int32_t R, const int32_t *row_vis, bool overlap, void *stream);
 // Block scorer rows: for v = h * R + r, vreq[v] = row_req[r] + h * num_reqs (or
 // -1 when row_req[r] is out of range), vtok[v] = row_token[r] + 1 visible
-// tokens (0 and flagged when negative), vblk[v] = visible 128-token blocks.
+// tokens (0 and flagged when negative; 0 at token 0 of a request without a first
+// page), vblk[v] = visible 128-token blocks.
 int launch_block_rows(const int32_t *row_req, const int32_t *row_token, int32_t R, int32_t H,
-                      int32_t num_reqs, int32_t *vreq, int32_t *vtok, int32_t *vblk, uint32_t *status,
-                      void *stream);
+                      int32_t num_reqs, const int32_t *block_table, int32_t max_blocks, int32_t num_pages,
+                      int32_t *vreq, int32_t *vtok, int32_t *vblk, uint32_t *status, void *stream);
 int launch_produce(const ProduceParams &p, int32_t max_tokens, void *stream);
 int launch_rope_table(float *table, int32_t n_blocks, int32_t rope_dim, double theta, void *stream);
 int launch_attend(const AttendParams &p, void *stream);

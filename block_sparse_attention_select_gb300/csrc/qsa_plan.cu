@@ -278,9 +278,12 @@ int launch_pad(float *logits, int64_t ld, int32_t R, const int32_t *row_vis, boo
 namespace qsa {
 namespace {
 
-// Virtual rows of the block scorer (one per query row and KV head).
+// Virtual rows of the block scorer (one per query row and KV head).  A row at token 0
+// whose page is not in the cache sees nothing: padding, of a batch with nothing in use or
+// of a request that has given its first page back.
 __global__ void block_rows_kernel(const int32_t *__restrict__ row_req, const int32_t *__restrict__ row_token,
-                                  int32_t R, int32_t H, int32_t num_reqs, int32_t *__restrict__ vreq,
+                                  int32_t R, int32_t H, int32_t num_reqs, const int32_t *__restrict__ block_table,
+                                  int32_t max_blocks, int32_t num_pages, int32_t *__restrict__ vreq,
                                   int32_t *__restrict__ vtok, int32_t *__restrict__ vblk, uint32_t *status)
 {
     const int64_t n = static_cast<int64_t>(R) * H;
@@ -292,7 +295,12 @@ __global__ void block_rows_kernel(const int32_t *__restrict__ row_req, const int
         const bool ok = b >= 0 && b < num_reqs && t >= 0;
         if (!ok && h == 0) record_error(status, ST_BAD_ROW);
         vreq[v] = ok ? b + h * num_reqs : -1;
-        const int32_t tok = ok ? t + 1 : 0;
+        bool sees = ok;
+        if (ok && t == 0) {
+            const int32_t page = block_table[static_cast<int64_t>(b) * max_blocks];
+            sees = page >= 0 && page < num_pages;
+        }
+        const int32_t tok = sees ? t + 1 : 0;
         vtok[v] = tok;
         vblk[v] = (tok + TILE_M - 1) / TILE_M;
     }
@@ -301,13 +309,13 @@ __global__ void block_rows_kernel(const int32_t *__restrict__ row_req, const int
 }  // namespace
 
 int launch_block_rows(const int32_t *row_req, const int32_t *row_token, int32_t R, int32_t H,
-                      int32_t num_reqs, int32_t *vreq, int32_t *vtok, int32_t *vblk, uint32_t *status,
-                      void *stream)
+                      int32_t num_reqs, const int32_t *block_table, int32_t max_blocks, int32_t num_pages,
+                      int32_t *vreq, int32_t *vtok, int32_t *vblk, uint32_t *status, void *stream)
 {
     const int64_t n = static_cast<int64_t>(R) * H;
     const int grid = static_cast<int>(std::min<int64_t>((n + 255) / 256, 1024));
-    block_rows_kernel<<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(row_req, row_token, R, H, num_reqs,
-                                                                          vreq, vtok, vblk, status);
+    block_rows_kernel<<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(row_req, row_token, R, H, num_reqs, block_table,
+                                                                          max_blocks, num_pages, vreq, vtok, vblk, status);
     return static_cast<int>(cudaGetLastError());
 }
 

@@ -187,7 +187,8 @@ qsa_status qsa_index_key_produce(const void *x, const float *pool_logit, int32_t
  * power of two in [8, 256].  Device-side problems (row_req out of range, a
  * token past the block table, a selected position at or past V, a page id
  * outside the cache) skip the token or the row and are reported by
- * qsa_get_device_status(). */
+ * qsa_get_device_status(), but for a row at token 0 whose page is outside the
+ * cache: it attends nothing, as padding (see qsa_batch_tables) has to. */
 qsa_status qsa_sparse_attention(const void *q, int32_t rows, int32_t hq, const void *k_cache, const void *v_cache,
                                 int32_t num_pages, int32_t page_tokens, int32_t hkv, int32_t head_dim,
                                 const int32_t *block_table, int32_t num_reqs, int32_t max_pages,
@@ -213,7 +214,9 @@ qsa_status qsa_sparse_attention(const void *q, int32_t rows, int32_t hq, const v
  * 1 <= H <= 16; 0 <= k <= QSA_MAX_K.  ws: qsa_block_select_workspace_bytes(rows,
  * H, max_blocks, k) bytes, 256-byte aligned.  Device-side problems (row_req
  * out of range, a negative token, a page id outside the cache) are reported
- * by qsa_get_device_status() (a bad page reads as zeros). */
+ * by qsa_get_device_status() (a bad page reads as zeros), but for a row at
+ * token 0 whose page is outside the cache: it selects nothing, as padding (see
+ * qsa_batch_tables) has to. */
 size_t qsa_block_select_workspace_bytes(int32_t rows, int32_t H, int32_t max_blocks, int32_t k);
 qsa_status qsa_block_select(const void *q, int32_t rows, int32_t H, const void *k_cache, int32_t num_pages,
                             const int32_t *block_table, int32_t num_reqs, int32_t max_blocks,
@@ -321,8 +324,10 @@ qsa_status qsa_chunk_attention(const void *q, int64_t q_stride, int32_t rows, in
  *   row_req, row_token, row_visible, slot [rows] (each NULL if not wanted): a row's
  *     request, its token's position t, (t + 1) / 4 (its visible compressed
  *     positions), its place page * page_tokens + t % page_tokens in the cache;
- *     rows behind the last request: the last row's request (0 if there is none), so
- *     that padding names a request with tokens, 0, 0 and -1;
+ *     rows behind the last request: the last row's request (0 if no row is in use),
+ *     0, 0 and -1.  Such a row sees token 0 at most, so the calls that take row maps
+ *     read little for it, and nothing where that request has no first page (yet, or
+ *     any more), which is no error then;
  *   state [3]: rows in use, free pages left, number of the first request that did
  *     not fit (n_reqs: none).  free_count may be state + 1.
  * No other two arrays may overlap.  A request with a negative length, or more
