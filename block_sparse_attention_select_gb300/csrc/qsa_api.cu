@@ -6,6 +6,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cfloat>
 #include <cmath>
 #include <cstring>
 #include <mutex>
@@ -1158,7 +1159,8 @@ qsa_status qsa_rotary_table(float *table, int32_t n_pos, int32_t rope_dim, doubl
     if (scaling) {
         const qsa_rope_scaling &s = *scaling;
         if (s.kind != QSA_ROPE_LINEAR && s.kind != QSA_ROPE_BASE && s.kind != QSA_ROPE_PARTS) return QSA_ERR_INVALID_ARG;
-        if (!positive(s.factor) || !positive(s.amplitude)) return QSA_ERR_INVALID_ARG;
+        // (the table is FP32: a larger amplitude would fill it with infinities)
+        if (!positive(s.factor) || !positive(s.amplitude) || s.amplitude > FLT_MAX) return QSA_ERR_INVALID_ARG;
         if (s.kind == QSA_ROPE_PARTS && (!positive(s.original) || !(s.slow >= 0.0) || !(s.fast > s.slow) || !std::isfinite(s.fast)))
             return QSA_ERR_INVALID_ARG;
         a.amplitude = s.amplitude;

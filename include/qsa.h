@@ -361,7 +361,8 @@ qsa_status qsa_batch_tables(const int32_t *new_len, const int32_t *ctx_len, int3
  *                    that turn `slow` times or less are slowed down, g = (original
  *                    f_j / 2 pi - slow) / (fast - slow) within [0, 1] in between.
  * rope_dim a multiple of 16 in [16, 256]; theta, factor, original and amplitude
- * positive and finite, 0 <= slow < fast, finite, and n_pos * f_j finite in FP64.
+ * positive and finite (the amplitude as an FP32 number), 0 <= slow < fast, finite, and
+ * n_pos * f_j finite in FP64.
  * table: 16-byte aligned, n_pos * rope_dim floats. */
 #define QSA_ROPE_LINEAR 1
 #define QSA_ROPE_BASE 2
