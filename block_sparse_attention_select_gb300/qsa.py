@@ -177,6 +177,10 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
+def _device_or_current(device):
+    return "cuda" if device is None else device              # (device number 0 is false)
+
+
 def _need(t, dtype, name):
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
@@ -210,7 +214,7 @@ def workspace_bytes(rows: int, row_capacity: int, k: int, flags: int = 0) -> int
 
 def alloc_workspace(rows: int, row_capacity: int, k: int, device=None) -> torch.Tensor:
     n = workspace_bytes(rows, row_capacity, k)
-    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+    return torch.empty(n, dtype=torch.uint8, device=_device_or_current(device))
 
 
 def index_score(q, w, keys: PagedKeys, row_req, row_visible, logits, ws=None, stream=None):
@@ -280,7 +284,7 @@ def select_paged_tokens_noalloc(q, w, keys: PagedKeys, row_req, row_visible, k: 
 def rope_table(n_blocks: int, rope_dim: int = 64, theta: float = 10000.0, device=None, stream=None):
     """cos / sin rows of the block-start positions 4i, i < n_blocks: FP32 [n_blocks, rope_dim]."""
     t = torch.empty((max(int(n_blocks), 1), max(int(rope_dim), 8)), dtype=torch.float32,
-                    device=device or "cuda")
+                    device=_device_or_current(device))
     _check(load().qsa_rope_table(_ptr(t), int(n_blocks), int(rope_dim), float(theta), _stream(stream)),
            "qsa_rope_table")
     return t
@@ -577,7 +581,7 @@ class Batch:
     def empty(cls, n_reqs: int, rows: int, device=None):
         """Uninitialised arrays for n_reqs requests and up to `rows` rows."""
         def make(k):
-            return torch.empty(int(k), dtype=torch.int32, device=device or "cuda")
+            return torch.empty(int(k), dtype=torch.int32, device=_device_or_current(device))
         return cls(make(n_reqs + 1), make(n_reqs), make(n_reqs), *(make(rows) for _ in range(4)), make(3))
 
 
@@ -621,7 +625,7 @@ class RopeScaling:
 
 def rotary_table(n_pos: int, rope_dim: int, theta: float = 10000.0, scaling: RopeScaling = None, device=None, stream=None):
     """Cosines and sines of positions 0 .. n_pos - 1: FP32 [n_pos, rope_dim]."""
-    device = torch.empty(0, device=device or "cuda").device
+    device = torch.empty(0, device=_device_or_current(device)).device
     with torch.cuda.device(device):
         t = torch.empty((int(n_pos), int(rope_dim)), dtype=torch.float32, device=device)
         _call(_device(device.index), stream, load().qsa_rotary_table, t.data_ptr(), int(n_pos), int(rope_dim), float(theta),
