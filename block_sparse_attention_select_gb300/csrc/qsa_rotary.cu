@@ -27,7 +27,7 @@ namespace {
 constexpr int ROT_THREADS = 256;
 constexpr int ROT_ROWS = 32;                 // rows of a CTA at most
 constexpr int ROT_BATCH = 4;                 // heads whose loads are in flight
-constexpr int ROT_HEADS = 10;                // heads that a thread goes through at most
+constexpr int ROT_HEADS = 10;                // heads that a thread goes through (more where a row has too many for its threads)
 
 // Eight pairs: a and b of each as FP16 halves of four words; neighbours: a0 b0 a1 b1 ...
 template <bool NEIGHBOURS>
@@ -93,24 +93,19 @@ rotary_kernel(const RotaryParams p)
     const int32_t items = p.items, per_row = items * p.slices, total = n_rows * per_row;
     const int32_t heads = p.q_heads + p.k_heads;
     // a thread's work: a row, a piece of each head (as two vectors of dims), every slices-th head
-    int32_t r, slice, item, d0, d1;
-    int64_t row;
-    auto decode = [&](int32_t i) {
-        r = i / per_row;
-        const int32_t in = i - r * per_row;
-        slice = in / items;
-        item = in - slice * items;
-        row = row0 + r;
-        if (item < turned) {
-            d0 = p.first + (NEIGHBOURS ? 16 : 8) * item;
-            d1 = d0 + (NEIGHBOURS ? 8 : p.rope_dim / 2);
-        } else {
-            // vectors outside the rotated part, in order
-            const int32_t v = 2 * (item - turned), skip = p.rope_dim / 8, before = p.first / 8;
-            d0 = 8 * (v < before ? v : v + skip);
-            d1 = 8 * (v + 1 < before ? v + 1 : v + 1 + skip);
-        }
-    };
+    const int32_t r = t / per_row, in_row = t - r * per_row, slice = in_row / items, item = in_row - slice * items;
+    const int64_t row = row0 + r;
+    const bool mine = t < total, turn = item < turned;
+    int32_t d0, d1;
+    if (turn) {
+        d0 = p.first + (NEIGHBOURS ? 16 : 8) * item;
+        d1 = d0 + (NEIGHBOURS ? 8 : p.rope_dim / 2);
+    } else {
+        // vectors outside the rotated part, in order
+        const int32_t v = 2 * (item - turned), skip = p.rope_dim / 8, before = p.first / 8;
+        d0 = 8 * (v < before ? v : v + skip);
+        d1 = 8 * (v + 1 < before ? v + 1 : v + 1 + skip);
+    }
     auto in_of = [&](int32_t h) {
         return h < p.q_heads ? p.q + (row * p.q_stride + static_cast<int64_t>(h) * p.head_dim)
                              : p.k + (row * p.k_stride + static_cast<int64_t>(h - p.q_heads) * p.head_dim);
@@ -129,50 +124,39 @@ rotary_kernel(const RotaryParams p)
         }
     };
     // the first values are on their way while the rows' positions are looked up
-    if (t < total) {
-        decode(t);
-        load(slice);
-    }
+    if (mine) load(slice);
     if (blockIdx.x == 0) flag_bad_requests(p.seq);
     Seq s;
     const int32_t b = requests_of_rows(p.seq, row0, n_rows, &s);
     if (t < n_rows) pos_s[t] = b < 0 ? -1 : s.p0 + (row0 + t - s.s0);
     __syncthreads();
 
-    for (int32_t i = t; i < total;) {
-        const int32_t at = pos_s[r];
-        const bool turn = item < turned;
-        float cs[8], sn[8];
-        if (at >= 0 && turn) {
-            const float4 *tab = reinterpret_cast<const float4 *>(p.table + static_cast<int64_t>(at) * p.rope_dim + 8 * item);
-            const float4 *tbs = reinterpret_cast<const float4 *>(p.table + static_cast<int64_t>(at) * p.rope_dim + p.rope_dim / 2 + 8 * item);
+    const int32_t at = mine ? pos_s[r] : -1;
+    float cs[8], sn[8];
+    if (at >= 0 && turn) {
+        const float4 *tab = reinterpret_cast<const float4 *>(p.table + static_cast<int64_t>(at) * p.rope_dim + 8 * item);
+        const float4 *tbs = reinterpret_cast<const float4 *>(p.table + static_cast<int64_t>(at) * p.rope_dim + p.rope_dim / 2 + 8 * item);
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const float4 c = __ldg(tab + k), s = __ldg(tbs + k);
-                cs[4 * k] = c.x, cs[4 * k + 1] = c.y, cs[4 * k + 2] = c.z, cs[4 * k + 3] = c.w;
-                sn[4 * k] = s.x, sn[4 * k + 1] = s.y, sn[4 * k + 2] = s.z, sn[4 * k + 3] = s.w;
-            }
-        } else {
+        for (int k = 0; k < 2; ++k) {
+            const float4 c = __ldg(tab + k), s = __ldg(tbs + k);
+            cs[4 * k] = c.x, cs[4 * k + 1] = c.y, cs[4 * k + 2] = c.z, cs[4 * k + 3] = c.w;
+            sn[4 * k] = s.x, sn[4 * k + 1] = s.y, sn[4 * k + 2] = s.z, sn[4 * k + 3] = s.w;
+        }
+    } else {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) cs[k] = 1.0f, sn[k] = 0.0f;
-        }
-        for (int32_t h0 = slice; at >= 0 && h0 < heads;) {
+        for (int k = 0; k < 8; ++k) cs[k] = 1.0f, sn[k] = 0.0f;
+    }
+    for (int32_t h0 = slice; at >= 0 && h0 < heads;) {
 #pragma unroll
-            for (int k = 0; k < ROT_BATCH; ++k) {
-                const int32_t h = h0 + k * p.slices;
-                if (h >= heads) break;
-                if (!turn && in_of(h) == out_of(h)) continue;     // in place
-                if (turn) rotate8<NEIGHBOURS>(x[k], y[k], cs, sn);
-                store_two<WIDE>(out_of(h) + d0, out_of(h) + d1, x[k], y[k]);
-            }
-            h0 += p.slices * ROT_BATCH;
-            if (h0 < heads) load(h0);
+        for (int k = 0; k < ROT_BATCH; ++k) {
+            const int32_t h = h0 + k * p.slices;
+            if (h >= heads) break;
+            if (!turn && in_of(h) == out_of(h)) continue;     // in place
+            if (turn) rotate8<NEIGHBOURS>(x[k], y[k], cs, sn);
+            store_two<WIDE>(out_of(h) + d0, out_of(h) + d1, x[k], y[k]);
         }
-        i += blockDim.x;
-        if (i < total) {
-            decode(i);
-            load(slice);
-        }
+        h0 += p.slices * ROT_BATCH;
+        if (h0 < heads) load(h0);
     }
     allow_next_grid();
 }
