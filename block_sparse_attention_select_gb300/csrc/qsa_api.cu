@@ -960,6 +960,17 @@ bool few_rows(int32_t rows, int32_t group, int32_t n_reqs)
 //   FP16, 256-wide                       83, 83   153, 113  136, 99   215, 120
 //   E4M3, 128-wide                       45, 74    86, 101   80, 87   134, 104
 //   E4M3, 256-wide                       63, 87    99, 119  114, 104  196, 125
+// and with other heads and batches (tokens x heads):
+//                                        1 x 16   16 x 1   3 x 8     24 x 1    32 x 1    6 x 8
+//   FP16, 128-wide, 8 over 32,768        12, 22   23, 31   21, 24    27, 33    29, 37    24, 27
+//   FP16, 128-wide, 64 over 16,384       29, 48   71, 84   57, 60    99, 94   110, 102   91, 69
+//   FP16, 256-wide, 200 over 8,192      148, 162 282, 289 316, 211  508, 318  541, 341  510, 244
+//   E4M3, 128-wide, 64 over 16,384       26, 64   76, 121  66, 84   112, 135  121, 147   96, 99
+//   E4M3, 256-wide, 200 over 8,192       94, 178 167, 320 188, 232  290, 353  307, 377  294, 269
+// So from the FP16 cache 24 is right for units of one token (9 heads and more, straight
+// from the selections) and for small batches; with fewer heads and many requests, 17 to
+// 24 pairs (two units to a request) are up to 1.6 times slower than in the other kernel.
+// The rows are those of the arrays, padding among them: the host knows no others.
 // The first takes whole tokens, so no more than 16 query heads to a KV head.
 bool few_block_rows(int32_t rows, int32_t group, int32_t n_reqs, bool e4m3)
 {

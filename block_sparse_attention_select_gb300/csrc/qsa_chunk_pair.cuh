@@ -75,7 +75,11 @@
 // which the lists and the join of partial results are some 8; tensor pipe 64%, as in
 // dense attention with such heads.  Four prompts of 8,192 (32 tokens, 25 blocks to a
 // list, 58% of use): 1,145 to 1,190 us, 67%.  Three E4M3 chunks of up to 517 (256-wide
-// heads, 34 blocks): 86 us, 46%, the helpers' codes again.  UNIT_COST 1, 2, 6 and 8
+// heads, 34 blocks): 86 us, 46%, the helpers' codes again.  Those cost most with whole
+// prompts of 128-wide heads, 2,085 us where the FP16 cache takes 1,153: each unit turns
+// each block of its list anew, and reading the contexts back first (qsa_kv_load, 25 us)
+// and attending the FP16 copy takes 1,158 in all, with the same bits (256-wide heads,
+// 24 over 2: 1,735 and 1,336; three chunks of 512: 171 and 170).  UNIT_COST 1, 2, 6 and 8
 // for lists: the prompts take 1,281, 1,231, 1,190 and 1,190 us, the E4M3 chunks 91, 89,
 // 91 and 92.  (An entry and its bits are loaded a tile ahead: looked up at the tile they
 // cost the softmax 180 clocks of 3,000.)
@@ -123,8 +127,8 @@ struct PairGeometry {
 struct BlockPairGeometry : PairGeometry {       // tiles are the blocks of a list
     static constexpr bool BLOCKS = true;
     // As measured, the reason has not been found: 128-wide prompts with 4, 3 and 2 slots,
-    // lists (4 of 8,192) 2,168, 2,086 and 2,181 us, dense (4 of 4,096) 613, 619 and 657;
-    // 256-wide heads differ by 1%.
+    // lists (4 of 8,192, 32 heads over 4) 2,168, 2,086 and 2,181 us, dense (4 of 4,096, 32
+    // over 8) 613, 619 and 657; 256-wide heads differ by 1%.
     static constexpr int RAWS = 3;
 };
 

@@ -36,9 +36,9 @@
 // while units are few a cluster of CTAs shares each, its sums joined through
 // distributed shared memory: no lists, no workspace, one launch.  16 of 1,440 blocks for
 // one token, 24 query heads over 2 KV heads of 128: 9.3 us (through lists and a join
-// 15.7).  64 tokens: 27 us (42), 5.0 TB/s with its first loads and last sums, 6.7
-// in between.  200 tokens from the E4M3 cache, 256-wide heads: 92 us (125 before the
-// lookups went piece by piece), 400 units in three rounds of 152.
+// 15.7).  64 tokens: 27 us (42) in a graph of equal calls, where most of their 135 MB
+// stay in the L2 cache, 29 in a stream of calls, 4.5 TB/s.  200 tokens from the E4M3 cache, 256-wide heads: 92 us (125 before the
+// lookups went piece by piece; 94 in a stream), 400 units in three rounds of 152.
 #pragma once
 #include <cuda.h>
 #include <cuda_fp16.h>

@@ -10,7 +10,12 @@
 // neighbours (6.3 and 6.4 TB/s; neighbours as two 16-byte accesses 59 us; 4 or 20
 // heads to a thread 57 to 60 us).  The 1,616-row chunk, 26 heads of 256 of which 64
 // dims rotate: 9 us (a thread for every head or two: 11 us), 64 single tokens 4 us,
-// a launch and two memory latencies.
+// a launch and two memory latencies.  (Times of ten equal calls in a graph, which find
+// what fits in the L2 cache there; in a stream of calls on other inputs 55, 13 and 11 us.)
+//
+// The table is made once per model: an FP64 sine and cosine per pair and position, 17.8
+// billion a second (184,320 positions of 64 dims 334 us, 2^20 of 128 3.8 ms), 50 times
+// what writing it takes, bound by the few FP64 units.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 

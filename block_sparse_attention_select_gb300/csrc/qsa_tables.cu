@@ -26,7 +26,9 @@ namespace cg = cooperative_groups;
 constexpr int TB_CTAS = 8, TB_THREADS = 1024, TB_WARPS = TB_THREADS / 32;
 // One CTA for small batches: it needs no barriers across the cluster, which cost 3 us
 // (64 single tokens 5.4 us, 8.3 with eight CTAs; 1,000 requests with 8,192 rows 9.5, 10.9;
-// 16 prompts of 16,384 rows 12.1, 9.8; of 65,536 rows 34.6, 12.9).
+// 2,048 with 8,192 rows 13.0, 11.7; 16 prompts of 16,384 rows 12.1, 9.8; of 65,536 rows
+// 34.6, 12.9; 1,024 single tokens 6.7, 9.4; 2,048 8.2, 10.0; 3,000 10.2, 10.5; 4,096
+// 12.5, 11.4; 8,192 36, 14).
 constexpr int TB_ONE_REQS = 2048, TB_ONE_ROWS = 8192;
 constexpr int TB_NEAR = 8191;                    // requests whose starts and positions fit in shared memory
 

@@ -612,7 +612,8 @@ class RopeScaling:
     """How a rotary table is scaled for long contexts: kind "linear" (angles over
     factor), "base" (a larger theta) or "parts" (slow pairs over factor, fast ones
     as they are: the ramp goes from `slow` to `fast` turns over the `original`
-    positions); amplitude multiplies cosines and sines."""
+    positions, linear in the turns, not in the pair's number, as some models have
+    it: those need a table of their own); amplitude multiplies cosines and sines."""
 
     KINDS = {"linear": QSA_ROPE_LINEAR, "base": QSA_ROPE_BASE, "parts": QSA_ROPE_PARTS}
 
@@ -710,7 +711,9 @@ def block_attention(q, sel, seq_start, pos_start, cache: KVCache, recent: int = 
     g, tokens up to p of the blocks sel[row, g, :] (int32 [T, hkv, k], -1 for none)
     and of its `recent` last blocks.  q FP16 [T, hq, head_dim] (rows may be
     strided); returns FP16 [T, hq, head_dim], zeros for a row that attends
-    nothing, rows past the last request left as they are."""
+    nothing, rows past the last request left as they are.  These rows count where
+    the call chooses its kernel: a captured decode step is quickest with T near the
+    number of requests."""
     n = _requests(seq_start, pos_start, cache)
     hq = q.shape[1] if q.dim() == 3 else 0
     qs = _row_stride(q, cache, hq, "q")

@@ -360,6 +360,9 @@ qsa_status qsa_batch_tables(const int32_t *new_len, const int32_t *ctx_len, int3
  *                    more over the `original` positions keep their speed, those
  *                    that turn `slow` times or less are slowed down, g = (original
  *                    f_j / 2 pi - slow) / (fast - slow) within [0, 1] in between.
+ *                    (A ramp in the turns.  Models whose ramp goes over the pair's
+ *                    number j, between two rounded ones, have other angles between
+ *                    the two: they need a table of their own making.)
  * rope_dim a multiple of 16 in [16, 256]; theta, factor, original and amplitude
  * positive and finite (the amplitude as an FP32 number), 0 <= slow < fast, finite, and
  * n_pos * f_j finite in FP64.
@@ -407,11 +410,19 @@ qsa_status qsa_rotary(const void *q, int64_t q_stride, int32_t q_heads, void *ou
  * batch, the cache and the workspace are as for qsa_chunk_attention (where falling
  * starts make two requests claim a row, the results of both are undefined); cache
  * slots that no row attends may hold anything, keys and values that some row attends
- * must be finite FP16 numbers.  One of two kernels serves the whole
- * batch, by its average of rows * (hq / hkv) / n_reqs (up to 24, or 32 from the E4M3
- * cache: the one for few rows, quickest with up to 32 blocks a row), so many single
- * tokens and a long chunk take less time in two calls.  0 <= k <= QSA_MAX_K, 0 <= recent <=
- * QSA_MAX_K, hq / hkv <= 128, max_pages * page_tokens <= 2^25
+ * must be finite FP16 numbers.  One of two kernels serves the whole batch: the one
+ * for few rows where hq / hkv <= 16 and rows * (hq / hkv) / n_reqs is 24 at most (32
+ * from the E4M3 cache), else the one for many.  `rows` is the length of the row
+ * arrays: rows behind the last request count, so a step captured for many more rows
+ * than it has tokens runs on the kernel for many (64 single tokens in 256 rows take
+ * 1.7 times as long as in 128, from the E4M3 cache twice); capture decode steps for
+ * rows near their number of requests.  The kernel for few rows is quickest with k +
+ * recent <= 32 (and rows <= n_reqs where hq / hkv <= 8): one launch, no lists.  A
+ * step's single tokens and a long chunk in one batch mostly take up to 15% less time
+ * than in two calls from the FP16 cache, but up to 40% more from the E4M3 cache.  Many
+ * rows over an E4M3 context (whole prompts) are quicker from an FP16 copy of it: read
+ * back by qsa_kv_load into rows that serve as the pages of another cache.  0 <= k <=
+ * QSA_MAX_K, 0 <= recent <= QSA_MAX_K, hq / hkv <= 128, max_pages * page_tokens <= 2^25
  * (QSA_ERR_UNSUPPORTED otherwise).  ws: qsa_block_attention_workspace_bytes(...)
  * bytes, with row_capacity = max_pages * page_tokens of the cache. */
 size_t qsa_block_attention_workspace_bytes(int32_t rows, int32_t hq, int32_t hkv, int32_t head_dim, int32_t k,

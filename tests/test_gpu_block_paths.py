@@ -121,3 +121,25 @@ def test_memory_made_for_a_stream_that_is_behind(lens, group, k, monkeypatch):
     side.synchronize()
     ok()
     check(b, copy, caches, sel, 1)
+
+
+@pytest.mark.parametrize("D,hkv,group", [(128, 2, 8), (256, 2, 12)])
+def test_many_rows_over_an_fp16_copy_of_an_e4m3_context(D, hkv, group):
+    """Contexts read back into rows that serve as another cache's pages: the same bits."""
+    P, lens = 32, [(300, 960), (270, 288), (1, 1408)]
+    b = Batch(87, lens, hkv=hkv, group=group, head_dim=D, page=P, quantised=True)
+    cache = device_cache(b, b.stored())
+    q, _, _, ss, ps = on_gpu(b)
+    dsel = torch.from_numpy(select(b, 4, 88)).cuda()
+    want = qsa.block_attention(q, dsel, ss, ps, cache, recent=1)
+    ends = np.cumsum([0] + [c for _, c in lens]).astype(np.int32)
+    k, v = qsa.kv_load(torch.from_numpy(ends).cuda(), torch.zeros_like(ps), int(ends[-1]), cache)
+    table = torch.full((3, 44), -1, dtype=torch.int32, device="cuda")
+    for r, (_, c) in enumerate(lens):
+        table[r, :c // P] = torch.arange(c // P, device="cuda") + int(ends[r]) // P
+    half = qsa.KVCache(k.view(-1, P, hkv, D), v.view(-1, P, hkv, D), table)
+    got = qsa.block_attention(q, dsel, ss, ps, half, recent=1)
+    assert qsa.last_launch_count() == 3
+    ok()
+    n = int(b.seq_start[-1])
+    assert torch.equal(got[:n], want[:n])
