@@ -154,7 +154,11 @@ attend_kernel(const AttendParams p)
         const int32_t tail0 = 4 * vis;                   // first token of the unfinished block
         // token stream: 4 tokens per selection slot (slots holding -1 or a bad
         // position contribute none), then the tail tokens tail0 .. tok_r
-        const int32_t n_stream = 4 * p.k + (tok_r - tail0 + 1);
+        // (no tail for a row at token 0 without a page: padding, of a batch with nothing in
+        // use or of a request that has given its first page back)
+        const bool paged = tok_r > 0 || static_cast<uint32_t>(p.block_table[static_cast<int64_t>(b) * p.max_pages]) <
+                                            static_cast<uint32_t>(p.num_pages);
+        const int32_t n_stream = 4 * p.k + (paged ? tok_r - tail0 + 1 : 0);
         const int32_t n_chunks = (n_stream + AT_CHUNK - 1) / AT_CHUNK;
         const int32_t *selr = p.sel + static_cast<int64_t>(r) * p.k;
         const __half *kc = static_cast<const __half *>(p.k_cache);
@@ -211,9 +215,7 @@ attend_kernel(const AttendParams p)
             int32_t line_mine = -1;                        // page-token row of the cache, -1 = none
             if (pos_c >= 0) {
                 if (page_c >= 0 && page_c < p.num_pages) line_mine = page_c * p.page_tokens + (pos_c & (p.page_tokens - 1));
-                else if (tok_r > 0) record_error(p.status, ST_BAD_PAGE);
-                // (a row at token 0: padding, of a batch with nothing in use or of a
-                // request that has given its first page back)
+                else record_error(p.status, ST_BAD_PAGE);
             }
 #pragma unroll
             for (int j = 0; j < AT_TPW; ++j) {
