@@ -9,7 +9,7 @@ from test_gpu_batch_tables import check, make, run
 pytestmark = pytest.mark.gpu
 
 
-@pytest.mark.parametrize("n", [2047, 2048, 2049, 3071, 3072, 5000, 8190, 8191, 8192])
+@pytest.mark.parametrize("n", [2047, 2048, 2049, 3071, 3073, 5000, 8190, 8191, 8192])
 def test_numbers_of_requests(n):
     new, ctx, table, free, fresh = make(75, n, 3, 60, 16)
     total = int(new.sum())
